@@ -30,6 +30,10 @@ BUF = dict(K_CODES=0, V_CODES=1, K_SCALE=2, V_SCALE=3, SLOT_POS=4, SCORE=5, SINK
            RING_K=15, RING_V=16, RING_SCORE=17)
 
 
+BLOCK_BUF = dict(K_CODES=0, V_CODES=1, K_SCALE=2, V_SCALE=3, K_EXACT=4, V_EXACT=5, TABLE=6, SEQ_POS=7, FREE=8,
+                 COUNTERS=9, TICKETS=10)
+
+
 class KvcConfig(ctypes.Structure):
     _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("bits", ctypes.c_int32),
@@ -40,6 +44,18 @@ class KvcConfig(ctypes.Structure):
 class KvcEvictParams(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("budget", ctypes.c_int32), ("recent", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("retention", ctypes.c_double)]
+
+
+class KvcPromptParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("d_slopes", ctypes.c_void_p), ("d_key_begin", ctypes.c_void_p), ("d_key_end", ctypes.c_void_p)]
+
+
+class KvcBlockConfig(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("max_batch", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("codes", ctypes.c_int32)]
 
 
 class KvcError(RuntimeError):
@@ -55,6 +71,25 @@ _I = ctypes.c_int32
 _SZ = ctypes.c_size_t
 
 _SIGS = {
+    "kvc_set_score_transform": (_I, [_P, ctypes.c_float, _P]),
+    "kvc_prompt_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "kvc_prompt_attention": (_I, [ctypes.POINTER(KvcPromptParams), _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "kvc_prefill_masked_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "kvc_prefill_attention_masked": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, ctypes.c_float, _I, _P, _P, _P, _SZ, _P]),
+    "kvc_block_state_bytes": (_SZ, [ctypes.POINTER(KvcBlockConfig)]),
+    "kvc_block_cache_create": (_I, [ctypes.POINTER(KvcBlockConfig), _P, _SZ, ctypes.POINTER(_P)]),
+    "kvc_block_cache_destroy": (None, [_P]),
+    "kvc_block_cache_reset": (_I, [_P, _P]),
+    "kvc_block_buffer": (_I, [_P, _I, ctypes.POINTER(_P), ctypes.POINTER(_SZ)]),
+    "kvc_block_length": (_I, [_P, _I, ctypes.POINTER(_I)]),
+    "kvc_block_sync_host": (_I, [_P, _P]),
+    "kvc_block_read_status": (_I, [_P, ctypes.POINTER(_I), _P]),
+    "kvc_block_last_launch_count": (_I, [_P]),
+    "kvc_block_release": (_I, [_P, _I, _I, _P]),
+    "kvc_block_append": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "kvc_block_workspace_bytes": (_SZ, [_P, _I]),
+    "kvc_block_attention": (_I, [_P, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
+    "kvc_block_read": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "kvc_version": (_I, []),
     "kvc_status_string": (ctypes.c_char_p, [_I]),
     "kvc_state_bytes": (_SZ, [ctypes.POINTER(KvcConfig)]),

@@ -139,6 +139,18 @@ class KVCache:
     def last_launch_count(self) -> int:
         return int(self.lib.kvc_last_launch_count(self.handle))
 
+    def set_score_transform(self, softcap: float = 0.0, slopes: torch.Tensor | None = None):
+        """Scores of every attention on this cache from now on: capped at
+        `softcap` by a tanh (0: not), then lowered by slopes[head] times the
+        distance between query and key (float32 [Hq], kept by the cache; None:
+        not)."""
+        if slopes is not None:
+            _need(slopes, torch.float32, "slopes", self.device, (self.num_q_heads,))
+        L.check(self.lib.kvc_set_score_transform(self.handle, ctypes.c_float(softcap),
+                                                 ctypes.c_void_p(slopes.data_ptr() if slopes is not None else None)),
+                "kvc_set_score_transform")
+        self._slopes = slopes
+
     # -- the decode step -----------------------------------------------------
     def quantize_append(self, k: torch.Tensor, v: torch.Tensor, seq_begin: int = 0, stream=None):
         """k, v: bf16 [batch, Hkv, n_new, 128]."""
@@ -201,11 +213,14 @@ class KVCache:
                                             ctypes.c_void_p(_stream_ptr(stream))), "kvc_compact_blocks")
 
     def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_begin: int = 0, out=None,
-                sm_scale: float | None = None, accumulate_h2o: bool = True, workspace=None, stream=None):
+                sm_scale: float | None = None, accumulate_h2o: bool = True, workspace=None, stream=None,
+                key_begin: torch.Tensor | None = None, key_end: torch.Tensor | None = None):
         """Prompt of fresh sequences: q bf16 [batch, Hq, n, 128], k/v bf16
         [batch, Hkv, n, 128] -> causal attention output bf16 [batch, Hq, n,
         128]; the tokens are appended and (accumulate_h2o) their H2O scores
-        set to the prompt attention's column sums."""
+        set to the prompt attention's column sums.  With key_begin or key_end
+        (int32 [batch, n]), query i sees the keys [key_begin[i], key_end[i])
+        instead (None: from 0, and up to itself)."""
         _need(q, torch.bfloat16, "q", self.device)
         _need(k, torch.bfloat16, "k", self.device)
         _need(v, torch.bfloat16, "v", self.device)
@@ -217,13 +232,28 @@ class KVCache:
         if out is None:
             out = torch.empty_like(q)
         _need(out, torch.bfloat16, "out", self.device, q.shape)
-        nbytes = self.lib.kvc_prefill_workspace_bytes(self.handle, batch, n)
+        masked = key_begin is not None or key_end is not None
+        for name, t in (("key_begin", key_begin), ("key_end", key_end)):
+            if t is not None:
+                _need(t, torch.int32, name, self.device, (batch, n))
+        nbytes = (self.lib.kvc_prefill_masked_workspace_bytes if masked
+                  else self.lib.kvc_prefill_workspace_bytes)(self.handle, batch, n)
         if workspace is None:
             raw = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
             off = (-raw.data_ptr()) % 256
             workspace = raw[off:off + nbytes]
         _need(workspace, torch.uint8, "workspace", self.device)
         scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
+        if masked:
+            L.check(self.lib.kvc_prefill_attention_masked(
+                self.handle, seq_begin, batch, n, ctypes.c_void_p(q.data_ptr()), ctypes.c_void_p(k.data_ptr()),
+                ctypes.c_void_p(v.data_ptr()), ctypes.c_void_p(out.data_ptr()), ctypes.c_float(scale),
+                L.KVC_ATTN_ACCUM_H2O if accumulate_h2o else 0,
+                ctypes.c_void_p(key_begin.data_ptr() if key_begin is not None else None),
+                ctypes.c_void_p(key_end.data_ptr() if key_end is not None else None),
+                ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), ctypes.c_void_p(_stream_ptr(stream))),
+                "kvc_prefill_attention_masked")
+            return out
         L.check(self.lib.kvc_prefill_attention(self.handle, seq_begin, batch, n, ctypes.c_void_p(q.data_ptr()),
                                                ctypes.c_void_p(k.data_ptr()), ctypes.c_void_p(v.data_ptr()),
                                                ctypes.c_void_p(out.data_ptr()), ctypes.c_float(scale),

@@ -16,9 +16,12 @@
 // the ring, only when a later append pushes it out of the window.
 #include "kvc_internal.h"
 #include "kvc_mma.h"
+#include "kvc_quant.h"
 
 namespace kvc {
 namespace {
+
+using namespace quant;
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
@@ -29,20 +32,6 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // (from its block-table row): codes, scale, and for K the position and the
 // initial score.  Integer codes, or with E4M3 codes (s.fp8) scale =
 // amax / 448 and each x / scale converted to FP8.
-// Four fp32 values -> four FP8 E4M3 codes (byte i = value i), rounded to
-// nearest even and saturated to +-448 by the conversion instruction (which
-// packs its first source into the upper byte).
-__device__ __forceinline__ uint32_t e4m3x4(float y0, float y1, float y2, float y3) {
-  uint32_t w;
-  asm("{\n .reg .b16 l, h;\n"
-      " cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
-      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
-      " mov.b32 %0, {l, h};\n}"
-      : "=r"(w)
-      : "f"(y0), "f"(y1), "f"(y2), "f"(y3));
-  return w;
-}
-
 template <int BITS>
 __device__ __forceinline__ void quantize_row_blk(const DevState& s, int blk, int h, int kv, int slot, int p,
                                                  float score, uint2 raw, int lane) {
@@ -269,59 +258,6 @@ __global__ void append_alloc_kernel(DevState s, int seq_begin, int batch, int n_
     s.plan[2 * b] = ok ? slots : -1;
     s.plan[2 * b + 1] = pos;
   }
-}
-
-// Integer codes of 8 values of a row, as words whose low byte is the
-// two's-complement 8-bit code and whose low nibble is the 4-bit one
-// (0x4B400000 + code: the fp32 bit pattern of 1.5 * 2^23 + code).
-//
-// code = round-half-even(x / scale) with x / scale the IEEE fp32 quotient,
-// clamped, as in quantize_row.  Here the code comes, where that decides it,
-// from the exact product P = x * inv, inv an approximate reciprocal of the
-// scale (relative error at most 2^-23, one ulp): P differs from the rounded
-// quotient by at most 2^-23 |x / scale| + 2^-24 |x / scale| < 2^-14.4,
-// because |x| <= amax gives |x / scale| <= qmax (1 + 2^-23) < 128 (the scale
-// is a normal number here; a subnormal one has an infinite reciprocal under
-// ftz).  One fused multiply-add rounds P + 1.5 * 2^23 to the integer r
-// nearest P (round to nearest even in the binade of unit spacing); a second
-// gives P - r.  Where |P - r| < 1/2 - 2^-12 the quotient lies in the same
-// unit interval around r and rounds to r, and |r| <= qmax needs no clamp.
-// Elsewhere (P within about 2^-12 of a half-integer, or not finite) the
-// division decides.  About one value in 2^11 takes that path.
-__device__ __forceinline__ float rcp_approx_ftz(float a) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
-  return r;
-}
-
-template <int BITS>
-__device__ __forceinline__ void int_codes8(const float* x, float scale, float inv, uint32_t (&w)[8]) {
-  constexpr float kM = 12582912.0f;  // 1.5 * 2^23
-  constexpr float kNear = 0.5f - 0x1p-12f;
-  constexpr int kLo = BITS == 8 ? -127 : -8;
-  constexpr int kHi = BITS == 8 ? 127 : 7;
-  bool slow = false;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float sm = __fmaf_rn(x[e], inv, kM);
-    w[e] = __float_as_uint(sm);
-    slow |= !(fabsf(__fmaf_rn(x[e], inv, -__fadd_rn(sm, -kM))) < kNear);
-  }
-  if (slow) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float r = __fadd_rn(__fmaf_rn(x[e], inv, kM), -kM);
-      if (!(fabsf(__fmaf_rn(x[e], inv, -r)) < kNear)) {
-        const int q = scale > 0.0f ? min(max(__float2int_rn(__fdiv_rn(x[e], scale)), kLo), kHi) : 0;
-        w[e] = 0x4B400000u + (uint32_t)q;
-      }
-    }
-  }
-}
-
-// the low bytes of four words, in order
-__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // Rows spread over (token chunk, sequence) CTAs.  A unit is 4 adjacent

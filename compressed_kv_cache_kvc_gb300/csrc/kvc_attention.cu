@@ -82,9 +82,10 @@ struct Geom {
   static constexpr int kV = 16 * kRowBytes;
   static constexpr int kKS = 32 * kRowBytes;
   static constexpr int kVS = kKS + 64;
-  static constexpr int kStage = kVS + 64;
+  static constexpr int kPos = kVS + 64;                  // 16 slot positions (distance bias only)
   static constexpr int kStages = 4;
-  static constexpr int kSmem = kWarps * kStages * kStage;
+  static __host__ __device__ constexpr int stage(bool bias) { return kPos + (bias ? 64 : 0); }
+  static __host__ __device__ constexpr int smem(bool bias) { return kWarps * kStages * stage(bias); }
   static constexpr int kChunksPerRow = kRowBytes / 16;
   static constexpr int kCopies = 16 * kRowBytes / 512;   // 16-byte copies per lane per K (or V) run
   static __host__ __device__ constexpr int chunk_off(int t, int j) {
@@ -127,7 +128,11 @@ __device__ __forceinline__ void copy_codes(bool pred, uint32_t sb, const uint32_
 
 // FP8: the 8-bit codes are FP8 E4M3 instead of INT8 (same layout, same
 // scales; only the code -> fp16 conversion differs, and no offset).
-template <int BITS, bool FP8 = false>
+// MOD: score transforms, kModCap | kModBias (the bias brings the slots'
+// positions into the stage, 64 bytes a page; the logits spilled for H2O are
+// the transformed ones).
+constexpr int kModCap = 1, kModBias = 2;
+template <int BITS, bool FP8 = false, int MOD = 0>
 __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int seq_begin, int batch,
                                                                  const uint16_t* __restrict__ q,
                                                                  float qk_scale_log2, AttnWork w,
@@ -135,6 +140,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
   using Gm = Geom<BITS>;
   constexpr int STAGES = Gm::kStages;
   constexpr int RB = Gm::kRowBytes;
+  constexpr bool kCap = (MOD & kModCap) != 0, kBias = (MOD & kModBias) != 0;
+  constexpr int kStageBytes = Gm::stage(kBias);
   static_assert((STAGES & (STAGES - 1)) == 0, "ring positions are page index & (STAGES - 1)");
   constexpr bool kOffset = !FP8;  // integer codes as offset subnormals
   // the code offset times 2^-24 (K: subtracted from each dot product in units
@@ -165,8 +172,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
   const long long F1 = (long long)(cta + 1) * T / N;
 
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t ring_s = smem_u32(smem) + warp * STAGES * Gm::kStage;
-  const uint8_t* ring = smem + warp * STAGES * Gm::kStage;
+  const uint32_t ring_s = smem_u32(smem) + warp * STAGES * kStageBytes;
+  const uint8_t* ring = smem + warp * STAGES * kStageBytes;
 
   // what this lane copies of a page: chunks lane + 32 i of the K and V runs,
   // and (lanes 0..7) one 16-byte chunk of the 16 K or 16 V scales
@@ -194,6 +201,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
   for (int k = 0; k < 4; ++k)
     v_off[k] = Gm::kV + (BITS == 8 ? Gm::chunk_off(4 * c + k, r) : Gm::chunk_off(4 * c + k, r >> 1) + 8 * (r & 1));
   const int s_off = Gm::kKS + 8 * r;
+  // lanes 8..11 copy the page's 16 positions
+  const uint32_t pos_soff = Gm::kPos + 16 * (lane & 3);
   // L2 policies: the KV stream is read once (evict first); the logit spill is
   // read back by the next kernel (evict last)
   const uint64_t kv_pol = l2_evict_first();
@@ -234,6 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
     const uint8_t* kb = s.k_codes + (size_t)h * (16 * RB) + 16 * lane;
     const uint8_t* vb = s.v_codes + (size_t)h * (16 * RB) + 16 * lane;
     const float* scb = sc_gbase + (size_t)h * kPage;
+    const int32_t* posb = s.slot_pos + (size_t)h * kPage + 4 * (lane & 3);
     const uint32_t code_stride = (uint32_t)hkv * (16 * RB), sc_stride = (uint32_t)hkv * kPage;
 
     // page k of this warp into stage k & (STAGES - 1), one commit group (empty
@@ -247,10 +257,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
       const bool ok = (unsigned)blk < (unsigned)s.num_blocks;
       const int slot_issue = k & (STAGES - 1);
       stage_ok = (stage_ok & ~(1u << slot_issue)) | ((uint32_t)ok << slot_issue);
-      const uint32_t sb = ring_s + slot_issue * Gm::kStage;
+      const uint32_t sb = ring_s + slot_issue * kStageBytes;
       const size_t off = (size_t)(uint32_t)blk * code_stride;
       copy_codes<BITS>(ok, sb, cp_d, kb + off, vb + off, kv_pol);
       cp_async16_if(ok && lane < 8, sb + sc_soff, scb + (size_t)(uint32_t)blk * sc_stride);
+      if (kBias) cp_async16_if(ok && lane >= 8 && lane < 12, sb + pos_soff, posb + (size_t)(uint32_t)blk * sc_stride);
       cp_async_commit();
     };
 
@@ -342,9 +353,15 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
       const int e0 = __shfl_sync(0xffffffffu, e, (2 * c) * 4);
       const int e1 = __shfl_sync(0xffffffffu, e, (2 * c + 1) * 4);
       // offset codes carry 2^-24: scale the dot products back by 2^24
-      cq0 = qk_scale_log2 * pow2i((kOffset ? 24 : 0) - e0);
-      cq1 = qk_scale_log2 * pow2i((kOffset ? 24 : 0) - e1);
+      const float qk = kCap ? w.mod.y_scale : qk_scale_log2;
+      cq0 = qk * pow2i((kOffset ? 24 : 0) - e0);
+      cq1 = qk * pow2i((kOffset ? 24 : 0) - e1);
     }
+
+    // distance bias: this lane's two slopes, the query's position
+    const float sl0 = kBias && 2 * c < G ? slope_log2(w.mod, h * G + 2 * c) : 0.0f;
+    const float sl1 = kBias && 2 * c + 1 < G ? slope_log2(w.mod, h * G + 2 * c + 1) : 0.0f;
+    const int q_pos = kBias ? s.seq_pos[b] - 1 : 0;
 
     float oacc[8][4];
 #pragma unroll
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
       for (int pp = 0; pp < NP; ++pp) {
         const int sc = (k + pp) & (STAGES - 1);
         const bool blk_ok = (stage_ok >> sc) & 1u;
-        st[pp] = ring + sc * Gm::kStage;
+        st[pp] = ring + sc * kStageBytes;
         slot0[pp] = (pg_a + warp + kWarps * (k + pp)) * kPage;
         v0[pp] = FULL || (blk_ok && (slot0[pp] + 2 * r < S));
         v1[pp] = FULL || (blk_ok && (slot0[pp] + 2 * r + 1 < S));
@@ -445,10 +462,23 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
       float lg[NP][4];
 #pragma unroll
       for (int pp = 0; pp < NP; ++pp) {
-        lg[pp][0] = v0[pp] ? acc[pp][0] * (skv[pp].x * cq0) : -INFINITY;  // slot 2r,   head 2c
-        lg[pp][1] = v0[pp] ? acc[pp][1] * (skv[pp].x * cq1) : -INFINITY;  // slot 2r,   head 2c+1
-        lg[pp][2] = v1[pp] ? acc[pp][2] * (skv[pp].y * cq0) : -INFINITY;  // slot 2r+1, head 2c
-        lg[pp][3] = v1[pp] ? acc[pp][3] * (skv[pp].y * cq1) : -INFINITY;  // slot 2r+1, head 2c+1
+        lg[pp][0] = acc[pp][0] * (skv[pp].x * cq0);  // slot 2r,   head 2c
+        lg[pp][1] = acc[pp][1] * (skv[pp].x * cq1);  // slot 2r,   head 2c+1
+        lg[pp][2] = acc[pp][2] * (skv[pp].y * cq0);  // slot 2r+1, head 2c
+        lg[pp][3] = acc[pp][3] * (skv[pp].y * cq1);  // slot 2r+1, head 2c+1
+        if (kCap) cap_scores(w.mod, lg[pp]);
+        if (kBias) {
+          const int2 ps = *reinterpret_cast<const int2*>(st[pp] + Gm::kPos + 8 * r);
+          const float d0 = (float)(q_pos - ps.x), d1 = (float)(q_pos - ps.y);
+          lg[pp][0] = fmaf(-sl0, d0, lg[pp][0]);
+          lg[pp][1] = fmaf(-sl1, d0, lg[pp][1]);
+          lg[pp][2] = fmaf(-sl0, d1, lg[pp][2]);
+          lg[pp][3] = fmaf(-sl1, d1, lg[pp][3]);
+        }
+        if (!FULL) {
+          if (!v0[pp]) lg[pp][0] = lg[pp][1] = -INFINITY;
+          if (!v1[pp]) lg[pp][2] = lg[pp][3] = -INFINITY;
+        }
         st2_if_hint(sp0, lg0p + slot0[pp], lg[pp][0], lg[pp][2], spill_pol);
         st2_if_hint(sp1, lg1p + slot0[pp], lg[pp][1], lg[pp][3], spill_pol);
       }
@@ -725,55 +755,78 @@ __global__ void __launch_bounds__(kMergeThreads, 2) attn_merge_kernel(DevState s
   }
 }
 
-// cudaFuncSetAttribute is per device and per kernel: one flag per (BITS, device).
-template <int BITS, bool FP8 = false>
+// cudaFuncSetAttribute is per device and per kernel: one flag per (variant, device).
+template <int BITS, bool FP8, int MOD>
 cudaError_t ensure_split_smem() {
   static int done[64] = {0};
-  return opt_in_smem(reinterpret_cast<const void*>(attn_split_kernel<BITS, FP8>), Geom<BITS>::kSmem, done);
+  return opt_in_smem(reinterpret_cast<const void*>(attn_split_kernel<BITS, FP8, MOD>),
+                     Geom<BITS>::smem((MOD & kModBias) != 0), done);
 }
 
-template <int BITS, bool FP8 = false>
+template <int BITS, bool FP8, int MOD>
 int split_ctas_per_sm() {
   static int cached[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   if (dev < 64 && cached[dev] > 0) return cached[dev];
-  if (ensure_split_smem<BITS, FP8>() != cudaSuccess) return 1;
+  if (ensure_split_smem<BITS, FP8, MOD>() != cudaSuccess) return 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_split_kernel<BITS, FP8>, kWarps * 32,
-                                                    Geom<BITS>::kSmem) !=
-          cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_split_kernel<BITS, FP8, MOD>, kWarps * 32,
+                                                    Geom<BITS>::smem((MOD & kModBias) != 0)) != cudaSuccess ||
       n < 1)
     n = 1;
   if (dev < 64) cached[dev] = n;
   return n;
 }
 
-}  // namespace
+template <int BITS, bool FP8>
+int split_ctas_per_sm_mod(int mod) {
+  switch (mod) {
+    case 0: return split_ctas_per_sm<BITS, FP8, 0>();
+    case kModCap: return split_ctas_per_sm<BITS, FP8, kModCap>();
+    case kModBias: return split_ctas_per_sm<BITS, FP8, kModBias>();
+    default: return split_ctas_per_sm<BITS, FP8, kModCap | kModBias>();
+  }
+}
 
-int attention_smem_bytes(int bits) { return bits == 8 ? Geom<8>::kSmem : Geom<4>::kSmem; }
+int mod_of(const ScoreMod& m) { return (m.c2 > 0.0f ? kModCap : 0) | (m.slopes != nullptr ? kModBias : 0); }
 
-int attention_ctas_per_sm(int bits, bool fp8) {
-  if (bits == 8) return fp8 ? split_ctas_per_sm<8, true>() : split_ctas_per_sm<8>();
-  return split_ctas_per_sm<4>();
+template <int BITS, bool FP8, int MOD>
+cudaError_t launch_split_t(const DevState& s, int seq_begin, int batch, const uint16_t* q, float qk_scale_log2,
+                           const AttnWork& w, bool spill, cudaStream_t st) {
+  const cudaError_t e = ensure_split_smem<BITS, FP8, MOD>();
+  if (e != cudaSuccess) return e;
+  attn_split_kernel<BITS, FP8, MOD><<<w.ncta, kWarps * 32, Geom<BITS>::smem((MOD & kModBias) != 0), st>>>(
+      s, seq_begin, batch, q, qk_scale_log2, w, spill);
+  return cudaGetLastError();
 }
 
 template <int BITS, bool FP8>
-cudaError_t launch_split_t(const DevState& s, int seq_begin, int batch, const uint16_t* q, float qk_scale_log2,
-                           const AttnWork& w, bool spill, cudaStream_t st) {
-  const cudaError_t e = ensure_split_smem<BITS, FP8>();
-  if (e != cudaSuccess) return e;
-  attn_split_kernel<BITS, FP8><<<w.ncta, kWarps * 32, Geom<BITS>::kSmem, st>>>(s, seq_begin, batch, q,
-                                                                               qk_scale_log2, w, spill);
-  return cudaGetLastError();
+cudaError_t launch_split_mod(const DevState& s, int seq_begin, int batch, const uint16_t* q, float qk_scale_log2,
+                             const AttnWork& w, bool spill, cudaStream_t st) {
+  switch (mod_of(w.mod)) {
+    case 0: return launch_split_t<BITS, FP8, 0>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
+    case kModCap: return launch_split_t<BITS, FP8, kModCap>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
+    case kModBias: return launch_split_t<BITS, FP8, kModBias>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
+    default:
+      return launch_split_t<BITS, FP8, kModCap | kModBias>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
+  }
+}
+
+}  // namespace
+
+int attention_ctas_per_sm(int bits, bool fp8, const ScoreMod& mod) {
+  const int m = mod_of(mod);
+  if (bits == 8) return fp8 ? split_ctas_per_sm_mod<8, true>(m) : split_ctas_per_sm_mod<8, false>(m);
+  return split_ctas_per_sm_mod<4, false>(m);
 }
 
 cudaError_t launch_attention_split(const DevState& s, int seq_begin, int batch, const uint16_t* q,
                                    float qk_scale_log2, const AttnWork& w, bool spill, cudaStream_t st) {
   if (s.bits == 8)
-    return s.fp8 ? launch_split_t<8, true>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st)
-                 : launch_split_t<8, false>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
-  return launch_split_t<4, false>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
+    return s.fp8 ? launch_split_mod<8, true>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st)
+                 : launch_split_mod<8, false>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
+  return launch_split_mod<4, false>(s, seq_begin, batch, q, qk_scale_log2, w, spill, st);
 }
 
 cudaError_t launch_attention_merge(const DevState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,

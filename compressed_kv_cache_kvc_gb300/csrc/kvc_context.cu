@@ -79,6 +79,7 @@ struct CtxArgs {
   int n, groups, s_cap;
   int cs_row;         // 4 + s_cap + W: sinks, pool slots, window positions from rlo
   float qk_scale_log2;
+  ScoreMod mod;
   int accumulate;
 };
 
@@ -125,9 +126,12 @@ constexpr int kRingStage = 2 * 16 * kRingRow * 2;
 // other forms keep the compiler's own choice (a minimum of 0 CTAs per SM
 // states none; a minimum of 1 made it spend up to 255 registers on pass 0
 // and INT4 pass 1; the 8-bit window forms would spill).
-template <int BITS, bool FP8, int PASS, bool WIN>
+// MOD: the scores are capped and / or biased by distance (a.mod), the
+// positions of the pool's slots read from global memory (L2).
+template <int BITS, bool FP8, int PASS, bool WIN, bool MOD>
 __global__ void __launch_bounds__(kCtxThreads,
-                                  (PASS == 1 && ((BITS == 8 && !FP8 && !WIN) || (BITS == 4 && WIN)))
+                                  MOD ? 0
+                                  : (PASS == 1 && ((BITS == 8 && !FP8 && !WIN) || (BITS == 4 && WIN)))
                                       ? 3
                                       : ((PASS == 0 && BITS == 4) ? 5 : 0))
     ctx_attn_kernel(DevState s, int seq_begin, CtxArgs a) {
@@ -236,6 +240,20 @@ __global__ void __launch_bounds__(kCtxThreads,
         for (int e2 = threadIdx.x; e2 < L.P1 - L.rlo; e2 += kCtxThreads) cs_ring[e2] = 0.0f;
     }
 
+    // score transforms: the rows' query positions and slopes
+    const float qk_scale = MOD && a.mod.c2 > 0.0f ? a.mod.y_scale : a.qk_scale_log2;
+    const int qp_lo = L.P0 + i_lo, qp_hi = L.P0 + i_hi;
+    const float sl_lo = MOD && ok_lo ? slope_log2(a.mod, h * G + r_lo % G) : 0.0f;
+    const float sl_hi = MOD && ok_hi ? slope_log2(a.mod, h * G + r_hi % G) : 0.0f;
+    // four logits, rows (lo, lo, hi, hi) x keys at positions (p0, p1)
+    auto transform4 = [&](float (&x)[4], int p0, int p1) {
+      if (a.mod.c2 > 0.0f) cap_scores(a.mod, x);
+      x[0] = fmaf(-sl_lo, (float)(qp_lo - p0), x[0]);
+      x[1] = fmaf(-sl_lo, (float)(qp_lo - p1), x[1]);
+      x[2] = fmaf(-sl_hi, (float)(qp_hi - p0), x[2]);
+      x[3] = fmaf(-sl_hi, (float)(qp_hi - p1), x[3]);
+    };
+
     // ---- query fragments (A operand), rows r_lo / r_hi, scaled by 2^e into
     // fp16 range; the offset sum per row; the sink logits per row
     uint32_t qa[8][4];
@@ -290,7 +308,8 @@ __global__ void __launch_bounds__(kCtxThreads,
           }
           acc += __shfl_xor_sync(0xffffffffu, acc, 1);
           acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-          sk_lg[rr][sk] = acc * a.qk_scale_log2;
+          sk_lg[rr][sk] = MOD ? transform_score(a.mod, acc * qk_scale, rr ? sl_hi : sl_lo, (rr ? qp_hi : qp_lo) - sk)
+                              : acc * a.qk_scale_log2;
         }
         const float f2e = pow2i(e[rr]);
 #pragma unroll
@@ -333,7 +352,7 @@ __global__ void __launch_bounds__(kCtxThreads,
           qs += __shfl_xor_sync(0xffffffffu, qs, 1);
           qs += __shfl_xor_sync(0xffffffffu, qs, 2);
         }
-        const float cq = a.qk_scale_log2 * pow2i((kOffset ? 24 : 0) - e[rr]);
+        const float cq = qk_scale * pow2i((kOffset ? 24 : 0) - e[rr]);
         if (rr == 0) {
           ch_lo = kOffK * qs;
           cq_lo = cq;
@@ -475,6 +494,12 @@ __global__ void __launch_bounds__(kCtxThreads,
           lg[t][1] = acc[t][1] * (sk.y * cq_lo);
           lg[t][2] = acc[t][2] * (sk.x * cq_hi);
           lg[t][3] = acc[t][3] * (sk.y * cq_hi);
+          if (MOD) {
+            int2 ps = make_int2(0, 0);
+            if (a.mod.slopes != nullptr)
+              ps = *reinterpret_cast<const int2*>(s.slot_pos + ((size_t)blk_of(p) * hkv + h) * kPage + 8 * t + 2 * tq);
+            transform4(lg[t], ps.x, ps.y);
+          }
           if (!full) {
             if (sl >= lim_lo) lg[t][0] = -INFINITY;
             if (sl + 1 >= lim_lo) lg[t][1] = -INFINITY;
@@ -669,7 +694,7 @@ __global__ void __launch_bounds__(kCtxThreads,
           qb[st][2 + rr] = pack_bf16x2(x2, x3);
         }
       }
-      const float cr_lo = a.qk_scale_log2 * pow2i(-e_row[0]), cr_hi = a.qk_scale_log2 * pow2i(-e_row[1]);
+      const float cr_lo = qk_scale * pow2i(-e_row[0]), cr_hi = qk_scale * pow2i(-e_row[1]);
       const int re_lo = ok_lo ? ctx_ring_end(L, i_lo) : 0, re_hi = ok_hi ? ctx_ring_end(L, i_hi) : 0;
       // the PV operand of window tokens: p in the units of the pool's
       // accumulators (their sum is scaled by 2^24 (2^20) and 2^E at the end)
@@ -726,10 +751,15 @@ __global__ void __launch_bounds__(kCtxThreads,
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int ps = pos0 + 8 * t + 2 * tq;
-            lg[t][0] = ps < re_lo ? acc[t][0] * cr_lo : -INFINITY;
-            lg[t][1] = ps + 1 < re_lo ? acc[t][1] * cr_lo : -INFINITY;
-            lg[t][2] = ps < re_hi ? acc[t][2] * cr_hi : -INFINITY;
-            lg[t][3] = ps + 1 < re_hi ? acc[t][3] * cr_hi : -INFINITY;
+            lg[t][0] = acc[t][0] * cr_lo;
+            lg[t][1] = acc[t][1] * cr_lo;
+            lg[t][2] = acc[t][2] * cr_hi;
+            lg[t][3] = acc[t][3] * cr_hi;
+            if (MOD) transform4(lg[t], ps, ps + 1);
+            if (ps >= re_lo) lg[t][0] = -INFINITY;
+            if (ps + 1 >= re_lo) lg[t][1] = -INFINITY;
+            if (ps >= re_hi) lg[t][2] = -INFINITY;
+            if (ps + 1 >= re_hi) lg[t][3] = -INFINITY;
           }
           if (PASS == 0) {
             const float t_lo = fmaxf(fmaxf(lg[0][0], lg[0][1]), fmaxf(lg[1][0], lg[1][1]));
@@ -940,30 +970,34 @@ __global__ void __launch_bounds__(kCtxThreads,
   }
 }
 
-template <int BITS, bool FP8, int PASS, bool WIN>
+template <int BITS, bool FP8, int PASS, bool WIN, bool MOD>
 cudaError_t launch_ctx_t(const DevState& s, int seq_begin, int batch, const CtxArgs& a, cudaStream_t st) {
   using Gm = CtxGeom<BITS>;
   const int ring_bytes = WIN && 2 * kRingStage > kCtxStages * Gm::kStage ? 2 * kRingStage : kCtxStages * Gm::kStage;
   const int smem = ring_bytes + kCtxBtStage * 4;
   static int done[64] = {0};
-  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(ctx_attn_kernel<BITS, FP8, PASS, WIN>), smem, done);
+  const cudaError_t e =
+      opt_in_smem(reinterpret_cast<const void*>(ctx_attn_kernel<BITS, FP8, PASS, WIN, MOD>), smem, done);
   if (e != cudaSuccess) return e;
   dim3 grid(a.groups, batch * s.hkv);
-  ctx_attn_kernel<BITS, FP8, PASS, WIN><<<grid, kCtxThreads, smem, st>>>(s, seq_begin, a);
+  ctx_attn_kernel<BITS, FP8, PASS, WIN, MOD><<<grid, kCtxThreads, smem, st>>>(s, seq_begin, a);
   return cudaGetLastError();
 }
 
-template <int BITS, bool FP8, bool WIN>
+template <int BITS, bool FP8, bool WIN, bool MOD>
 cudaError_t launch_ctx_passes(const DevState& s, int seq_begin, int batch, const CtxArgs& a, cudaStream_t st) {
-  cudaError_t e = launch_ctx_t<BITS, FP8, 0, WIN>(s, seq_begin, batch, a, st);
-  if (e == cudaSuccess) e = launch_ctx_t<BITS, FP8, 1, WIN>(s, seq_begin, batch, a, st);
+  cudaError_t e = launch_ctx_t<BITS, FP8, 0, WIN, MOD>(s, seq_begin, batch, a, st);
+  if (e == cudaSuccess) e = launch_ctx_t<BITS, FP8, 1, WIN, MOD>(s, seq_begin, batch, a, st);
   return e;
 }
 
 template <int BITS, bool FP8>
 cudaError_t launch_ctx_codes(const DevState& s, int seq_begin, int batch, const CtxArgs& a, cudaStream_t st) {
-  return s.ring > 0 ? launch_ctx_passes<BITS, FP8, true>(s, seq_begin, batch, a, st)
-                    : launch_ctx_passes<BITS, FP8, false>(s, seq_begin, batch, a, st);
+  if (a.mod.c2 > 0.0f || a.mod.slopes != nullptr)
+    return s.ring > 0 ? launch_ctx_passes<BITS, FP8, true, true>(s, seq_begin, batch, a, st)
+                      : launch_ctx_passes<BITS, FP8, false, true>(s, seq_begin, batch, a, st);
+  return s.ring > 0 ? launch_ctx_passes<BITS, FP8, true, false>(s, seq_begin, batch, a, st)
+                    : launch_ctx_passes<BITS, FP8, false, false>(s, seq_begin, batch, a, st);
 }
 
 }  // namespace
@@ -976,7 +1010,7 @@ int ctx_groups(int n, int group) {
 
 cudaError_t launch_ctx_attention(const DevState& s, int seq_begin, int batch, int n, const uint16_t* q,
                                  uint16_t* out, float* stats, float* colsum, int* ticket, int s_cap,
-                                 float qk_scale_log2, bool accumulate, cudaStream_t st) {
+                                 float qk_scale_log2, const ScoreMod& mod, bool accumulate, cudaStream_t st) {
   CtxArgs a;
   a.q = q;
   a.out = out;
@@ -988,6 +1022,7 @@ cudaError_t launch_ctx_attention(const DevState& s, int seq_begin, int batch, in
   a.s_cap = s_cap;
   a.cs_row = kSinks + s_cap + s.ring;
   a.qk_scale_log2 = qk_scale_log2;
+  a.mod = mod;
   a.accumulate = accumulate ? 1 : 0;
   cudaError_t e;
   if (s.bits == 8 && s.fp8)

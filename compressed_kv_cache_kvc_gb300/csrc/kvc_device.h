@@ -254,7 +254,17 @@ __device__ __forceinline__ void merge_phase(const DevState& s, int seq_begin, in
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-      if (lane == 0) ms.sl[g][j] = j < ns ? part * qk_scale_log2 : -INFINITY;
+      if (lane == 0) {
+        float lg = -INFINITY;
+        if (j < ns) {
+          if (w.mod.c2 > 0.0f || w.mod.slopes != nullptr)
+            lg = transform_score(w.mod, part * (w.mod.c2 > 0.0f ? w.mod.y_scale : qk_scale_log2),
+                                 slope_log2(w.mod, h * G + g), P - 1 - j);
+          else
+            lg = part * qk_scale_log2;
+        }
+        ms.sl[g][j] = lg;
+      }
     }
   }
   __syncthreads();

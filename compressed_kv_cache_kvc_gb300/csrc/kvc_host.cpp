@@ -105,6 +105,8 @@ struct kvc_cache {
   bool plan_block = false;  // the pending plan drops whole pages
   int32_t plan_begin = 0, plan_batch = 0;
   std::vector<int32_t> plan_new;
+  float softcap = 0.0f;           // score transform of every attention on this cache
+  const float* slopes = nullptr;  // (kvc_set_score_transform)
   void* trace_start = nullptr;
   void* trace_stop = nullptr;
   int32_t last_launches = 0;
@@ -210,10 +212,19 @@ kvc_status attention_check(const kvc_cache* c, int32_t seq_begin, int32_t batch,
   return KVC_OK;
 }
 
+// What the prompt kernels' grids and 32-bit indices take: query heads and
+// sequences on the grid's y and z, 128-row tiles of all heads on x, positions
+// with room for a tile past the end.
+bool prompt_shape_ok(int batch, int hq, int n) {
+  return batch <= 65535 && hq <= 65535 && n <= 0x7FFFFE00 &&
+         ((long long)n + 127) / 128 * batch <= 0x7FFFFFFFLL / hq;
+}
+
 // Stream-K grid and workspace carving of one attention call (host mirror
 // lengths as they are now).
-void attention_plan(kvc_cache* c, int32_t seq_begin, int32_t batch, void* d_workspace, kvc::AttnWork* w,
-                    long long* total_pages) {
+void attention_plan(kvc_cache* c, int32_t seq_begin, int32_t batch, float sm_scale, void* d_workspace,
+                    kvc::AttnWork* w, long long* total_pages) {
+  const kvc::ScoreMod mod = kvc::make_score_mod(sm_scale, c->softcap, c->slopes);
   const WsLayout wl = ws_layout(c, batch);
   long long tp = 0;
   for (int i = 0; i < batch; ++i) tp += (long long)pages_of(c->slots[seq_begin + i]) * c->cfg.num_kv_heads;
@@ -222,7 +233,7 @@ void attention_plan(kvc_cache* c, int32_t seq_begin, int32_t batch, void* d_work
   // replayed at other lengths stays correct)
   int ncta = 1;
   if (tp > 0) {
-    ncta = sm_count(c) * kvc::attention_ctas_per_sm(c->cfg.bits, c->cfg.codes == KVC_CODES_E4M3);
+    ncta = sm_count(c) * kvc::attention_ctas_per_sm(c->cfg.bits, c->cfg.codes == KVC_CODES_E4M3, mod);
     // fuller CTAs, but no fewer than one per SM while each still gets 4 pages
     const long long want = std::max<long long>(tp / kMinPagesPerCta, std::min<long long>(sm_count(c), tp / 4));
     ncta = (int)std::min<long long>(ncta, std::max<long long>(1, want));
@@ -242,6 +253,7 @@ void attention_plan(kvc_cache* c, int32_t seq_begin, int32_t batch, void* d_work
   w->ring_chunks = ring_chunks(c);
   w->ncta = ncta;
   w->s_cap = s_cap(c);
+  w->mod = mod;
   *total_pages = tp;
 }
 
@@ -590,7 +602,7 @@ kvc_status kvc_decode_attention(kvc_cache* c, int32_t seq_begin, int32_t batch, 
   if (st0 != KVC_OK) return st0;
   kvc::AttnWork w;
   long long total_pages = 0;
-  attention_plan(c, seq_begin, batch, d_workspace, &w, &total_pages);
+  attention_plan(c, seq_begin, batch, sm_scale, d_workspace, &w, &total_pages);
   const float qk_scale_log2 = sm_scale * 1.4426950408889634f;
   const bool h2o = (flags & KVC_ATTN_ACCUM_H2O) != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -747,7 +759,7 @@ kvc_status decode_step_impl(kvc_cache* c, int32_t seq_begin, int32_t batch, cons
   int launches = c->last_launches;
   kvc::AttnWork w;
   long long total_pages = 0;
-  attention_plan(c, seq_begin, batch, d_workspace, &w, &total_pages);
+  attention_plan(c, seq_begin, batch, sm_scale, d_workspace, &w, &total_pages);
   const float qk_scale_log2 = sm_scale * 1.4426950408889634f;
   const bool h2o = params->mode != KVC_EVICT_STREAMING;  // H2O scores (token or block selection)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -862,7 +874,137 @@ kvc_status kvc_decode_step_overlap(kvc_cache* c, int32_t seq_begin, int32_t batc
 
 size_t kvc_prefill_workspace_bytes(const kvc_cache* c, int32_t batch, int32_t n) {
   if (!c || batch <= 0 || n <= 0) return 0;
+  if (c->softcap > 0.0f || c->slopes != nullptr)
+    return kvc::prompt_ws(batch, c->cfg.num_q_heads, c->cfg.num_kv_heads, n, true).total;
   return align_up((size_t)batch * c->cfg.num_q_heads * n * 2 * 4);
+}
+
+namespace {
+
+bool prompt_transformed(const kvc_cache* c) { return c->softcap > 0.0f || c->slopes != nullptr; }
+
+// The fresh prompt's attention with the cache's score transform and, when
+// given, per-query runs of keys; the caller checked the arguments and the
+// append is done.
+kvc_status prefill_transformed(kvc_cache* c, int32_t seq_begin, int32_t batch, int32_t n, const void* d_q,
+                               const void* d_k, const void* d_v, void* d_out, float sm_scale, bool h2o,
+                               const int32_t* d_key_begin, const int32_t* d_key_end, void* d_workspace,
+                               cudaStream_t st) {
+  const kvc::PromptWs w = kvc::prompt_ws(batch, c->cfg.num_q_heads, c->cfg.num_kv_heads, n, true);
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  kvc::PromptArgs a{};
+  a.batch = batch;
+  a.hq = c->cfg.num_q_heads;
+  a.hkv = c->cfg.num_kv_heads;
+  a.group = a.hq / a.hkv;
+  a.n = n;
+  a.qk_scale_log2 = sm_scale * 1.4426950408889634f;
+  a.mod = kvc::make_score_mod(sm_scale, c->softcap, c->slopes);
+  a.key_begin = d_key_begin;
+  a.key_end = d_key_end;
+  a.out = static_cast<uint16_t*>(d_out);
+  a.v16 = reinterpret_cast<uint16_t*>(ws + w.v16);
+  a.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+  if (h2o) {
+    a.sums = reinterpret_cast<float*>(ws + w.sums);
+    a.stats = reinterpret_cast<float*>(ws + w.stats);
+    a.runs = reinterpret_cast<int4*>(ws + w.runs);
+  }
+  a.status = c->dev.counters + kvc::kCtrStatus;
+  const bool trace = c->trace_start && c->trace_stop;
+  if (trace && cudaEventRecord(static_cast<cudaEvent_t>(c->trace_start), st) != cudaSuccess) return KVC_ERR_CUDA;
+  if (kvc::launch_prompt(a, static_cast<const uint16_t*>(d_q), static_cast<const uint16_t*>(d_k),
+                         static_cast<const uint16_t*>(d_v), st) != cudaSuccess)
+    return KVC_ERR_CUDA;
+  if (trace && cudaEventRecord(static_cast<cudaEvent_t>(c->trace_stop), st) != cudaSuccess) return KVC_ERR_CUDA;
+  c->last_launches += h2o ? 3 : 2;
+  if (h2o) {
+    if (kvc::launch_prompt_scores(c->dev, seq_begin, batch, n, a.sums, st) != cudaSuccess) return KVC_ERR_CUDA;
+    ++c->last_launches;
+  }
+  return KVC_OK;
+}
+
+}  // namespace
+
+size_t kvc_prefill_masked_workspace_bytes(const kvc_cache* c, int32_t batch, int32_t n) {
+  if (!c || batch <= 0 || n <= 0) return 0;
+  return kvc::prompt_ws(batch, c->cfg.num_q_heads, c->cfg.num_kv_heads, n, true).total;
+}
+
+kvc_status kvc_prefill_attention_masked(kvc_cache* c, int32_t seq_begin, int32_t batch, int32_t n, const void* d_q,
+                                        const void* d_k, const void* d_v, void* d_out, float sm_scale, int32_t flags,
+                                        const int32_t* d_key_begin, const int32_t* d_key_end, void* d_workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (!c) return KVC_ERR_INVALID_ARG;
+  {
+    const kvc_status oe = order_after_eviction(c, static_cast<cudaStream_t>(stream));
+    if (oe != KVC_OK) return oe;
+  }
+  c->last_launches = 0;
+  if (!range_ok(c, seq_begin, batch) || n <= 0 || (flags & ~KVC_ATTN_ACCUM_H2O)) return KVC_ERR_INVALID_ARG;
+  if (!d_q || !d_out || !aligned(d_q, 16) || !aligned(d_out, 16) || !d_k || !d_v || !aligned(d_k, 16) ||
+      !aligned(d_v, 16) || !aligned(d_key_begin, 4) || !aligned(d_key_end, 4))
+    return KVC_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return KVC_ERR_INVALID_ARG;
+  if (!d_workspace || !aligned(d_workspace, kAlign) ||
+      workspace_bytes < kvc_prefill_masked_workspace_bytes(c, batch, n))
+    return KVC_ERR_INVALID_ARG;
+  if (!prompt_shape_ok(batch, c->cfg.num_q_heads, n)) return KVC_ERR_UNSUPPORTED;
+  for (int i = 0; i < batch; ++i)
+    if (c->pos[seq_begin + i] != 0) return KVC_ERR_STATE;  // a prompt starts a sequence
+  const kvc_status st0 = kvc_quantize_append(c, seq_begin, batch, n, d_k, d_v, stream);
+  if (st0 != KVC_OK) return st0;
+  return prefill_transformed(c, seq_begin, batch, n, d_q, d_k, d_v, d_out, sm_scale,
+                             (flags & KVC_ATTN_ACCUM_H2O) != 0, d_key_begin, d_key_end, d_workspace,
+                             static_cast<cudaStream_t>(stream));
+}
+
+size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t n, int32_t sums) {
+  if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || n <= 0 || num_q_heads % num_kv_heads != 0) return 0;
+  return kvc::prompt_ws(batch, num_q_heads, num_kv_heads, n, sums != 0).total;
+}
+
+kvc_status kvc_prompt_attention(const kvc_prompt_params* p, const void* d_q, const void* d_k, const void* d_v,
+                                void* d_out, float* d_sums, int32_t* d_status, void* d_workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (!p || p->batch <= 0 || p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->n <= 0 ||
+      p->num_q_heads % p->num_kv_heads != 0)
+    return KVC_ERR_INVALID_ARG;
+  if (!d_q || !aligned(d_q, 16) || !d_k || !aligned(d_k, 16) || !d_v || !aligned(d_v, 16) || !d_out ||
+      !aligned(d_out, 16) || !aligned(d_sums, 4) || !d_status || !aligned(d_status, 4) || !aligned(p->d_slopes, 4) ||
+      !aligned(p->d_key_begin, 4) || !aligned(p->d_key_end, 4))
+    return KVC_ERR_INVALID_ARG;
+  if (!(p->sm_scale > 0.0f) || !std::isfinite(p->sm_scale) || !(p->softcap >= 0.0f) || !std::isfinite(p->softcap))
+    return KVC_ERR_INVALID_ARG;
+  if (!prompt_shape_ok(p->batch, p->num_q_heads, p->n)) return KVC_ERR_UNSUPPORTED;
+  const bool sums = d_sums != nullptr;
+  const kvc::PromptWs w = kvc::prompt_ws(p->batch, p->num_q_heads, p->num_kv_heads, p->n, sums);
+  if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < w.total) return KVC_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  kvc::PromptArgs a{};
+  a.batch = p->batch;
+  a.hq = p->num_q_heads;
+  a.hkv = p->num_kv_heads;
+  a.group = a.hq / a.hkv;
+  a.n = p->n;
+  a.qk_scale_log2 = p->sm_scale * 1.4426950408889634f;
+  a.mod = kvc::make_score_mod(p->sm_scale, p->softcap, p->d_slopes);
+  a.key_begin = p->d_key_begin;
+  a.key_end = p->d_key_end;
+  a.out = static_cast<uint16_t*>(d_out);
+  a.v16 = reinterpret_cast<uint16_t*>(ws + w.v16);
+  a.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+  if (sums) {
+    a.sums = d_sums;
+    a.stats = reinterpret_cast<float*>(ws + w.stats);
+    a.runs = reinterpret_cast<int4*>(ws + w.runs);
+  }
+  a.status = d_status;
+  return kvc::launch_prompt(a, static_cast<const uint16_t*>(d_q), static_cast<const uint16_t*>(d_k),
+                            static_cast<const uint16_t*>(d_v), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVC_OK
+             : KVC_ERR_CUDA;
 }
 
 kvc_status kvc_prefill_attention(kvc_cache* c, int32_t seq_begin, int32_t batch, int32_t n, const void* d_q,
@@ -883,11 +1025,15 @@ kvc_status kvc_prefill_attention(kvc_cache* c, int32_t seq_begin, int32_t batch,
       workspace_bytes < kvc_prefill_workspace_bytes(c, batch, n))
     return KVC_ERR_INVALID_ARG;
   if ((long long)n * kvc::kHeadDim * c->cfg.num_q_heads * batch > 2000000000000LL) return KVC_ERR_UNSUPPORTED;
+  if (prompt_transformed(c) && !prompt_shape_ok(batch, c->cfg.num_q_heads, n)) return KVC_ERR_UNSUPPORTED;
   for (int i = 0; i < batch; ++i)
     if (c->pos[seq_begin + i] != 0) return KVC_ERR_STATE;  // a prompt starts a sequence
   kvc_status st0 = kvc_quantize_append(c, seq_begin, batch, n, d_k, d_v, stream);
   if (st0 != KVC_OK) return st0;
   const bool h2o = (flags & KVC_ATTN_ACCUM_H2O) != 0;
+  if (prompt_transformed(c))
+    return prefill_transformed(c, seq_begin, batch, n, d_q, d_k, d_v, d_out, sm_scale, h2o, nullptr, nullptr,
+                               d_workspace, static_cast<cudaStream_t>(stream));
   if (kvc::launch_prefill(c->dev, seq_begin, batch, n, static_cast<const uint16_t*>(d_q),
                           static_cast<const uint16_t*>(d_k), static_cast<const uint16_t*>(d_v),
                           static_cast<uint16_t*>(d_out), static_cast<float*>(d_workspace),
@@ -950,7 +1096,8 @@ kvc_status kvc_prefill_context(kvc_cache* c, int32_t seq_begin, int32_t batch, i
   if (kvc::launch_ctx_attention(c->dev, seq_begin, batch, n, static_cast<const uint16_t*>(d_q),
                                 static_cast<uint16_t*>(d_out), reinterpret_cast<float*>(ws + wl.stats),
                                 reinterpret_cast<float*>(ws + wl.colsum), reinterpret_cast<int*>(ws + wl.ticket),
-                                s_cap(c), sm_scale * 1.4426950408889634f, (flags & KVC_ATTN_ACCUM_H2O) != 0,
+                                s_cap(c), sm_scale * 1.4426950408889634f,
+                                kvc::make_score_mod(sm_scale, c->softcap, c->slopes), (flags & KVC_ATTN_ACCUM_H2O) != 0,
                                 static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     c->last_launches = launches;
     return KVC_ERR_CUDA;
@@ -977,6 +1124,13 @@ kvc_status kvc_read_status(kvc_cache* c, int32_t* h_status, void* stream) {
       return KVC_ERR_CUDA;
     return KVC_ERR_DEVICE;
   }
+  return KVC_OK;
+}
+
+kvc_status kvc_set_score_transform(kvc_cache* c, float softcap, const float* d_slopes) {
+  if (!c || !(softcap >= 0.0f) || !std::isfinite(softcap) || !aligned(d_slopes, 4)) return KVC_ERR_INVALID_ARG;
+  c->softcap = softcap;
+  c->slopes = d_slopes;
   return KVC_OK;
 }
 

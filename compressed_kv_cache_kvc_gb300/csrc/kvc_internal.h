@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "kvc_score.h"
+
 namespace kvc {
 
 constexpr int kHeadDim = 128;
@@ -88,6 +90,7 @@ struct AttnWork {
   int ring_chunks;  // ceil(W / kRingChunk), 0 without a window
   int ncta;         // grid size of the split kernel
   int s_cap;
+  ScoreMod mod;     // cap and distance bias (neither: c2 = 0, slopes null)
 };
 
 constexpr int kMaxCallBatch = 1024;  // sequences per attention call (prefix table in shared memory)
@@ -189,7 +192,34 @@ constexpr int kMaxCtxGroups = 64;   // CTAs per (sequence, KV head)
 int ctx_groups(int n, int group);
 cudaError_t launch_ctx_attention(const DevState& s, int seq_begin, int batch, int n, const uint16_t* q,
                                  uint16_t* out, float* stats, float* colsum, int* ticket, int s_cap,
-                                 float qk_scale_log2, bool accumulate, cudaStream_t st);
+                                 float qk_scale_log2, const ScoreMod& mod, bool accumulate,
+                                 cudaStream_t st);
+
+// Prompt attention with score transforms and per-query runs of keys
+// (kvc_prompt.cu): device views of one call.
+struct PromptArgs {
+  int batch, hq, hkv, group, n;
+  float qk_scale_log2;       // sm_scale * log2(e)
+  ScoreMod mod;
+  const int32_t* key_begin;  // [batch][n] or null (0)
+  const int32_t* key_end;    // [batch][n] or null (i + 1)
+  uint16_t* out;             // bf16 [batch][hq][n][128]
+  float* sums;               // [batch][hkv][n] column sums, or null
+  float* stats;              // [batch][hq][n][2] row (max, sum); null without sums
+  uint16_t* v16;             // fp16 [batch][hkv][n][128]
+  uint32_t* bad;             // [batch][hkv][tiles][4] keys whose V row is not finite
+  int4* runs;                // [batch][tiles] bounds of the runs per 128 queries; null without sums
+  int32_t* status;           // KVC_DEV_* bits
+};
+struct PromptWs {
+  size_t v16, bad, runs, stats, sums, total;
+};
+PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums);
+cudaError_t launch_prompt(const PromptArgs& a, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                          cudaStream_t st);
+// sums ([batch][hkv][n]) of a fresh prompt into its tokens' score slots
+cudaError_t launch_prompt_scores(const DevState& s, int seq_begin, int batch, int n, const float* sums,
+                                 cudaStream_t st);
 
 // Fused merge + H2O scores + selection + compaction (kvc_decode_step).
 struct StepArgs {
@@ -214,8 +244,8 @@ cudaError_t launch_step_moves(const DevState& s, int batch, const StepArgs& a, i
                               cudaStream_t st);
 int step_max_smem_bytes();  // dynamic shared memory of the post kernel (a multiple of 16)
 
-int attention_smem_bytes(int bits);
-int attention_ctas_per_sm(int bits, bool fp8);  // resident split CTAs per SM (occupancy API, cached)
+// resident split CTAs per SM (occupancy API, cached)
+int attention_ctas_per_sm(int bits, bool fp8, const ScoreMod& mod);
 int select_max_smem_slots();
 
 }  // namespace kvc

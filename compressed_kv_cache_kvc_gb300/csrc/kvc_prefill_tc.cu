@@ -46,17 +46,18 @@
 // a wait that runs out sets KVC_DEV_WAIT_TIMEOUT, every role leaves its loop,
 // the issuing thread waits (bounded) for its products in flight, and the
 // CTA frees its tensor memory.
-#include <cuda.h>  // CUtensorMap; the encoder comes through the runtime's driver entry point
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "kvc_device.h"
 #include "kvc_internal.h"
+#include "kvc_tc.h"
 
 namespace kvc {
 namespace {
 
 using namespace dev;
+using namespace tc;
 
 constexpr int kWg = 128;                  // threads per warpgroup
 constexpr int kTcThreads = 3 * kWg + 64;  // query tiles A and B, producer, two MMA warps
@@ -69,7 +70,6 @@ constexpr uint32_t kTcCols = 512;         // TMEM columns allocated
 constexpr uint32_t kColS = 0;             // S of query tile x at kColS + 64 x
 constexpr uint32_t kColO = 128;           // O of query tile x at kColO + 128 x
 constexpr uint32_t kColP = 384;           // P of query tile x at kColP + 32 x
-constexpr int kTcWaitLimit = 1 << 22;
 
 constexpr int kTileBytes = kTcKeys * kHeadDim * 2;           // 16 KB
 constexpr int kOffQ = 0;                                      // 2 x 32 KB: Q_A, Q_B (TMA, 128-byte swizzle)
@@ -97,8 +97,6 @@ __device__ __forceinline__ int vstage_off(int r, int c) {
   return ((c >> 3) << 13) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 // Byte offset of 16-byte chunk c (elements 8c .. 8c + 7) of row r in the
 // operand layout of a tile with `kch` chunks per row: core matrices of 8 rows
 // x 16 bytes, row groups kch * 128 bytes apart, chunks 128 bytes apart.
@@ -112,14 +110,6 @@ __device__ __forceinline__ uint64_t op_desc(uint32_t addr, uint32_t lbo, uint32_
          ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | ((uint64_t)1 << 46);
 }
 
-// Descriptor of a K-major operand with the 128-byte swizzle (as TMA writes
-// it): 8-row groups of 128-byte rows 1 KB apart; the leading byte offset is
-// unused; layout type 2 at bit 61.  A K step of 16 elements advances the
-// start address by 32 bytes inside the 128-byte row.
-__device__ __forceinline__ uint64_t op_desc_sw128(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 // fp16 bits of 65504, its largest finite value.  bf16 magnitudes from 65536
 // up saturate to it; 65280, the bf16 value below, converts exactly.
 constexpr uint32_t kF16Max = 0x7BFFu;
@@ -130,77 +120,6 @@ __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// Instruction descriptor of kind::f16: f32 accumulator, A and B both bf16
-// (`bf16`) or both fp16, both K-major, N / 8 at bit 17, M / 16 at bit 24.
-__device__ __forceinline__ uint32_t instr_desc(int m, int n, bool bf16) {
-  const uint32_t ab = bf16 ? ((1u << 7) | (1u << 10)) : 0u;
-  return (1u << 4) | ab | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(dtmem),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc));
-}
-
-// The same with A (M x K, K-major) read from tensor memory at `atmem`.
-__device__ __forceinline__ void mma_f16_ts(uint32_t dtmem, uint32_t atmem, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(dtmem),
-      "r"(atmem), "l"(b), "r"(idesc), "r"((uint32_t)acc));
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-
-// One TMA box of a 3-d tensor map into shared memory, counted on `bar`.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(bar) : "memory");
-}
-
-// Whether the mbarrier's phase `parity` has completed (does not wait).
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-// Bounded wait for the mbarrier's phase `parity`; true when it completed.
-// With `abort` it also gives up once another thread has set that flag.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  uint32_t done = 0;
-  for (int it = 0; it < kTcWaitLimit && !done; ++it) {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (!done && abort != nullptr && (it & 63) == 63 && *abort) break;
-  }
-  return done != 0;
 }
 
 // A failed wait: flag it for the host and tell the other warpgroups.
@@ -221,54 +140,6 @@ __device__ __forceinline__ bool wg_and(int id, bool v) {
       : "r"((uint32_t)v), "r"(id)
       : "memory");
   return r != 0;
-}
-
-__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
-      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])),
-      "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
-      "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])));
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Key tiles a 128-query tile starting at q0 attends to.
@@ -832,48 +703,13 @@ __global__ void __launch_bounds__(kScThreads, 2)
 
 int prefill_fwd_tc_smem_bytes() { return kTcSmem; }
 
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn tensor_map_encoder() {
-  static const EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) !=
-            cudaSuccess ||
-        qr != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiledFn>(nullptr);
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
-// A [planes][n][128] bf16 tensor as a 3-d tensor map with 64 x `rows` x 1
-// boxes (64 dims) and the 128-byte swizzle; rows past n read as zeros.
-bool encode_kv_map(CUtensorMap* map, const uint16_t* base, int n, int planes, int rows) {
-  const EncodeTiledFn enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)n, (cuuint64_t)planes};
-  const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)n * kHeadDim * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
 cudaError_t launch_prefill_scores_tc(const DevState& s, int seq_begin, int batch, int n, const uint16_t* q,
                                     const uint16_t* k, const float* stats, float qk_scale_log2, cudaStream_t st) {
   static int done[64] = {0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prefill_scores_tc_kernel), kScSmem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap tm_q, tm_k;
-  if (!encode_kv_map(&tm_q, q, n, batch * s.hq, kScTile) || !encode_kv_map(&tm_k, k, n, batch * s.hkv, kScTile))
+  if (!tc::encode_rows_map(&tm_q, q, n, batch * s.hq, kScTile) || !tc::encode_rows_map(&tm_k, k, n, batch * s.hkv, kScTile))
     return cudaErrorInvalidValue;
   const int tiles = (n + kScTile - 1) / kScTile;
   prefill_scores_tc_kernel<<<dim3(tiles, s.hkv, batch), kScThreads, kScSmem, st>>>(s, n, tm_q, tm_k, stats,
@@ -888,8 +724,8 @@ cudaError_t launch_prefill_fwd_tc(const DevState& s, int batch, int n, const uin
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prefill_fwd_tc_kernel), kTcSmem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap tm_q, tm_k, tm_v;
-  if (!encode_kv_map(&tm_q, q, n, batch * s.hq, kTcQ) || !encode_kv_map(&tm_k, k, n, batch * s.hkv, kTcKeys) ||
-      !encode_kv_map(&tm_v, v, n, batch * s.hkv, kTcKeys))
+  if (!tc::encode_rows_map(&tm_q, q, n, batch * s.hq, kTcQ) || !tc::encode_rows_map(&tm_k, k, n, batch * s.hkv, kTcKeys) ||
+      !tc::encode_rows_map(&tm_v, v, n, batch * s.hkv, kTcKeys))
     return cudaErrorInvalidValue;
   const int blocks = (n + kTcBlock - 1) / kTcBlock;
   prefill_fwd_tc_kernel<<<dim3(blocks, s.hq, batch), kTcThreads, kTcSmem, st>>>(s, n, tm_q, tm_k, tm_v, out, stats,

@@ -1,0 +1,856 @@
+// Attention of a prompt over itself with capped scores, a distance bias and
+// per-query runs of keys, on the fifth-generation tensor cores.
+//
+// Query i of a sequence sees the keys [begin_i, end_i) (causal when no runs
+// are given); with s = sm_scale * q_i . k_j, z = cap * tanh(s / cap) - slope_h
+// |i - j| (kvc_score.h), the output is softmax(z) . v over the keys it sees (0
+// when it sees none) and, on request, every key's column sum of the
+// probabilities over the queries and the query heads of its KV head.
+//
+// Three kernels:
+//   prompt_prep_kernel   V from bf16 to fp16 in the workspace (exact below
+//                        2^16 and above the fp16 subnormals), the keys whose V
+//                        row is not finite as bit masks, the runs' bounds per
+//                        128-query tile;
+//   prompt_fwd_kernel    outputs and (for the sums) row statistics;
+//   prompt_sums_kernel   column sums from the row statistics.
+//
+// prompt_fwd_kernel.  4 * 128 flops per visible pair: bound by the tensor
+// pipe.  One 320-thread CTA per (256 queries, query head, sequence), longest
+// blocks first:
+//   * warps 0-3 and 4-7 own one 128-query tile each ("A", "B"), a thread per
+//     query row; TMEM columns: S_x at 128 x (its first 64 columns become P in
+//     fp16), O_x at 256 + 128 x;
+//   * warp 8 issues the products, warp 9 the TMA loads: K and V tiles of 128
+//     keys into two slots each.  K is read K-major and V in its own layout
+//     (MN-major), both with the 128-byte swizzle, so nothing is transposed.
+// Order of the products: P V_A(j - 1), S_A(j), P V_B(j - 1), S_B(j): the
+// pipe runs them in order, so S_x(j) may overwrite P_x(j - 1) without a wait,
+// S_x(j) complete implies P V_x(j - 1) complete, and one tile's softmax runs
+// under the other tile's products.  M = N = 128 products cost 64 cycles each,
+// 2048 a round of both tiles; the softmax takes two values per instruction
+// where the ISA has the form.
+// The running maximum is lazy (O is rescaled when a row's maximum grows by
+// more than 8 in log2 units), P is rounded to fp16 (11 significant bits; p <=
+// 2^8), the sums add the unrounded p in fp32.
+// Key tiles no query of a 128-query tile sees are skipped; tiles every row of
+// a warp sees whole take no mask.  Masked scores are replaced before the
+// maximum, and P is exactly 0 there; V rows that are not finite enter the
+// product as 0 and give NaN only to the rows that see them.
+//
+// Synchronisation: mbarriers, every wait bounded as in the prefill kernels (a
+// wait that runs out sets KVC_DEV_WAIT_TIMEOUT, all roles leave, the TMEM is
+// freed).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kvc_device.h"
+#include "kvc_internal.h"
+#include "kvc_tc.h"
+
+namespace kvc {
+namespace {
+
+using namespace dev;
+using namespace tc;
+
+constexpr int kTile = 128;                        // queries per tile, keys per tile
+constexpr int kFwdThreads = 320;
+constexpr int kFwdBlock = 2 * kTile;
+constexpr float kLazyMax = 8.0f;
+constexpr int kTileB = kTile * kHeadDim * 2;      // 32 KB: a Q, K or V tile, two boxes of 64 dims
+constexpr int kBoxB = kTileB / 2;
+constexpr int kFOffQ = 0;                         // 2 tiles
+constexpr int kFOffK = kFOffQ + 2 * kTileB;       // 2 slots
+constexpr int kFOffV = kFOffK + 2 * kTileB;       // 2 slots
+constexpr int kFOffBar = kFOffV + 2 * kTileB;
+// mbarriers: Q landed (per tile), K / V landed and free (per slot), S
+// complete, P written, O complete (per tile), all products complete
+constexpr int kFBarQ = 0, kFBarK = 2, kFBarV = 4, kFBarKe = 6, kFBarVe = 8, kFBarS = 10, kFBarP = 12, kFBarO = 14,
+              kFBarDone = 16, kFNumBars = 17;
+constexpr int kFOffMisc = kFOffBar + 8 * kFNumBars;  // TMEM base, abort flag, [8][2] run bounds per warp
+constexpr int kFwdSmem = kFOffMisc + 8 + 64;
+constexpr uint32_t kFwdCols = 512;
+
+__device__ __forceinline__ void set_abort(int* status, volatile int* abort) {
+  if (!*abort) {
+    *abort = 1;
+    atomicOr(status, kDevWaitTimeout);
+  }
+}
+
+// The keys [lo, hi) query `i` of sequence `bl` sees; an empty run is (0, 0).
+__device__ __forceinline__ int2 run_of(const PromptArgs& a, int bl, int i) {
+  int lo = 0, hi = i + 1;
+  if (a.key_begin != nullptr) lo = max(a.key_begin[(size_t)bl * a.n + i], 0);
+  if (a.key_end != nullptr) hi = min(a.key_end[(size_t)bl * a.n + i], a.n);
+  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+
+__global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a, const uint16_t* __restrict__ v) {
+  __shared__ uint32_t sh_bad[4];
+  __shared__ int sh_run[4];
+  const int tiles = (a.n + kTile - 1) / kTile;
+  const int tile = blockIdx.x % tiles, plane = blockIdx.x / tiles, tid = threadIdx.x, lane = tid & 31;
+  const int k0 = tile * kTile, rows = min(kTile, a.n - k0);
+  if (tid < 4) sh_bad[tid] = 0;
+  if (tid == 0) {
+    sh_run[0] = INT_MAX;
+    sh_run[1] = 0;
+    sh_run[2] = 0;
+    sh_run[3] = INT_MAX;
+  }
+  __syncthreads();
+  // 16 bytes a lane, 16 lanes a row, 16 rows a pass
+  const int r0 = tid >> 4, ch = tid & 15;
+  const uint4* src = reinterpret_cast<const uint4*>(v + ((size_t)plane * a.n + k0) * kHeadDim) + ch;
+  uint4* dst = reinterpret_cast<uint4*>(a.v16 + ((size_t)plane * a.n + k0) * kHeadDim) + ch;
+  uint4 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + 16 * i < rows) w[i] = src[(size_t)(r0 + 16 * i) * 16];
+  bool range = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    bool bad = false;
+    if (r < rows) {
+      uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float lo = bf16f(x[e] & 0xFFFFu), hi = bf16f(x[e] >> 16);
+        range |= !(fabsf(lo) < 65536.0f) || !(fabsf(hi) < 65536.0f);
+        if ((x[e] & 0x7F80u) == 0x7F80u) bad = true, lo = 0.0f;
+        if ((x[e] & 0x7F800000u) == 0x7F800000u) bad = true, hi = 0.0f;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(x[e]) : "f"(hi), "f"(lo));
+      }
+      dst[(size_t)r * 16] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, bad);
+    if (vote != 0 && (lane & 15) == 0 && ((vote >> lane) & 0xFFFFu) != 0) atomicOr(&sh_bad[r >> 5], 1u << (r & 31));
+  }
+  if (range) atomicOr(a.status, kDevPrefillRange);
+  // bounds of the runs of query tile `tile`, once per sequence
+  if (a.runs != nullptr && plane % a.hkv == 0 && tid < kTile && tid < rows) {
+    const int2 run = run_of(a, plane / a.hkv, k0 + tid);
+    const bool any = run.x < run.y;
+    if (any) {
+      atomicMin(&sh_run[0], run.x);
+      atomicMax(&sh_run[1], run.y);
+    }
+    atomicMax(&sh_run[2], any ? run.x : INT_MAX);
+    atomicMin(&sh_run[3], any ? run.y : 0);
+  }
+  __syncthreads();
+  if (tid < 4) a.bad[((size_t)plane * tiles + tile) * 4 + tid] = sh_bad[tid];
+  if (a.runs != nullptr && plane % a.hkv == 0 && tid == 0)
+    a.runs[(size_t)(plane / a.hkv) * tiles + tile] = make_int4(sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Scores in log2 units of 32 raw products of a row (keys from the one at
+// dist0 positions from the query: key - query).  Without a cap and a bias the
+// products stay as they are (the caller scales them).  `beyond`: some key may
+// lie after the query.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void chunk_scores(const PromptArgs& a, float (&z)[32], float slope2, float dist0,
+                                             bool beyond) {
+  if (CAP) {
+    float top[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      top[0] = fmaxf(fmaxf(top[0], fabsf(z[i])), fabsf(z[i + 1]));
+      top[1] = fmaxf(fmaxf(top[1], fabsf(z[i + 2])), fabsf(z[i + 3]));
+    }
+    if (!(fmaxf(top[0], top[1]) * a.mod.y_scale > kCapPolyMax)) {  // (a NaN stays NaN in the polynomial)
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 y = mul2(make_float2(z[i], z[i + 1]), make_float2(a.mod.y_scale, a.mod.y_scale));
+        const float2 u = mul2(y, y);
+        float2 h = fma2(make_float2(a.mod.poly[5], a.mod.poly[5]), u, make_float2(a.mod.poly[4], a.mod.poly[4]));
+        h = fma2(h, u, make_float2(a.mod.poly[3], a.mod.poly[3]));
+        h = fma2(h, u, make_float2(a.mod.poly[2], a.mod.poly[2]));
+        h = fma2(h, u, make_float2(a.mod.poly[1], a.mod.poly[1]));
+        h = fma2(h, u, make_float2(a.mod.poly[0], a.mod.poly[0]));
+        const float2 r = mul2(y, h);
+        z[i] = r.x;
+        z[i + 1] = r.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = cap_score(a.mod, z[i] * a.mod.y_scale);
+    }
+  }
+  if (BIAS) {
+    // slope2 * (key - query) for keys at or before the query, else its negative
+    const float2 sl = make_float2(slope2, slope2), d0 = make_float2(dist0, dist0);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float2 d = add2(d0, make_float2((float)i, (float)(i + 1)));
+      if (beyond) d = make_float2(-fabsf(d.x), -fabsf(d.y));
+      float2 b = make_float2(z[i], z[i + 1]);
+      if (!CAP) b = mul2(b, make_float2(a.qk_scale_log2, a.qk_scale_log2));
+      const float2 r = fma2(d, sl, b);
+      z[i] = r.x;
+      z[i + 1] = r.y;
+    }
+  }
+}
+
+// -inf outside [b, e) (key indices relative to the chunk).
+__device__ __forceinline__ void chunk_mask(float (&z)[32], int b, int e) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!(i >= b && i < e)) z[i] = -INFINITY;
+}
+
+__device__ __forceinline__ float chunk_max(const float (&z)[32], float m) {
+  float t0 = m, t1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    t0 = fmaxf(fmaxf(t0, z[i]), z[i + 1]);
+    t1 = fmaxf(fmaxf(t1, z[i + 2]), z[i + 3]);
+  }
+  return fmaxf(t0, t1);
+}
+
+// 32 scores (raw products for `raw`) -> probabilities 2^(z - m) in fp16 pairs;
+// their unrounded sum is added to ls.
+__device__ __forceinline__ void chunk_probs(const float (&z)[32], bool raw, float scale, float m, uint32_t (&pw)[16],
+                                            float2 (&ls)[2]) {
+  const float2 nm = make_float2(-m, -m), sc = make_float2(scale, scale);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 zz = make_float2(z[2 * e], z[2 * e + 1]);
+    const float2 d = raw ? fma2(zz, sc, nm) : add2(zz, nm);
+    const float2 p = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+    ls[e & 1] = add2(ls[e & 1], p);
+    const __half2 hh = __floats2half2_rn(p.x, p.y);
+    pw[e] = *reinterpret_cast<const uint32_t*>(&hh);
+  }
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    prompt_fwd_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t fsm[];
+  const uint32_t base = saddr(fsm);
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(fsm + kFOffMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(fsm + kFOffMisc + 4);
+  int* sh_run = reinterpret_cast<int*>(fsm + kFOffMisc + 8);
+  auto bar = [&](int i) { return base + kFOffBar + 8 * i; };
+
+  const int n = a.n;
+  const int qb = gridDim.x - 1 - blockIdx.x, hqi = blockIdx.y, bl = blockIdx.z;
+  const int plane_q = bl * a.hq + hqi, plane_kv = bl * a.hkv + hqi / a.group;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int qblk = qb * kFwdBlock;
+  const int qi = qblk + tid;  // (softmax threads) this thread's query row
+
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kFwdCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == kFwdBlock + 32) {
+    for (int i = 0; i < kFNumBars; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)),
+                   "r"(i == kFBarP || i == kFBarP + 1 ? 4u : 1u));
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // the rows' runs; per warp the keys some row sees and those every row sees
+  int2 run = make_int2(0, 0);
+  int all_lo = 0, all_hi = INT_MAX;
+  if (warp < 8) {
+    int lo = INT_MAX, hi = 0;
+    if (qi < n) {
+      run = run_of(a, bl, qi);
+      const bool any = run.x < run.y;
+      lo = any ? run.x : INT_MAX;
+      hi = run.y;
+      all_lo = lo;
+      all_hi = hi;
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    if (lane == 0) {
+      sh_run[2 * warp] = lo;
+      sh_run[2 * warp + 1] = hi;
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tbase;
+  // key tiles [x_lo, x_hi) of query tile x; [t_lo, t_hi) of both
+  int x_lo[2], x_hi[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    int lo = INT_MAX, hi = 0;
+#pragma unroll
+    for (int w = 4 * x; w < 4 * x + 4; ++w) {
+      lo = min(lo, sh_run[2 * w]);
+      hi = max(hi, sh_run[2 * w + 1]);
+    }
+    x_lo[x] = lo < hi ? lo / kTile : 0;
+    x_hi[x] = lo < hi ? (hi + kTile - 1) / kTile : 0;
+  }
+  const bool on0 = x_lo[0] < x_hi[0], on1 = x_lo[1] < x_hi[1];
+  const int t_lo = on0 && on1 ? min(x_lo[0], x_lo[1]) : on0 ? x_lo[0] : x_lo[1];
+  const int t_hi = max(x_hi[0], x_hi[1]);
+
+  if (warp == 9) {
+    // ------------------------------------------------------------- TMA loads
+    if (lane == 0 && t_lo < t_hi) {
+      int issued = 0;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t dst = base + kFOffQ + x * kTileB;
+        bar_expect_tx(bar(kFBarQ + x), kTileB);
+        tma_load_3d(dst, &tm_q, 0, qblk + x * kTile, plane_q, bar(kFBarQ + x));
+        tma_load_3d(dst + kBoxB, &tm_q, 64, qblk + x * kTile, plane_q, bar(kFBarQ + x));
+      }
+      bool ok = true;
+      for (int j = t_lo; j < t_hi && ok; ++j) {
+        const int it = j - t_lo, sl = it & 1;
+        const uint32_t par = (uint32_t)((it >> 1) & 1) ^ 1u;  // the slot's previous tile released
+        if (it >= 2 && !bar_wait(bar(kFBarKe + sl), par, abort)) ok = false;
+        if (ok) {
+          const uint32_t dst = base + kFOffK + sl * kTileB, b = bar(kFBarK + sl);
+          bar_expect_tx(b, kTileB);
+          tma_load_3d(dst, &tm_k, 0, j * kTile, plane_kv, b);
+          tma_load_3d(dst + kBoxB, &tm_k, 64, j * kTile, plane_kv, b);
+          issued = 2 * it + 1;
+        }
+        if (ok && it >= 2 && !bar_wait(bar(kFBarVe + sl), par, abort)) ok = false;
+        if (ok) {
+          const uint32_t dst = base + kFOffV + sl * kTileB, b = bar(kFBarV + sl);
+          bar_expect_tx(b, kTileB);
+          tma_load_3d(dst, &tm_v, 0, j * kTile, plane_kv, b);
+          tma_load_3d(dst + kBoxB, &tm_v, 64, j * kTile, plane_kv, b);
+          issued = 2 * it + 2;
+        }
+        if (!ok) set_abort(a.status, abort);
+      }
+      // the last copies into every slot land before the CTA goes away (they may
+      // not have been waited for when another role gave up)
+      for (int x = 0; x < 2; ++x) bar_wait(bar(kFBarQ + x), 0, nullptr);
+      for (int e = max(0, issued - 4); e < issued; ++e)
+        bar_wait(bar((e & 1 ? kFBarV : kFBarK) + ((e >> 1) & 1)), (uint32_t)((e >> 2) & 1), nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // -------------------------------------------------------------- products
+    const bool el = elect_one();
+    const uint32_t id_s = instr_desc(kTile, kTile, true);
+    const uint32_t id_o = instr_desc(kTile, kHeadDim, false) | kInstrTransB;
+    bool ok = true;
+    auto wait = [&](int b, uint32_t par) {
+      if (ok && !__all_sync(0xffffffffu, bar_wait(bar(b), par, abort))) {
+        ok = false;
+        set_abort(a.status, abort);
+      }
+    };
+    for (int j = t_lo; t_lo < t_hi && j <= t_hi && ok; ++j) {
+      const int it = j - t_lo, sk = it & 1, sv = (it - 1) & 1;
+      if (j > t_lo) wait(kFBarV + sv, (uint32_t)(((it - 1) >> 1) & 1));
+      if (j < t_hi) wait(kFBarK + sk, (uint32_t)((it >> 1) & 1));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t t_s = tmem + kTile * x, t_o = tmem + 256 + kTile * x;
+        if (j - 1 >= x_lo[x] && j - 1 < x_hi[x]) {
+          const int idx = j - 1 - x_lo[x];
+          wait(kFBarP + x, (uint32_t)(idx & 1));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (el) {
+            const uint32_t va = base + kFOffV + sv * kTileB;
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_f16_ts(t_o, t_s + 8 * ks, op_desc_mn_sw128(va + ks * 2048, kBoxB), id_o, idx > 0 || ks > 0);
+            if (j == x_hi[x]) mma_commit(bar(kFBarO + x));
+          }
+        }
+        if (j >= x_lo[x] && j < x_hi[x]) {
+          if (j == x_lo[x]) wait(kFBarQ + x, 0);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (el) {
+            const uint32_t qa = base + kFOffQ + x * kTileB, ka = base + kFOffK + sk * kTileB;
+#pragma unroll
+            for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
+              mma_f16(t_s, op_desc_sw128(qa + off), op_desc_sw128(ka + off), id_s, ks > 0);
+            }
+            mma_commit(bar(kFBarS + x));
+          }
+        }
+      }
+      if (ok && el) {
+        if (j < t_hi) mma_commit(bar(kFBarKe + sk));
+        if (j > t_lo) mma_commit(bar(kFBarVe + sv));
+      }
+      __syncwarp();
+    }
+    if (t_lo < t_hi) {
+      // every product complete before the tensor memory goes back
+      if (el) mma_commit(bar(kFBarDone));
+      bar_wait(bar(kFBarDone), 0, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- query rows
+    const int x = warp >> 2;
+    const int lo = x == 0 ? x_lo[0] : x_lo[1], hi = x == 0 ? x_hi[0] : x_hi[1];
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = trow + kTile * x, t_o = trow + 256 + kTile * x;
+    const float slope2 = BIAS ? slope_log2(a.mod, hqi) : 0.0f;
+    const int tiles = (n + kTile - 1) / kTile;
+    const uint4* bad_masks = reinterpret_cast<const uint4*>(a.bad) + (size_t)plane_kv * tiles;
+    const int qi_first = qblk + (tid & ~31);
+    bool ok = true, poison = false;
+    float m = kNegBig, l = 0.0f;
+#pragma unroll 1
+    for (int j = lo; j < hi; ++j) {
+      const int k0 = j * kTile, idx = j - lo;
+      const uint4 bad = bad_masks[j];
+      if (!__all_sync(0xffffffffu, bar_wait(bar(kFBarS + x), (uint32_t)(idx & 1), abort))) {
+        ok = false;
+        set_abort(a.status, abort);
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (bad.x | bad.y | bad.z | bad.w) {  // V rows that are not finite (rare)
+        const uint32_t w[4] = {bad.x, bad.y, bad.z, bad.w};
+        for (int i = 0; i < 128; ++i)
+          if ((w[i >> 5] >> (i & 31)) & 1u) poison |= k0 + i >= run.x && k0 + i < run.y;
+      }
+      // Two passes over the 128 scores in chunks of 32, the next chunk's load
+      // in flight: the maximum, then the probabilities (few registers live; a
+      // row of 128 held at once spilled).  The scores of the second pass are
+      // formed again from the products, but for cap and bias together, which
+      // the first pass leaves in the place of the products.
+      const bool masked = k0 < all_lo || k0 + kTile > all_hi;  // (the same for the warp)
+      const bool beyond = k0 + kTile - 1 > qi_first;
+      const float dist0 = (float)(k0 - qi);
+      constexpr bool kKeep = CAP && BIAS, kRaw = !CAP && !BIAS;
+      float za[32], zb[32];
+      tmem_ld32(t_s, za);
+      float mx = -INFINITY;
+      auto first = [&](float (&z)[32], int c) {
+        if (BIAS) chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + (float)(32 * c), beyond);
+        if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+        if (kKeep) tmem_st32(t_s + 32 * c, z);
+        mx = chunk_max(z, mx);
+      };
+      tmem_wait(za);
+      tmem_ld32(t_s + 32, zb);
+      first(za, 0);
+      tmem_wait(zb);
+      tmem_ld32(t_s + 64, za);
+      first(zb, 1);
+      tmem_wait(za);
+      tmem_ld32(t_s + 96, zb);
+      first(za, 2);
+      tmem_wait(zb);
+      if (kKeep) tmem_st_wait();
+      tmem_ld32(t_s, za);
+      first(zb, 3);
+      // scale > 0 and a cap keep the order: the maximum commutes with them
+      if (kRaw) mx *= a.qk_scale_log2;
+      if (CAP && !BIAS) mx = mx > -INFINITY ? cap_score(a.mod, mx * a.mod.y_scale) : mx;
+      const bool grow = mx > m + kLazyMax;
+      const float alpha = grow ? fast_exp2(m - mx) : 1.0f;
+      if (grow) {
+        l *= alpha;
+        m = mx;
+      }
+      tmem_wait(za);
+      // S(j) complete implies P V(j - 1) complete: O may be rescaled
+      if (idx > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
+          float t[16];
+          ld16(t_o + c0, t);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) t[i] *= alpha;
+          st16(t_o + c0, t);
+        }
+      }
+      // P over the products' first half: chunk c's 16 columns lie before the
+      // products of chunk c + 1
+      float2 ls[2] = {};
+      auto second = [&](float (&z)[32], int c) {
+        if (!kKeep) {
+          chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + (float)(32 * c), beyond);
+          if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+        }
+        uint32_t pw[16];
+        chunk_probs(z, kRaw, a.qk_scale_log2, m, pw, ls);
+        tmem_st16(t_s + 16 * c, pw);
+      };
+      if (kKeep) tmem_st_wait();
+      tmem_ld32(t_s + 32, zb);
+      second(za, 0);
+      tmem_wait(zb);
+      tmem_ld32(t_s + 64, za);
+      second(zb, 1);
+      tmem_wait(za);
+      tmem_ld32(t_s + 96, zb);
+      second(za, 2);
+      tmem_wait(zb);
+      second(zb, 3);
+      const float2 lt = add2(ls[0], ls[1]);
+      l += lt.x + lt.y;
+      tmem_st_wait();
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kFBarP + x));
+    }
+    const bool any = lo < hi;
+    if (ok && any && !__all_sync(0xffffffffu, bar_wait(bar(kFBarO + x), 0, abort))) {
+      ok = false;
+      set_abort(a.status, abort);
+    }
+    if (ok) {
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const bool row_ok = qi < n;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // a row that sees nothing is 0
+      uint16_t* orow = a.out + ((size_t)plane_q * n + (row_ok ? qi : 0)) * kHeadDim;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+        float t[32];
+        if (any) {
+          ld32(t_o + c0, t);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) t[i] = 0.0f;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat162 pr = __floats2bfloat162_rn(t[2 * e] * inv, t[2 * e + 1] * inv);
+          w[e] = poison ? 0x7FFF7FFFu : *reinterpret_cast<const uint32_t*>(&pr);
+        }
+        if (row_ok) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(orow + c0 + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        }
+      }
+      if (row_ok && a.stats != nullptr)
+        *reinterpret_cast<float2*>(a.stats + ((size_t)plane_q * n + qi) * 2) = make_float2(m, l);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFwdCols));
+}
+
+// ---------------------------------------------------------------------------
+// Column sums: key j's sum over the queries that see it and the query heads of
+// its KV head of exp2(z - m_i) / l_i, with the forward's row statistics.
+//
+// One 320-thread CTA per (128-key tile, KV head, sequence), two per SM, keys
+// on the TMEM lanes: S^T = K Q^T (M 128, N 128), so thread t of a warpgroup
+// owns key t and adds in a register; no atomics, a fixed order.  Warpgroups 0
+// and 1 take alternate (query head, query tile) blocks, warp 8 loads the query
+// tiles and stages (m, 1 / l, run) per query, warp 9 issues the products.
+// Query tiles none of whose queries sees the key tile are skipped.
+constexpr int kSumThreads = 320;
+constexpr int kSOffK = 0;
+constexpr int kSOffQ = kSOffK + kTileB;                    // 2 slots
+constexpr int kSOffStat = kSOffQ + 2 * kTileB;             // 2 x 128 x (m, 1 / l)
+constexpr int kSOffRun = kSOffStat + 2 * kTile * 8;        // 2 x 128 x (begin, end)
+constexpr int kSOffRed = kSOffRun + 2 * kTile * 8;         // 128 sums
+constexpr int kSOffBar = kSOffRed + kTile * 4;
+constexpr int kSBarK = 0, kSBarFull = 1, kSBarEmpty = 3, kSBarS = 5, kSBarSfree = 7, kSBarDone = 9, kSNumBars = 10;
+constexpr int kSumSmem = kSOffBar + 8 * kSNumBars + 16;
+constexpr uint32_t kSumCols = 256;
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kSumThreads, 2)
+    prompt_sums_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
+  extern __shared__ __align__(1024) uint8_t ssm[];
+  const uint32_t base = saddr(ssm);
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(ssm + kSOffBar + 8 * kSNumBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(ssm + kSOffBar + 8 * kSNumBars + 4);
+  auto bar = [&](int i) { return base + kSOffBar + 8 * i; };
+  const int n = a.n, G = a.group;
+  const int kt = blockIdx.x, h = blockIdx.y, bl = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int k0 = kt * kTile, k1 = min(k0 + kTile, n);
+  const int tiles = gridDim.x;
+  const int4* runs = a.runs + (size_t)bl * tiles;
+  auto seen = [&](int qt) {
+    const int4 r = runs[qt];
+    return r.x < k1 && r.y > k0;
+  };
+
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kSumCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSNumBars; ++i) {
+      const uint32_t cnt = i >= kSBarFull && i < kSBarFull + 2     ? 2
+                           : i >= kSBarEmpty && i < kSBarEmpty + 2 ? 5
+                           : i >= kSBarSfree && i < kSBarSfree + 2 ? 4
+                                                                   : 1;
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(cnt));
+    }
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tbase;
+  float sum = 0.0f;
+
+  if (warp == 8) {
+    // ------------------------------------------ K, query tiles, row statistics
+    if (lane == 0) {
+      bar_expect_tx(bar(kSBarK), kTileB);
+      tma_load_3d(base + kSOffK, &tm_k, 0, k0, bl * a.hkv + h, bar(kSBarK));
+      tma_load_3d(base + kSOffK + kBoxB, &tm_k, 64, k0, bl * a.hkv + h, bar(kSBarK));
+    }
+    int it = 0;
+    bool ok = true;
+    for (int g = 0; g < G && ok; ++g) {
+      const int plane = bl * a.hq + h * G + g;
+      for (int qt = 0; qt < tiles && ok; ++qt) {
+        if (!seen(qt)) continue;
+        const int x = it & 1;
+        if (it >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(kSBarEmpty + x), (uint32_t)(((it - 2) >> 1) & 1), abort))) {
+          set_abort(a.status, abort);
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t dst = base + kSOffQ + x * kTileB, b = bar(kSBarFull + x);
+          bar_expect_tx(b, kTileB);
+          tma_load_3d(dst, &tm_q, 0, qt * kTile, plane, b);
+          tma_load_3d(dst + kBoxB, &tm_q, 64, qt * kTile, plane, b);
+        }
+        float2* st = reinterpret_cast<float2*>(ssm + kSOffStat) + x * kTile;
+        int2* rn = reinterpret_cast<int2*>(ssm + kSOffRun) + x * kTile;
+#pragma unroll
+        for (int e = 0; e < kTile / 32; ++e) {
+          const int i = lane + 32 * e, qi = qt * kTile + i;
+          float2 s = make_float2(0.0f, 0.0f);  // past the prompt, or seeing nothing: probability 0
+          int2 r = make_int2(0, 0);
+          if (qi < n) {
+            s = *reinterpret_cast<const float2*>(a.stats + ((size_t)plane * n + qi) * 2);
+            s = s.y != 0.0f ? make_float2(s.x, 1.0f / s.y) : make_float2(0.0f, 0.0f);
+            r = run_of(a, bl, qi);
+          }
+          st[i] = s;
+          rn[i] = r;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(kSBarFull + x));
+        ++it;
+      }
+    }
+    if (lane == 0) {
+      // the last copies land before the CTA goes away
+      bar_wait(bar(kSBarK), 0, nullptr);
+      for (int e = max(0, it - 2); e < it; ++e) bar_wait(bar(kSBarFull + (e & 1)), (uint32_t)((e >> 1) & 1), nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ----------------------------------------------------------------- products
+    const bool el = elect_one();
+    const uint32_t id_s = instr_desc(kTile, kTile, true);
+    bool ok = __all_sync(0xffffffffu, bar_wait(bar(kSBarK), 0, abort));
+    if (!ok) set_abort(a.status, abort);
+    int it = 0;
+    for (int g = 0; g < G && ok; ++g) {
+      for (int qt = 0; qt < tiles && ok; ++qt) {
+        if (!seen(qt)) continue;
+        const int x = it & 1;
+        if (!__all_sync(0xffffffffu,
+                        bar_wait(bar(kSBarFull + x), (uint32_t)((it >> 1) & 1), abort) &&
+                            (it < 2 || bar_wait(bar(kSBarSfree + x), (uint32_t)(((it - 2) >> 1) & 1), abort)))) {
+          set_abort(a.status, abort);
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (el) {
+          const uint32_t ka = base + kSOffK, qa = base + kSOffQ + x * kTileB;
+#pragma unroll
+          for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
+            mma_f16(tmem + kTile * x, op_desc_sw128(ka + off), op_desc_sw128(qa + off), id_s, ks > 0);
+          }
+          mma_commit(bar(kSBarS + x));
+          mma_commit(bar(kSBarEmpty + x));
+        }
+        __syncwarp();
+        ++it;
+      }
+    }
+    if (el) mma_commit(bar(kSBarDone));
+    bar_wait(bar(kSBarDone), 0, nullptr);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ sums over the queries
+    const int x = warp >> 2, t = tid & (kTile - 1);
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kTile * x;
+    const float2* st = reinterpret_cast<const float2*>(ssm + kSOffStat) + x * kTile;
+    const int2* rn = reinterpret_cast<const int2*>(ssm + kSOffRun) + x * kTile;
+    const int key = k0 + t;
+    int it = 0;
+    bool ok = true;
+    for (int g = 0; g < G && ok; ++g) {
+      const float slope2 = BIAS ? slope_log2(a.mod, h * G + g) : 0.0f;
+      for (int qt = 0; qt < tiles && ok; ++qt) {
+        if (!seen(qt)) continue;
+        if ((it++ & 1) != x) continue;
+        const int use = it - 1;
+        const uint32_t par = (uint32_t)((use >> 1) & 1);
+        if (!__all_sync(0xffffffffu, bar_wait(bar(kSBarS + x), par, abort) && bar_wait(bar(kSBarFull + x), par, abort))) {
+          set_abort(a.status, abort);
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const int4 r = runs[qt];
+        const bool whole = r.z <= k0 && r.w >= k1;  // every query sees the whole key tile
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTile; c0 += 32) {
+          float v[32];
+          ld32(trow + c0, v);
+          if (CAP) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= a.mod.y_scale;
+            cap_scores(a.mod, v);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 s = st[c0 + i];
+            float zz = CAP ? v[i] : v[i] * a.qk_scale_log2;
+            if (BIAS) zz = fmaf(-slope2, fabsf((float)(qt * kTile + c0 + i - key)), zz);
+            float p = fast_exp2(zz - s.x);
+            if (!whole) {
+              const int2 b = rn[c0 + i];
+              p = key >= b.x && key < b.y ? p : 0.0f;
+            }
+            // (1 / l is 0 for a row that sees nothing; its p may be infinite)
+            acc[i & 3] = s.y != 0.0f ? fmaf(p, s.y, acc[i & 3]) : acc[i & 3];
+          }
+        }
+        sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar(kSBarSfree + x));
+          bar_arrive(bar(kSBarEmpty + x));
+        }
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(ssm + kSOffRed);
+  if (tid < kTile) red[tid] = sum;
+  __syncthreads();
+  if (tid >= kTile && tid < 2 * kTile && !*abort) {
+    const int t = tid - kTile, key = k0 + t;
+    if (key < n) a.sums[((size_t)bl * a.hkv + h) * n + key] = sum + red[t];
+  }
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSumCols));
+}
+
+// Column sums of a fresh prompt into the score slots of a cache's tokens.
+__global__ void prompt_scores_kernel(DevState s, int seq_begin, int n, const float* __restrict__ sums) {
+  const int p = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y, bl = blockIdx.z;
+  if (p >= n) return;
+  const int b = seq_begin + bl;
+  const float v = sums[((size_t)bl * s.hkv + h) * n + p];
+  int lo, hi;
+  pool_range(0, n, s.ring, &lo, &hi);
+  if (p < kSinks) {
+    s.sink_score[((size_t)b * s.hkv + h) * kSinks + p] = v;
+  } else if (p < hi) {
+    const int slot = p - lo;
+    const int blk = s.block_table[(size_t)b * s.max_bps + slot / kPage];
+    if ((unsigned)blk < (unsigned)s.num_blocks)
+      s.score[((size_t)blk * s.hkv + h) * kPage + slot % kPage] = v;
+    else
+      atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
+  } else {
+    s.ring_score[((size_t)b * s.hkv + h) * s.ring + (p - kSinks) % s.ring] = v;
+  }
+}
+
+template <bool CAP, bool BIAS>
+cudaError_t launch_fwd(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                       cudaStream_t st) {
+  static int done[64] = {0};
+  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_fwd_kernel<CAP, BIAS>), kFwdSmem, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.n + kFwdBlock - 1) / kFwdBlock, a.hq, a.batch);
+  prompt_fwd_kernel<CAP, BIAS><<<grid, kFwdThreads, kFwdSmem, st>>>(a, q, k, v);
+  return cudaGetLastError();
+}
+
+template <bool CAP, bool BIAS>
+cudaError_t launch_sums(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, cudaStream_t st) {
+  static int done[64] = {0};
+  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_sums_kernel<CAP, BIAS>), kSumSmem, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.n + kTile - 1) / kTile, a.hkv, a.batch);
+  prompt_sums_kernel<CAP, BIAS><<<grid, kSumThreads, kSumSmem, st>>>(a, q, k);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t tiles = ((size_t)n + kTile - 1) / kTile, planes = (size_t)batch * hkv;
+  PromptWs w{};
+  w.v16 = 0;
+  w.bad = up(planes * n * kHeadDim * 2);
+  w.runs = w.bad + up(planes * tiles * 16);
+  w.stats = w.runs + up(sums ? batch * tiles * 16 : 0);
+  w.sums = w.stats + up(sums ? (size_t)batch * hq * n * 8 : 0);
+  w.total = w.sums + up(sums ? planes * n * 4 : 0);
+  return w;
+}
+
+cudaError_t launch_prompt_scores(const DevState& s, int seq_begin, int batch, int n, const float* sums,
+                                 cudaStream_t st) {
+  prompt_scores_kernel<<<dim3((n + 255) / 256, s.hkv, batch), 256, 0, st>>>(s, seq_begin, n, sums);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prompt(const PromptArgs& a, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                          cudaStream_t st) {
+  CUtensorMap tm_q, tm_k, tm_v;
+  if (!encode_rows_map(&tm_q, q, a.n, a.batch * a.hq, kTile) || !encode_rows_map(&tm_k, k, a.n, a.batch * a.hkv, kTile) ||
+      !encode_rows_map(&tm_v, a.v16, a.n, a.batch * a.hkv, kTile, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
+    return cudaErrorInvalidValue;
+  prompt_prep_kernel<<<(a.n + kTile - 1) / kTile * (a.batch * a.hkv), kPrepThreads, 0, st>>>(a, v);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool cap = a.mod.c2 > 0.0f, bias = a.mod.slopes != nullptr;
+  e = cap ? (bias ? launch_fwd<true, true>(a, tm_q, tm_k, tm_v, st) : launch_fwd<true, false>(a, tm_q, tm_k, tm_v, st))
+          : (bias ? launch_fwd<false, true>(a, tm_q, tm_k, tm_v, st)
+                  : launch_fwd<false, false>(a, tm_q, tm_k, tm_v, st));
+  if (e != cudaSuccess || a.sums == nullptr) return e;
+  return cap ? (bias ? launch_sums<true, true>(a, tm_q, tm_k, st) : launch_sums<true, false>(a, tm_q, tm_k, st))
+             : (bias ? launch_sums<false, true>(a, tm_q, tm_k, st) : launch_sums<false, false>(a, tm_q, tm_k, st));
+}
+
+}  // namespace kvc

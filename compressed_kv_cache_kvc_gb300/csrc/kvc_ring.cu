@@ -109,7 +109,13 @@ __global__ void __launch_bounds__(kRingThreads) attn_ring_kernel(DevState s, int
       const int row = 16 * warp + r + (e >= 2 ? 8 : 0);
       const int g = 2 * c + (e & 1);
       const bool ok = row < n_here && g < G;
-      const float lg = ok ? acc[e] * qk_scale_log2 : -INFINITY;
+      float lg = ok ? acc[e] * qk_scale_log2 : -INFINITY;
+      if (ok && (w.mod.c2 > 0.0f || w.mod.slopes != nullptr)) {
+        // ring slot t holds the last position p < P with (p - 4) mod W = t
+        const int last = s.seq_pos[b] - 1, back = ((last - kSinks - slot0 - row) % W + W) % W;
+        lg = transform_score(w.mod, acc[e] * (w.mod.c2 > 0.0f ? w.mod.y_scale : qk_scale_log2),
+                             slope_log2(w.mod, h * G + g), back);
+      }
       sp[row][g] = lg;
       if (ok) w.ring_lg[((size_t)pair * G + g) * W + slot0 + row] = lg;
     }

@@ -462,6 +462,190 @@ kvc_status kvc_prefill_context(kvc_cache* cache, int32_t seq_begin, int32_t batc
                                const void* d_k, const void* d_v, void* d_out, float sm_scale, int32_t flags,
                                void* d_workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------ score transforms -- */
+
+/* Score transform of every attention on this cache (a property of the model's
+ * layer): with s = sm_scale * q . k,
+ *   z = softcap * tanh(s / softcap) - slope[j] * |p_q - p_k|
+ * for query head j at position p_q and a key at position p_k, and the softmax
+ * (and with it the H2O scores) runs over z.  In a decode step p_q is the
+ * sequence's newest position; keys have the positions they were appended at,
+ * also after evictions.  softcap 0: no cap; d_slopes null: no bias.
+ *   d_slopes: f32 [Hq] on the device, any finite values; borrowed until the
+ *   next kvc_set_score_transform or kvc_cache_destroy (and by every CUDA graph
+ *   captured meanwhile).
+ * Honoured by kvc_decode_attention, kvc_decode_attention_noalloc,
+ * kvc_decode_step, kvc_decode_step_overlap, kvc_prefill_attention,
+ * kvc_prefill_attention_masked and kvc_prefill_context, with every code
+ * format and with a bf16 window.  kvc_prefill_workspace_bytes grows while a
+ * transform is set.  Enqueues nothing; takes effect with the next call.
+ * The cap is accurate to 4e-7 relative, the bias to fp32 rounding.
+ * Errors: KVC_ERR_INVALID_ARG for a softcap that is negative or not finite,
+ * or a misaligned d_slopes (the transform set before stays). */
+kvc_status kvc_set_score_transform(kvc_cache* cache, float softcap, const float* d_slopes);
+
+/* ------------------------------------------------------- masked prompts ---- */
+
+/* Attention of prompts over themselves, without a cache: query i of a
+ * sequence sees the keys [key_begin[i], key_end[i]) of its sequence, so one
+ * run of keys per query: causal (both null), packed documents (begin = the
+ * document's first token), a prefix whose tokens see each other both ways
+ * (end = the prefix's end), a sliding window, padding rows (an empty run:
+ * output 0).  Scores are transformed as kvc_set_score_transform says, with
+ * the distance |i - j|. */
+typedef struct {
+  int32_t batch, num_q_heads, num_kv_heads; /* Hq % Hkv == 0                      */
+  int32_t n;                                /* tokens per sequence                */
+  float sm_scale;                           /* > 0                                */
+  float softcap;                            /* 0: none                            */
+  const float* d_slopes;                    /* f32 [Hq], or null                  */
+  const int32_t* d_key_begin;               /* i32 [batch][n], or null: 0         */
+  const int32_t* d_key_end;                 /* i32 [batch][n], or null: i + 1     */
+} kvc_prompt_params;
+
+/* Workspace of kvc_prompt_attention (`sums`: whether d_sums is given): V in
+ * fp16, 256 bytes a token and KV head, and with sums 8 bytes a token and query
+ * head.  0 for sizes that are not positive. */
+size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t n, int32_t sums);
+
+/*   d_q:   bf16 [batch][Hq][n][128];  d_k, d_v: bf16 [batch][Hkv][n][128];
+ *   d_out: bf16 [batch][Hq][n][128];  all 16-byte aligned, head_dim 128;
+ *   d_sums: null, or f32 [batch][Hkv][n]: every key's sum over the queries and
+ *   the query heads of its KV head of the probability they give it;
+ *   d_status: one i32 on the device; KVC_DEV_* bits are or'ed into it
+ *   (KVC_DEV_WAIT_TIMEOUT, KVC_DEV_PREFILL_RANGE), never cleared.
+ * Runs are clamped to [0, n); products are bf16 x bf16 (Q K^T, exact) and fp16
+ * (P V, P rounded to 11 bits), sums fp32.  A K or Q value that is not finite
+ * makes the rows that see it not finite; a row that sees a key whose V row
+ * holds a NaN or an infinity is NaN; rows that do not see them are not
+ * touched by them (the status bit KVC_DEV_PREFILL_RANGE is set all the same).
+ * Two launches, three with sums; results do not depend on the order of
+ * execution.  Errors, before any launch: KVC_ERR_INVALID_ARG for sizes that
+ * are not positive, Hq % Hkv != 0, a null or misaligned pointer, an sm_scale
+ * that is not positive and finite, a softcap that is negative or not finite, a
+ * short workspace; KVC_ERR_UNSUPPORTED for more than 65535 sequences or query
+ * heads or 2^31 tiles of 128 queries. */
+kvc_status kvc_prompt_attention(const kvc_prompt_params* params, const void* d_q, const void* d_k, const void* d_v,
+                                void* d_out, float* d_sums, int32_t* d_status, void* d_workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* kvc_prefill_attention with a run of keys per query (as in
+ * kvc_prompt_params; null: causal) and the cache's score transform: append the
+ * prompt, run the attention over its exact bf16 keys and values and, with
+ * KVC_ATTN_ACCUM_H2O, set every prompt token's H2O score to its column sum.
+ * The decode steps that follow see every token: the runs belong to this call.
+ * d_workspace: kvc_prefill_masked_workspace_bytes(cache, batch, n) bytes.
+ * Launches: the append's, then two, four with scores.  Errors as
+ * kvc_prefill_attention. */
+size_t kvc_prefill_masked_workspace_bytes(const kvc_cache* cache, int32_t batch, int32_t n);
+kvc_status kvc_prefill_attention_masked(kvc_cache* cache, int32_t seq_begin, int32_t batch, int32_t n, const void* d_q,
+                                        const void* d_k, const void* d_v, void* d_out, float sm_scale, int32_t flags,
+                                        const int32_t* d_key_begin, const int32_t* d_key_end, void* d_workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------- block-scaled cache ---- */
+
+/* A second form of the cache: 8-bit codes with ONE scale per block of
+ * `block_tokens` tokens and KV head (one for K, one for V) instead of one per
+ * token, for models whose serving keeps scales per block.  Per sequence and
+ * KV head, positions 0..3 (sinks) and the open block (the newest
+ * (P - 4) mod block_tokens tokens) are held exactly, in bf16; a block is
+ * quantised as a whole when its last token arrives, so the result does not
+ * depend on how the tokens were split into appends.  With amax over the
+ * block's block_tokens x 128 values, scale = amax / 127 (INT8) or amax / 448
+ * (E4M3), code = x / scale (both IEEE fp32 divisions) rounded half to even
+ * (clamped to [-127, 127]; saturated to +-448); a zero block has scale 0 and
+ * codes 0.  Inputs are finite (a NaN gets code 0, an infinity an infinite
+ * scale).  There is no token-granular eviction: a block's tokens share their
+ * scale.  Handles follow the conventions above (caller-owned device memory,
+ * asynchronous calls, one status word per cache, not thread-safe). */
+typedef struct {
+  int32_t num_q_heads;        /* Hq                                             */
+  int32_t num_kv_heads;       /* Hkv; Hq % Hkv == 0 and Hq / Hkv <= 8           */
+  int32_t head_dim;           /* must be 128                                    */
+  int32_t block_tokens;       /* 16, 32, 64 or 128                              */
+  int32_t num_blocks;         /* physical blocks in the pool                    */
+  int32_t max_batch;          /* sequences the cache holds, at most 1024        */
+  int32_t max_blocks_per_seq; /* block-table row length                         */
+  int32_t codes;              /* KVC_CODES_INT (8 bits) or KVC_CODES_E4M3       */
+} kvc_block_config;
+
+typedef struct kvc_block_cache kvc_block_cache;
+
+/* Buffers carved out of the state (kvc_block_buffer). */
+typedef enum {
+  KVC_BLOCK_BUF_K_CODES = 0, /* u8   [num_blocks][Hkv][block_tokens][128]        */
+  KVC_BLOCK_BUF_V_CODES = 1,
+  KVC_BLOCK_BUF_K_SCALE = 2, /* f32  [num_blocks][Hkv]                           */
+  KVC_BLOCK_BUF_V_SCALE = 3,
+  KVC_BLOCK_BUF_K_EXACT = 4, /* bf16 [max_batch][Hkv][4 + block_tokens][128]: the
+                                sinks, then the open block's rows               */
+  KVC_BLOCK_BUF_V_EXACT = 5,
+  KVC_BLOCK_BUF_TABLE = 6,   /* i32  [max_batch][max_blocks_per_seq]             */
+  KVC_BLOCK_BUF_SEQ_POS = 7, /* i32  [max_batch] tokens held                     */
+  KVC_BLOCK_BUF_FREE = 8,    /* i32  [num_blocks] free block ids (stack)         */
+  KVC_BLOCK_BUF_COUNTERS = 9,/* i32  [64]: [0] free-stack top, [1] status word   */
+  KVC_BLOCK_BUF_TICKETS = 10,/* i32  [max_batch * Hkv + 1]; zero between calls   */
+  KVC_BLOCK_BUF_COUNT = 11
+} kvc_block_buffer_id;
+
+/* State bytes (0 for an invalid or unsupported config), handle, buffers,
+ * lengths, status: as their kvc_cache_* counterparts.  kvc_block_cache_reset
+ * empties the cache (blocks handed out in ascending order) and synchronises;
+ * kvc_block_sync_host reloads the host mirror after the caller restored the
+ * state bytes, kvc_block_read_status reads and clears the status word; both
+ * synchronise `stream`. */
+size_t kvc_block_state_bytes(const kvc_block_config* cfg);
+kvc_status kvc_block_cache_create(const kvc_block_config* cfg, void* d_state, size_t state_bytes,
+                                  kvc_block_cache** out);
+void kvc_block_cache_destroy(kvc_block_cache* cache);
+kvc_status kvc_block_cache_reset(kvc_block_cache* cache, void* stream);
+kvc_status kvc_block_buffer(const kvc_block_cache* cache, int32_t which, void** d_ptr, size_t* bytes);
+kvc_status kvc_block_length(const kvc_block_cache* cache, int32_t seq, int32_t* positions);
+kvc_status kvc_block_sync_host(kvc_block_cache* cache, void* stream);
+kvc_status kvc_block_read_status(kvc_block_cache* cache, int32_t* h_status, void* stream);
+int32_t kvc_block_last_launch_count(const kvc_block_cache* cache);
+
+/* Free the sequences [seq_begin, seq_begin + batch): their blocks go back to
+ * the pool, their lengths become 0 (idempotent).  One launch, none when they
+ * are all empty. */
+kvc_status kvc_block_release(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, void* stream);
+
+/* Append n_new tokens to each sequence of the slice.
+ *   d_k, d_v: bf16 [batch][Hkv][n_new][128], 16-byte aligned.
+ * One launch; n_new == 0 is a no-op.  Blocks come from the free stack in
+ * sequence order.  Errors: KVC_ERR_INVALID_ARG (slice, n_new < 0, pointers);
+ * KVC_ERR_CAPACITY when a sequence would need more than max_blocks_per_seq
+ * blocks or the pool has too few (nothing is written). */
+kvc_status kvc_block_append(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t n_new, const void* d_k,
+                            const void* d_v, void* stream);
+
+/* Single-query attention over everything the slice's sequences hold, the
+ * newest token included: d_q, d_out bf16 [batch][Hq][128], 16-byte aligned;
+ * scores transformed as kvc_set_score_transform says (softcap 0 and d_slopes
+ * null: plain), the query at the newest position.  Accumulated in fp32.
+ *   d_workspace: kvc_block_workspace_bytes(cache, batch) bytes, 256-byte
+ *   aligned, contents arbitrary.
+ * One launch: the CTA that finishes a (sequence, KV head) last joins its
+ * partial results, in a fixed order.  Calls on the same cache run one after
+ * another (they share its tickets); two graphs may share a workspace if their
+ * replays do not overlap.
+ * Errors: KVC_ERR_INVALID_ARG (slice, pointers, sm_scale, softcap, workspace,
+ * an empty sequence). */
+size_t kvc_block_workspace_bytes(const kvc_block_cache* cache, int32_t batch);
+kvc_status kvc_block_attention(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, const void* d_q, void* d_out,
+                               float sm_scale, float softcap, const float* d_slopes, void* d_workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Read the cache back as dense tensors: the values of positions [pos_begin,
+ * pos_begin + n) of every sequence of the slice as the attention sees them
+ * (code * scale rounded to bf16; sinks and the open block as appended).
+ *   d_k, d_v: bf16 [batch][Hkv][n][128], 16-byte aligned.
+ * Rows at or past a sequence's length are left as they were.  One launch.
+ * Errors: KVC_ERR_INVALID_ARG (slice, pos_begin < 0, n <= 0, pointers). */
+kvc_status kvc_block_read(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t pos_begin, int32_t n,
+                          void* d_k, void* d_v, void* stream);
+
 /* ---------------------------------------------------------------- misc ---- */
 
 /* Synchronise `stream`, copy the device status word to *h_status and clear
