@@ -740,13 +740,13 @@ __global__ void __launch_bounds__(kSumThreads, 2)
             const float2 s = st[c0 + i];
             float zz = CAP ? v[i] : v[i] * a.qk_scale_log2;
             if (BIAS) zz = fmaf(-slope2, fabsf((float)(qt * kTile + c0 + i - key)), zz);
-            float p = fast_exp2(zz - s.x);
+            const float p = fast_exp2(zz - s.x);
+            bool on = s.y != 0.0f;  // 1 / l is 0 for a row that sees nothing (its p may be infinite)
             if (!whole) {
               const int2 b = rn[c0 + i];
-              p = key >= b.x && key < b.y ? p : 0.0f;
+              on = on && key >= b.x && key < b.y;
             }
-            // (1 / l is 0 for a row that sees nothing; its p may be infinite)
-            acc[i & 3] = s.y != 0.0f ? fmaf(p, s.y, acc[i & 3]) : acc[i & 3];
+            acc[i & 3] = on ? fmaf(p, s.y, acc[i & 3]) : acc[i & 3];
           }
         }
         sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
