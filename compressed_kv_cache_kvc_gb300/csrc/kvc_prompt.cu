@@ -181,7 +181,7 @@ __device__ __forceinline__ void chunk_scores(const PromptArgs& a, float (&z)[32]
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = cap_score(a.mod, z[i] * a.mod.y_scale);
+      for (int i = 0; i < 32; ++i) z[i] = cap_far(a.mod, z[i] * a.mod.y_scale);
     }
   }
   if (BIAS) {
@@ -449,19 +449,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (kKeep) tmem_st32(t_s + 32 * c, z);
         mx = chunk_max(z, mx);
       };
-      tmem_wait(za);
-      tmem_ld32(t_s + 32, zb);
-      first(za, 0);
-      tmem_wait(zb);
-      tmem_ld32(t_s + 64, za);
-      first(zb, 1);
-      tmem_wait(za);
-      tmem_ld32(t_s + 96, zb);
-      first(za, 2);
-      tmem_wait(zb);
-      if (kKeep) tmem_st_wait();
-      tmem_ld32(t_s, za);
-      first(zb, 3);
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {
+        tmem_wait(za);
+        tmem_ld32(t_s + 32 * c + 32, zb);
+        first(za, c);
+        tmem_wait(zb);
+        if (kKeep) tmem_st_wait();
+        tmem_ld32(t_s + (32 * c + 64) % 128, za);  // after the last chunk: the first again
+        first(zb, c + 1);
+      }
       // scale > 0 and a cap keep the order: the maximum commutes with them
       if (kRaw) mx *= a.qk_scale_log2;
       if (CAP && !BIAS) mx = mx > -INFINITY ? cap_score(a.mod, mx * a.mod.y_scale) : mx;
@@ -496,16 +493,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_st16(t_s + 16 * c, pw);
       };
       if (kKeep) tmem_st_wait();
-      tmem_ld32(t_s + 32, zb);
-      second(za, 0);
-      tmem_wait(zb);
-      tmem_ld32(t_s + 64, za);
-      second(zb, 1);
-      tmem_wait(za);
-      tmem_ld32(t_s + 96, zb);
-      second(za, 2);
-      tmem_wait(zb);
-      second(zb, 3);
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {
+        tmem_ld32(t_s + 32 * c + 32, zb);
+        second(za, c);
+        tmem_wait(zb);
+        if (c == 0) tmem_ld32(t_s + 64, za);
+        second(zb, c + 1);
+        if (c == 0) tmem_wait(za);
+      }
       const float2 lt = add2(ls[0], ls[1]);
       l += lt.x + lt.y;
       tmem_st_wait();

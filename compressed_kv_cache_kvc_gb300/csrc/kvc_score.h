@@ -13,10 +13,14 @@
 //                relative error 2.6e-9, 7.5e-8 as evaluated in fp32.  c2 is
 //                multiplied into the coefficients, so z costs seven
 //                multiply-adds and no MUFU instruction.
-//   else         (1 - e) / (1 + e), e = 2^(-2 log2(e) |y|) <= 0.31: no
-//                cancellation, relative error below 4e-7, 1 from |y| = 9 on.
-// Logits rarely leave the first interval with the caps that models use (30 to
-// 50), so the second is taken only by threads that hold such a score.
+//   else         (1 - e) / (1 + e), e = 2^(-2 log2(e) |y|): 1 from |y| = 9 on;
+//                ex2 is off by at most 2^-22 e, rcp by 2^-23 of its value, so
+//                tanh is off by at most 2 * 2^-22 + 2^-23 + 2 * 2^-24 < 7.2e-7
+//                for every y, also where a group of scores takes this form
+//                because one of them left the first interval.
+// A score is so accurate to 7.2e-7 of the cap.  Scores rarely leave the first
+// interval with the caps that models use (30 to 50); the second form costs two
+// MUFU instructions a score.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -76,6 +80,7 @@ __device__ __forceinline__ float cap_score(const ScoreMod& m, float y) {
   return fabsf(y) <= kCapPolyMax ? cap_poly(m, y) : cap_far(m, y);
 }
 
+// N scores in place: the polynomial when all are within its interval.
 template <int N>
 __device__ __forceinline__ void cap_scores(const ScoreMod& m, float (&y)[N]) {
   float top = 0.0f;
@@ -86,7 +91,7 @@ __device__ __forceinline__ void cap_scores(const ScoreMod& m, float (&y)[N]) {
     for (int i = 0; i < N; ++i) y[i] = cap_poly(m, y[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = cap_score(m, y[i]);
+    for (int i = 0; i < N; ++i) y[i] = cap_far(m, y[i]);
   }
 }
 

@@ -479,7 +479,7 @@ kvc_status kvc_prefill_context(kvc_cache* cache, int32_t seq_begin, int32_t batc
  * kvc_prefill_attention_masked and kvc_prefill_context, with every code
  * format and with a bf16 window.  kvc_prefill_workspace_bytes grows while a
  * transform is set.  Enqueues nothing; takes effect with the next call.
- * The cap is accurate to 4e-7 relative, the bias to fp32 rounding.
+ * Capped scores are accurate to 7.2e-7 of softcap, the bias to fp32 rounding.
  * Errors: KVC_ERR_INVALID_ARG for a softcap that is negative or not finite,
  * or a misaligned d_slopes (the transform set before stays). */
 kvc_status kvc_set_score_transform(kvc_cache* cache, float softcap, const float* d_slopes);

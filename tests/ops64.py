@@ -8,8 +8,9 @@ sum_j p_j |v_j| (all products and sums in fp32):
     bf16 parts, less: 2^-11 A;
   * scores z (log2 units, |z| <= Z) off by at most dz: the fp32 rounding of the
     product, scale and bias and of z itself, 4 steps of 2^-24 Z, and the cap's
-    4e-7 Z: every p off by dz ln 2 relative, both in the numerator and in the
-    sum: 2 ln 2 dz A;
+    7.2e-7 of the cap (ex2 2^-22 twice, rcp 2^-23 and two roundings of 2^-24):
+    every p off by dz ln 2 relative, both in the numerator and in the sum: 2 ln 2
+    dz A;
   * fp32 sums of n terms: n 2^-24 A covers any order;
   * P below fp16's normal range: an absolute 2^-25 of the largest p scaled by up
     to 2^5, for each of n terms: n 2^-20 max|v| is 2^-24 n max|v| with the
@@ -55,7 +56,7 @@ def scores(q, k, scale, cap, slope, q_pos, k_pos):
 def score_error(z, cap, visible):
     """dz (log2 units): see the module's docstring."""
     big = np.abs(np.where(visible, z, 0.0)).max() * LOG2E if visible.any() else 0.0
-    return big * (4 * 2.0 ** -24 + (4e-7 if cap else 0.0)) + 2.0 ** -24
+    return big * 4 * 2.0 ** -24 + 7.2e-7 * cap * LOG2E + 2.0 ** -24
 
 
 def offset_terms(q, k_scale, v_scale, p, scale):
