@@ -16,23 +16,29 @@
 //   prompt_sums_kernel   column sums from the row statistics.
 //
 // prompt_fwd_kernel.  4 * 128 flops per visible pair: bound by the tensor
-// pipe.  One 320-thread CTA per (256 queries, query head, sequence), longest
-// blocks first:
-//   * warps 0-3 and 4-7 own one 128-query tile each ("A", "B"), a thread per
-//     query row; TMEM columns: S_x at 128 x (its first 64 columns become P in
-//     fp16), O_x at 256 + 128 x;
-//   * warp 8 issues the products, warp 9 the TMA loads: K and V tiles of 128
+// pipe and, with a cap or a bias, by the issue of the softmax.  One 576-thread
+// CTA per (256 queries, query head, sequence), longest blocks first:
+//   * warps 0-7 and 8-15 own one 128-query tile each ("A", "B"), two threads
+//     per query row: warps 0-3 (8-11) the first 64 keys of a key tile, warps
+//     4-7 (12-15) the others, so that four warps per scheduler hide each
+//     other's latencies and a row's half lives in registers;
+//   * warp 16 issues the products, warp 17 the TMA loads: K and V tiles of 128
 //     keys into two slots each.  K is read K-major and V in its own layout
 //     (MN-major), both with the 128-byte swizzle, so nothing is transposed.
-// Order of the products: P V_A(j - 1), S_A(j), P V_B(j - 1), S_B(j): the
-// pipe runs them in order, so S_x(j) may overwrite P_x(j - 1) without a wait,
-// S_x(j) complete implies P V_x(j - 1) complete, and one tile's softmax runs
-// under the other tile's products.  M = N = 128 products cost 64 cycles each,
-// 2048 a round of both tiles; the softmax takes two values per instruction
-// where the ISA has the form.
-// The running maximum is lazy (O is rescaled when a row's maximum grows by
-// more than 8 in log2 units), P is rounded to fp16 (11 significant bits; p <=
-// 2^8), the sums add the unrounded p in fp32.
+// TMEM columns: S_x at 128 x, O_x at 256 + 128 x; the first 32 columns of each
+// half of S_x become that half's P in fp16.  Order of the products: P V_A(prev), S_A(next), P V_B(prev),
+// S_B(next): the pipe runs them in order, so S_x may overwrite the P_x before
+// it without a wait, S_x complete implies the P V_x before it complete, and one
+// tile's softmax runs under the other tile's products.  M = N = 128 products
+// cost 64 cycles each, 2048 a round of both tiles.
+// Key tiles go from the last to the first: with a distance bias the nearest
+// keys, which set the maximum, come first.  The running maximum is lazy (O is
+// rescaled when a row's maximum grows by more than 8 in log2 units), P is
+// rounded to fp16 (11 significant bits; p <= 2^8), the sums add the unrounded p
+// in fp32.  Per tile the two threads of a row exchange their maxima through
+// shared memory (a named barrier of the tile's eight warps).  A half is read
+// from TMEM twice, for the maximum and for P, instead of being held across the
+// exchange: 96 registers a thread is what 18 warps leave.
 // Key tiles no query of a 128-query tile sees are skipped; tiles every row of
 // a warp sees whole take no mask.  Masked scores are replaced before the
 // maximum, and P is exactly 0 there; V rows that are not finite enter the
@@ -43,6 +49,8 @@
 // freed).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "kvc_device.h"
 #include "kvc_internal.h"
@@ -55,7 +63,7 @@ using namespace dev;
 using namespace tc;
 
 constexpr int kTile = 128;                        // queries per tile, keys per tile
-constexpr int kFwdThreads = 320;
+constexpr int kFwdThreads = 576;
 constexpr int kFwdBlock = 2 * kTile;
 constexpr float kLazyMax = 8.0f;
 constexpr int kTileB = kTile * kHeadDim * 2;      // 32 KB: a Q, K or V tile, two boxes of 64 dims
@@ -68,8 +76,10 @@ constexpr int kFOffBar = kFOffV + 2 * kTileB;
 // complete, P written, O complete (per tile), all products complete
 constexpr int kFBarQ = 0, kFBarK = 2, kFBarV = 4, kFBarKe = 6, kFBarVe = 8, kFBarS = 10, kFBarP = 12, kFBarO = 14,
               kFBarDone = 16, kFNumBars = 17;
-constexpr int kFOffMisc = kFOffBar + 8 * kFNumBars;  // TMEM base, abort flag, [8][2] run bounds per warp
-constexpr int kFwdSmem = kFOffMisc + 8 + 64;
+constexpr int kFOffMisc = kFOffBar + 8 * kFNumBars;  // TMEM base, abort flag, [8][2] run bounds per 32 rows
+constexpr int kFOffMax = kFOffMisc + 8 + 64;         // [2 parities][2 tiles][2 halves][128] row maxima
+constexpr int kFwdSmem = kFOffMax + 2 * 2 * 2 * kTile * 4;
+constexpr int kNbTile = 1;  // named barriers of the tiles' warps: 1, 2
 constexpr uint32_t kFwdCols = 512;
 
 __device__ __forceinline__ void set_abort(int* status, volatile int* abort) {
@@ -162,22 +172,34 @@ __device__ __forceinline__ void chunk_scores(const PromptArgs& a, float (&z)[32]
     float top[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-      top[0] = fmaxf(fmaxf(top[0], fabsf(z[i])), fabsf(z[i + 1]));
-      top[1] = fmaxf(fmaxf(top[1], fabsf(z[i + 2])), fabsf(z[i + 3]));
+      top[0] = max3_abs(top[0], z[i], z[i + 1]);
+      top[1] = max3_abs(top[1], z[i + 2], z[i + 3]);
     }
-    if (!(fmaxf(top[0], top[1]) * a.mod.y_scale > kCapPolyMax)) {  // (a NaN stays NaN in the polynomial)
+    const float most = fmaxf(top[0], top[1]);
+    if (!(most > a.near_max)) {  // (a NaN stays NaN in the polynomials)
+      f32x2 c[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) c[i] = pack2(a.near[i], a.near[i]);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const float2 y = mul2(make_float2(z[i], z[i + 1]), make_float2(a.mod.y_scale, a.mod.y_scale));
-        const float2 u = mul2(y, y);
-        float2 h = fma2(make_float2(a.mod.poly[5], a.mod.poly[5]), u, make_float2(a.mod.poly[4], a.mod.poly[4]));
-        h = fma2(h, u, make_float2(a.mod.poly[3], a.mod.poly[3]));
-        h = fma2(h, u, make_float2(a.mod.poly[2], a.mod.poly[2]));
-        h = fma2(h, u, make_float2(a.mod.poly[1], a.mod.poly[1]));
-        h = fma2(h, u, make_float2(a.mod.poly[0], a.mod.poly[0]));
-        const float2 r = mul2(y, h);
-        z[i] = r.x;
-        z[i + 1] = r.y;
+        const f32x2 x = pack2(z[i], z[i + 1]);
+        const f32x2 u = mul2(x, x);
+        f32x2 h = fma2(c[4], u, c[3]);
+        h = fma2(h, u, c[2]);
+        h = fma2(h, u, c[1]);
+        h = fma2(h, u, c[0]);
+        unpack2(mul2(x, h), z[i], z[i + 1]);
+      }
+    } else if (most <= a.mid_max) {
+      const f32x2 ys = pack2(a.mod.y_scale, a.mod.y_scale);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const f32x2 y = mul2(pack2(z[i], z[i + 1]), ys);
+        const f32x2 u = mul2(y, y);
+        f32x2 h = pack2(a.mid[9], a.mid[9]);
+#pragma unroll
+        for (int e = 8; e >= 0; --e) h = fma2(h, u, pack2(a.mid[e], a.mid[e]));
+        unpack2(mul2(y, h), z[i], z[i + 1]);
       }
     } else {
 #pragma unroll
@@ -186,17 +208,25 @@ __device__ __forceinline__ void chunk_scores(const PromptArgs& a, float (&z)[32]
   }
   if (BIAS) {
     // slope2 * (key - query) for keys at or before the query, else its negative
-    const float2 sl = make_float2(slope2, slope2), d0 = make_float2(dist0, dist0);
+    const f32x2 sl = pack2(slope2, slope2), d0 = pack2(dist0, dist0), sc = pack2(a.qk_scale_log2, a.qk_scale_log2);
+    auto run = [&](auto abs_tag) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float2 d = add2(d0, make_float2((float)i, (float)(i + 1)));
-      if (beyond) d = make_float2(-fabsf(d.x), -fabsf(d.y));
-      float2 b = make_float2(z[i], z[i + 1]);
-      if (!CAP) b = mul2(b, make_float2(a.qk_scale_log2, a.qk_scale_log2));
-      const float2 r = fma2(d, sl, b);
-      z[i] = r.x;
-      z[i + 1] = r.y;
-    }
+      for (int i = 0; i < 32; i += 2) {
+        f32x2 d = add2(d0, pack2((float)i, (float)(i + 1)));
+        if (decltype(abs_tag)::value) {
+          float x, y;
+          unpack2(d, x, y);
+          d = pack2(-fabsf(x), -fabsf(y));
+        }
+        f32x2 b = pack2(z[i], z[i + 1]);
+        if (!CAP) b = mul2(b, sc);
+        unpack2(fma2(d, sl, b), z[i], z[i + 1]);
+      }
+    };
+    if (beyond)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
   }
 }
 
@@ -211,24 +241,27 @@ __device__ __forceinline__ float chunk_max(const float (&z)[32], float m) {
   float t0 = m, t1 = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    t0 = fmaxf(fmaxf(t0, z[i]), z[i + 1]);
-    t1 = fmaxf(fmaxf(t1, z[i + 2]), z[i + 3]);
+    t0 = max3(t0, z[i], z[i + 1]);
+    t1 = max3(t1, z[i + 2], z[i + 3]);
   }
   return fmaxf(t0, t1);
 }
 
-// 32 scores (raw products for `raw`) -> probabilities 2^(z - m) in fp16 pairs;
+// 32 scores (raw products for RAW) -> probabilities 2^(z - m) in fp16 pairs;
 // their unrounded sum is added to ls.
-__device__ __forceinline__ void chunk_probs(const float (&z)[32], bool raw, float scale, float m, uint32_t (&pw)[16],
-                                            float2 (&ls)[2]) {
-  const float2 nm = make_float2(-m, -m), sc = make_float2(scale, scale);
+template <bool RAW>
+__device__ __forceinline__ void chunk_probs(const float (&z)[32], float scale, float m, uint32_t (&pw)[16],
+                                            f32x2 (&ls)[2]) {
+  const f32x2 nm = pack2(-m, -m), sc = pack2(scale, scale);
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const float2 zz = make_float2(z[2 * e], z[2 * e + 1]);
-    const float2 d = raw ? fma2(zz, sc, nm) : add2(zz, nm);
-    const float2 p = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-    ls[e & 1] = add2(ls[e & 1], p);
-    const __half2 hh = __floats2half2_rn(p.x, p.y);
+    const f32x2 zz = pack2(z[2 * e], z[2 * e + 1]);
+    float x, y;
+    unpack2(RAW ? fma2(zz, sc, nm) : add2(zz, nm), x, y);
+    x = fast_exp2(x);
+    y = fast_exp2(y);
+    ls[e & 1] = add2(ls[e & 1], pack2(x, y));
+    const __half2 hh = __floats2half2_rn(x, y);
     pw[e] = *reinterpret_cast<const uint32_t*>(&hh);
   }
 }
@@ -249,23 +282,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int plane_q = bl * a.hq + hqi, plane_kv = bl * a.hkv + hqi / a.group;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int qblk = qb * kFwdBlock;
-  const int qi = qblk + tid;  // (softmax threads) this thread's query row
+  // (softmax threads) query tile, half of the key tile, query row
+  const int x = warp >> 3, half = (warp >> 2) & 1, row = tid & (kTile - 1);
+  const int qi = qblk + x * kTile + row;
 
-  if (warp == 8) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kFwdCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (tid == kFwdBlock + 32) {
+  if (tid == 17 * 32) {
     for (int i = 0; i < kFNumBars; ++i)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)),
-                   "r"(i == kFBarP || i == kFBarP + 1 ? 4u : 1u));
+                   "r"(i == kFBarP || i == kFBarP + 1 ? 8u : 1u));
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // the rows' runs; per warp the keys some row sees and those every row sees
   int2 run = make_int2(0, 0);
   int all_lo = 0, all_hi = INT_MAX;
-  if (warp < 8) {
+  if (warp < 16) {
     int lo = INT_MAX, hi = 0;
     if (qi < n) {
       run = run_of(a, bl, qi);
@@ -279,9 +314,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     hi = __reduce_max_sync(0xffffffffu, hi);
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-    if (lane == 0) {
-      sh_run[2 * warp] = lo;
-      sh_run[2 * warp + 1] = hi;
+    if (lane == 0 && half == 0) {
+      sh_run[2 * (4 * x + (warp & 3))] = lo;
+      sh_run[2 * (4 * x + (warp & 3)) + 1] = hi;
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -291,34 +326,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   // key tiles [x_lo, x_hi) of query tile x; [t_lo, t_hi) of both
   int x_lo[2], x_hi[2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int y = 0; y < 2; ++y) {
     int lo = INT_MAX, hi = 0;
 #pragma unroll
-    for (int w = 4 * x; w < 4 * x + 4; ++w) {
+    for (int w = 4 * y; w < 4 * y + 4; ++w) {
       lo = min(lo, sh_run[2 * w]);
       hi = max(hi, sh_run[2 * w + 1]);
     }
-    x_lo[x] = lo < hi ? lo / kTile : 0;
-    x_hi[x] = lo < hi ? (hi + kTile - 1) / kTile : 0;
+    x_lo[y] = lo < hi ? lo / kTile : 0;
+    x_hi[y] = lo < hi ? (hi + kTile - 1) / kTile : 0;
   }
   const bool on0 = x_lo[0] < x_hi[0], on1 = x_lo[1] < x_hi[1];
   const int t_lo = on0 && on1 ? min(x_lo[0], x_lo[1]) : on0 ? x_lo[0] : x_lo[1];
   const int t_hi = max(x_hi[0], x_hi[1]);
+  const int n_it = t_hi - t_lo;  // key tiles, from t_hi - 1 down
 
-  if (warp == 9) {
+  if (warp == 17) {
     // ------------------------------------------------------------- TMA loads
-    if (lane == 0 && t_lo < t_hi) {
+    if (lane == 0 && n_it > 0) {
       int issued = 0;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t dst = base + kFOffQ + x * kTileB;
-        bar_expect_tx(bar(kFBarQ + x), kTileB);
-        tma_load_3d(dst, &tm_q, 0, qblk + x * kTile, plane_q, bar(kFBarQ + x));
-        tma_load_3d(dst + kBoxB, &tm_q, 64, qblk + x * kTile, plane_q, bar(kFBarQ + x));
-      }
       bool ok = true;
-      for (int j = t_lo; j < t_hi && ok; ++j) {
-        const int it = j - t_lo, sl = it & 1;
+      for (int it = 0; it < n_it && ok; ++it) {
+        const int j = t_hi - 1 - it, sl = it & 1;
         const uint32_t par = (uint32_t)((it >> 1) & 1) ^ 1u;  // the slot's previous tile released
         if (it >= 2 && !bar_wait(bar(kFBarKe + sl), par, abort)) ok = false;
         if (ok) {
@@ -327,6 +356,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           tma_load_3d(dst, &tm_k, 0, j * kTile, plane_kv, b);
           tma_load_3d(dst + kBoxB, &tm_k, 64, j * kTile, plane_kv, b);
           issued = 2 * it + 1;
+        }
+        if (it == 0) {
+#pragma unroll
+          for (int y = 1; y >= 0; --y) {
+            const uint32_t dst = base + kFOffQ + y * kTileB;
+            bar_expect_tx(bar(kFBarQ + y), kTileB);
+            tma_load_3d(dst, &tm_q, 0, qblk + y * kTile, plane_q, bar(kFBarQ + y));
+            tma_load_3d(dst + kBoxB, &tm_q, 64, qblk + y * kTile, plane_q, bar(kFBarQ + y));
+          }
         }
         if (ok && it >= 2 && !bar_wait(bar(kFBarVe + sl), par, abort)) ok = false;
         if (ok) {
@@ -340,12 +378,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       // the last copies into every slot land before the CTA goes away (they may
       // not have been waited for when another role gave up)
-      for (int x = 0; x < 2; ++x) bar_wait(bar(kFBarQ + x), 0, nullptr);
+      for (int y = 0; y < 2; ++y) bar_wait(bar(kFBarQ + y), 0, nullptr);
       for (int e = max(0, issued - 4); e < issued; ++e)
         bar_wait(bar((e & 1 ? kFBarV : kFBarK) + ((e >> 1) & 1)), (uint32_t)((e >> 2) & 1), nullptr);
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // -------------------------------------------------------------- products
     const bool el = elect_one();
     const uint32_t id_s = instr_desc(kTile, kTile, true);
@@ -357,48 +395,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         set_abort(a.status, abort);
       }
     };
-    for (int j = t_lo; t_lo < t_hi && j <= t_hi && ok; ++j) {
-      const int it = j - t_lo, sk = it & 1, sv = (it - 1) & 1;
-      if (j > t_lo) wait(kFBarV + sv, (uint32_t)(((it - 1) >> 1) & 1));
-      if (j < t_hi) wait(kFBarK + sk, (uint32_t)((it >> 1) & 1));
+    for (int it = 0; n_it > 0 && it <= n_it && ok; ++it) {
+      const int j = t_hi - 1 - it, sk = it & 1, sv = (it - 1) & 1;  // S of tile j, P V of tile j + 1
+      if (it > 0) wait(kFBarV + sv, (uint32_t)(((it - 1) >> 1) & 1));
+      if (it < n_it) wait(kFBarK + sk, (uint32_t)((it >> 1) & 1));
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t t_s = tmem + kTile * x, t_o = tmem + 256 + kTile * x;
-        if (j - 1 >= x_lo[x] && j - 1 < x_hi[x]) {
-          const int idx = j - 1 - x_lo[x];
-          wait(kFBarP + x, (uint32_t)(idx & 1));
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t t_s = tmem + kTile * y, t_o = tmem + 256 + kTile * y;
+        if (j + 1 >= x_lo[y] && j + 1 < x_hi[y]) {
+          const int idx = x_hi[y] - 1 - (j + 1);
+          wait(kFBarP + y, (uint32_t)(idx & 1));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (el) {
             const uint32_t va = base + kFOffV + sv * kTileB;
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_f16_ts(t_o, t_s + 8 * ks, op_desc_mn_sw128(va + ks * 2048, kBoxB), id_o, idx > 0 || ks > 0);
-            if (j == x_hi[x]) mma_commit(bar(kFBarO + x));
+              mma_f16_ts(t_o, t_s + 8 * ks + 32 * (ks >> 2), op_desc_mn_sw128(va + ks * 2048, kBoxB), id_o, idx > 0 || ks > 0);
+            if (j + 1 == x_lo[y]) mma_commit(bar(kFBarO + y));
           }
         }
-        if (j >= x_lo[x] && j < x_hi[x]) {
-          if (j == x_lo[x]) wait(kFBarQ + x, 0);
+        if (j >= x_lo[y] && j < x_hi[y]) {
+          if (j == x_hi[y] - 1) wait(kFBarQ + y, 0);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (el) {
-            const uint32_t qa = base + kFOffQ + x * kTileB, ka = base + kFOffK + sk * kTileB;
+            const uint32_t qa = base + kFOffQ + y * kTileB, ka = base + kFOffK + sk * kTileB;
 #pragma unroll
             for (int ks = 0; ks < kHeadDim / 16; ++ks) {
               const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
               mma_f16(t_s, op_desc_sw128(qa + off), op_desc_sw128(ka + off), id_s, ks > 0);
             }
-            mma_commit(bar(kFBarS + x));
+            mma_commit(bar(kFBarS + y));
           }
         }
       }
       if (ok && el) {
-        if (j < t_hi) mma_commit(bar(kFBarKe + sk));
-        if (j > t_lo) mma_commit(bar(kFBarVe + sv));
+        if (it < n_it) mma_commit(bar(kFBarKe + sk));
+        if (it > 0) mma_commit(bar(kFBarVe + sv));
       }
       __syncwarp();
     }
-    if (t_lo < t_hi) {
+    if (n_it > 0) {
       // every product complete before the tensor memory goes back
       if (el) mma_commit(bar(kFBarDone));
       bar_wait(bar(kFBarDone), 0, nullptr);
@@ -406,73 +444,89 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __syncwarp();
   } else {
     // ----------------------------------------------------------- query rows
-    const int x = warp >> 2;
     const int lo = x == 0 ? x_lo[0] : x_lo[1], hi = x == 0 ? x_hi[0] : x_hi[1];
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = trow + kTile * x, t_o = trow + 256 + kTile * x;
+    const uint32_t t_h = trow + kTile * x + 64 * half, t_o = trow + 256 + kTile * x + 64 * half;
     const float slope2 = BIAS ? slope_log2(a.mod, hqi) : 0.0f;
     const int tiles = (n + kTile - 1) / kTile;
-    const uint4* bad_masks = reinterpret_cast<const uint4*>(a.bad) + (size_t)plane_kv * tiles;
-    const int qi_first = qblk + (tid & ~31);
+    const uint2* bad_masks = reinterpret_cast<const uint2*>(a.bad) + (size_t)plane_kv * tiles * 2 + half;
+    float* sh_max = reinterpret_cast<float*>(fsm + kFOffMax) + x * 2 * kTile + row;
+    const int q_first = qi - (tid & 31);
     bool ok = true, poison = false;
+    // whether any V row of the tiles ahead is not finite (under the first loads:
+    // a mask read in the loop would put a global load's latency into every tile)
+    uint32_t any_bad = 0;
+    for (int j = lo + (tid & 255); j < hi; j += 256) {
+      const uint4 w = reinterpret_cast<const uint4*>(a.bad)[(size_t)plane_kv * tiles + j];
+      any_bad |= w.x | w.y | w.z | w.w;
+    }
+    {
+      uint32_t r;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          : "=r"(r)
+          : "r"(any_bad), "r"(kNbTile + x)
+          : "memory");
+      any_bad = r;
+    }
     float m = kNegBig, l = 0.0f;
 #pragma unroll 1
-    for (int j = lo; j < hi; ++j) {
-      const int k0 = j * kTile, idx = j - lo;
-      const uint4 bad = bad_masks[j];
+    for (int j = hi - 1; j >= lo; --j) {
+      const int idx = hi - 1 - j, k0 = j * kTile + 64 * half;
       if (!__all_sync(0xffffffffu, bar_wait(bar(kFBarS + x), (uint32_t)(idx & 1), abort))) {
         ok = false;
         set_abort(a.status, abort);
+      }
+      // (a warp that gave up still meets the others at the tile's barrier)
+      float mx = -INFINITY;
+      float z[32];
+      const bool masked = k0 < all_lo || k0 + 64 > all_hi;  // (the same for the warp)
+      const bool beyond = k0 + 63 > q_first;
+      const float dist0 = (float)(k0 - qi);
+      if (ok) {
+        // the maximum of this half: with a bias, over the scores, which then
+        // take the products' place; else over the products (a cap and the
+        // scale keep their order)
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld32(t_h + 32 * c, z);
+          tmem_wait(z);
+          if (BIAS) chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + 32.0f * c, beyond);
+          if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+          if (BIAS) tmem_st32(t_h + 32 * c, z);
+          mx = chunk_max(z, mx);
+        }
+        if (!BIAS && mx > -INFINITY) mx = CAP ? cap_score(a.mod, mx * a.mod.y_scale) : mx * a.qk_scale_log2;
+        if (any_bad) {  // V rows that are not finite (rare)
+          const uint2 bad = bad_masks[2 * j];
+#pragma unroll 1
+          for (int i = 0; i < 64; ++i)
+            if (((i < 32 ? bad.x : bad.y) >> (i & 31)) & 1u) poison |= k0 + i >= run.x && k0 + i < run.y;
+        }
+        if (BIAS) tmem_st_wait();
+      }
+      // the row's maximum over both halves
+      float* exch = sh_max + (idx & 1) * 4 * kTile;
+      exch[half * kTile] = mx;
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (!ok || *abort) {
+        ok = false;
         break;
       }
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (bad.x | bad.y | bad.z | bad.w) {  // V rows that are not finite (rare)
-        const uint32_t w[4] = {bad.x, bad.y, bad.z, bad.w};
-        for (int i = 0; i < 128; ++i)
-          if ((w[i >> 5] >> (i & 31)) & 1u) poison |= k0 + i >= run.x && k0 + i < run.y;
-      }
-      // Two passes over the 128 scores in chunks of 32, the next chunk's load
-      // in flight: the maximum, then the probabilities (few registers live; a
-      // row of 128 held at once spilled).  The scores of the second pass are
-      // formed again from the products, but for cap and bias together, which
-      // the first pass leaves in the place of the products.
-      const bool masked = k0 < all_lo || k0 + kTile > all_hi;  // (the same for the warp)
-      const bool beyond = k0 + kTile - 1 > qi_first;
-      const float dist0 = (float)(k0 - qi);
-      constexpr bool kKeep = CAP && BIAS, kRaw = !CAP && !BIAS;
-      float za[32], zb[32];
-      tmem_ld32(t_s, za);
-      float mx = -INFINITY;
-      auto first = [&](float (&z)[32], int c) {
-        if (BIAS) chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + (float)(32 * c), beyond);
-        if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
-        if (kKeep) tmem_st32(t_s + 32 * c, z);
-        mx = chunk_max(z, mx);
-      };
-#pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {
-        tmem_wait(za);
-        tmem_ld32(t_s + 32 * c + 32, zb);
-        first(za, c);
-        tmem_wait(zb);
-        if (kKeep) tmem_st_wait();
-        tmem_ld32(t_s + (32 * c + 64) % 128, za);  // after the last chunk: the first again
-        first(zb, c + 1);
-      }
-      // scale > 0 and a cap keep the order: the maximum commutes with them
-      if (kRaw) mx *= a.qk_scale_log2;
-      if (CAP && !BIAS) mx = mx > -INFINITY ? cap_score(a.mod, mx * a.mod.y_scale) : mx;
+      mx = fmaxf(mx, exch[(half ^ 1) * kTile]);
       const bool grow = mx > m + kLazyMax;
       const float alpha = grow ? fast_exp2(m - mx) : 1.0f;
       if (grow) {
         l *= alpha;
         m = mx;
       }
-      tmem_wait(za);
-      // S(j) complete implies P V(j - 1) complete: O may be rescaled
+      // S(j) complete implies the P V before it complete: O may be rescaled
       if (idx > 0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
+        for (int c0 = 0; c0 < 64; c0 += 16) {
           float t[16];
           ld16(t_o + c0, t);
 #pragma unroll
@@ -480,30 +534,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           st16(t_o + c0, t);
         }
       }
-      // P over the products' first half: chunk c's 16 columns lie before the
-      // products of chunk c + 1
-      float2 ls[2] = {};
-      auto second = [&](float (&z)[32], int c) {
-        if (!kKeep) {
-          chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + (float)(32 * c), beyond);
-          if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
-        }
+      // P (fp16) over the front of this half's products: chunk c's 16 columns
+      // lie before the products of chunk c + 1
+      f32x2 ls[2] = {0, 0};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         uint32_t pw[16];
-        chunk_probs(z, kRaw, a.qk_scale_log2, m, pw, ls);
-        tmem_st16(t_s + 16 * c, pw);
-      };
-      if (kKeep) tmem_st_wait();
-#pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {
-        tmem_ld32(t_s + 32 * c + 32, zb);
-        second(za, c);
-        tmem_wait(zb);
-        if (c == 0) tmem_ld32(t_s + 64, za);
-        second(zb, c + 1);
-        if (c == 0) tmem_wait(za);
+        tmem_ld32(t_h + 32 * c, z);
+        tmem_wait(z);
+        if (CAP && !BIAS) chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + 32.0f * c, beyond);
+        if (!BIAS && masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+        chunk_probs<!CAP && !BIAS>(z, a.qk_scale_log2, m, pw, ls);
+        tmem_st16(t_h + 16 * c, pw);
       }
-      const float2 lt = add2(ls[0], ls[1]);
-      l += lt.x + lt.y;
+      float lx, ly;
+      unpack2(add2(ls[0], ls[1]), lx, ly);
+      l += lx + ly;
       tmem_st_wait();
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
@@ -514,13 +560,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       ok = false;
       set_abort(a.status, abort);
     }
-    if (ok) {
+    // the row's sum and poison over both halves (every warp of the tile has read
+    // the last exchange: O complete follows their arrivals)
+    sh_max[half * kTile] = l;
+    sh_max[(4 + half) * kTile] = poison ? 1.0f : 0.0f;
+    asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
+    const float other = sh_max[(half ^ 1) * kTile];
+    poison |= sh_max[(4 + (half ^ 1)) * kTile] != 0.0f;
+    if (ok && !*abort) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const bool row_ok = qi < n;
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // a row that sees nothing is 0
-      uint16_t* orow = a.out + ((size_t)plane_q * n + (row_ok ? qi : 0)) * kHeadDim;
+      const float total = half == 0 ? l + other : other + l;  // the same order in both threads
+      const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a row that sees nothing is 0
+      uint16_t* orow = a.out + ((size_t)plane_q * n + (row_ok ? qi : 0)) * kHeadDim + 64 * half;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
+      for (int c0 = 0; c0 < 64; c0 += 32) {
         float t[32];
         if (any) {
           ld32(t_o + c0, t);
@@ -540,13 +594,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             *reinterpret_cast<uint4*>(orow + c0 + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         }
       }
-      if (row_ok && a.stats != nullptr)
-        *reinterpret_cast<float2*>(a.stats + ((size_t)plane_q * n + qi) * 2) = make_float2(m, l);
+      if (row_ok && half == 0 && a.stats != nullptr)
+        *reinterpret_cast<float2*>(a.stats + ((size_t)plane_q * n + qi) * 2) = make_float2(m, total);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFwdCols));
+  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFwdCols));
 }
 
 // ---------------------------------------------------------------------------
@@ -831,8 +885,30 @@ cudaError_t launch_prompt_scores(const DevState& s, int seq_begin, int batch, in
   return cudaGetLastError();
 }
 
-cudaError_t launch_prompt(const PromptArgs& a, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+// The degree-3 polynomial takes q . k itself: x (c0 + u (c1 + ...)), u = x^2, so
+// its coefficients carry powers of y_scale up to the ninth; a y_scale for which
+// those leave fp32's range (caps no model uses) goes without it.
+void prompt_polynomials(PromptArgs* a) {
+  a->near_max = a->mid_max = -1.0f;
+  const double ys = a->mod.y_scale, c2 = a->mod.c2;
+  if (!(c2 > 0.0) || !(ys > 0.0)) return;
+  a->mid_max = (float)(kCapMid / ys);
+  a->mid[0] = (float)c2;
+  for (int i = 0; i < 9; ++i) a->mid[i + 1] = (float)(c2 * kCapP8[i]);
+  if (ys < 5e-4 || ys > 1e3) return;
+  a->near_max = (float)(kCapNear / ys);
+  double pw = ys;
+  a->near[0] = (float)(c2 * pw);
+  for (int i = 0; i < 4; ++i) {
+    pw *= ys * ys;
+    a->near[i + 1] = (float)(c2 * kCapP3[i] * pw);
+  }
+}
+
+cudaError_t launch_prompt(const PromptArgs& args, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                           cudaStream_t st) {
+  PromptArgs a = args;
+  prompt_polynomials(&a);
   CUtensorMap tm_q, tm_k, tm_v;
   if (!encode_rows_map(&tm_q, q, a.n, a.batch * a.hq, kTile) || !encode_rows_map(&tm_k, k, a.n, a.batch * a.hkv, kTile) ||
       !encode_rows_map(&tm_v, a.v16, a.n, a.batch * a.hkv, kTile, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))

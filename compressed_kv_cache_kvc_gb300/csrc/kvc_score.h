@@ -7,20 +7,21 @@
 // z * log2(e): the cap is stored as c2 = cap * log2(e), the slopes are
 // multiplied by log2(e) as they are read.
 //
-// tanh(y), y = x / cap:
-//   |y| <= 0.6   y * (1 + u * P(u)), u = y^2, P of degree 4 fitted here to
-//                (tanh(y) / y - 1) / u by iterated weighted least squares:
-//                relative error 2.6e-9, 7.5e-8 as evaluated in fp32.  c2 is
-//                multiplied into the coefficients, so z costs seven
-//                multiply-adds and no MUFU instruction.
+// tanh(y), y = x / cap, with P fitted here to (tanh(y) / y - 1) / u, u = y^2,
+// by iterated weighted least squares:
+//   |y| <= 0.6   y * (1 + u * P(u)), P of degree 3: relative error 1.6e-7 as
+//                evaluated in fp32.  The cap is multiplied into the
+//                coefficients: six multiply-adds a score and no MUFU.
+//   |y| <= 1.5   the same with P of degree 8, 2.0e-7 (prompts, which form
+//                scores by the thousand per thread).
 //   else         (1 - e) / (1 + e), e = 2^(-2 log2(e) |y|): 1 from |y| = 9 on;
 //                ex2 is off by at most 2^-22 e, rcp by 2^-23 of its value, so
 //                tanh is off by at most 2 * 2^-22 + 2^-23 + 2 * 2^-24 < 7.2e-7
 //                for every y, also where a group of scores takes this form
-//                because one of them left the first interval.
-// A score is so accurate to 7.2e-7 of the cap.  Scores rarely leave the first
-// interval with the caps that models use (30 to 50); the second form costs two
-// MUFU instructions a score.
+//                because one of them left the intervals above.  Two MUFU
+//                instructions a score.
+// A score is so accurate to 7.2e-7 of the cap.  With the caps that models use
+// (30 to 50) scores rarely leave the first interval.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -29,20 +30,21 @@
 namespace kvc {
 
 constexpr float kLog2E = 1.4426950408889634f;
-constexpr float kCapPolyMax = 0.6f;  // |x / cap| up to which the polynomial serves
+constexpr float kCapNear = 0.6f;  // |x / cap| up to which the polynomial of degree 3 serves
+constexpr float kCapMid = 1.5f;   // and the one of degree 8
+constexpr double kCapP3[4] = {-0.3333262160369896, 0.13313520721608138, -0.052231106454585126, 0.01564048021294071};
+constexpr double kCapP8[9] = {-0.3333324241639356, 0.13331582011696386, -0.053850984564149926, 0.021477584226268928, -0.008099126689853861, 0.002642995882885061, -0.000656591311100134, 0.00010466406356551689, -7.770424672509535e-06};
 
 // By value in kernel arguments.
 struct ScoreMod {
   float c2;             // cap * log2(e); 0: no cap
   float y_scale;        // sm_scale / cap: q . k -> y
-  float poly[6];        // c2 * (1, P's coefficients)
+  float poly[5];        // c2 * (1, the coefficients of P of degree 3)
   const float* slopes;  // [hq] (natural-log units) or null: no bias
 };
 
 // sm_scale and cap as the caller gave them (cap 0: none).
 inline ScoreMod make_score_mod(float sm_scale, float cap, const float* slopes) {
-  constexpr double kP[5] = {-0.33333298563957214, 0.13331958651542664, -0.053786683827638626, 0.02080538310110569,
-                            -0.005905867554247379};
   ScoreMod m{};
   m.slopes = slopes;
   if (cap > 0.0f) {
@@ -50,7 +52,7 @@ inline ScoreMod make_score_mod(float sm_scale, float cap, const float* slopes) {
     m.c2 = (float)c2;
     m.y_scale = (float)((double)sm_scale / (double)cap);
     m.poly[0] = (float)c2;
-    for (int i = 0; i < 5; ++i) m.poly[i + 1] = (float)(c2 * kP[i]);
+    for (int i = 0; i < 4; ++i) m.poly[i + 1] = (float)(c2 * kCapP3[i]);
   }
   return m;
 }
@@ -60,8 +62,7 @@ namespace dev {
 
 __device__ __forceinline__ float cap_poly(const ScoreMod& m, float y) {
   const float u = y * y;
-  float h = fmaf(m.poly[5], u, m.poly[4]);
-  h = fmaf(h, u, m.poly[3]);
+  float h = fmaf(m.poly[4], u, m.poly[3]);
   h = fmaf(h, u, m.poly[2]);
   h = fmaf(h, u, m.poly[1]);
   h = fmaf(h, u, m.poly[0]);
@@ -77,7 +78,7 @@ __device__ __forceinline__ float cap_far(const ScoreMod& m, float y) {
 
 // z (log2 units) of y = x / cap; NaN stays NaN, infinities give +-c2.
 __device__ __forceinline__ float cap_score(const ScoreMod& m, float y) {
-  return fabsf(y) <= kCapPolyMax ? cap_poly(m, y) : cap_far(m, y);
+  return fabsf(y) <= kCapNear ? cap_poly(m, y) : cap_far(m, y);
 }
 
 // N scores in place: the polynomial when all are within its interval.
@@ -86,7 +87,7 @@ __device__ __forceinline__ void cap_scores(const ScoreMod& m, float (&y)[N]) {
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(y[i]));
-  if (top <= kCapPolyMax) {  // (a NaN alone stays NaN in the polynomial)
+  if (top <= kCapNear) {  // (a NaN alone stays NaN in the polynomial)
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = cap_poly(m, y[i]);
   } else {
