@@ -201,9 +201,9 @@ struct PromptArgs {
   int batch, hq, hkv, group, n;
   float qk_scale_log2;       // sm_scale * log2(e)
   ScoreMod mod;
-  // the cap's polynomials for prompts (prompt_polynomials): degree 3 over q . k
-  // itself up to near_max, degree 8 over q . k / (cap / sm_scale) up to mid_max
-  float near_max, mid_max, near[5], mid[10];
+  // the cap's polynomials for prompts (prompt_polynomials): degree 2 over q . k
+  // itself up to close_max, degree 8 over q . k * sm_scale / cap up to mid_max
+  float close_max, mid_max, close[4], mid[10];
   const int32_t* key_begin;  // [batch][n] or null (0)
   const int32_t* key_end;    // [batch][n] or null (i + 1)
   uint16_t* out;             // bf16 [batch][hq][n][128]

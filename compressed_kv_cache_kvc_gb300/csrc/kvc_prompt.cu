@@ -161,72 +161,65 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
 }
 
 // ---------------------------------------------------------------------------
-// Scores in log2 units of 32 raw products of a row (keys from the one at
-// dist0 positions from the query: key - query).  Without a cap and a bias the
-// products stay as they are (the caller scales them).  `beyond`: some key may
-// lie after the query.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ void chunk_scores(const PromptArgs& a, float (&z)[32], float slope2, float dist0,
-                                             bool beyond) {
-  if (CAP) {
-    float top[2] = {0.0f, 0.0f};
+// Capped scores less m (log2 units) of 32 raw products of a row.
+__device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], float m) {
+  float top[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      top[0] = max3_abs(top[0], z[i], z[i + 1]);
-      top[1] = max3_abs(top[1], z[i + 2], z[i + 3]);
-    }
-    const float most = fmaxf(top[0], top[1]);
-    if (!(most > a.near_max)) {  // (a NaN stays NaN in the polynomials)
-      f32x2 c[5];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) c[i] = pack2(a.near[i], a.near[i]);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const f32x2 x = pack2(z[i], z[i + 1]);
-        const f32x2 u = mul2(x, x);
-        f32x2 h = fma2(c[4], u, c[3]);
-        h = fma2(h, u, c[2]);
-        h = fma2(h, u, c[1]);
-        h = fma2(h, u, c[0]);
-        unpack2(mul2(x, h), z[i], z[i + 1]);
-      }
-    } else if (most <= a.mid_max) {
-      const f32x2 ys = pack2(a.mod.y_scale, a.mod.y_scale);
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const f32x2 y = mul2(pack2(z[i], z[i + 1]), ys);
-        const f32x2 u = mul2(y, y);
-        f32x2 h = pack2(a.mid[9], a.mid[9]);
-#pragma unroll
-        for (int e = 8; e >= 0; --e) h = fma2(h, u, pack2(a.mid[e], a.mid[e]));
-        unpack2(mul2(y, h), z[i], z[i + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = cap_far(a.mod, z[i] * a.mod.y_scale);
-    }
+  for (int i = 0; i < 32; i += 4) {
+    top[0] = max3_abs(top[0], z[i], z[i + 1]);
+    top[1] = max3_abs(top[1], z[i + 2], z[i + 3]);
   }
-  if (BIAS) {
-    // slope2 * (key - query) for keys at or before the query, else its negative
-    const f32x2 sl = pack2(slope2, slope2), d0 = pack2(dist0, dist0), sc = pack2(a.qk_scale_log2, a.qk_scale_log2);
-    auto run = [&](auto abs_tag) {
+  const float most = fmaxf(top[0], top[1]);
+  const f32x2 nm = pack2(-m, -m);
+  if (!(most > a.close_max)) {  // (a NaN stays NaN in the polynomials)
+    f32x2 c[4];
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        f32x2 d = add2(d0, pack2((float)i, (float)(i + 1)));
-        if (decltype(abs_tag)::value) {
-          float x, y;
-          unpack2(d, x, y);
-          d = pack2(-fabsf(x), -fabsf(y));
-        }
-        f32x2 b = pack2(z[i], z[i + 1]);
-        if (!CAP) b = mul2(b, sc);
-        unpack2(fma2(d, sl, b), z[i], z[i + 1]);
-      }
-    };
-    if (beyond)
-      run(std::true_type{});
-    else
-      run(std::false_type{});
+    for (int i = 0; i < 4; ++i) c[i] = pack2(a.close[i], a.close[i]);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const f32x2 x = pack2(z[i], z[i + 1]);
+      const f32x2 u = mul2(x, x);
+      f32x2 h = fma2(c[3], u, c[2]);
+      h = fma2(h, u, c[1]);
+      h = fma2(h, u, c[0]);
+      unpack2(fma2(x, h, nm), z[i], z[i + 1]);
+    }
+  } else if (most <= a.mid_max) {
+    const f32x2 ys = pack2(a.mod.y_scale, a.mod.y_scale);
+    f32x2 c[10];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) c[i] = pack2(a.mid[i], a.mid[i]);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const f32x2 y = mul2(pack2(z[i], z[i + 1]), ys);
+      const f32x2 u = mul2(y, y);
+      f32x2 h = c[9];
+#pragma unroll
+      for (int e = 8; e >= 0; --e) h = fma2(h, u, c[e]);
+      unpack2(fma2(y, h, nm), z[i], z[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z[i] = cap_far(a.mod, z[i] * a.mod.y_scale) - m;
+  }
+}
+
+// The distance bias of 32 scores times scale (keys from the one at dist0
+// positions from the query: key - query): z = z scale + slope2 (key - query) for
+// keys at or before the query, with the negative after it (`beyond`: there may
+// be such keys).
+__device__ __forceinline__ void chunk_bias(float (&z)[32], float scale, float slope2, float dist0, bool beyond) {
+  const f32x2 sl = pack2(slope2, slope2), sc = pack2(scale, scale), two = pack2(2.0f, 2.0f);
+  f32x2 d = pack2(dist0, dist0 + 1.0f);
+  if (!beyond) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      unpack2(fma2(d, sl, mul2(pack2(z[i], z[i + 1]), sc)), z[i], z[i + 1]);
+      d = add2(d, two);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope2, fabsf(dist0 + (float)i), z[i] * scale);
   }
 }
 
@@ -247,23 +240,23 @@ __device__ __forceinline__ float chunk_max(const float (&z)[32], float m) {
   return fmaxf(t0, t1);
 }
 
-// 32 scores (raw products for RAW) -> probabilities 2^(z - m) in fp16 pairs;
-// their unrounded sum is added to ls.
-template <bool RAW>
-__device__ __forceinline__ void chunk_probs(const float (&z)[32], float scale, float m, uint32_t (&pw)[16],
-                                            f32x2 (&ls)[2]) {
-  const f32x2 nm = pack2(-m, -m), sc = pack2(scale, scale);
+// 32 scores less m -> probabilities in fp16 pairs; their unrounded sum is added
+// to ls.
+__device__ __forceinline__ void chunk_probs(const float (&z)[32], uint32_t (&pw)[16], f32x2 (&ls)[2]) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const f32x2 zz = pack2(z[2 * e], z[2 * e + 1]);
-    float x, y;
-    unpack2(RAW ? fma2(zz, sc, nm) : add2(zz, nm), x, y);
-    x = fast_exp2(x);
-    y = fast_exp2(y);
+    const float x = fast_exp2(z[2 * e]), y = fast_exp2(z[2 * e + 1]);
     ls[e & 1] = add2(ls[e & 1], pack2(x, y));
     const __half2 hh = __floats2half2_rn(x, y);
     pw[e] = *reinterpret_cast<const uint32_t*>(&hh);
   }
+}
+
+// z scale - m
+__device__ __forceinline__ void chunk_shift(float (&z)[32], float scale, float m) {
+  const f32x2 nm = pack2(-m, -m), sc = pack2(scale, scale);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) unpack2(fma2(pack2(z[i], z[i + 1]), sc, nm), z[i], z[i + 1]);
 }
 
 template <bool CAP, bool BIAS>
@@ -488,11 +481,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // take the products' place; else over the products (a cap and the
         // scale keep their order)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           tmem_ld32(t_h + 32 * c, z);
           tmem_wait(z);
-          if (BIAS) chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + 32.0f * c, beyond);
+          if (CAP && BIAS) chunk_cap(a, z, 0.0f);
+          if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, dist0 + 32.0f * c, beyond);
           if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
           if (BIAS) tmem_st32(t_h + 32 * c, z);
           mx = chunk_max(z, mx);
@@ -537,14 +531,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // P (fp16) over the front of this half's products: chunk c's 16 columns
       // lie before the products of chunk c + 1
       f32x2 ls[2] = {0, 0};
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t pw[16];
         tmem_ld32(t_h + 32 * c, z);
         tmem_wait(z);
-        if (CAP && !BIAS) chunk_scores<CAP, BIAS>(a, z, slope2, dist0 + 32.0f * c, beyond);
+        if (CAP && !BIAS)
+          chunk_cap(a, z, m);
+        else
+          chunk_shift(z, BIAS ? 1.0f : a.qk_scale_log2, m);
         if (!BIAS && masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
-        chunk_probs<!CAP && !BIAS>(z, a.qk_scale_log2, m, pw, ls);
+        chunk_probs(z, pw, ls);
         tmem_st16(t_h + 16 * c, pw);
       }
       float lx, ly;
@@ -885,23 +882,23 @@ cudaError_t launch_prompt_scores(const DevState& s, int seq_begin, int batch, in
   return cudaGetLastError();
 }
 
-// The degree-3 polynomial takes q . k itself: x (c0 + u (c1 + ...)), u = x^2, so
-// its coefficients carry powers of y_scale up to the ninth; a y_scale for which
+// The degree-2 polynomial takes q . k itself: x (c0 + u (c1 + ...)), u = x^2, so
+// its coefficients carry powers of y_scale up to the seventh; a y_scale for which
 // those leave fp32's range (caps no model uses) goes without it.
 void prompt_polynomials(PromptArgs* a) {
-  a->near_max = a->mid_max = -1.0f;
+  a->close_max = a->mid_max = -1.0f;
   const double ys = a->mod.y_scale, c2 = a->mod.c2;
   if (!(c2 > 0.0) || !(ys > 0.0)) return;
   a->mid_max = (float)(kCapMid / ys);
   a->mid[0] = (float)c2;
   for (int i = 0; i < 9; ++i) a->mid[i + 1] = (float)(c2 * kCapP8[i]);
   if (ys < 5e-4 || ys > 1e3) return;
-  a->near_max = (float)(kCapNear / ys);
+  a->close_max = (float)(kCapClose / ys);
   double pw = ys;
-  a->near[0] = (float)(c2 * pw);
-  for (int i = 0; i < 4; ++i) {
+  a->close[0] = (float)(c2 * pw);
+  for (int i = 0; i < 3; ++i) {
     pw *= ys * ys;
-    a->near[i + 1] = (float)(c2 * kCapP3[i] * pw);
+    a->close[i + 1] = (float)(c2 * kCapP2[i] * pw);
   }
 }
 

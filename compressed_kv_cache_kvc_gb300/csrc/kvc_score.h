@@ -12,8 +12,9 @@
 //   |y| <= 0.6   y * (1 + u * P(u)), P of degree 3: relative error 1.6e-7 as
 //                evaluated in fp32.  The cap is multiplied into the
 //                coefficients: six multiply-adds a score and no MUFU.
-//   |y| <= 1.5   the same with P of degree 8, 2.0e-7 (prompts, which form
-//                scores by the thousand per thread).
+//   |y| <= 0.4   (prompts, which form scores by the thousand per thread) the
+//                same with P of degree 2, 1.8e-7;
+//   |y| <= 1.5   (prompts) with P of degree 8, 2.0e-7.
 //   else         (1 - e) / (1 + e), e = 2^(-2 log2(e) |y|): 1 from |y| = 9 on;
 //                ex2 is off by at most 2^-22 e, rcp by 2^-23 of its value, so
 //                tanh is off by at most 2 * 2^-22 + 2^-23 + 2 * 2^-24 < 7.2e-7
@@ -31,7 +32,9 @@ namespace kvc {
 
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kCapNear = 0.6f;  // |x / cap| up to which the polynomial of degree 3 serves
-constexpr float kCapMid = 1.5f;   // and the one of degree 8
+constexpr float kCapClose = 0.4f;  // the one of degree 2
+constexpr float kCapMid = 1.5f;    // and the one of degree 8
+constexpr double kCapP2[3] = {-0.3333190183144874, 0.13278022829794303, -0.047811859768676745};
 constexpr double kCapP3[4] = {-0.3333262160369896, 0.13313520721608138, -0.052231106454585126, 0.01564048021294071};
 constexpr double kCapP8[9] = {-0.3333324241639356, 0.13331582011696386, -0.053850984564149926, 0.021477584226268928, -0.008099126689853861, 0.002642995882885061, -0.000656591311100134, 0.00010466406356551689, -7.770424672509535e-06};
 
