@@ -26,10 +26,12 @@
 //     keys into two slots each.  K is read K-major and V in its own layout
 //     (MN-major), both with the 128-byte swizzle, so nothing is transposed.
 // TMEM columns: S_x at 128 x, O_x at 256 + 128 x; the first 32 columns of each
-// half of S_x become that half's P in fp16.  Order of the products: P V_A(prev), S_A(next), P V_B(prev),
+// half of S_x become that half's P in fp16.  The warp issues P V_A(prev), S_A(next), P V_B(prev),
 // S_B(next): the pipe runs them in order, so S_x may overwrite the P_x before
 // it without a wait, S_x complete implies the P V_x before it complete, and one
-// tile's softmax runs under the other tile's products.  M = N = 128 products
+// tile's softmax runs under the other tile's products (a warp per query tile,
+// whose products then mix in the pipe, was slower: 520 against 486 us for 32
+// heads of 8192 plain causal tokens).  M = N = 128 products
 // cost 64 cycles each, 2048 a round of both tiles.
 // Key tiles go from the last to the first: with a distance bias the nearest
 // keys, which set the maximum, come first.  The running maximum is lazy (O is
@@ -72,10 +74,11 @@ constexpr int kFOffQ = 0;                         // 2 tiles
 constexpr int kFOffK = kFOffQ + 2 * kTileB;       // 2 slots
 constexpr int kFOffV = kFOffK + 2 * kTileB;       // 2 slots
 constexpr int kFOffBar = kFOffV + 2 * kTileB;
-// mbarriers: Q landed (per tile), K / V landed and free (per slot), S
+// mbarriers: Q landed (per tile), a round's K and V landed (per parity), K and V
+// slots free, S
 // complete, P written, O complete (per tile), all products complete
-constexpr int kFBarQ = 0, kFBarK = 2, kFBarV = 4, kFBarKe = 6, kFBarVe = 8, kFBarS = 10, kFBarP = 12, kFBarO = 14,
-              kFBarDone = 16, kFNumBars = 17;
+constexpr int kFBarQ = 0, kFBarKv = 2, kFBarKe = 4, kFBarVe = 6, kFBarS = 8, kFBarP = 10, kFBarO = 12, kFBarDone = 14,
+              kFNumBars = 15;
 constexpr int kFOffMisc = kFOffBar + 8 * kFNumBars;  // TMEM base, abort flag, [8][2] run bounds per 32 rows
 constexpr int kFOffMax = kFOffMisc + 8 + 64;         // [2 parities][2 tiles][2 halves][128] row maxima
 constexpr int kFwdSmem = kFOffMax + 2 * 2 * 2 * kTile * 4;
@@ -161,15 +164,19 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
 }
 
 // ---------------------------------------------------------------------------
-// Capped scores less m (log2 units) of 32 raw products of a row.
-__device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], float m) {
-  float top[2] = {0.0f, 0.0f};
+__device__ __forceinline__ float chunk_most(const float (&z)[32], float most) {
+  float t0 = most, t1 = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    top[0] = max3_abs(top[0], z[i], z[i + 1]);
-    top[1] = max3_abs(top[1], z[i + 2], z[i + 3]);
+    t0 = max3_abs(t0, z[i], z[i + 1]);
+    t1 = max3_abs(t1, z[i + 2], z[i + 3]);
   }
-  const float most = fmaxf(top[0], top[1]);
+  return fmaxf(t0, t1);
+}
+
+// Capped scores less m (log2 units) of 32 raw products of a row, none larger
+// in magnitude than `most`.
+__device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], float most, float m) {
   const f32x2 nm = pack2(-m, -m);
   if (!(most > a.close_max)) {  // (a NaN stays NaN in the polynomials)
     f32x2 c[4];
@@ -336,20 +343,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (warp == 17) {
     // ------------------------------------------------------------- TMA loads
+    // Round it brings K of tile t_hi - 1 - it and V of the tile before it (the
+    // products of that round: S of the one, P V of the other) on one barrier.
     if (lane == 0 && n_it > 0) {
-      int issued = 0;
+      int rounds = 0;
       bool ok = true;
-      for (int it = 0; it < n_it && ok; ++it) {
-        const int j = t_hi - 1 - it, sl = it & 1;
-        const uint32_t par = (uint32_t)((it >> 1) & 1) ^ 1u;  // the slot's previous tile released
-        if (it >= 2 && !bar_wait(bar(kFBarKe + sl), par, abort)) ok = false;
-        if (ok) {
-          const uint32_t dst = base + kFOffK + sl * kTileB, b = bar(kFBarK + sl);
-          bar_expect_tx(b, kTileB);
+      for (int it = 0; it <= n_it && ok; ++it) {
+        const int j = t_hi - 1 - it, b = bar(kFBarKv + (it & 1));
+        // the slots' previous tiles released, K's also before the last round,
+        // which brings none: it shows that round it - 2 was seen landed, so that
+        // its barrier may take a new phase
+        if (it >= 2) ok = bar_wait(bar(kFBarKe + (it & 1)), (uint32_t)((it >> 1) & 1) ^ 1u, abort);
+        if (ok && it >= 3) ok = bar_wait(bar(kFBarVe + ((it - 1) & 1)), (uint32_t)(((it - 1) >> 1) & 1) ^ 1u, abort);
+        if (!ok) {
+          set_abort(a.status, abort);
+          break;
+        }
+        bar_expect_tx(b, (it < n_it ? kTileB : 0) + (it > 0 ? kTileB : 0));
+        if (it < n_it) {
+          const uint32_t dst = base + kFOffK + (it & 1) * kTileB;
           tma_load_3d(dst, &tm_k, 0, j * kTile, plane_kv, b);
           tma_load_3d(dst + kBoxB, &tm_k, 64, j * kTile, plane_kv, b);
-          issued = 2 * it + 1;
         }
+        if (it > 0) {
+          const uint32_t dst = base + kFOffV + ((it - 1) & 1) * kTileB;
+          tma_load_3d(dst, &tm_v, 0, (j + 1) * kTile, plane_kv, b);
+          tma_load_3d(dst + kBoxB, &tm_v, 64, (j + 1) * kTile, plane_kv, b);
+        }
+        rounds = it + 1;
         if (it == 0) {
 #pragma unroll
           for (int y = 1; y >= 0; --y) {
@@ -359,21 +380,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tma_load_3d(dst + kBoxB, &tm_q, 64, qblk + y * kTile, plane_q, bar(kFBarQ + y));
           }
         }
-        if (ok && it >= 2 && !bar_wait(bar(kFBarVe + sl), par, abort)) ok = false;
-        if (ok) {
-          const uint32_t dst = base + kFOffV + sl * kTileB, b = bar(kFBarV + sl);
-          bar_expect_tx(b, kTileB);
-          tma_load_3d(dst, &tm_v, 0, j * kTile, plane_kv, b);
-          tma_load_3d(dst + kBoxB, &tm_v, 64, j * kTile, plane_kv, b);
-          issued = 2 * it + 2;
-        }
-        if (!ok) set_abort(a.status, abort);
       }
-      // the last copies into every slot land before the CTA goes away (they may
-      // not have been waited for when another role gave up)
+      // the last copies land before the CTA goes away (they may not have been
+      // waited for when another role gave up)
       for (int y = 0; y < 2; ++y) bar_wait(bar(kFBarQ + y), 0, nullptr);
-      for (int e = max(0, issued - 4); e < issued; ++e)
-        bar_wait(bar((e & 1 ? kFBarV : kFBarK) + ((e >> 1) & 1)), (uint32_t)((e >> 2) & 1), nullptr);
+      for (int e = max(0, rounds - 2); e < rounds; ++e)
+        bar_wait(bar(kFBarKv + (e & 1)), (uint32_t)((e >> 1) & 1), nullptr);
     }
     __syncwarp();
   } else if (warp == 16) {
@@ -383,28 +395,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t id_o = instr_desc(kTile, kHeadDim, false) | kInstrTransB;
     bool ok = true;
     auto wait = [&](int b, uint32_t par) {
-      if (ok && !__all_sync(0xffffffffu, bar_wait(bar(b), par, abort))) {
+      if (!__all_sync(0xffffffffu, bar_try(bar(b), par)) && !__all_sync(0xffffffffu, bar_wait(bar(b), par, abort))) {
         ok = false;
         set_abort(a.status, abort);
       }
     };
-    for (int it = 0; n_it > 0 && it <= n_it && ok; ++it) {
-      const int j = t_hi - 1 - it, sk = it & 1, sv = (it - 1) & 1;  // S of tile j, P V of tile j + 1
-      if (it > 0) wait(kFBarV + sv, (uint32_t)(((it - 1) >> 1) & 1));
-      if (it < n_it) wait(kFBarK + sk, (uint32_t)((it >> 1) & 1));
+    const uint64_t dq = op_desc_sw128(base + kFOffQ), dk = op_desc_sw128(base + kFOffK),
+                   dv = op_desc_mn_sw128(base + kFOffV, kBoxB);
+    for (int it = 0; n_it > 0 && it <= n_it; ++it) {
+      const int j = t_hi - 1 - it, sk = it & 1, sv = sk ^ 1;  // S of tile j, P V of tile j + 1
+      wait(kFBarKv + sk, (uint32_t)((it >> 1) & 1));
+      if (!ok) break;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const uint32_t t_s = tmem + kTile * y, t_o = tmem + 256 + kTile * y;
         if (j + 1 >= x_lo[y] && j + 1 < x_hi[y]) {
-          const int idx = x_hi[y] - 1 - (j + 1);
-          wait(kFBarP + y, (uint32_t)(idx & 1));
+          wait(kFBarP + y, (uint32_t)((x_hi[y] - 2 - j) & 1));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (el) {
-            const uint32_t va = base + kFOffV + sv * kTileB;
+            const bool acc = j + 2 < x_hi[y];
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_f16_ts(t_o, t_s + 8 * ks + 32 * (ks >> 2), op_desc_mn_sw128(va + ks * 2048, kBoxB), id_o, idx > 0 || ks > 0);
+              mma_f16_ts(t_o, t_s + 8 * ks + 32 * (ks >> 2), dv + (uint64_t)((sv * kTileB + ks * 2048) >> 4), id_o,
+                         acc || ks > 0);
             if (j + 1 == x_lo[y]) mma_commit(bar(kFBarO + y));
           }
         }
@@ -413,17 +427,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (el) {
-            const uint32_t qa = base + kFOffQ + y * kTileB, ka = base + kFOffK + sk * kTileB;
 #pragma unroll
             for (int ks = 0; ks < kHeadDim / 16; ++ks) {
               const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
-              mma_f16(t_s, op_desc_sw128(qa + off), op_desc_sw128(ka + off), id_s, ks > 0);
+              mma_f16(t_s, dq + (uint64_t)((y * kTileB + off) >> 4), dk + (uint64_t)((sk * kTileB + off) >> 4), id_s,
+                      ks > 0);
             }
             mma_commit(bar(kFBarS + y));
           }
         }
       }
-      if (ok && el) {
+      if (!ok) break;
+      if (el) {
         if (it < n_it) mma_commit(bar(kFBarKe + sk));
         if (it > 0) mma_commit(bar(kFBarVe + sv));
       }
@@ -466,12 +481,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
     for (int j = hi - 1; j >= lo; --j) {
       const int idx = hi - 1 - j, k0 = j * kTile + 64 * half;
-      if (!__all_sync(0xffffffffu, bar_wait(bar(kFBarS + x), (uint32_t)(idx & 1), abort))) {
+      if (!__all_sync(0xffffffffu, bar_try(bar(kFBarS + x), (uint32_t)(idx & 1))) &&
+          !__all_sync(0xffffffffu, bar_wait(bar(kFBarS + x), (uint32_t)(idx & 1), abort))) {
         ok = false;
         set_abort(a.status, abort);
       }
       // (a warp that gave up still meets the others at the tile's barrier)
-      float mx = -INFINITY;
+      float mx = -INFINITY, most = 0.0f;
       float z[32];
       const bool masked = k0 < all_lo || k0 + 64 > all_hi;  // (the same for the warp)
       const bool beyond = k0 + 63 > q_first;
@@ -479,19 +495,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (ok) {
         // the maximum of this half: with a bias, over the scores, which then
         // take the products' place; else over the products (a cap and the
-        // scale keep their order)
+        // scale keep their order).  With a cap alone the largest magnitude,
+        // which the choice of the polynomial needs anyway, bounds it: where
+        // that bound would not move the running maximum, the maximum itself is
+        // not looked for.
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (CAP && !BIAS) {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld32(t_h + 32 * c, z);
-          tmem_wait(z);
-          if (CAP && BIAS) chunk_cap(a, z, 0.0f);
-          if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, dist0 + 32.0f * c, beyond);
-          if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
-          if (BIAS) tmem_st32(t_h + 32 * c, z);
-          mx = chunk_max(z, mx);
+          for (int c = 0; c < 2; ++c) {
+            ld32(t_h + 32 * c, z);
+            most = chunk_most(z, most);
+          }
+          mx = cap_score(a.mod, most * a.mod.y_scale);
         }
-        if (!BIAS && mx > -INFINITY) mx = CAP ? cap_score(a.mod, mx * a.mod.y_scale) : mx * a.qk_scale_log2;
+        if (!CAP || BIAS || __any_sync(0xffffffffu, !(mx <= m + kLazyMax))) {
+          mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            ld32(t_h + 32 * c, z);
+            if (CAP && BIAS) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
+            if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, dist0 + 32.0f * c, beyond);
+            if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+            if (BIAS) tmem_st32(t_h + 32 * c, z);
+            mx = chunk_max(z, mx);
+          }
+          if (!BIAS && mx > -INFINITY) mx = CAP ? cap_score(a.mod, mx * a.mod.y_scale) : mx * a.qk_scale_log2;
+        }
         if (any_bad) {  // V rows that are not finite (rare)
           const uint2 bad = bad_masks[2 * j];
 #pragma unroll 1
@@ -534,10 +563,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t pw[16];
-        tmem_ld32(t_h + 32 * c, z);
-        tmem_wait(z);
+        ld32(t_h + 32 * c, z);
         if (CAP && !BIAS)
-          chunk_cap(a, z, m);
+          chunk_cap(a, z, most, m);
         else
           chunk_shift(z, BIAS ? 1.0f : a.qk_scale_log2, m);
         if (!BIAS && masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);

@@ -80,6 +80,17 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// The same, waiting up to the hardware's own time limit.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded wait for the mbarrier's phase `parity`; true when it completed.
 // With `abort` it also gives up once another thread has set that flag.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
