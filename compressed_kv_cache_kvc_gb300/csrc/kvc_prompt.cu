@@ -16,31 +16,36 @@
 //   prompt_sums_kernel   column sums from the row statistics.
 //
 // prompt_fwd_kernel.  4 * 128 flops per visible pair: bound by the tensor
-// pipe and, with a cap or a bias, by the issue of the softmax.  One 576-thread
-// CTA per (256 queries, query head, sequence), longest blocks first:
-//   * warps 0-7 and 8-15 own one 128-query tile each ("A", "B"), two threads
-//     per query row: warps 0-3 (8-11) the first 64 keys of a key tile, warps
-//     4-7 (12-15) the others, so that four warps per scheduler hide each
-//     other's latencies and a row's half lives in registers;
-//   * warp 16 issues the products, warp 17 the TMA loads: K and V tiles of 128
-//     keys into two slots each.  K is read K-major and V in its own layout
+// pipe and, with a cap or a bias, by the FMA pipe.  One 576-thread CTA per (256
+// queries, query head, sequence), longest blocks first:
+//   * warps 0-7 and 8-15 own one 128-query tile each ("A", "B"), two threads a
+//     query row: of each eight the first four warps take the even key tiles,
+//     the others the odd ones, so that four warps per scheduler hide each
+//     other's latencies (eight warps, a thread a row, took 729 against 597 us for 32
+//     capped heads of 8192 causal tokens);
+//   * warp 16 issues the products, warp 17 the TMA loads: K and V tiles of 64
+//     keys into four slots each.  K is read K-major and V in its own layout
 //     (MN-major), both with the 128-byte swizzle, so nothing is transposed.
-// TMEM columns: S_x at 128 x, O_x at 256 + 128 x; the first 32 columns of each
-// half of S_x become that half's P in fp16.  The warp issues P V_A(prev), S_A(next), P V_B(prev),
-// S_B(next): the pipe runs them in order, so S_x may overwrite the P_x before
-// it without a wait, S_x complete implies the P V_x before it complete, and one
-// tile's softmax runs under the other tile's products (a warp per query tile,
-// whose products then mix in the pipe, was slower: 520 against 486 us for 32
-// heads of 8192 plain causal tokens).  M = N = 128 products
-// cost 64 cycles each, 2048 a round of both tiles.
+// TMEM columns: S_x of key tile t at 128 x + 64 (t % 2), O_x at 256 + 128 x; the
+// first 32 columns of an S become its P in fp16.  In round r the MMA warp issues
+// P V_A(r - 2), S_A(r), P V_B(r - 2), S_B(r): the pipe runs them in order, so
+// S(r) may overwrite P(r - 2) without a wait, and with two S per query tile its
+// softmax has the next scores ready.  The other form, one S of 128 keys per
+// query tile, halves the products' issue (N = 64 products cost 48 cycles, not
+// 32) but every tile waits for its own products and runs are rounded to 128
+// keys: 4 % slower over prompts of 1 to 8000 tokens and all masks (packed biased
+// documents 213 against 199 us, capped and biased prefixes 167 against 157 us),
+// faster for long causal prompts without a cap (32 heads of 8192 tokens: 454
+// against 561 us plain, 582 against 594 us capped).
 // Key tiles go from the last to the first: with a distance bias the nearest
 // keys, which set the maximum, come first.  The running maximum is lazy (O is
-// rescaled when a row's maximum grows by more than 8 in log2 units), P is
-// rounded to fp16 (11 significant bits; p <= 2^8), the sums add the unrounded p
-// in fp32.  Per tile the two threads of a row exchange their maxima through
-// shared memory (a named barrier of the tile's eight warps).  A half is read
-// from TMEM twice, for the maximum and for P, instead of being held across the
-// exchange: 96 registers a thread is what 18 warps leave.
+// rescaled when a row's maximum grows by more than 8 in log2 units, after a
+// wait for the P V before), P is rounded to fp16 (11 significant bits; p <=
+// 2^8), the sums add the unrounded p in fp32.  The two threads of a row pass
+// the running maximum on from tile to tile through shared memory (an mbarrier
+// per warp); each sums its own tiles' p.  A tile's scores are read from TMEM
+// twice, for the maximum and for P: 96 registers a thread is what 18 warps
+// leave.
 // Key tiles no query of a 128-query tile sees are skipped; tiles every row of
 // a warp sees whole take no mask.  Masked scores are replaced before the
 // maximum, and P is exactly 0 there; V rows that are not finite enter the
@@ -64,25 +69,29 @@ namespace {
 using namespace dev;
 using namespace tc;
 
-constexpr int kTile = 128;                        // queries per tile, keys per tile
+constexpr int kTile = 128;                        // queries per tile; keys per tile of the column sums
+constexpr int kKeys = 64;                         // keys per tile of the forward
 constexpr int kFwdThreads = 576;
 constexpr int kFwdBlock = 2 * kTile;
 constexpr float kLazyMax = 8.0f;
-constexpr int kTileB = kTile * kHeadDim * 2;      // 32 KB: a Q, K or V tile, two boxes of 64 dims
+constexpr int kTileB = kTile * kHeadDim * 2;      // 32 KB: a 128-row tile, two boxes of 64 dims
 constexpr int kBoxB = kTileB / 2;
+constexpr int kKeyB = kKeys * kHeadDim * 2;       // 16 KB: a K or V tile, two boxes of 64 dims
+constexpr int kKeyBox = kKeyB / 2;
+constexpr int kSlots = 4;
 constexpr int kFOffQ = 0;                         // 2 tiles
-constexpr int kFOffK = kFOffQ + 2 * kTileB;       // 2 slots
-constexpr int kFOffV = kFOffK + 2 * kTileB;       // 2 slots
-constexpr int kFOffBar = kFOffV + 2 * kTileB;
-// mbarriers: Q landed (per tile), a round's K and V landed (per parity), K and V
-// slots free, S
-// complete, P written, O complete (per tile), all products complete
-constexpr int kFBarQ = 0, kFBarKv = 2, kFBarKe = 4, kFBarVe = 6, kFBarS = 8, kFBarP = 10, kFBarO = 12, kFBarDone = 14,
-              kFNumBars = 15;
+constexpr int kFOffK = kFOffQ + 2 * kTileB;
+constexpr int kFOffV = kFOffK + kSlots * kKeyB;
+constexpr int kFOffBar = kFOffV + kSlots * kKeyB;
+// mbarriers: Q landed (per query tile); a round's K and V landed, its slots
+// free (per round % 4); S complete, P written, P V complete (per query tile and
+// tile parity); all products complete; the running maximum passed on (per warp)
+constexpr int kFBarQ = 0, kFBarKv = 2, kFBarFree = 6, kFBarS = 10, kFBarP = 14, kFBarO = 18, kFBarDone = 22,
+              kFBarM = 23, kFNumBars = 39;
 constexpr int kFOffMisc = kFOffBar + 8 * kFNumBars;  // TMEM base, abort flag, [8][2] run bounds per 32 rows
-constexpr int kFOffMax = kFOffMisc + 8 + 64;         // [2 parities][2 tiles][2 halves][128] row maxima
-constexpr int kFwdSmem = kFOffMax + 2 * 2 * 2 * kTile * 4;
-constexpr int kNbTile = 1;  // named barriers of the tiles' warps: 1, 2
+constexpr int kFOffMax = kFOffMisc + 8 + 64;         // [2 query tiles][2 parities][128] row maxima, then sums
+constexpr int kFwdSmem = kFOffMax + 2 * 2 * kTile * 4;
+constexpr int kNbTile = 1;                           // named barriers of a query tile's warps: 1, 2
 constexpr uint32_t kFwdCols = 512;
 
 __device__ __forceinline__ void set_abort(int* status, volatile int* abort) {
@@ -174,10 +183,10 @@ __device__ __forceinline__ float chunk_most(const float (&z)[32], float most) {
   return fmaxf(t0, t1);
 }
 
-// Capped scores less m (log2 units) of 32 raw products of a row, none larger
-// in magnitude than `most`.
-__device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], float most, float m) {
-  const f32x2 nm = pack2(-m, -m);
+// Capped scores (log2 units) plus nm(i) of 32 raw products of a row, none larger
+// in magnitude than `most`; nm(i) is the packed pair for products i and i + 1.
+template <typename NM>
+__device__ __forceinline__ void chunk_cap_plus(const PromptArgs& a, float (&z)[32], float most, NM nm) {
   if (!(most > a.close_max)) {  // (a NaN stays NaN in the polynomials)
     f32x2 c[4];
 #pragma unroll
@@ -189,7 +198,7 @@ __device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], f
       f32x2 h = fma2(c[3], u, c[2]);
       h = fma2(h, u, c[1]);
       h = fma2(h, u, c[0]);
-      unpack2(fma2(x, h, nm), z[i], z[i + 1]);
+      unpack2(fma2(x, h, nm(i)), z[i], z[i + 1]);
     }
   } else if (most <= a.mid_max) {
     const f32x2 ys = pack2(a.mod.y_scale, a.mod.y_scale);
@@ -203,22 +212,29 @@ __device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], f
       f32x2 h = c[9];
 #pragma unroll
       for (int e = 8; e >= 0; --e) h = fma2(h, u, c[e]);
-      unpack2(fma2(y, h, nm), z[i], z[i + 1]);
+      unpack2(fma2(y, h, nm(i)), z[i], z[i + 1]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) z[i] = cap_far(a.mod, z[i] * a.mod.y_scale) - m;
+    for (int i = 0; i < 32; i += 2) {
+      const float x = cap_far(a.mod, z[i] * a.mod.y_scale), y = cap_far(a.mod, z[i + 1] * a.mod.y_scale);
+      unpack2(add2(pack2(x, y), nm(i)), z[i], z[i + 1]);
+    }
   }
 }
 
-// The distance bias of 32 scores times scale (keys from the one at dist0
-// positions from the query: key - query): z = z scale + slope2 (key - query) for
-// keys at or before the query, with the negative after it (`beyond`: there may
-// be such keys).
-__device__ __forceinline__ void chunk_bias(float (&z)[32], float scale, float slope2, float dist0, bool beyond) {
-  const f32x2 sl = pack2(slope2, slope2), sc = pack2(scale, scale), two = pack2(2.0f, 2.0f);
-  f32x2 d = pack2(dist0, dist0 + 1.0f);
-  if (!beyond) {
+__device__ __forceinline__ void chunk_cap(const PromptArgs& a, float (&z)[32], float most, float m) {
+  const f32x2 nm = pack2(-m, -m);
+  chunk_cap_plus(a, z, most, [&](int) { return nm; });
+}
+
+// The distance bias of 32 scores: z scale - slope2 |d|, d = d0, d0 + 1, ..., all
+// of the sign of `toward` (slope2 or -slope2 with it) unless `both`.
+__device__ __forceinline__ void chunk_bias(float (&z)[32], float scale, float slope2, float toward, float d0,
+                                           bool both) {
+  const f32x2 sl = pack2(toward, toward), sc = pack2(scale, scale), two = pack2(2.0f, 2.0f);
+  if (!both) {
+    f32x2 d = pack2(d0, d0 + 1.0f);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       unpack2(fma2(d, sl, mul2(pack2(z[i], z[i + 1]), sc)), z[i], z[i + 1]);
@@ -226,7 +242,7 @@ __device__ __forceinline__ void chunk_bias(float (&z)[32], float scale, float sl
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope2, fabsf(dist0 + (float)i), z[i] * scale);
+    for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope2, fabsf(d0 + (float)i), z[i] * scale);
   }
 }
 
@@ -268,7 +284,7 @@ __device__ __forceinline__ void chunk_shift(float (&z)[32], float scale, float m
 
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
-    prompt_fwd_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    prompt_fwd_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ __align__(1024) uint8_t fsm[];
   const uint32_t base = saddr(fsm);
@@ -280,11 +296,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int n = a.n;
   const int qb = gridDim.x - 1 - blockIdx.x, hqi = blockIdx.y, bl = blockIdx.z;
   const int plane_q = bl * a.hq + hqi, plane_kv = bl * a.hkv + hqi / a.group;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (what steers a whole warp goes through a shuffle: the compiler then keeps it,
+  // and the operands of the products that hang on it, in uniform registers)
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int qblk = qb * kFwdBlock;
-  // (softmax threads) query tile, half of the key tile, query row
-  const int x = warp >> 3, half = (warp >> 2) & 1, row = tid & (kTile - 1);
-  const int qi = qblk + x * kTile + row;
+  // (softmax threads) query tile, parity of the key tiles, query row
+  const int x = warp >> 3, odd = (warp >> 2) & 1, row = tid & (kTile - 1);
+  const int qi = qblk + kTile * x + row;
 
   if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kFwdCols));
@@ -293,7 +312,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (tid == 17 * 32) {
     for (int i = 0; i < kFNumBars; ++i)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)),
-                   "r"(i == kFBarP || i == kFBarP + 1 ? 8u : 1u));
+                   "r"(i >= kFBarP && i < kFBarP + 4 ? 4u : 1u));
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -314,7 +333,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     hi = __reduce_max_sync(0xffffffffu, hi);
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-    if (lane == 0 && half == 0) {
+    if (lane == 0 && !odd) {
       sh_run[2 * (4 * x + (warp & 3))] = lo;
       sh_run[2 * (4 * x + (warp & 3)) + 1] = hi;
     }
@@ -322,7 +341,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *tbase;
+  const uint32_t tmem = (uint32_t)uniform((int)*tbase);
   // key tiles [x_lo, x_hi) of query tile x; [t_lo, t_hi) of both
   int x_lo[2], x_hi[2];
 #pragma unroll
@@ -333,45 +352,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       lo = min(lo, sh_run[2 * w]);
       hi = max(hi, sh_run[2 * w + 1]);
     }
-    x_lo[y] = lo < hi ? lo / kTile : 0;
-    x_hi[y] = lo < hi ? (hi + kTile - 1) / kTile : 0;
+    x_lo[y] = uniform(lo < hi ? lo / kKeys : 0);
+    x_hi[y] = uniform(lo < hi ? (hi + kKeys - 1) / kKeys : 0);
   }
   const bool on0 = x_lo[0] < x_hi[0], on1 = x_lo[1] < x_hi[1];
   const int t_lo = on0 && on1 ? min(x_lo[0], x_lo[1]) : on0 ? x_lo[0] : x_lo[1];
   const int t_hi = max(x_hi[0], x_hi[1]);
-  const int n_it = t_hi - t_lo;  // key tiles, from t_hi - 1 down
+  const int n_t = t_hi - t_lo;  // key tiles; the one of round r is t_hi - 1 - r
 
   if (warp == 17) {
     // ------------------------------------------------------------- TMA loads
-    // Round it brings K of tile t_hi - 1 - it and V of the tile before it (the
-    // products of that round: S of the one, P V of the other) on one barrier.
-    if (lane == 0 && n_it > 0) {
+    // Round r brings K of its tile and V of the tile two rounds before, on one
+    // barrier; both are consumed by the products of round r.
+    if (lane == 0 && n_t > 0) {
       int rounds = 0;
-      bool ok = true;
-      for (int it = 0; it <= n_it && ok; ++it) {
-        const int j = t_hi - 1 - it, b = bar(kFBarKv + (it & 1));
-        // the slots' previous tiles released, K's also before the last round,
-        // which brings none: it shows that round it - 2 was seen landed, so that
-        // its barrier may take a new phase
-        if (it >= 2) ok = bar_wait(bar(kFBarKe + (it & 1)), (uint32_t)((it >> 1) & 1) ^ 1u, abort);
-        if (ok && it >= 3) ok = bar_wait(bar(kFBarVe + ((it - 1) & 1)), (uint32_t)(((it - 1) >> 1) & 1) ^ 1u, abort);
-        if (!ok) {
+      for (int r = 0; r < n_t + 2; ++r) {
+        const int j = t_hi - 1 - r;
+        const uint32_t b = bar(kFBarKv + (r & 3));
+        if (r >= kSlots && !bar_wait(bar(kFBarFree + (r & 3)), (uint32_t)((r >> 2) & 1) ^ 1u, abort)) {
           set_abort(a.status, abort);
           break;
         }
-        bar_expect_tx(b, (it < n_it ? kTileB : 0) + (it > 0 ? kTileB : 0));
-        if (it < n_it) {
-          const uint32_t dst = base + kFOffK + (it & 1) * kTileB;
-          tma_load_3d(dst, &tm_k, 0, j * kTile, plane_kv, b);
-          tma_load_3d(dst + kBoxB, &tm_k, 64, j * kTile, plane_kv, b);
+        bar_expect_tx(b, (r < n_t ? kKeyB : 0) + (r >= 2 ? kKeyB : 0));
+        if (r < n_t) {
+          const uint32_t dst = base + kFOffK + (r & 3) * kKeyB;
+          tma_load_3d(dst, &tm_k, 0, j * kKeys, plane_kv, b);
+          tma_load_3d(dst + kKeyBox, &tm_k, 64, j * kKeys, plane_kv, b);
         }
-        if (it > 0) {
-          const uint32_t dst = base + kFOffV + ((it - 1) & 1) * kTileB;
-          tma_load_3d(dst, &tm_v, 0, (j + 1) * kTile, plane_kv, b);
-          tma_load_3d(dst + kBoxB, &tm_v, 64, (j + 1) * kTile, plane_kv, b);
+        if (r >= 2) {
+          const uint32_t dst = base + kFOffV + ((r - 2) & 3) * kKeyB;
+          tma_load_3d(dst, &tm_v, 0, (j + 2) * kKeys, plane_kv, b);
+          tma_load_3d(dst + kKeyBox, &tm_v, 64, (j + 2) * kKeys, plane_kv, b);
         }
-        rounds = it + 1;
-        if (it == 0) {
+        rounds = r + 1;
+        if (r == 0) {
 #pragma unroll
           for (int y = 1; y >= 0; --y) {
             const uint32_t dst = base + kFOffQ + y * kTileB;
@@ -384,14 +398,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // the last copies land before the CTA goes away (they may not have been
       // waited for when another role gave up)
       for (int y = 0; y < 2; ++y) bar_wait(bar(kFBarQ + y), 0, nullptr);
-      for (int e = max(0, rounds - 2); e < rounds; ++e)
-        bar_wait(bar(kFBarKv + (e & 1)), (uint32_t)((e >> 1) & 1), nullptr);
+      for (int e = max(0, rounds - kSlots); e < rounds; ++e)
+        bar_wait(bar(kFBarKv + (e & 3)), (uint32_t)((e >> 2) & 1), nullptr);
     }
     __syncwarp();
   } else if (warp == 16) {
     // -------------------------------------------------------------- products
     const bool el = elect_one();
-    const uint32_t id_s = instr_desc(kTile, kTile, true);
+    const uint32_t id_s = instr_desc(kTile, kKeys, true);
     const uint32_t id_o = instr_desc(kTile, kHeadDim, false) | kInstrTransB;
     bool ok = true;
     auto wait = [&](int b, uint32_t par) {
@@ -401,50 +415,46 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
     };
     const uint64_t dq = op_desc_sw128(base + kFOffQ), dk = op_desc_sw128(base + kFOffK),
-                   dv = op_desc_mn_sw128(base + kFOffV, kBoxB);
-    for (int it = 0; n_it > 0 && it <= n_it; ++it) {
-      const int j = t_hi - 1 - it, sk = it & 1, sv = sk ^ 1;  // S of tile j, P V of tile j + 1
-      wait(kFBarKv + sk, (uint32_t)((it >> 1) & 1));
+                   dv = op_desc_mn_sw128(base + kFOffV, kKeyBox);
+    for (int r = 0; n_t > 0 && r < n_t + 2; ++r) {
+      wait(kFBarKv + (r & 3), (uint32_t)((r >> 2) & 1));
       if (!ok) break;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const uint32_t t_s = tmem + kTile * y, t_o = tmem + 256 + kTile * y;
-        if (j + 1 >= x_lo[y] && j + 1 < x_hi[y]) {
-          wait(kFBarP + y, (uint32_t)((x_hi[y] - 2 - j) & 1));
+        const uint32_t t_o = tmem + 256 + kTile * y;
+        const int i = r - (t_hi - x_hi[y]), n_y = x_hi[y] - x_lo[y];  // this round's tile of y, y's tiles
+        const uint32_t t_s = tmem + kTile * y + kKeys * (i & 1);
+        if (i >= 2 && i - 2 < n_y) {
+          wait(kFBarP + 2 * y + (i & 1), (uint32_t)(((i - 2) >> 1) & 1));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (el) {
-            const bool acc = j + 2 < x_hi[y];
+            const uint64_t d = dv + (uint64_t)((((r - 2) & 3) * kKeyB) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_f16_ts(t_o, t_s + 8 * ks + 32 * (ks >> 2), dv + (uint64_t)((sv * kTileB + ks * 2048) >> 4), id_o,
-                         acc || ks > 0);
-            if (j + 1 == x_lo[y]) mma_commit(bar(kFBarO + y));
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              mma_f16_ts(t_o, t_s + 8 * ks, d + (uint64_t)((ks * 2048) >> 4), id_o, i > 2 || ks > 0);
+            mma_commit(bar(kFBarO + 2 * y + (i & 1)));
           }
         }
-        if (j >= x_lo[y] && j < x_hi[y]) {
-          if (j == x_hi[y] - 1) wait(kFBarQ + y, 0);
+        if (i >= 0 && i < n_y) {
+          if (i == 0) wait(kFBarQ + y, 0);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (el) {
+            const uint64_t d = dk + (uint64_t)(((r & 3) * kKeyB) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-              const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
-              mma_f16(t_s, dq + (uint64_t)((y * kTileB + off) >> 4), dk + (uint64_t)((sk * kTileB + off) >> 4), id_s,
-                      ks > 0);
-            }
-            mma_commit(bar(kFBarS + y));
+            for (int ks = 0; ks < kHeadDim / 16; ++ks)
+              mma_f16(t_s, dq + (uint64_t)((y * kTileB + (ks >> 2) * kBoxB + (ks & 3) * 32) >> 4),
+                      d + (uint64_t)(((ks >> 2) * kKeyBox + (ks & 3) * 32) >> 4), id_s, ks > 0);
+            mma_commit(bar(kFBarS + 2 * y + (i & 1)));
           }
         }
       }
       if (!ok) break;
-      if (el) {
-        if (it < n_it) mma_commit(bar(kFBarKe + sk));
-        if (it > 0) mma_commit(bar(kFBarVe + sv));
-      }
+      if (el) mma_commit(bar(kFBarFree + (r & 3)));
       __syncwarp();
     }
-    if (n_it > 0) {
+    if (n_t > 0) {
       // every product complete before the tensor memory goes back
       if (el) mma_commit(bar(kFBarDone));
       bar_wait(bar(kFBarDone), 0, nullptr);
@@ -454,123 +464,128 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // ----------------------------------------------------------- query rows
     const int lo = x == 0 ? x_lo[0] : x_lo[1], hi = x == 0 ? x_hi[0] : x_hi[1];
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_h = trow + kTile * x + 64 * half, t_o = trow + 256 + kTile * x + 64 * half;
+    const uint32_t t_s = trow + kTile * x + kKeys * odd, t_o = trow + 256 + kTile * x;
     const float slope2 = BIAS ? slope_log2(a.mod, hqi) : 0.0f;
-    const int tiles = (n + kTile - 1) / kTile;
-    const uint2* bad_masks = reinterpret_cast<const uint2*>(a.bad) + (size_t)plane_kv * tiles * 2 + half;
-    float* sh_max = reinterpret_cast<float*>(fsm + kFOffMax) + x * 2 * kTile + row;
-    const int q_first = qi - (tid & 31);
+    const size_t bad_row = (size_t)plane_kv * ((n + kTile - 1) / kTile) * 4;  // a word per 32 keys
+    float* sh_m = reinterpret_cast<float*>(fsm + kFOffMax) + x * 2 * kTile + row;
+    const int bar_m = kFBarM + 8 * x + (warp & 3);  // + 4 * parity
+    const int n_x = hi - lo;
     bool ok = true, poison = false;
     // whether any V row of the tiles ahead is not finite (under the first loads:
     // a mask read in the loop would put a global load's latency into every tile)
     uint32_t any_bad = 0;
-    for (int j = lo + (tid & 255); j < hi; j += 256) {
-      const uint4 w = reinterpret_cast<const uint4*>(a.bad)[(size_t)plane_kv * tiles + j];
-      any_bad |= w.x | w.y | w.z | w.w;
-    }
-    {
-      uint32_t r;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-          : "=r"(r)
-          : "r"(any_bad), "r"(kNbTile + x)
-          : "memory");
-      any_bad = r;
-    }
-    float m = kNegBig, l = 0.0f;
-#pragma unroll 1
-    for (int j = hi - 1; j >= lo; --j) {
-      const int idx = hi - 1 - j, k0 = j * kTile + 64 * half;
-      if (!__all_sync(0xffffffffu, bar_try(bar(kFBarS + x), (uint32_t)(idx & 1))) &&
-          !__all_sync(0xffffffffu, bar_wait(bar(kFBarS + x), (uint32_t)(idx & 1), abort))) {
+    for (int j = 2 * lo + lane; j < 2 * hi; j += 32)
+      if (32 * j < n) any_bad |= a.bad[bad_row + j];
+    any_bad = __reduce_or_sync(0xffffffffu, any_bad);
+    auto wait = [&](int b, uint32_t par) {
+      if (!__all_sync(0xffffffffu, bar_try(bar(b), par)) && !__all_sync(0xffffffffu, bar_wait(bar(b), par, abort))) {
         ok = false;
         set_abort(a.status, abort);
       }
-      // (a warp that gave up still meets the others at the tile's barrier)
-      float mx = -INFINITY, most = 0.0f;
-      float z[32];
-      const bool masked = k0 < all_lo || k0 + 64 > all_hi;  // (the same for the warp)
-      const bool beyond = k0 + 63 > q_first;
-      const float dist0 = (float)(k0 - qi);
-      if (ok) {
-        // the maximum of this half: with a bias, over the scores, which then
-        // take the products' place; else over the products (a cap and the
-        // scale keep their order).  With a cap alone the largest magnitude,
-        // which the choice of the polynomial needs anyway, bounds it: where
-        // that bound would not move the running maximum, the maximum itself is
-        // not looked for.
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (CAP && !BIAS) {
+    };
+    float m = kNegBig, l = 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            ld32(t_h + 32 * c, z);
-            most = chunk_most(z, most);
-          }
-          mx = cap_score(a.mod, most * a.mod.y_scale);
-        }
-        if (!CAP || BIAS || __any_sync(0xffffffffu, !(mx <= m + kLazyMax))) {
-          mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            ld32(t_h + 32 * c, z);
-            if (CAP && BIAS) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
-            if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, dist0 + 32.0f * c, beyond);
-            if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
-            if (BIAS) tmem_st32(t_h + 32 * c, z);
-            mx = chunk_max(z, mx);
-          }
-          if (!BIAS && mx > -INFINITY) mx = CAP ? cap_score(a.mod, mx * a.mod.y_scale) : mx * a.qk_scale_log2;
-        }
-        if (any_bad) {  // V rows that are not finite (rare)
-          const uint2 bad = bad_masks[2 * j];
-#pragma unroll 1
-          for (int i = 0; i < 64; ++i)
-            if (((i < 32 ? bad.x : bad.y) >> (i & 31)) & 1u) poison |= k0 + i >= run.x && k0 + i < run.y;
-        }
-        if (BIAS) tmem_st_wait();
-      }
-      // the row's maximum over both halves
-      float* exch = sh_max + (idx & 1) * 4 * kTile;
-      exch[half * kTile] = mx;
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
+    for (int i = odd; i < n_x; i += 2) {
+      const int k0 = (hi - 1 - i) * kKeys;
+      const uint32_t par = (uint32_t)((i >> 1) & 1);
+      wait(kFBarS + 2 * x + odd, par);
+      if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (!ok || *abort) {
-        ok = false;
-        break;
-      }
-      mx = fmaxf(mx, exch[(half ^ 1) * kTile]);
-      const bool grow = mx > m + kLazyMax;
-      const float alpha = grow ? fast_exp2(m - mx) : 1.0f;
-      if (grow) {
-        l *= alpha;
-        m = mx;
-      }
-      // S(j) complete implies the P V before it complete: O may be rescaled
-      if (idx > 0 && __any_sync(0xffffffffu, grow)) {
+      float z[32];
+      const bool masked = k0 < all_lo || k0 + kKeys > all_hi;  // (the same for the warp)
+      const bool beyond = k0 + kKeys - 1 > qi - lane;
+      const float dist0 = (float)(k0 - qi);
+      // the maximum: with a bias, over the scores, which then take the products'
+      // place; else over the products (a cap and the scale keep their order).
+      // With a cap alone the largest magnitude, which the choice of the
+      // polynomial needs anyway, bounds it: where that bound would not move the
+      // running maximum, the maximum itself is not looked for.
+      float mx = -INFINITY, most = 0.0f;
+      if (CAP && !BIAS) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < 64; c0 += 16) {
+        for (int c = 0; c < 2; ++c) {
+          ld32(t_s + 32 * c, z);
+          most = chunk_most(z, most);
+        }
+        mx = cap_score(a.mod, most * a.mod.y_scale);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          ld32(t_s + 32 * c, z);
+          if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
+          if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, slope2, dist0 + 32.0f * c, beyond);
+          if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+          if (BIAS) tmem_st32(t_s + 32 * c, z);
+          mx = chunk_max(z, mx);
+        }
+        if (!BIAS) mx *= a.qk_scale_log2;  // scale > 0; -inf stays
+      }
+      // the running maximum as the tile before left it
+      const float m_old = m;
+      if (i > 0) {
+        wait(bar_m + 4 * (odd ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
+        if (!ok) break;
+        m = sh_m[(odd ^ 1) * kTile];
+      }
+      float top = m + kLazyMax;
+      if (CAP && !BIAS) {
+        const bool ask = !(mx <= top);
+        if (__any_sync(0xffffffffu, ask)) {
+          float exact = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            ld32(t_s + 32 * c, z);
+            if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
+            exact = chunk_max(z, exact);
+          }
+          // (a row asks for itself: the others' results do not depend on it)
+          if (ask) {
+            mx = exact > -INFINITY ? cap_score(a.mod, exact * a.mod.y_scale) : exact;
+            top = m;  // so that the bound will not ask again soon
+          }
+        }
+      }
+      const float m_prev = m;
+      const bool grow = mx > top;
+      if (grow) m = mx;
+      sh_m[odd * kTile] = m;
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bar_m + 4 * odd));
+      if (__any_sync(0xffffffffu, m != m_old)) l *= fast_exp2(m_old - m);
+      if (i > 0 && __any_sync(0xffffffffu, grow)) {
+        const float alpha = fast_exp2(m_prev - m);
+        wait(kFBarO + 2 * x + (odd ^ 1), (uint32_t)(((i - 1) >> 1) & 1));  // the P V before
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+        for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
           float t[16];
           ld16(t_o + c0, t);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) t[i] *= alpha;
+          for (int e = 0; e < 16; ++e) t[e] *= alpha;
           st16(t_o + c0, t);
         }
       }
-      // P (fp16) over the front of this half's products: chunk c's 16 columns
-      // lie before the products of chunk c + 1
+      if (any_bad) {  // V rows that are not finite (rare)
+#pragma unroll 1
+        for (int e = 0; e < kKeys && k0 + e < n; ++e)
+          if ((a.bad[bad_row + (k0 + e) / 32] >> (e & 31)) & 1u) poison |= k0 + e >= run.x && k0 + e < run.y;
+      }
+      // P (fp16) over the front of the products: chunk c's 16 columns lie before
+      // the products of chunk c + 1
       f32x2 ls[2] = {0, 0};
+      if (BIAS) tmem_st_wait();
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t pw[16];
-        ld32(t_h + 32 * c, z);
+        ld32(t_s + 32 * c, z);
         if (CAP && !BIAS)
           chunk_cap(a, z, most, m);
         else
           chunk_shift(z, BIAS ? 1.0f : a.qk_scale_log2, m);
         if (!BIAS && masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
         chunk_probs(z, pw, ls);
-        tmem_st16(t_h + 16 * c, pw);
+        tmem_st16(t_s + 16 * c, pw);
       }
       float lx, ly;
       unpack2(add2(ls[0], ls[1]), lx, ly);
@@ -578,34 +593,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tmem_st_wait();
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(bar(kFBarP + x));
+      if (lane == 0) bar_arrive(bar(kFBarP + 2 * x + odd));
     }
-    const bool any = lo < hi;
-    if (ok && any && !__all_sync(0xffffffffu, bar_wait(bar(kFBarO + x), 0, abort))) {
-      ok = false;
-      set_abort(a.status, abort);
-    }
-    // the row's sum and poison over both halves (every warp of the tile has read
-    // the last exchange: O complete follows their arrivals)
-    sh_max[half * kTile] = l;
-    sh_max[(4 + half) * kTile] = poison ? 1.0f : 0.0f;
-    asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
-    const float other = sh_max[(half ^ 1) * kTile];
-    poison |= sh_max[(4 + (half ^ 1)) * kTile] != 0.0f;
-    if (ok && !*abort) {
+    // the final maximum, the sum and poison of both threads of the row
+    const int last = n_x - 1;
+    if (ok && last >= 0) {
+      if (odd != (last & 1)) {
+        wait(bar_m + 4 * (odd ^ 1), (uint32_t)((last >> 1) & 1));
+        const float m_last = sh_m[(odd ^ 1) * kTile];
+        l *= fast_exp2(m - m_last);
+        m = m_last;
+      }
+      wait(kFBarO + 2 * x + (last & 1), (uint32_t)((last >> 1) & 1));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");  // every maximum is read
+    sh_m[odd * kTile] = l;
+    asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
+    const float total = sh_m[0] + sh_m[kTile];
+    asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
+    sh_m[odd * kTile] = poison ? 1.0f : 0.0f;
+    asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
+    poison = sh_m[0] + sh_m[kTile] != 0.0f;
+    if (ok && !*abort) {
       const bool row_ok = qi < n;
-      const float total = half == 0 ? l + other : other + l;  // the same order in both threads
       const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a row that sees nothing is 0
-      uint16_t* orow = a.out + ((size_t)plane_q * n + (row_ok ? qi : 0)) * kHeadDim + 64 * half;
+      uint16_t* orow = a.out + ((size_t)plane_q * n + (row_ok ? qi : 0)) * kHeadDim + 64 * odd;
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 32) {
         float t[32];
-        if (any) {
-          ld32(t_o + c0, t);
+        if (last >= 0) {
+          ld32(t_o + 64 * odd + c0, t);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) t[i] = 0.0f;
+          for (int e = 0; e < 32; ++e) t[e] = 0.0f;
         }
         uint32_t w[16];
 #pragma unroll
@@ -619,7 +640,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             *reinterpret_cast<uint4*>(orow + c0 + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         }
       }
-      if (row_ok && half == 0 && a.stats != nullptr)
+      if (row_ok && !odd && a.stats != nullptr)
         *reinterpret_cast<float2*>(a.stats + ((size_t)plane_q * n + qi) * 2) = make_float2(m, total);
     }
   }
@@ -634,14 +655,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 //
 // One 320-thread CTA per (128-key tile, KV head, sequence), two per SM, keys
 // on the TMEM lanes: S^T = K Q^T (M 128, N 128), so thread t of a warpgroup
-// owns key t and adds in a register; no atomics, a fixed order.  Warpgroups 0
+// owns key t and adds in registers; no atomics, a fixed order.  Warpgroups 0
 // and 1 take alternate (query head, query tile) blocks, warp 8 loads the query
-// tiles and stages (m, 1 / l, run) per query, warp 9 issues the products.
-// Query tiles none of whose queries sees the key tile are skipped.
+// tiles and stages -m, 1 / l and the run per query, warp 9 issues the products.
+// Two queries go through each instruction (their -m and 1 / l are pairs in
+// shared memory; the cap ends in an addition, which takes -m along).
+// Query tiles none of whose queries sees the key tile are skipped; tiles seen
+// whole take no mask.
 constexpr int kSumThreads = 320;
 constexpr int kSOffK = 0;
 constexpr int kSOffQ = kSOffK + kTileB;                    // 2 slots
-constexpr int kSOffStat = kSOffQ + 2 * kTileB;             // 2 x 128 x (m, 1 / l)
+constexpr int kSOffStat = kSOffQ + 2 * kTileB;             // 2 x (128 x -m, 128 x 1 / l)
 constexpr int kSOffRun = kSOffStat + 2 * kTile * 8;        // 2 x 128 x (begin, end)
 constexpr int kSOffRed = kSOffRun + 2 * kTile * 8;         // 128 sums
 constexpr int kSOffBar = kSOffRed + kTile * 4;
@@ -651,7 +675,7 @@ constexpr uint32_t kSumCols = 256;
 
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kSumThreads, 2)
-    prompt_sums_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
+    prompt_sums_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
   extern __shared__ __align__(1024) uint8_t ssm[];
   const uint32_t base = saddr(ssm);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(ssm + kSOffBar + 8 * kSNumBars);
@@ -659,7 +683,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
   auto bar = [&](int i) { return base + kSOffBar + 8 * i; };
   const int n = a.n, G = a.group;
   const int kt = blockIdx.x, h = blockIdx.y, bl = blockIdx.z;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int k0 = kt * kTile, k1 = min(k0 + kTile, n);
   const int tiles = gridDim.x;
   const int4* runs = a.runs + (size_t)bl * tiles;
@@ -686,7 +710,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *tbase;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tbase, 0);
   float sum = 0.0f;
 
   if (warp == 8) {
@@ -714,19 +738,20 @@ __global__ void __launch_bounds__(kSumThreads, 2)
           tma_load_3d(dst, &tm_q, 0, qt * kTile, plane, b);
           tma_load_3d(dst + kBoxB, &tm_q, 64, qt * kTile, plane, b);
         }
-        float2* st = reinterpret_cast<float2*>(ssm + kSOffStat) + x * kTile;
+        float* st = reinterpret_cast<float*>(ssm + kSOffStat) + x * 2 * kTile;
         int2* rn = reinterpret_cast<int2*>(ssm + kSOffRun) + x * kTile;
 #pragma unroll
         for (int e = 0; e < kTile / 32; ++e) {
           const int i = lane + 32 * e, qi = qt * kTile + i;
-          float2 s = make_float2(0.0f, 0.0f);  // past the prompt, or seeing nothing: probability 0
+          float2 s = make_float2(INFINITY, 0.0f);  // past the prompt: p = 2^-inf
           int2 r = make_int2(0, 0);
           if (qi < n) {
             s = *reinterpret_cast<const float2*>(a.stats + ((size_t)plane * n + qi) * 2);
-            s = s.y != 0.0f ? make_float2(s.x, 1.0f / s.y) : make_float2(0.0f, 0.0f);
+            s = s.y != 0.0f ? make_float2(s.x, 1.0f / s.y) : make_float2(INFINITY, 0.0f);
             r = run_of(a, bl, qi);
           }
-          st[i] = s;
+          st[i] = -s.x;
+          st[kTile + i] = s.y;
           rn[i] = r;
         }
         __syncwarp();
@@ -780,7 +805,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     // ------------------------------------------------------ sums over the queries
     const int x = warp >> 2, t = tid & (kTile - 1);
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kTile * x;
-    const float2* st = reinterpret_cast<const float2*>(ssm + kSOffStat) + x * kTile;
+    const float* st = reinterpret_cast<const float*>(ssm + kSOffStat) + x * 2 * kTile;
     const int2* rn = reinterpret_cast<const int2*>(ssm + kSOffRun) + x * kTile;
     const int key = k0 + t;
     int it = 0;
@@ -800,31 +825,50 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const int4 r = runs[qt];
         const bool whole = r.z <= k0 && r.w >= k1;  // every query sees the whole key tile
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int q0 = qt * kTile;
+        f32x2 acc[2] = {0, 0};
 #pragma unroll 1
         for (int c0 = 0; c0 < kTile; c0 += 32) {
-          float v[32];
-          ld32(trow + c0, v);
-          if (CAP) {
+          float z[32];
+          ld32(trow + c0, z);
+          auto nm = [&](int i) { return *reinterpret_cast<const f32x2*>(st + c0 + i); };
+          const float d0 = (float)(q0 + c0 - key);
+          const bool both = q0 + c0 < key - lane + 31;  // some key of the warp lies after the query
+          if (CAP && !BIAS) {
+            chunk_cap_plus(a, z, chunk_most(z, 0.0f), nm);
+          } else {
+            if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
+            if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, -slope2, d0, both);
+            const f32x2 sc = pack2(BIAS ? 1.0f : a.qk_scale_log2, BIAS ? 1.0f : a.qk_scale_log2);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= a.mod.y_scale;
-            cap_scores(a.mod, v);
+            for (int i = 0; i < 32; i += 2)
+              unpack2(BIAS ? add2(pack2(z[i], z[i + 1]), nm(i)) : fma2(pack2(z[i], z[i + 1]), sc, nm(i)), z[i],
+                      z[i + 1]);
           }
+          if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 s = st[c0 + i];
-            float zz = CAP ? v[i] : v[i] * a.qk_scale_log2;
-            if (BIAS) zz = fmaf(-slope2, fabsf((float)(qt * kTile + c0 + i - key)), zz);
-            const float p = fast_exp2(zz - s.x);
-            bool on = s.y != 0.0f;  // 1 / l is 0 for a row that sees nothing (its p may be infinite)
-            if (!whole) {
-              const int2 b = rn[c0 + i];
-              on = on && key >= b.x && key < b.y;
+            for (int i = 0; i < 32; i += 2) {
+              const f32x2 p = pack2(fast_exp2(z[i]), fast_exp2(z[i + 1]));
+              acc[(i >> 1) & 1] = fma2(p, *reinterpret_cast<const f32x2*>(st + kTile + c0 + i), acc[(i >> 1) & 1]);
             }
-            acc[i & 3] = on ? fmaf(p, s.y, acc[i & 3]) : acc[i & 3];
+          } else {
+            // (statistics of a row that does not see the key may be anything)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const int4 b = *reinterpret_cast<const int4*>(rn + c0 + i);
+              float x0, x1;
+              unpack2(mul2(pack2(fast_exp2(z[i]), fast_exp2(z[i + 1])),
+                           *reinterpret_cast<const f32x2*>(st + kTile + c0 + i)),
+                      x0, x1);
+              x0 = key >= b.x && key < b.y ? x0 : 0.0f;
+              x1 = key >= b.z && key < b.w ? x1 : 0.0f;
+              acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pack2(x0, x1));
+            }
           }
         }
-        sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        float ax, ay;
+        unpack2(add2(acc[0], acc[1]), ax, ay);
+        sum += ax + ay;
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -934,9 +978,10 @@ cudaError_t launch_prompt(const PromptArgs& args, const uint16_t* q, const uint1
                           cudaStream_t st) {
   PromptArgs a = args;
   prompt_polynomials(&a);
-  CUtensorMap tm_q, tm_k, tm_v;
-  if (!encode_rows_map(&tm_q, q, a.n, a.batch * a.hq, kTile) || !encode_rows_map(&tm_k, k, a.n, a.batch * a.hkv, kTile) ||
-      !encode_rows_map(&tm_v, a.v16, a.n, a.batch * a.hkv, kTile, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
+  CUtensorMap tm_q, tm_k, tm_v, tm_ks;
+  if (!encode_rows_map(&tm_q, q, a.n, a.batch * a.hq, kTile) || !encode_rows_map(&tm_k, k, a.n, a.batch * a.hkv, kKeys) ||
+      !encode_rows_map(&tm_v, a.v16, a.n, a.batch * a.hkv, kKeys, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) ||
+      (a.sums != nullptr && !encode_rows_map(&tm_ks, k, a.n, a.batch * a.hkv, kTile)))
     return cudaErrorInvalidValue;
   prompt_prep_kernel<<<(a.n + kTile - 1) / kTile * (a.batch * a.hkv), kPrepThreads, 0, st>>>(a, v);
   cudaError_t e = cudaGetLastError();
@@ -946,8 +991,8 @@ cudaError_t launch_prompt(const PromptArgs& args, const uint16_t* q, const uint1
           : (bias ? launch_fwd<false, true>(a, tm_q, tm_k, tm_v, st)
                   : launch_fwd<false, false>(a, tm_q, tm_k, tm_v, st));
   if (e != cudaSuccess || a.sums == nullptr) return e;
-  return cap ? (bias ? launch_sums<true, true>(a, tm_q, tm_k, st) : launch_sums<true, false>(a, tm_q, tm_k, st))
-             : (bias ? launch_sums<false, true>(a, tm_q, tm_k, st) : launch_sums<false, false>(a, tm_q, tm_k, st));
+  return cap ? (bias ? launch_sums<true, true>(a, tm_q, tm_ks, st) : launch_sums<true, false>(a, tm_q, tm_ks, st))
+             : (bias ? launch_sums<false, true>(a, tm_q, tm_ks, st) : launch_sums<false, false>(a, tm_q, tm_ks, st));
 }
 
 }  // namespace kvc
