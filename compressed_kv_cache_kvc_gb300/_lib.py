@@ -81,7 +81,7 @@ _SIGS = {
     "kvc_block_cache_destroy": (None, [_P]),
     "kvc_block_cache_reset": (_I, [_P, _P]),
     "kvc_block_buffer": (_I, [_P, _I, ctypes.POINTER(_P), ctypes.POINTER(_SZ)]),
-    "kvc_block_length": (_I, [_P, _I, ctypes.POINTER(_I)]),
+    "kvc_block_lengths": (_I, [_P, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "kvc_block_sync_host": (_I, [_P, _P]),
     "kvc_block_read_status": (_I, [_P, ctypes.POINTER(_I), _P]),
     "kvc_block_last_launch_count": (_I, [_P]),

@@ -9,7 +9,7 @@ import math
 import torch
 
 from . import _lib as L
-from .cache import HEAD_DIM, _need, _stream_ptr
+from .cache import HEAD_DIM, _current_device, _need, _stream_ptr
 from .prompt import _ptr, _slopes, prompt_attention
 
 
@@ -32,6 +32,8 @@ class BlockScaledCache:
                                                                               codes)
         self.num_blocks, self.max_batch, self.max_blocks_per_seq = num_blocks, max_batch, max_blocks_per_seq
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type != "cuda":
+            raise ValueError("device must be a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         # (the caching allocator's blocks are 512-byte aligned)
@@ -50,8 +52,11 @@ class BlockScaledCache:
             self.handle = None
 
     def _call(self, name, *args, stream=None):
+        if _current_device() == self.device.index:
+            L.check(getattr(self.lib, name)(self.handle, *args, _stream_ptr(stream)), name)
+            return
         with torch.cuda.device(self.device):
-            L.check(getattr(self.lib, name)(self.handle, *args, ctypes.c_void_p(_stream_ptr(stream))), name)
+            L.check(getattr(self.lib, name)(self.handle, *args, _stream_ptr(stream)), name)
 
     # -- state ---------------------------------------------------------------
     def reset(self, stream=None):
@@ -72,10 +77,15 @@ class BlockScaledCache:
         off = ptr.value - self.state.data_ptr()
         return self.state[off:off + nb.value]
 
+    def lengths(self, seq_begin: int, batch: int):
+        """Tokens held: (least, most) of the sequences."""
+        lo, hi = ctypes.c_int32(), ctypes.c_int32()
+        L.check(self.lib.kvc_block_lengths(self.handle, seq_begin, batch, ctypes.byref(lo), ctypes.byref(hi)),
+                "kvc_block_lengths")
+        return lo.value, hi.value
+
     def length(self, seq: int) -> int:
-        p = ctypes.c_int32()
-        L.check(self.lib.kvc_block_length(self.handle, seq, ctypes.byref(p)), "kvc_block_length")
-        return p.value
+        return self.lengths(seq, 1)[0]
 
     def read_status(self, stream=None) -> int:
         v = ctypes.c_int32()
@@ -92,10 +102,10 @@ class BlockScaledCache:
         return int(self.lib.kvc_block_workspace_bytes(self.handle, batch))
 
     def workspace(self, batch: int) -> torch.Tensor:
-        nb = self.workspace_bytes(batch)
-        ws = self._ws.get(nb)
+        ws = self._ws.get(batch)
         if ws is None:
-            ws = self._ws[nb] = torch.empty(max(nb, 1), dtype=torch.uint8, device=self.device)
+            ws = self._ws[batch] = torch.empty(max(self.workspace_bytes(batch), 1), dtype=torch.uint8,
+                                               device=self.device)
         return ws
 
     # -- operators -----------------------------------------------------------
@@ -122,17 +132,16 @@ class BlockScaledCache:
         ws = self.workspace(q.shape[0]) if workspace is None else workspace
         _need(ws, torch.uint8, "workspace", self.device)
         scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
-        self._call("kvc_block_attention", seq_begin, q.shape[0], _ptr(q), _ptr(out), ctypes.c_float(scale),
-                   ctypes.c_float(softcap), _ptr(slopes), _ptr(ws), ws.numel(), stream=stream)
+        self._call("kvc_block_attention", seq_begin, q.shape[0], _ptr(q), _ptr(out), scale,
+                   softcap, _ptr(slopes), _ptr(ws), ws.numel(), stream=stream)
         return out
 
     def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, status: torch.Tensor, seq_begin: int = 0,
                 stream=None, **attention) -> torch.Tensor:
         """A fresh prompt: append it and return `prompt_attention` of it (over
         its exact bf16 keys and values; `attention` goes to it unchanged)."""
-        for b in range(seq_begin, min(seq_begin + k.shape[0], self.max_batch)):
-            if seq_begin >= 0 and self.length(b) != 0:
-                raise L.KvcError(L.KVC_ERR_STATE, "prefill")
+        if self.lengths(seq_begin, k.shape[0])[1] != 0:
+            raise L.KvcError(L.KVC_ERR_STATE, "prefill")
         got = prompt_attention(q, k, v, status=status, stream=stream, **attention)
         self.append(k, v, seq_begin=seq_begin, stream=stream)
         return got
@@ -143,15 +152,14 @@ class BlockScaledCache:
         bf16 (k, v), [batch, Hkv, n, 128] each, as the attention sees them; rows
         at or past a sequence's length are left as they are in `out` (zero
         without `out`)."""
+        least, most = self.lengths(seq_begin, batch)
         if n is None:
-            n = max(self.length(b) for b in range(seq_begin, seq_begin + batch)) - pos_begin
+            n = most - pos_begin
         shape = (batch, self.num_kv_heads, n, HEAD_DIM)
         if out is None:
             if batch < 1 or n < 1:
                 raise ValueError("batch and n must be positive")
-            held = 0 <= seq_begin and seq_begin + batch <= self.max_batch and \
-                min(self.length(b) for b in range(seq_begin, seq_begin + batch)) >= pos_begin + n
-            make = torch.empty if held else torch.zeros
+            make = torch.empty if pos_begin + n <= least else torch.zeros
             out = tuple(make(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
         for name, t in zip(("k", "v"), out):
             _need(t, torch.bfloat16, name, self.device, shape)

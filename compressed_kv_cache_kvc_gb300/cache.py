@@ -19,7 +19,15 @@ HEAD_DIM = 128
 NUM_SINK = 4
 
 
+# the current stream's handle without a Stream object around it (0.3 against
+# 2.9 us, a tenth of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_ptr(stream=None) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -115,13 +123,13 @@ class KVCache:
         return int(self.lib.kvc_workspace_bytes(self.handle, batch))
 
     def workspace(self, batch: int) -> torch.Tensor:
-        nb = self.workspace_bytes(batch)
-        ws = self._ws.get(nb)
+        ws = self._ws.get(batch)
         if ws is None:
+            nb = self.workspace_bytes(batch)
             ws = torch.empty(nb + 256, dtype=torch.uint8, device=self.device)
             off = (-ws.data_ptr()) % 256
             ws = ws[off:off + nb]
-            self._ws[nb] = ws
+            self._ws[batch] = ws
         return ws
 
     def read_status(self, stream=None) -> int:

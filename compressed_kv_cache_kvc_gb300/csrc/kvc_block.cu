@@ -343,6 +343,19 @@ constexpr int kBStages = 4;
 constexpr int kBStage = 4096;  // K page, V page
 constexpr int kBSmem = kBWarps * kBStages * kBStage;
 constexpr float kBLazy = 4.0f;
+constexpr int kJoinRow = kHeadDim + 4;  // one warp's joined row: 128 sums, the maximum, the sum
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
 constexpr int kBCap = 1, kBBias = 2;
 
 // chunk j (16 bytes) of row t of a page: every copy and read instruction of
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
   constexpr bool kOffset = !FP8;
   constexpr float kOffK = 128.0f * 0x1p-24f, kOffV = 128.0f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int cum[kMaxCallBatch + 1];
+  __shared__ int cum[kMaxCallBatch + 1], len[kMaxCallBatch];
   __shared__ int sh_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bt = s.bt, ppb = bt / kPage;  // pages per block
@@ -368,7 +381,9 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
     if (lane == 0) cum[0] = 0;
     for (int base = 0; base < batch; base += 32) {
       const int i = base + lane;
-      int v = i < batch ? block_units(s.seq_pos[seq_begin + i], bt) : 0;
+      const int held = i < batch ? s.seq_pos[seq_begin + i] : 0;
+      int v = block_units(held, bt);
+      if (i < batch) len[i] = held;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, v, o);
@@ -412,7 +427,7 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
     const long long Pf = pbase + (long long)h * nu;
     const int u_a = (int)(F - Pf);
     const int u_e = (int)((F1 < Pf + nu ? F1 : Pf + nu) - Pf);
-    const int P = s.seq_pos[b];
+    const int P = len[bl];
     const int closed = block_closed(P, bt), npg = closed * ppb;
     const int pair = bl * hkv + h;
 
@@ -737,6 +752,19 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
       const bool on0 = 2 * r < rows, on1 = 2 * r + 1 < rows;
       const uint4* ka = reinterpret_cast<const uint4*>(s.k_exact + (eb + (on0 ? 2 * r : 0)) * kHeadDim + 32 * c);
       const uint4* kc = reinterpret_cast<const uint4*>(s.k_exact + (eb + (on1 ? 2 * r + 1 : 0)) * kHeadDim + 32 * c);
+      // V rows 2r (first K half) and 2r + 1 (second) of the tile, dims 32c ..:
+      // head dims 16r' + 2j and 16r' + 2j + 1 on the MMA's rows
+      const uint4* va = reinterpret_cast<const uint4*>(s.v_exact + (eb + (on0 ? 2 * r : 0)) * kHeadDim + 32 * c);
+      const uint4* vc = reinterpret_cast<const uint4*>(s.v_exact + (eb + (on1 ? 2 * r + 1 : 0)) * kHeadDim + 32 * c);
+      uint32_t wa[16], wc[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 x = va[i], y = vc[i];
+        if (!on0) x = make_uint4(0u, 0u, 0u, 0u);
+        if (!on1) y = make_uint4(0u, 0u, 0u, 0u);
+        wa[4 * i] = x.x; wa[4 * i + 1] = x.y; wa[4 * i + 2] = x.z; wa[4 * i + 3] = x.w;
+        wc[4 * i] = y.x; wc[4 * i + 1] = y.y; wc[4 * i + 2] = y.z; wc[4 * i + 3] = y.w;
+      }
       const uint4* qp = reinterpret_cast<const uint4*>(qrow + 32 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -776,19 +804,6 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
       h1 = movmatrix_t(h1);
       q0 = movmatrix_t(q0);
       q1 = movmatrix_t(q1);
-      // V rows 2r (first K half) and 2r + 1 (second) of the tile, dims 32c ..:
-      // head dims 16r' + 2j and 16r' + 2j + 1 on the MMA's rows
-      const uint4* va = reinterpret_cast<const uint4*>(s.v_exact + (eb + (on0 ? 2 * r : 0)) * kHeadDim + 32 * c);
-      const uint4* vc = reinterpret_cast<const uint4*>(s.v_exact + (eb + (on1 ? 2 * r + 1 : 0)) * kHeadDim + 32 * c);
-      uint32_t wa[16], wc[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 x = va[i], y = vc[i];
-        if (!on0) x = make_uint4(0u, 0u, 0u, 0u);
-        if (!on1) y = make_uint4(0u, 0u, 0u, 0u);
-        wa[4 * i] = x.x; wa[4 * i + 1] = x.y; wa[4 * i + 2] = x.z; wa[4 * i + 3] = x.w;
-        wc[4 * i] = y.x; wc[4 * i + 1] = y.y; wc[4 * i + 2] = y.z; wc[4 * i + 3] = y.w;
-      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t a0 = movmatrix_t(prmt(wa[j], wa[8 + j], 0x5410u)), a1 = movmatrix_t(prmt(wa[j], wa[8 + j], 0x7632u));
@@ -865,18 +880,68 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
       }
       __syncthreads();
       if (sh_last) {
-        for (int g = 0; g < G; ++g) {
-          float M = kNegBig;
-          for (int i = i_first; i <= i_last; ++i) M = fmaxf(M, __ldcg(a.part_ml + (((size_t)pair + i) * G + g) * 2));
-          float o = 0.0f, l = 0.0f;
-          for (int i = i_first; i <= i_last; ++i) {
-            const size_t ps = ((size_t)pair + i) * G + g;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + ps * 2));
-            const float wt = fast_exp2(ml.x - M);
-            o += wt * __ldcg(a.part_o + ps * kHeadDim + d);
-            l += wt * ml.y;
+        // a warp per head (several when there are fewer heads than warps, each
+        // with every wph-th part): 32 parts' maxima and sums across the lanes,
+        // then their rows, eight of 16 bytes a lane in flight
+        const int cnt = i_last - i_first + 1;
+        const int wph = G >= kBWarps ? 1 : kBWarps / G, share = warp % wph;
+        const size_t base = ((size_t)pair + i_first) * G;
+        float* sm_j = reinterpret_cast<float*>(smem);  // [kBWarps][kHeadDim + 2]
+        for (int g = warp / wph; g < G; g += kBWarps / wph) {
+          float M = kNegBig, l = 0.0f;
+          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + base + g;
+          const float4* po = reinterpret_cast<const float4*>(a.part_o + (base + g) * kHeadDim) + lane;
+          const int mine = (cnt - share + wph - 1) / wph;  // parts share + wph j
+          for (int j0 = 0; j0 < mine; j0 += 32) {
+            const bool on = j0 + lane < mine;
+            const float2 x = on ? __ldcg(ml + (size_t)(share + wph * (j0 + lane)) * G) : make_float2(kNegBig, 0.0f);
+            const float top = fmaxf(M, warp_max(x.x));
+            const float al = fast_exp2(M - top), wt = on ? fast_exp2(x.x - top) : 0.0f;
+            M = top;
+            l = l * al + warp_sum(wt * x.y);
+            o.x *= al; o.y *= al; o.z *= al; o.w *= al;
+            for (int i0 = 0; i0 < min(32, mine - j0); i0 += 8) {
+              float4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)  // past the end: the last part again, weight 0
+                y[i] = __ldcg(po + (size_t)(share + wph * min(j0 + i0 + i, mine - 1)) * G * (kHeadDim / 4));
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float w = __shfl_sync(0xffffffffu, wt, i0 + i);
+                if (j0 + i0 + i < mine) {
+                  o.x += w * y[i].x; o.y += w * y[i].y; o.z += w * y[i].z; o.w += w * y[i].w;
+                }
+              }
+            }
           }
-          orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(l != 0.0f ? o * (1.0f / l) : 0.0f));
+          if (wph > 1) {  // (kBWarps >= wph G: every warp with a head comes here once)
+            *reinterpret_cast<float4*>(sm_j + warp * kJoinRow + 4 * lane) = o;
+            if (lane == 0) {
+              sm_j[warp * kJoinRow + kHeadDim] = M;
+              sm_j[warp * kJoinRow + kHeadDim + 1] = l;
+            }
+          } else {
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            uint2 w;
+            w.x = pack_bf16x2(o.x * inv, o.y * inv);
+            w.y = pack_bf16x2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(out + ((size_t)bl * s.hq + h * G + g) * kHeadDim + 4 * lane) = w;
+          }
+        }
+        if (wph > 1) {
+          __syncthreads();
+          for (int g = 0; g < G; ++g) {
+            const float* row = sm_j + g * wph * kJoinRow;
+            float M = kNegBig, o = 0.0f, l = 0.0f;
+            for (int i = 0; i < wph; ++i) M = fmaxf(M, row[i * kJoinRow + kHeadDim]);
+            for (int i = 0; i < wph; ++i) {
+              const float wt = fast_exp2(row[i * kJoinRow + kHeadDim] - M);
+              o += wt * row[i * kJoinRow + d];
+              l += wt * row[i * kJoinRow + kHeadDim + 1];
+            }
+            orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(l != 0.0f ? o * (1.0f / l) : 0.0f));
+          }
         }
         if (threadIdx.x == 0) s.tickets[b * hkv + h] = 0;
       }

@@ -14,9 +14,8 @@
 namespace {
 
 constexpr size_t kAlign = 256;
-// As in the per-token cache's split: at least this many 16-token units per CTA
-// where the work would not fill the GPU anyway.
-constexpr int kMinUnitsPerCta = 32;
+constexpr int kMinUnitsPerCta = 16;  // 16-token units: a CTA's share of a pair
+constexpr int kWholePairUnits = 64;  // pairs up to this long are not cut to even out a wave
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -92,6 +91,33 @@ WsLayout ws_layout(const kvc_block_cache* c, int batch) {
   w.part_ml = align_up(slots * G * kvc::kHeadDim * 4);
   w.total = w.part_ml + align_up(slots * G * 2 * 4);
   return w;
+}
+
+// CTAs of an attention over `units` 16-token units of `pairs` (sequence, KV
+// head) pairs; any number is right for any lengths, so that a graph replayed at
+// other lengths stays right.  A CTA that ends inside a pair leaves a partial to
+// be joined (a store, a ticket and the last CTA's reads: about 5 us), so where
+// sequences are alike CTAs end with pairs:
+// - up to two CTAs per SM, k per pair of at least kMinUnitsPerCta units each
+//   (batch 8 x 8 KV heads, 1,000 tokens: 11.1 us at k = 4, 16.1 at 152 CTAs;
+//   1 x 8, 32,000: 18.9 at k = 38, 19.4 at 456 CTAs; 32 x 8, 8,192: 82.8 at one
+//   per pair, 90.5 at 456 CTAs);
+// - more pairs than that, and short: whole pairs per CTA (64 x 8, 352: 18.1 with
+//   two, 26.0 at 352 CTAs);
+// - more pairs, and long: one full wave, whatever it cuts (64 x 8, 4,000: 85.2;
+//   89.6 with two pairs per CTA, 107.6 with one).
+int grid_of(long long sms, long long per_sm, long long pairs, long long units) {
+  const long long wave = std::min(sms * per_sm, (long long)kvc::kMaxSplitCtas);
+  const long long per_pair = (units + pairs - 1) / pairs;
+  if (pairs <= std::min(2 * sms, wave)) {
+    const long long k = std::min(std::min(2 * sms, wave) / pairs, (per_pair + kMinUnitsPerCta - 1) / kMinUnitsPerCta);
+    return (int)(k * pairs);
+  }
+  if (per_pair <= kWholePairUnits) {
+    const long long m = (pairs + wave - 1) / wave;
+    return (int)((pairs + m - 1) / m);
+  }
+  return (int)wave;
 }
 
 int sm_count(kvc_block_cache* c) {
@@ -182,9 +208,12 @@ kvc_status kvc_block_buffer(const kvc_block_cache* c, int32_t which, void** d_pt
   return KVC_OK;
 }
 
-kvc_status kvc_block_length(const kvc_block_cache* c, int32_t seq, int32_t* positions) {
-  if (!c || seq < 0 || seq >= c->cfg.max_batch || !positions) return KVC_ERR_INVALID_ARG;
-  *positions = c->pos[seq];
+kvc_status kvc_block_lengths(const kvc_block_cache* c, int32_t seq_begin, int32_t batch, int32_t* shortest,
+                             int32_t* longest) {
+  if (!c || !range_ok(c, seq_begin, batch)) return KVC_ERR_INVALID_ARG;
+  const auto mm = std::minmax_element(c->pos.begin() + seq_begin, c->pos.begin() + seq_begin + batch);
+  if (shortest) *shortest = *mm.first;
+  if (longest) *longest = *mm.second;
   return KVC_OK;
 }
 
@@ -279,13 +308,7 @@ kvc_status kvc_block_attention(kvc_block_cache* c, int32_t seq_begin, int32_t ba
   a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + wl.part_ml);
   a.mod = kvc::make_score_mod(sm_scale, softcap, d_slopes);
   a.qk_scale_log2 = sm_scale * kvc::kLog2E;
-  // one wave of resident CTAs with at least kMinUnitsPerCta units each, but no
-  // fewer CTAs than SMs while each still gets 4 (any grid size is correct for
-  // any lengths, so a graph replayed at other lengths stays correct)
-  const long long sms = sm_count(c);
-  const long long want = std::max(units / kMinUnitsPerCta, std::min(sms, units / 4));
-  const long long wave = sms * kvc::block_attention_ctas_per_sm(c->dev, a.mod);
-  a.ncta = (int)std::max(1LL, std::min({wave, want, (long long)kvc::kMaxSplitCtas}));
+  a.ncta = grid_of(sm_count(c), kvc::block_attention_ctas_per_sm(c->dev, a.mod), batch * c->cfg.num_kv_heads, units);
   if (kvc::launch_block_attention(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
                                   static_cast<uint16_t*>(d_out), a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return KVC_ERR_CUDA;

@@ -8,11 +8,11 @@ import math
 import torch
 
 from . import _lib as L
-from .cache import HEAD_DIM, _need, _stream_ptr
+from .cache import HEAD_DIM, _current_device, _need, _stream_ptr
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr() if t is not None else None)
+    return t.data_ptr() if t is not None else None
 
 
 def _slopes(slopes, num_q_heads, device):
@@ -56,17 +56,24 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, statu
         out = torch.empty_like(q)
     _need(out, torch.bfloat16, "out", dev, q.shape)
     lib = L.lib()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            # (the caching allocator's blocks are 512-byte aligned)
-            nbytes = lib.kvc_prompt_workspace_bytes(batch, hq, hkv, n, sums is not None)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _need(workspace, torch.uint8, "workspace", dev)
-        scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
-        params = L.KvcPromptParams(batch, hq, hkv, n, scale, softcap, _ptr(slopes), _ptr(key_begin), _ptr(key_end))
-        L.check(lib.kvc_prompt_attention(ctypes.byref(params), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(sums),
-                                         _ptr(status), _ptr(workspace), workspace.numel(),
-                                         ctypes.c_void_p(_stream_ptr(stream))), "kvc_prompt_attention")
+    if workspace is None:
+        # (the caching allocator's blocks are 512-byte aligned)
+        nbytes = lib.kvc_prompt_workspace_bytes(batch, hq, hkv, n, sums is not None)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _need(workspace, torch.uint8, "workspace", dev)
+    scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
+    params = L.KvcPromptParams(batch, hq, hkv, n, scale, softcap, _ptr(slopes), _ptr(key_begin), _ptr(key_end))
+
+    def call():
+        L.check(lib.kvc_prompt_attention(ctypes.byref(params), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                         _ptr(sums), status.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                         _stream_ptr(stream)), "kvc_prompt_attention")
+
+    if _current_device() == dev.index:
+        call()
+    else:
+        with torch.cuda.device(dev):
+            call()
     return out if sums is None else (out, sums)
 
 

@@ -601,7 +601,8 @@ kvc_status kvc_block_cache_create(const kvc_block_config* cfg, void* d_state, si
 void kvc_block_cache_destroy(kvc_block_cache* cache);
 kvc_status kvc_block_cache_reset(kvc_block_cache* cache, void* stream);
 kvc_status kvc_block_buffer(const kvc_block_cache* cache, int32_t which, void** d_ptr, size_t* bytes);
-kvc_status kvc_block_length(const kvc_block_cache* cache, int32_t seq, int32_t* positions);
+kvc_status kvc_block_lengths(const kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t* shortest,
+                             int32_t* longest); /* tokens held, least and most of the slice (either may be null) */
 kvc_status kvc_block_sync_host(kvc_block_cache* cache, void* stream);
 kvc_status kvc_block_read_status(kvc_block_cache* cache, int32_t* h_status, void* stream);
 int32_t kvc_block_last_launch_count(const kvc_block_cache* cache);

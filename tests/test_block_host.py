@@ -65,8 +65,8 @@ def test_block_calls(lib):
     assert L.kvc_block_buffer(h, 0, ctypes.byref(ptr), ctypes.byref(nb)) == lib.KVC_OK
     assert ptr.value == buf.addr and nb.value == 3 * 2 * 16 * 128
     assert L.kvc_block_buffer(h, 11, ctypes.byref(ptr), ctypes.byref(nb)) == lib.KVC_ERR_INVALID_ARG
-    assert L.kvc_block_length(h, 1, ctypes.byref(v)) == lib.KVC_OK and v.value == 0
-    assert L.kvc_block_length(h, 2, ctypes.byref(v)) == lib.KVC_ERR_INVALID_ARG
+    assert L.kvc_block_lengths(h, 1, 1, ctypes.byref(v), None) == lib.KVC_OK and v.value == 0
+    assert L.kvc_block_lengths(h, 1, 2, ctypes.byref(v), None) == lib.KVC_ERR_INVALID_ARG
     bad = lib.KVC_ERR_INVALID_ARG
     assert L.kvc_block_append(None, 0, 1, 1, p, p, None) == bad
     for args, want in [((1, 2, 1), bad), ((0, 1, -1), bad), ((-1, 1, 1), bad), ((0, 0, 1), bad),
