@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kvc_block.h"
@@ -27,149 +28,236 @@ using namespace quant;
 __host__ __device__ constexpr int kExactRows(int bt) { return kSinks + bt; }
 
 // ------------------------------------------------------------------- append
-// One launch.  A CTA takes 128 body rows (128 / bt blocks) of one (sequence,
-// KV head, K or V); a warp holds its 16 rows in registers (8 loads of 16 bytes
-// a lane in flight), so every value is read once and the block's maximum
-// needs no second pass; bt / 16 warps share a block's maximum through shared
-// memory.  Bound by DRAM: 2 bytes read and 1 written a value.
+// One launch.  The work is tiles of 128 body rows (128 / bt blocks) of one
+// (sequence, KV head, K or V), of which every resident CTA takes an equal run.
+// A warp has 16 rows of a tile; its rows of the next tiles are on their way to
+// shared memory (cp.async, each lane reads back what it copied itself), so the
+// loads do not wait for the quantisation: first the block's maximum (bt / 16
+// warps share one through a named barrier), then the codes.  Bound by DRAM: 2
+// bytes read and 1 written a value.
 //
-// Every CTA derives the blocks its sequence takes from the lengths alone
-// (the free stack's top and an exclusive prefix of the blocks that the slice's
+// Every CTA derives the blocks its sequences take from the lengths alone (the
+// free stack's top and an exclusive prefix of the blocks that the slice's
 // earlier sequences complete), so no CTA waits for an allocation; the CTA that
 // finishes last (an atomic ticket) advances the lengths and the stack.  A
 // block's first rows may lie in the open block's buffer, which the rows left
-// over after the last completed block overwrite: the CTA of the first block
-// writes those rows, after it has read its own.
+// over after the last completed block overwrite: the CTA of a pair's first
+// tile, the only one with rows of that buffer, writes the rows left over once
+// the tile is in shared memory.
 constexpr int kAppThreads = 256;
-constexpr int kAppRows = 128;
+constexpr int kAppWarps = kAppThreads / 32;
+constexpr int kAppRows = 16 * kAppWarps;
+constexpr int kAppStages = 2;
+constexpr int kAppCtas = 3;  // per SM; with three stages and two CTAs 299 us where this takes 276
+constexpr int kAppStage = 16 * kHeadDim * 2 + 128;  // a warp's rows, and a lane's copy of the block's id
+constexpr int kAppSmem = kAppWarps * kAppStages * kAppStage;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
 
 template <bool FP8>
-__global__ void __launch_bounds__(kAppThreads, 4) block_append_kernel(BlockState s, int seq_begin, int batch, int n_new,
+__global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(BlockState s, int seq_begin, int batch, int n_new,
+                                                                      int tiles_per_pair,
                                                                       const uint16_t* __restrict__ kin,
                                                                       const uint16_t* __restrict__ vin) {
-  __shared__ int sh_before, sh_total, sh_bad, sh_last;
-  __shared__ float sh_amax[kAppThreads / 32];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int before[kMaxCallBatch], held[kMaxCallBatch];  // blocks completed before it; its length
+  __shared__ int sh_total, sh_bad, sh_last;
+  __shared__ float sh_amax[2][kAppWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hkv = s.hkv, bt = s.bt;
-  const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, bl = blockIdx.z;
-  const int b = seq_begin + bl;
   const int top = s.counters[kCtrFreeTop];
   if (warp == 0) {
-    // blocks completed by the sequences before this one, and by all
-    int before = 0, total = 0, bad = 0;
-    for (int i = lane; i < batch; i += 32) {
-      const int P = s.seq_pos[seq_begin + i];
-      const int c0 = block_closed(P, bt), c1 = block_closed(P + n_new, bt);
-      if (i < bl) before += c1 - c0;
-      total += c1 - c0;
+    int total = 0, bad = 0;
+    for (int base = 0; base < batch; base += 32) {
+      const int i = base + lane;
+      const int P = i < batch ? s.seq_pos[seq_begin + i] : 0;
+      const int c1 = i < batch ? block_closed(P + n_new, bt) : 0, nb = i < batch ? c1 - block_closed(P, bt) : 0;
       bad |= c1 > s.max_bps;
+      int v = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (i < batch) {
+        before[i] = total + v - nb;
+        held[i] = P;
+      }
+      total += __shfl_sync(0xffffffffu, v, 31);
     }
-    before = __reduce_add_sync(0xffffffffu, before);
-    total = __reduce_add_sync(0xffffffffu, total);
-    bad = __reduce_or_sync(0xffffffffu, (unsigned)bad);
+    bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-      sh_before = before;
       sh_total = total;
       sh_bad = (bad ? kDevTableOverflow : 0) | (total > top || top > s.num_blocks ? kDevOutOfBlocks : 0);
     }
   }
-  const int P = s.seq_pos[b];
   __syncthreads();
   const bool ok = sh_bad == 0;  // the same for every CTA
   if (ok) {
-    const int c0 = block_closed(P, bt), nb = block_closed(P + n_new, bt) - c0;
-    const int wpb = bt / 16;  // warps per block
-    const uint16_t* in = (kv ? vin : kin) + ((size_t)bl * hkv + h) * n_new * kHeadDim;
-    uint16_t* exact = (kv ? s.v_exact : s.k_exact) + ((size_t)b * hkv + h) * kExactRows(bt) * kHeadDim;
-    // this warp's 16 rows: body rows row0.. of the sequence's new blocks
-    const int row0 = blockIdx.x * kAppRows + warp * 16;
-    const int c = row0 / bt;  // new block
-    const bool live = c < nb;
-    uint4 w[8];
-    float amax = 0.0f;
-    if (live) {
-      const int p0 = kSinks + c0 * bt + row0;  // position of the warp's first row
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int p = p0 + 2 * i + (lane >> 4);
-        const uint16_t* src =
-            p < P ? exact + (size_t)(kSinks + (p - kSinks) % bt) * kHeadDim : in + (size_t)(p - P) * kHeadDim;
-        w[i] = reinterpret_cast<const uint4*>(src)[lane & 15];
+    const long long T = 2LL * batch * hkv * tiles_per_pair;
+    const long long t0 = (long long)blockIdx.x * T / gridDim.x;
+    const int n_my = (int)((long long)(blockIdx.x + 1) * T / gridDim.x - t0);
+    const int wpb = bt / 16, w0 = warp & ~(wpb - 1);  // warps per block, the block's first
+    uint8_t* ring = smem + warp * kAppStages * kAppStage + 16 * lane;
+    const uint8_t* ring_id = smem + warp * kAppStages * kAppStage + 16 * kHeadDim * 2 + 4 * lane;
+    const uint32_t ring_s = smem_u32(ring), ring_id_s = smem_u32(ring_id);
+    const size_t exact_rows = kExactRows(bt);
+
+    const int sh = __ffs(bt) - 1;  // (bt is a power of two)
+    auto closed_at = [&](int P) { return P > kSinks ? (P - kSinks) >> sh : 0; };
+
+    // a tile: the x-th of sequence bl's K (kv = 0) or V of KV head h
+    struct Tile {
+      int bl, h, kv, x;
+    };
+    auto advance = [&](Tile& t) {
+      if (++t.x == tiles_per_pair) {
+        t.x = 0;
+        t.kv ^= 1;
+        if (t.kv == 0 && ++t.h == hkv) {
+          t.h = 0;
+          ++t.bl;
+        }
       }
-      __nv_bfloat162 mx = __floats2bfloat162_rn(0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[e])));
-      }
-      amax = fmaxf(__low2float(mx), __high2float(mx));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    };
+    Tile cur;
+    {
+      const long long pair = t0 / tiles_per_pair;
+      cur.x = (int)(t0 % tiles_per_pair);
+      cur.kv = (int)(pair & 1);
+      cur.h = (int)(pair / 2 % hkv);
+      cur.bl = (int)(pair / 2 / hkv);
     }
-    if (lane == 0) sh_amax[warp] = amax;
-    __syncthreads();  // the block's maxima; the open block's rows are in registers
-    if (live) {
-      if (wpb > 1) {
-        const int w0 = warp / wpb * wpb;
-        for (int i = w0; i < w0 + wpb; ++i) amax = fmaxf(amax, sh_amax[i]);
+
+    // the copies of the CTA's next tile
+    int i_next = 0, st_next = 0;
+    Tile nxt = cur;
+    auto issue = [&]() {
+      if (i_next < n_my) {
+        const int P = held[nxt.bl];
+        const int c0 = closed_at(P), nb = closed_at(P + n_new) - c0;
+        const long long row0 = (long long)nxt.x * kAppRows + warp * 16;
+        if (row0 < (long long)nb << sh) {
+          const size_t pair = (size_t)nxt.bl * hkv + nxt.h;
+          const int p0 = kSinks + (c0 << sh) + (int)row0 + (lane >> 4);  // the lane's first row
+          const uint16_t* in =
+              (nxt.kv ? vin : kin) + (pair * n_new + (p0 - P)) * (ptrdiff_t)kHeadDim + 8 * (lane & 15);
+          if (nxt.x == 0) {  // may begin in the open block's rows
+            const uint16_t* exact = (nxt.kv ? s.v_exact : s.k_exact) +
+                                    (((size_t)seq_begin * hkv + pair) * exact_rows + kSinks) * kHeadDim + 8 * (lane & 15);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int p = p0 + 2 * i;
+              cp_async16(ring_s + st_next * kAppStage + 512 * i,
+                         p < P ? exact + (size_t)((p - kSinks) & (bt - 1)) * kHeadDim : in + 2 * i * kHeadDim);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cp_async16(ring_s + st_next * kAppStage + 512 * i, in + 2 * i * kHeadDim);
+          }
+          cp_async4(ring_id_s + st_next * kAppStage, s.free_stack + (top - 1 - (before[nxt.bl] + ((int)row0 >> sh))));
+        }
+        ++i_next;
+        st_next = st_next + 1 == kAppStages ? 0 : st_next + 1;
+        advance(nxt);
       }
-      const float scale = __fdiv_rn(amax, FP8 ? 448.0f : 127.0f);
-      const float inv = rcp_approx_ftz(scale);
-      const bool exact_div = !(scale >= 0x1p-126f && scale < INFINITY);
-      const int blk = s.free_stack[top - 1 - (sh_before + c)];
-      if ((unsigned)blk < (unsigned)s.num_blocks) {
-        const size_t hb = (size_t)blk * hkv + h;
-        uint8_t* dst = (kv ? s.v_codes : s.k_codes) + (hb * bt + row0 % bt) * kHeadDim + 8 * (lane & 15);
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kAppStages - 1; ++i) issue();
+
+    int st = 0, flip = 0;
+#pragma unroll 1
+    for (int j = 0; j < n_my; ++j) {
+      issue();
+      cp_async_wait<kAppStages - 1>();
+      __syncwarp();
+      const int bl = cur.bl, h = cur.h, kv = cur.kv, b = seq_begin + bl, P = held[bl];
+      const int c0 = closed_at(P), nb = closed_at(P + n_new) - c0;
+      const long long row0 = (long long)cur.x * kAppRows + warp * 16;
+      const bool live = row0 < (long long)nb << sh;
+      const int c = live ? (int)row0 >> sh : 0;
+      const uint8_t* rows = ring + st * kAppStage;
+      float amax = 0.0f;
+      if (live) {
+        __nv_bfloat162 mx = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t wd[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          float x[8];
+          const uint4 w = *reinterpret_cast<const uint4*>(rows + 512 * i);
+          const uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(wd[e] << 16);
-            x[2 * e + 1] = __uint_as_float(wd[e] & 0xFFFF0000u);
-          }
-          uint2 o;
-          if (FP8) {
-            o.x = e4m3_codes4(x, scale, inv, exact_div);
-            o.y = e4m3_codes4(x + 4, scale, inv, exact_div);
-          } else {
-            uint32_t wc[8];
-            int_codes8<8>(x, scale, inv, wc);
-            o = make_uint2(low_bytes(wc[0], wc[1], wc[2], wc[3]), low_bytes(wc[4], wc[5], wc[6], wc[7]));
-          }
-          *reinterpret_cast<uint2*>(dst + (size_t)(2 * i + (lane >> 4)) * kHeadDim) = o;
+          for (int e = 0; e < 4; ++e) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[e])));
         }
-        if (row0 % bt == 0 && lane == 0) {
-          (kv ? s.v_scale : s.k_scale)[hb] = scale;
-          if (blockIdx.y == 0) s.table[(size_t)b * s.max_bps + c0 + c] = blk;
+        amax = fmaxf(__low2float(mx), __high2float(mx));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (wpb > 1) {  // (a block's warps are all live or none)
+          if (lane == 0) sh_amax[flip][warp] = amax;
+          named_sync(1 + w0, 32 * wpb);
+          for (int i = w0; i < w0 + wpb; ++i) amax = fmaxf(amax, sh_amax[flip][i]);
+          flip ^= 1;  // the next maxima go beside these, which a slower warp may still read
         }
-      } else if (lane == 0) {
-        atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
       }
-    }
-    if (blockIdx.x == 0) {
-      // sinks, and the rows of the block that stays open
-      const int open0 = kSinks + (c0 + nb) * bt;
-      const int n_sink = max(0, min(kSinks - P, n_new));
-      const int first = min(max(open0 - P, n_sink), n_new);  // first new token of the open block
-      for (int r = threadIdx.x >> 4; r < n_sink + (n_new - first); r += kAppThreads / 16) {
-        const int i = r < n_sink ? r : first + (r - n_sink);
-        const int p = P + i;
-        const int row = p < kSinks ? p : kSinks + (p - kSinks) % bt;
-        reinterpret_cast<uint4*>(exact + (size_t)row * kHeadDim)[threadIdx.x & 15] =
-            reinterpret_cast<const uint4*>(in + (size_t)i * kHeadDim)[threadIdx.x & 15];
+      if (cur.x == 0) {
+        // sinks, and the rows of the block that stays open, now that the first
+        // block's rows are in shared memory
+        __syncthreads();
+        const uint16_t* in = (kv ? vin : kin) + ((size_t)bl * hkv + h) * n_new * kHeadDim;
+        uint16_t* exact = (kv ? s.v_exact : s.k_exact) + ((size_t)b * hkv + h) * exact_rows * kHeadDim;
+        const int open0 = kSinks + ((c0 + nb) << sh);
+        const int n_sink = max(0, min(kSinks - P, n_new));
+        const int first = min(max(open0 - P, n_sink), n_new);  // first new token of the open block
+#pragma unroll 4
+        for (int r = threadIdx.x >> 4; r < n_sink + (n_new - first); r += kAppThreads / 16) {
+          const int i = r < n_sink ? r : first + (r - n_sink);
+          const int p = P + i;
+          const int row = p < kSinks ? p : kSinks + ((p - kSinks) & (bt - 1));
+          reinterpret_cast<uint4*>(exact + (size_t)row * kHeadDim)[threadIdx.x & 15] =
+              reinterpret_cast<const uint4*>(in + (size_t)i * kHeadDim)[threadIdx.x & 15];
+        }
       }
+      if (live) {
+        const float scale = __fdiv_rn(amax, FP8 ? 448.0f : 127.0f);
+        const float inv = rcp_approx_ftz(scale);
+        const bool exact_div = !(scale >= 0x1p-126f && scale < INFINITY);
+        const int blk = *reinterpret_cast<const int*>(ring_id + st * kAppStage);
+        if ((unsigned)blk < (unsigned)s.num_blocks) {
+          const size_t hblk = (size_t)blk * hkv + h;
+          const int in_block = (int)row0 & (bt - 1);
+          uint8_t* dst = (kv ? s.v_codes : s.k_codes) + ((hblk << sh) + in_block + (lane >> 4)) * kHeadDim +
+                         8 * (lane & 15);
+#pragma unroll 4
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint2*>(dst + 2 * i * kHeadDim) =
+                block_codes8<FP8>(*reinterpret_cast<const uint4*>(rows + 512 * i), scale, inv, exact_div);
+          if (in_block == 0 && lane == 0) {
+            (kv ? s.v_scale : s.k_scale)[hblk] = scale;
+            if (h == 0 && kv == 0) s.table[(size_t)b * s.max_bps + c0 + c] = blk;
+          }
+        } else if (lane == 0) {
+          atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
+        }
+      }
+      st = st + 1 == kAppStages ? 0 : st + 1;
+      advance(cur);
     }
+    cp_async_wait<0>();
   }
   // the last CTA advances the lengths and the stack (every CTA has read them)
   __syncthreads();
   int32_t* ticket = s.tickets + s.max_batch * hkv;
   if (threadIdx.x == 0) {
     __threadfence();
-    const int all = gridDim.x * gridDim.y * gridDim.z;
-    sh_last = atomicAdd(ticket, 1) == all - 1;
+    sh_last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!sh_last) return;
@@ -1005,6 +1093,21 @@ int block_attn_ctas_mod(int mod) {
   }
 }
 
+template <bool FP8>
+cudaError_t append_launch(const BlockState& s, int seq_begin, int batch, int n_new, int tpp, long long tiles,
+                          const uint16_t* k, const uint16_t* v, cudaStream_t st) {
+  static int done[64] = {0};
+  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(block_append_kernel<FP8>), kAppSmem, done);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  const int grid = (int)std::min(tiles, (long long)kAppCtas * sms);
+  block_append_kernel<FP8><<<grid, kAppThreads, kAppSmem, st>>>(s, seq_begin, batch, n_new, tpp, k, v);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 int block_attention_ctas_per_sm(const BlockState& s, const ScoreMod& mod) {
@@ -1021,12 +1124,10 @@ cudaError_t launch_block_append(const BlockState& s, int seq_begin, int batch, i
                                 const uint16_t* v, cudaStream_t st) {
   // rows of the most blocks an append of n_new tokens completes (at any state)
   const long long rows = ((long long)n_new + s.bt - 1) / s.bt * s.bt;
-  const dim3 grid((unsigned)((rows + kAppRows - 1) / kAppRows), 2 * s.hkv, batch);
-  if (s.fp8)
-    block_append_kernel<true><<<grid, kAppThreads, 0, st>>>(s, seq_begin, batch, n_new, k, v);
-  else
-    block_append_kernel<false><<<grid, kAppThreads, 0, st>>>(s, seq_begin, batch, n_new, k, v);
-  return cudaGetLastError();
+  const int tpp = (int)((rows + kAppRows - 1) / kAppRows);
+  const long long tiles = 2LL * batch * s.hkv * tpp;
+  return s.fp8 ? append_launch<true>(s, seq_begin, batch, n_new, tpp, tiles, k, v, st)
+               : append_launch<false>(s, seq_begin, batch, n_new, tpp, tiles, k, v, st);
 }
 
 cudaError_t launch_block_release(const BlockState& s, int seq_begin, int batch, cudaStream_t st) {

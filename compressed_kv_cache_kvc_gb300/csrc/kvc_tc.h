@@ -211,6 +211,12 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// NaN if any of the three is
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // 32 columns of this thread's TMEM lane, on their way: the registers hold them
 // after tmem_wait (which takes them as operands, so no use moves before it).
