@@ -125,12 +125,17 @@ class BlockScaledCache:
         _need(q, torch.bfloat16, "q", self.device)
         if q.dim() != 3 or q.shape[1] != self.num_q_heads or q.shape[2] != HEAD_DIM:
             raise ValueError("q must be [batch, num_q_heads, 128]")
-        _slopes(slopes, self.num_q_heads, self.device)
+        if slopes is not None:
+            _slopes(slopes, self.num_q_heads, self.device)
         if out is None:
             out = torch.empty_like(q)
-        _need(out, torch.bfloat16, "out", self.device, q.shape)
-        ws = self.workspace(q.shape[0]) if workspace is None else workspace
-        _need(ws, torch.uint8, "workspace", self.device)
+        else:
+            _need(out, torch.bfloat16, "out", self.device, q.shape)
+        if workspace is None:
+            ws = self.workspace(q.shape[0])
+        else:
+            ws = workspace
+            _need(ws, torch.uint8, "workspace", self.device)
         scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
         self._call("kvc_block_attention", seq_begin, q.shape[0], _ptr(q), _ptr(out), scale,
                    softcap, _ptr(slopes), _ptr(ws), ws.numel(), stream=stream)
@@ -160,8 +165,11 @@ class BlockScaledCache:
             if batch < 1 or n < 1:
                 raise ValueError("batch and n must be positive")
             make = torch.empty if pos_begin + n <= least else torch.zeros
-            out = tuple(make(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
-        for name, t in zip(("k", "v"), out):
-            _need(t, torch.bfloat16, name, self.device, shape)
-        self._call("kvc_block_read", seq_begin, batch, pos_begin, n, _ptr(out[0]), _ptr(out[1]), stream=stream)
-        return tuple(out)
+            k = make(shape, dtype=torch.bfloat16, device=self.device)
+            v = make(shape, dtype=torch.bfloat16, device=self.device)
+        else:
+            k, v = out
+            _need(k, torch.bfloat16, "k", self.device, shape)
+            _need(v, torch.bfloat16, "v", self.device, shape)
+        self._call("kvc_block_read", seq_begin, batch, pos_begin, n, k.data_ptr(), v.data_ptr(), stream=stream)
+        return k, v

@@ -40,7 +40,7 @@ def _need(t: torch.Tensor, dtype, name: str, device=None, shape=None):
         raise ValueError(f"{name} must be a contiguous CUDA tensor of dtype {dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 

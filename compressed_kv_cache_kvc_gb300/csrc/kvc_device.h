@@ -12,6 +12,13 @@
 namespace kvc {
 namespace dev {
 
+// Programmatic launch order: a kernel launched with programmatic stream
+// serialisation starts once every CTA of the kernel before it has called
+// launch_dependents (or ended); wait_for_previous returns when that kernel has
+// completed and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr float kNegBig = -1.0e30f;
 
 __device__ __forceinline__ float fast_exp2(float x) {

@@ -115,6 +115,7 @@ constexpr int kPrepThreads = 256;
 __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a, const uint16_t* __restrict__ v) {
   __shared__ uint32_t sh_bad[4];
   __shared__ int sh_run[4];
+  launch_dependents();
   const int tiles = (a.n + kTile - 1) / kTile;
   const int tile = blockIdx.x % tiles, plane = blockIdx.x / tiles, tid = threadIdx.x, lane = tid & 31;
   const int k0 = tile * kTile, rows = min(kTile, a.n - k0);
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           tma_load_3d(dst, &tm_k, 0, j * kKeys, plane_kv, b);
           tma_load_3d(dst + kKeyBox, &tm_k, 64, j * kKeys, plane_kv, b);
         }
+        if (r == 2) wait_for_previous();  // V in fp16
         if (r >= 2) {
           const uint32_t dst = base + kFOffV + ((r - 2) & 3) * kKeyB;
           tma_load_3d(dst, &tm_v, 0, (j + 2) * kKeys, plane_kv, b);
@@ -473,6 +475,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool ok = true, poison = false;
     // whether any V row of the tiles ahead is not finite (under the first loads:
     // a mask read in the loop would put a global load's latency into every tile)
+    wait_for_previous();
     uint32_t any_bad = 0;
     for (int j = 2 * lo + lane; j < 2 * hi; j += 32)
       if (32 * j < n) any_bad |= a.bad[bad_row + j];
@@ -919,8 +922,18 @@ cudaError_t launch_fwd(const PromptArgs& a, const CUtensorMap& q, const CUtensor
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_fwd_kernel<CAP, BIAS>), kFwdSmem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.n + kFwdBlock - 1) / kFwdBlock, a.hq, a.batch);
-  prompt_fwd_kernel<CAP, BIAS><<<grid, kFwdThreads, kFwdSmem, st>>>(a, q, k, v);
-  return cudaGetLastError();
+  // may start while the prep kernel's last CTAs run (wait_for_previous)
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kFwdThreads);
+  cfg.dynamicSmemBytes = kFwdSmem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_fwd_kernel<CAP, BIAS>, a, q, k, v);
 }
 
 template <bool CAP, bool BIAS>

@@ -32,48 +32,52 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, statu
     (float32 [Hq]).  column_sums: True, or a float32 [batch, Hkv, n] tensor,
     returns (out, sums) with every key's sum of probabilities.  status: int32
     [1], zeroed by the caller; KVC_DEV_* bits are or'ed into it."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != HEAD_DIM:
+    bf16 = torch.bfloat16
+    _need(q, bf16, "q")
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
         raise ValueError("q must be [batch, num_q_heads, n, 128]")
-    _need(q, torch.bfloat16, "q")
     dev = q.device
-    batch, hq, n = q.shape[0], q.shape[1], q.shape[2]
-    _need(k, torch.bfloat16, "k", dev)
-    if k.dim() != 4 or k.shape[0] != batch or k.shape[2] != n or k.shape[3] != HEAD_DIM or k.shape[1] < 1 or \
-            hq % k.shape[1] != 0:
+    batch, hq, n, _ = q.shape
+    _need(k, bf16, "k", dev)
+    hkv = k.shape[1] if k.dim() == 4 else 0
+    if hkv < 1 or hq % hkv != 0 or k.shape != (batch, hkv, n, HEAD_DIM):
         raise ValueError("k, v must be [batch, num_kv_heads, n, 128], num_kv_heads a divisor of num_q_heads")
-    hkv = k.shape[1]
-    _need(v, torch.bfloat16, "v", dev, k.shape)
+    _need(v, bf16, "v", dev, k.shape)
     _need(status, torch.int32, "status", dev, (1,))
-    _slopes(slopes, hq, dev)
-    for name, t in (("key_begin", key_begin), ("key_end", key_end)):
-        if t is not None:
-            _need(t, torch.int32, name, dev, (batch, n))
+    if slopes is not None:
+        _slopes(slopes, hq, dev)
+    if key_begin is not None:
+        _need(key_begin, torch.int32, "key_begin", dev, (batch, n))
+    if key_end is not None:
+        _need(key_end, torch.int32, "key_end", dev, (batch, n))
     sums = None
-    if column_sums is not False:
-        sums = torch.empty(batch, hkv, n, dtype=torch.float32, device=dev) if column_sums is True else column_sums
+    if column_sums is True:
+        sums = torch.empty(batch, hkv, n, dtype=torch.float32, device=dev)
+    elif column_sums is not False:
+        sums = column_sums
         _need(sums, torch.float32, "column_sums", dev, (batch, hkv, n))
     if out is None:
         out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out", dev, q.shape)
+    else:
+        _need(out, bf16, "out", dev, q.shape)
     lib = L.lib()
     if workspace is None:
         # (the caching allocator's blocks are 512-byte aligned)
-        nbytes = lib.kvc_prompt_workspace_bytes(batch, hq, hkv, n, sums is not None)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _need(workspace, torch.uint8, "workspace", dev)
+        ws_bytes = lib.kvc_prompt_workspace_bytes(batch, hq, hkv, n, sums is not None)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, torch.uint8, "workspace", dev)
+        ws_bytes = workspace.numel()
     scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
     params = L.KvcPromptParams(batch, hq, hkv, n, scale, softcap, _ptr(slopes), _ptr(key_begin), _ptr(key_end))
-
-    def call():
-        L.check(lib.kvc_prompt_attention(ctypes.byref(params), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                         _ptr(sums), status.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                         _stream_ptr(stream)), "kvc_prompt_attention")
-
+    args = (ctypes.byref(params), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(sums),
+            status.data_ptr(), workspace.data_ptr(), ws_bytes)
     if _current_device() == dev.index:
-        call()
+        st = lib.kvc_prompt_attention(*args, _stream_ptr(stream))
     else:
         with torch.cuda.device(dev):
-            call()
+            st = lib.kvc_prompt_attention(*args, _stream_ptr(stream))
+    L.check(st, "kvc_prompt_attention")
     return out if sums is None else (out, sums)
 
 
