@@ -676,6 +676,38 @@ constexpr int kSBarK = 0, kSBarFull = 1, kSBarEmpty = 3, kSBarS = 5, kSBarSfree 
 constexpr int kSumSmem = kSOffBar + 8 * kSNumBars + 16;
 constexpr uint32_t kSumCols = 256;
 
+// The (query head, query tile) blocks some of whose queries see the keys [k0,
+// k1), in order, for a warp: 32 tiles' bounds are read at a time, one a lane (a
+// load per tile would put its latency into every block).
+struct SeenBlocks {
+  const int4* runs;
+  int tiles, heads, k0, k1, lane;
+  int g, qt, base;
+  uint32_t left, whole;
+  bool all;  // every query of the block sees every key
+  __device__ SeenBlocks(const int4* r, int t, int G, int a, int b, int l)
+      : runs(r), tiles(t), heads(G), k0(a), k1(b), lane(l), g(0), qt(0), base(-32), left(0), whole(0), all(false) {}
+  __device__ bool next() {
+    while (left == 0) {
+      base += 32;
+      if (base >= tiles) {
+        base = -32;
+        if (++g >= heads) return false;
+        continue;
+      }
+      const int4 r = base + lane < tiles ? runs[base + lane] : make_int4(INT_MAX, 0, 0, 0);
+      const bool sees = r.x < k1 && r.y > k0;
+      left = __ballot_sync(0xffffffffu, sees);
+      whole = __ballot_sync(0xffffffffu, r.z <= k0 && r.w >= k1);
+    }
+    const int b = __ffs(left) - 1;
+    left &= left - 1;
+    qt = base + b;
+    all = (whole >> b) & 1u;
+    return true;
+  }
+};
+
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kSumThreads, 2)
     prompt_sums_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
@@ -689,11 +721,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int k0 = kt * kTile, k1 = min(k0 + kTile, n);
   const int tiles = gridDim.x;
-  const int4* runs = a.runs + (size_t)bl * tiles;
-  auto seen = [&](int qt) {
-    const int4 r = runs[qt];
-    return r.x < k1 && r.y > k0;
-  };
+  SeenBlocks blk(a.runs + (size_t)bl * tiles, tiles, G, k0, k1, lane);
 
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kSumCols));
@@ -724,43 +752,52 @@ __global__ void __launch_bounds__(kSumThreads, 2)
       tma_load_3d(base + kSOffK + kBoxB, &tm_k, 64, k0, bl * a.hkv + h, bar(kSBarK));
     }
     int it = 0;
-    bool ok = true;
-    for (int g = 0; g < G && ok; ++g) {
-      const int plane = bl * a.hq + h * G + g;
-      for (int qt = 0; qt < tiles && ok; ++qt) {
-        if (!seen(qt)) continue;
-        const int x = it & 1;
-        if (it >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(kSBarEmpty + x), (uint32_t)(((it - 2) >> 1) & 1), abort))) {
-          set_abort(a.status, abort);
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t dst = base + kSOffQ + x * kTileB, b = bar(kSBarFull + x);
-          bar_expect_tx(b, kTileB);
-          tma_load_3d(dst, &tm_q, 0, qt * kTile, plane, b);
-          tma_load_3d(dst + kBoxB, &tm_q, 64, qt * kTile, plane, b);
-        }
-        float* st = reinterpret_cast<float*>(ssm + kSOffStat) + x * 2 * kTile;
-        int2* rn = reinterpret_cast<int2*>(ssm + kSOffRun) + x * kTile;
+    // the statistics and runs of a block, read while the one before is waited for
+    float2 s[kTile / 32];
+    int2 r[kTile / 32];
+    auto read = [&]() {
+      const int plane = bl * a.hq + h * G + blk.g;
 #pragma unroll
-        for (int e = 0; e < kTile / 32; ++e) {
-          const int i = lane + 32 * e, qi = qt * kTile + i;
-          float2 s = make_float2(INFINITY, 0.0f);  // past the prompt: p = 2^-inf
-          int2 r = make_int2(0, 0);
-          if (qi < n) {
-            s = *reinterpret_cast<const float2*>(a.stats + ((size_t)plane * n + qi) * 2);
-            s = s.y != 0.0f ? make_float2(s.x, 1.0f / s.y) : make_float2(INFINITY, 0.0f);
-            r = run_of(a, bl, qi);
-          }
-          st[i] = -s.x;
-          st[kTile + i] = s.y;
-          rn[i] = r;
+      for (int e = 0; e < kTile / 32; ++e) {
+        const int qi = blk.qt * kTile + lane + 32 * e;
+        s[e] = make_float2(INFINITY, 0.0f);  // past the prompt: p = 2^-inf
+        r[e] = make_int2(0, 0);
+        if (qi < n) {
+          s[e] = *reinterpret_cast<const float2*>(a.stats + ((size_t)plane * n + qi) * 2);
+          r[e] = run_of(a, bl, qi);
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(kSBarFull + x));
-        ++it;
       }
+    };
+    bool more = blk.next();
+    if (more) read();
+    while (more) {
+      const int x = it & 1;
+      if (it >= 2 && !__all_sync(0xffffffffu, bar_wait(bar(kSBarEmpty + x), (uint32_t)(((it - 2) >> 1) & 1), abort))) {
+        set_abort(a.status, abort);
+        break;
+      }
+      if (lane == 0) {
+        const int plane = bl * a.hq + h * G + blk.g;
+        const uint32_t dst = base + kSOffQ + x * kTileB, b = bar(kSBarFull + x);
+        bar_expect_tx(b, kTileB);
+        tma_load_3d(dst, &tm_q, 0, blk.qt * kTile, plane, b);
+        tma_load_3d(dst + kBoxB, &tm_q, 64, blk.qt * kTile, plane, b);
+      }
+      float* st = reinterpret_cast<float*>(ssm + kSOffStat) + x * 2 * kTile;
+      int2* rn = reinterpret_cast<int2*>(ssm + kSOffRun) + x * kTile;
+#pragma unroll
+      for (int e = 0; e < kTile / 32; ++e) {
+        const int i = lane + 32 * e;
+        const bool some = s[e].y != 0.0f;
+        st[i] = some ? -s[e].x : -INFINITY;
+        st[kTile + i] = some ? 1.0f / s[e].y : 0.0f;
+        rn[i] = r[e];
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kSBarFull + x));
+      ++it;
+      more = blk.next();
+      if (more) read();
     }
     if (lane == 0) {
       // the last copies land before the CTA goes away
@@ -774,32 +811,25 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     const uint32_t id_s = instr_desc(kTile, kTile, true);
     bool ok = __all_sync(0xffffffffu, bar_wait(bar(kSBarK), 0, abort));
     if (!ok) set_abort(a.status, abort);
-    int it = 0;
-    for (int g = 0; g < G && ok; ++g) {
-      for (int qt = 0; qt < tiles && ok; ++qt) {
-        if (!seen(qt)) continue;
-        const int x = it & 1;
-        if (!__all_sync(0xffffffffu,
-                        bar_wait(bar(kSBarFull + x), (uint32_t)((it >> 1) & 1), abort) &&
-                            (it < 2 || bar_wait(bar(kSBarSfree + x), (uint32_t)(((it - 2) >> 1) & 1), abort)))) {
-          set_abort(a.status, abort);
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (el) {
-          const uint32_t ka = base + kSOffK, qa = base + kSOffQ + x * kTileB;
-#pragma unroll
-          for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
-            mma_f16(tmem + kTile * x, op_desc_sw128(ka + off), op_desc_sw128(qa + off), id_s, ks > 0);
-          }
-          mma_commit(bar(kSBarS + x));
-          mma_commit(bar(kSBarEmpty + x));
-        }
-        __syncwarp();
-        ++it;
+    for (int it = 0; ok && blk.next(); ++it) {
+      const int x = it & 1;
+      if (!__all_sync(0xffffffffu, bar_wait(bar(kSBarFull + x), (uint32_t)((it >> 1) & 1), abort) &&
+                                       (it < 2 || bar_wait(bar(kSBarSfree + x), (uint32_t)(((it - 2) >> 1) & 1), abort)))) {
+        set_abort(a.status, abort);
+        break;
       }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (el) {
+        const uint32_t ka = base + kSOffK, qa = base + kSOffQ + x * kTileB;
+#pragma unroll
+        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * kBoxB + (ks & 3) * 32;
+          mma_f16(tmem + kTile * x, op_desc_sw128(ka + off), op_desc_sw128(qa + off), id_s, ks > 0);
+        }
+        mma_commit(bar(kSBarS + x));
+        mma_commit(bar(kSBarEmpty + x));
+      }
+      __syncwarp();
     }
     if (el) mma_commit(bar(kSBarDone));
     bar_wait(bar(kSBarDone), 0, nullptr);
@@ -811,73 +841,70 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     const float* st = reinterpret_cast<const float*>(ssm + kSOffStat) + x * 2 * kTile;
     const int2* rn = reinterpret_cast<const int2*>(ssm + kSOffRun) + x * kTile;
     const int key = k0 + t;
-    int it = 0;
-    bool ok = true;
-    for (int g = 0; g < G && ok; ++g) {
-      const float slope2 = BIAS ? slope_log2(a.mod, h * G + g) : 0.0f;
-      for (int qt = 0; qt < tiles && ok; ++qt) {
-        if (!seen(qt)) continue;
-        if ((it++ & 1) != x) continue;
-        const int use = it - 1;
-        const uint32_t par = (uint32_t)((use >> 1) & 1);
-        if (!__all_sync(0xffffffffu, bar_wait(bar(kSBarS + x), par, abort) && bar_wait(bar(kSBarFull + x), par, abort))) {
-          set_abort(a.status, abort);
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const int4 r = runs[qt];
-        const bool whole = r.z <= k0 && r.w >= k1;  // every query sees the whole key tile
-        const int q0 = qt * kTile;
-        f32x2 acc[2] = {0, 0};
+    int g = -1;
+    float slope2 = 0.0f;
+    for (int it = 0; blk.next(); ++it) {
+      if ((it & 1) != x) continue;
+      if (BIAS && blk.g != g) {
+        g = blk.g;
+        slope2 = slope_log2(a.mod, h * G + g);
+      }
+      const uint32_t par = (uint32_t)((it >> 1) & 1);
+      if (!__all_sync(0xffffffffu, bar_wait(bar(kSBarS + x), par, abort) && bar_wait(bar(kSBarFull + x), par, abort))) {
+        set_abort(a.status, abort);
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const bool whole = blk.all;
+      const int q0 = blk.qt * kTile;
+      f32x2 acc[2] = {0, 0};
 #pragma unroll 1
-        for (int c0 = 0; c0 < kTile; c0 += 32) {
-          float z[32];
-          ld32(trow + c0, z);
-          auto nm = [&](int i) { return *reinterpret_cast<const f32x2*>(st + c0 + i); };
-          const float d0 = (float)(q0 + c0 - key);
-          const bool both = q0 + c0 < key - lane + 31;  // some key of the warp lies after the query
-          if (CAP && !BIAS) {
-            chunk_cap_plus(a, z, chunk_most(z, 0.0f), nm);
-          } else {
-            if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
-            if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, -slope2, d0, both);
-            const f32x2 sc = pack2(BIAS ? 1.0f : a.qk_scale_log2, BIAS ? 1.0f : a.qk_scale_log2);
+      for (int c0 = 0; c0 < kTile; c0 += 32) {
+        float z[32];
+        ld32(trow + c0, z);
+        auto nm = [&](int i) { return *reinterpret_cast<const f32x2*>(st + c0 + i); };
+        const float d0 = (float)(q0 + c0 - key);
+        const bool both = q0 + c0 < key - lane + 31;  // some key of the warp lies after the query
+        if (CAP && !BIAS) {
+          chunk_cap_plus(a, z, chunk_most(z, 0.0f), nm);
+        } else {
+          if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
+          if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, -slope2, d0, both);
+          const f32x2 sc = pack2(BIAS ? 1.0f : a.qk_scale_log2, BIAS ? 1.0f : a.qk_scale_log2);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              unpack2(BIAS ? add2(pack2(z[i], z[i + 1]), nm(i)) : fma2(pack2(z[i], z[i + 1]), sc, nm(i)), z[i],
-                      z[i + 1]);
+          for (int i = 0; i < 32; i += 2)
+            unpack2(BIAS ? add2(pack2(z[i], z[i + 1]), nm(i)) : fma2(pack2(z[i], z[i + 1]), sc, nm(i)), z[i],
+                    z[i + 1]);
+        }
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const f32x2 p = pack2(fast_exp2(z[i]), fast_exp2(z[i + 1]));
+            acc[(i >> 1) & 1] = fma2(p, *reinterpret_cast<const f32x2*>(st + kTile + c0 + i), acc[(i >> 1) & 1]);
           }
-          if (whole) {
+        } else {
+          // (statistics of a row that does not see the key may be anything)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const f32x2 p = pack2(fast_exp2(z[i]), fast_exp2(z[i + 1]));
-              acc[(i >> 1) & 1] = fma2(p, *reinterpret_cast<const f32x2*>(st + kTile + c0 + i), acc[(i >> 1) & 1]);
-            }
-          } else {
-            // (statistics of a row that does not see the key may be anything)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const int4 b = *reinterpret_cast<const int4*>(rn + c0 + i);
-              float x0, x1;
-              unpack2(mul2(pack2(fast_exp2(z[i]), fast_exp2(z[i + 1])),
-                           *reinterpret_cast<const f32x2*>(st + kTile + c0 + i)),
-                      x0, x1);
-              x0 = key >= b.x && key < b.y ? x0 : 0.0f;
-              x1 = key >= b.z && key < b.w ? x1 : 0.0f;
-              acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pack2(x0, x1));
-            }
+          for (int i = 0; i < 32; i += 2) {
+            const int4 b = *reinterpret_cast<const int4*>(rn + c0 + i);
+            float x0, x1;
+            unpack2(mul2(pack2(fast_exp2(z[i]), fast_exp2(z[i + 1])),
+                         *reinterpret_cast<const f32x2*>(st + kTile + c0 + i)),
+                    x0, x1);
+            x0 = key >= b.x && key < b.y ? x0 : 0.0f;
+            x1 = key >= b.z && key < b.w ? x1 : 0.0f;
+            acc[(i >> 1) & 1] = add2(acc[(i >> 1) & 1], pack2(x0, x1));
           }
         }
-        float ax, ay;
-        unpack2(add2(acc[0], acc[1]), ax, ay);
-        sum += ax + ay;
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(bar(kSBarSfree + x));
-          bar_arrive(bar(kSBarEmpty + x));
-        }
+      }
+      float ax, ay;
+      unpack2(add2(acc[0], acc[1]), ax, ay);
+      sum += ax + ay;
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(bar(kSBarSfree + x));
+        bar_arrive(bar(kSBarEmpty + x));
       }
     }
   }
