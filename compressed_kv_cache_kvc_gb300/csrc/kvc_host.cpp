@@ -212,9 +212,9 @@ kvc_status attention_check(const kvc_cache* c, int32_t seq_begin, int32_t batch,
   return KVC_OK;
 }
 
-// What the prompt kernels' grids and 32-bit indices take: query heads and
-// sequences on the grid's y and z, 128-row tiles of all heads on x, positions
-// with room for a tile past the end.
+// What the prompt kernels' grids and 32-bit indices take: 128-row tiles of all
+// heads of all sequences on the grid's x, positions with room for a tile past
+// the end.
 bool prompt_shape_ok(int batch, int hq, int n) {
   return batch <= 65535 && hq <= 65535 && n <= 0x7FFFFE00 &&
          ((long long)n + 127) / 128 * batch <= 0x7FFFFFFFLL / hq;

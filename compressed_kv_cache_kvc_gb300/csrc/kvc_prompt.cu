@@ -295,8 +295,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   auto bar = [&](int i) { return base + kFOffBar + 8 * i; };
 
   const int n = a.n;
-  const int qb = gridDim.x - 1 - blockIdx.x, hqi = blockIdx.y, bl = blockIdx.z;
-  const int plane_q = bl * a.hq + hqi, plane_kv = bl * a.hkv + hqi / a.group;
+  // the longest blocks of all heads first (head by head, the last heads' blocks
+  // left the SMs idle at the end)
+  const int planes = a.hq * a.batch, plane_q = blockIdx.x % planes;
+  const int qb = (n + kFwdBlock - 1) / kFwdBlock - 1 - blockIdx.x / planes;
+  const int bl = plane_q / a.hq, hqi = plane_q % a.hq;
+  const int plane_kv = bl * a.hkv + hqi / a.group;
   // (what steers a whole warp goes through a shuffle: the compiler then keeps it,
   // and the operands of the products that hang on it, in uniform registers)
   auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
@@ -717,10 +721,11 @@ __global__ void __launch_bounds__(kSumThreads, 2)
   volatile int* abort = reinterpret_cast<volatile int*>(ssm + kSOffBar + 8 * kSNumBars + 4);
   auto bar = [&](int i) { return base + kSOffBar + 8 * i; };
   const int n = a.n, G = a.group;
-  const int kt = blockIdx.x, h = blockIdx.y, bl = blockIdx.z;
+  const int planes = a.hkv * a.batch, plane_kv = blockIdx.x % planes, kt = blockIdx.x / planes;
+  const int h = plane_kv % a.hkv, bl = plane_kv / a.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int k0 = kt * kTile, k1 = min(k0 + kTile, n);
-  const int tiles = gridDim.x;
+  const int tiles = (n + kTile - 1) / kTile;
   SeenBlocks blk(a.runs + (size_t)bl * tiles, tiles, G, k0, k1, lane);
 
   if (warp == 9) {
@@ -948,7 +953,7 @@ cudaError_t launch_fwd(const PromptArgs& a, const CUtensorMap& q, const CUtensor
   static int done[64] = {0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_fwd_kernel<CAP, BIAS>), kFwdSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.n + kFwdBlock - 1) / kFwdBlock, a.hq, a.batch);
+  const dim3 grid((unsigned)((a.n + kFwdBlock - 1) / kFwdBlock * (a.hq * a.batch)));
   // may start while the prep kernel's last CTAs run (wait_for_previous)
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -968,7 +973,7 @@ cudaError_t launch_sums(const PromptArgs& a, const CUtensorMap& q, const CUtenso
   static int done[64] = {0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_sums_kernel<CAP, BIAS>), kSumSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.n + kTile - 1) / kTile, a.hkv, a.batch);
+  const dim3 grid((unsigned)((a.n + kTile - 1) / kTile * (a.hkv * a.batch)));
   prompt_sums_kernel<CAP, BIAS><<<grid, kSumThreads, kSumSmem, st>>>(a, q, k);
   return cudaGetLastError();
 }
