@@ -286,7 +286,7 @@ __device__ __forceinline__ void chunk_shift(float (&z)[32], float scale, float m
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     prompt_fwd_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v) {
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o) {
   extern __shared__ __align__(1024) uint8_t fsm[];
   const uint32_t base = saddr(fsm);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(fsm + kFOffMisc);
@@ -320,6 +320,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                    "r"(i >= kFBarP && i < kFBarP + 4 ? 4u : 1u));
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
+    // Q comes while the runs are read
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+#pragma unroll
+    for (int y = 1; y >= 0; --y) {
+      const uint32_t dst = base + kFOffQ + y * kTileB;
+      bar_expect_tx(bar(kFBarQ + y), kTileB);
+      tma_load_3d(dst, &tm_q, 0, qblk + y * kTile, plane_q, bar(kFBarQ + y));
+      tma_load_3d(dst + kBoxB, &tm_q, 64, qblk + y * kTile, plane_q, bar(kFBarQ + y));
+    }
+    tma_prefetch_map(&tm_o);
   }
   // the rows' runs; per warp the keys some row sees and those every row sees
   int2 run = make_int2(0, 0);
@@ -369,9 +381,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // ------------------------------------------------------------- TMA loads
     // Round r brings K of its tile and V of the tile two rounds before, on one
     // barrier; both are consumed by the products of round r.
-    if (lane == 0 && n_t > 0) {
+    if (lane == 0) {
       int rounds = 0;
-      for (int r = 0; r < n_t + 2; ++r) {
+      for (int r = 0; n_t > 0 && r < n_t + 2; ++r) {
         const int j = t_hi - 1 - r;
         const uint32_t b = bar(kFBarKv + (r & 3));
         if (r >= kSlots && !bar_wait(bar(kFBarFree + (r & 3)), (uint32_t)((r >> 2) & 1) ^ 1u, abort)) {
@@ -391,15 +403,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           tma_load_3d(dst + kKeyBox, &tm_v, 64, (j + 2) * kKeys, plane_kv, b);
         }
         rounds = r + 1;
-        if (r == 0) {
-#pragma unroll
-          for (int y = 1; y >= 0; --y) {
-            const uint32_t dst = base + kFOffQ + y * kTileB;
-            bar_expect_tx(bar(kFBarQ + y), kTileB);
-            tma_load_3d(dst, &tm_q, 0, qblk + y * kTile, plane_q, bar(kFBarQ + y));
-            tma_load_3d(dst + kBoxB, &tm_q, 64, qblk + y * kTile, plane_q, bar(kFBarQ + y));
-          }
-        }
       }
       // the last copies land before the CTA goes away (they may not have been
       // waited for when another role gave up)
@@ -622,10 +625,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     sh_m[odd * kTile] = poison ? 1.0f : 0.0f;
     asm volatile("bar.sync %0, 256;" ::"r"(kNbTile + x) : "memory");
     poison = sh_m[0] + sh_m[kTile] != 0.0f;
+    // (where the tile has no keys nothing above has waited for its Q)
+    if (last < 0) wait(kFBarQ + x, 0);
     if (ok && !*abort) {
-      const bool row_ok = qi < n;
+      // the output takes Q's place in shared memory (every S of the tile is
+      // complete) and leaves by TMA, 32 rows of 64 dims a warp: stores of a row
+      // a thread took 2800 cycles of the load-store unit a block
       const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a row that sees nothing is 0
-      uint16_t* orow = a.out + ((size_t)plane_q * n + (row_ok ? qi : 0)) * kHeadDim + 64 * odd;
+      uint8_t* orow = fsm + kFOffQ + x * kTileB + odd * kBoxB + row * 128;
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 32) {
         float t[32];
@@ -641,12 +648,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const __nv_bfloat162 pr = __floats2bfloat162_rn(t[2 * e] * inv, t[2 * e + 1] * inv);
           w[e] = poison ? 0x7FFF7FFFu : *reinterpret_cast<const uint32_t*>(&pr);
         }
-        if (row_ok) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(orow + c0 + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        }
+        for (int e = 0; e < 4; ++e)  // (chunks of 16 bytes in the 128-byte swizzle)
+          *reinterpret_cast<uint4*>(orow + (((c0 >> 3) + e) ^ (row & 7)) * 16) =
+              make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
       }
+      fence_async();
+      __syncwarp();
+      if (lane == 0 && qi < n) {
+        tma_store_3d(&tm_o, base + kFOffQ + x * kTileB + odd * kBoxB + row * 128, 64 * odd, qi, plane_q);
+        tma_stores_read();
+      }
+      const bool row_ok = qi < n;
       if (row_ok && !odd && a.stats != nullptr)
         *reinterpret_cast<float2*>(a.stats + ((size_t)plane_q * n + qi) * 2) = make_float2(m, total);
     }
@@ -949,7 +962,7 @@ __global__ void prompt_scores_kernel(DevState s, int seq_begin, int n, const flo
 
 template <bool CAP, bool BIAS>
 cudaError_t launch_fwd(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                       cudaStream_t st) {
+                       const CUtensorMap& o, cudaStream_t st) {
   static int done[64] = {0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_fwd_kernel<CAP, BIAS>), kFwdSmem, done);
   if (e != cudaSuccess) return e;
@@ -965,7 +978,7 @@ cudaError_t launch_fwd(const PromptArgs& a, const CUtensorMap& q, const CUtensor
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_fwd_kernel<CAP, BIAS>, a, q, k, v);
+  return cudaLaunchKernelEx(&cfg, prompt_fwd_kernel<CAP, BIAS>, a, q, k, v, o);
 }
 
 template <bool CAP, bool BIAS>
@@ -1023,18 +1036,19 @@ cudaError_t launch_prompt(const PromptArgs& args, const uint16_t* q, const uint1
                           cudaStream_t st) {
   PromptArgs a = args;
   prompt_polynomials(&a);
-  CUtensorMap tm_q, tm_k, tm_v, tm_ks;
+  CUtensorMap tm_q, tm_k, tm_v, tm_o, tm_ks;
   if (!encode_rows_map(&tm_q, q, a.n, a.batch * a.hq, kTile) || !encode_rows_map(&tm_k, k, a.n, a.batch * a.hkv, kKeys) ||
       !encode_rows_map(&tm_v, a.v16, a.n, a.batch * a.hkv, kKeys, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) ||
+      !encode_rows_map(&tm_o, a.out, a.n, a.batch * a.hq, 32) ||
       (a.sums != nullptr && !encode_rows_map(&tm_ks, k, a.n, a.batch * a.hkv, kTile)))
     return cudaErrorInvalidValue;
   prompt_prep_kernel<<<(a.n + kTile - 1) / kTile * (a.batch * a.hkv), kPrepThreads, 0, st>>>(a, v);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const bool cap = a.mod.c2 > 0.0f, bias = a.mod.slopes != nullptr;
-  e = cap ? (bias ? launch_fwd<true, true>(a, tm_q, tm_k, tm_v, st) : launch_fwd<true, false>(a, tm_q, tm_k, tm_v, st))
-          : (bias ? launch_fwd<false, true>(a, tm_q, tm_k, tm_v, st)
-                  : launch_fwd<false, false>(a, tm_q, tm_k, tm_v, st));
+  e = cap ? (bias ? launch_fwd<true, true>(a, tm_q, tm_k, tm_v, tm_o, st) : launch_fwd<true, false>(a, tm_q, tm_k, tm_v, tm_o, st))
+          : (bias ? launch_fwd<false, true>(a, tm_q, tm_k, tm_v, tm_o, st)
+                  : launch_fwd<false, false>(a, tm_q, tm_k, tm_v, tm_o, st));
   if (e != cudaSuccess || a.sums == nullptr) return e;
   return cap ? (bias ? launch_sums<true, true>(a, tm_q, tm_ks, st) : launch_sums<true, false>(a, tm_q, tm_ks, st))
              : (bias ? launch_sums<false, true>(a, tm_q, tm_ks, st) : launch_sums<false, false>(a, tm_q, tm_ks, st));
