@@ -180,15 +180,17 @@ class KVCache:
         batch = q.shape[0]
         if out is None:
             out = torch.empty_like(q)
-        _need(out, torch.bfloat16, "out", self.device, q.shape)
-        ws = self.workspace(batch) if workspace is None else workspace
-        _need(ws, torch.uint8, "workspace", self.device)
+        else:
+            _need(out, torch.bfloat16, "out", self.device, q.shape)
+        if workspace is None:
+            ws = self.workspace(batch)
+        else:
+            ws = workspace
+            _need(ws, torch.uint8, "workspace", self.device)
         scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
         flags = L.KVC_ATTN_ACCUM_H2O if accumulate_h2o else 0
-        L.check(self.lib.kvc_decode_attention(self.handle, seq_begin, batch, ctypes.c_void_p(q.data_ptr()),
-                                              ctypes.c_void_p(out.data_ptr()), ctypes.c_float(scale), flags,
-                                              ctypes.c_void_p(ws.data_ptr()), ws.numel(),
-                                              ctypes.c_void_p(_stream_ptr(stream))), "kvc_decode_attention")
+        L.check(self.lib.kvc_decode_attention(self.handle, seq_begin, batch, q.data_ptr(), out.data_ptr(), scale, flags,
+                                              ws.data_ptr(), ws.numel(), _stream_ptr(stream)), "kvc_decode_attention")
         return out
 
     def new_keep_mask(self, batch: int) -> torch.Tensor:
