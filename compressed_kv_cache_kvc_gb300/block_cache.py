@@ -122,6 +122,9 @@ class BlockScaledCache:
                          workspace=None, stream=None) -> torch.Tensor:
         """q: bf16 [batch, Hq, 128], at the newest position -> bf16 [batch,
         Hq, 128]; scores transformed as in `prompt_attention`."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.decode_attention(q, out, seq_begin, sm_scale, softcap, slopes, workspace)
         _need(q, torch.bfloat16, "q", self.device)
         if q.dim() != 3 or q.shape[1] != self.num_q_heads or q.shape[2] != HEAD_DIM:
             raise ValueError("q must be [batch, num_q_heads, 128]")
@@ -138,7 +141,7 @@ class BlockScaledCache:
             _need(ws, torch.uint8, "workspace", self.device)
         scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
         self._call("kvc_block_attention", seq_begin, q.shape[0], _ptr(q), _ptr(out), scale,
-                   softcap, _ptr(slopes), _ptr(ws), ws.numel(), stream=stream)
+                   softcap, _ptr(slopes), _ptr(ws), ws.numel())
         return out
 
     def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, status: torch.Tensor, seq_begin: int = 0,
@@ -157,6 +160,9 @@ class BlockScaledCache:
         bf16 (k, v), [batch, Hkv, n, 128] each, as the attention sees them; rows
         at or past a sequence's length are left as they are in `out` (zero
         without `out`)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):  # (the zeros too)
+                return self.read(seq_begin, batch, pos_begin, n, out)
         least, most = self.lengths(seq_begin, batch)
         if n is None:
             n = most - pos_begin
@@ -171,5 +177,5 @@ class BlockScaledCache:
             k, v = out
             _need(k, torch.bfloat16, "k", self.device, shape)
             _need(v, torch.bfloat16, "v", self.device, shape)
-        self._call("kvc_block_read", seq_begin, batch, pos_begin, n, k.data_ptr(), v.data_ptr(), stream=stream)
+        self._call("kvc_block_read", seq_begin, batch, pos_begin, n, k.data_ptr(), v.data_ptr())
         return k, v

@@ -487,6 +487,11 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
   const int r = lane >> 2, c = lane & 3;
   const long long T = (long long)hkv * cum[batch];
   const int N = gridDim.x, cta = blockIdx.x;
+  // (a replayed graph may find a sequence empty)
+  for (int i = cta; i < batch; i += N)
+    if (len[i] <= 0)
+      for (int e = threadIdx.x; e < s.hq * (kHeadDim / 8); e += kBThreads)
+        reinterpret_cast<uint4*>(out + (size_t)i * s.hq * kHeadDim)[e] = make_uint4(0u, 0u, 0u, 0u);
   long long F = (long long)cta * T / N;
   const long long F1 = (long long)(cta + 1) * T / N;
   const uint32_t ring_s = smem_u32(smem) + warp * kBStages * kBStage;

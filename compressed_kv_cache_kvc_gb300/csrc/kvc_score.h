@@ -52,9 +52,13 @@ inline ScoreMod make_score_mod(float sm_scale, float cap, const float* slopes) {
   m.slopes = slopes;
   if (cap > 0.0f) {
     const double c2 = (double)cap * 1.4426950408889634;
-    m.c2 = (float)c2;
-    m.y_scale = (float)((double)sm_scale / (double)cap);
-    m.poly[0] = (float)c2;
+    // (finite for every cap, with room for the kernels' powers of two beside it:
+    // an infinite factor would make NaN of a product of 0)
+    constexpr double kMost = 3.4028234663852886e38, kMostY = 1152921504606846976.0;  // 2^60
+    m.c2 = (float)(c2 < kMost ? c2 : kMost);
+    const double ys = (double)sm_scale / (double)cap;
+    m.y_scale = (float)(ys < kMostY ? ys : kMostY);
+    m.poly[0] = m.c2;
     for (int i = 0; i < 4; ++i) m.poly[i + 1] = (float)(c2 * kCapP3[i]);
   }
   return m;

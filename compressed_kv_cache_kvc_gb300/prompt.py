@@ -32,6 +32,12 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, statu
     (float32 [Hq]).  column_sums: True, or a float32 [batch, Hkv, n] tensor,
     returns (out, sums) with every key's sum of probabilities.  status: int32
     [1], zeroed by the caller; KVC_DEV_* bits are or'ed into it."""
+    if stream is not None:
+        # what is allocated below then belongs to that stream, as the kernels do
+        with torch.cuda.stream(stream):
+            return prompt_attention(q, k, v, status=status, out=out, sm_scale=sm_scale, softcap=softcap, slopes=slopes,
+                                    key_begin=key_begin, key_end=key_end, column_sums=column_sums,
+                                    workspace=workspace)
     bf16 = torch.bfloat16
     _need(q, bf16, "q")
     if q.dim() != 4 or q.shape[3] != HEAD_DIM:
@@ -73,10 +79,10 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, statu
     args = (ctypes.byref(params), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(sums),
             status.data_ptr(), workspace.data_ptr(), ws_bytes)
     if _current_device() == dev.index:
-        st = lib.kvc_prompt_attention(*args, _stream_ptr(stream))
+        st = lib.kvc_prompt_attention(*args, _stream_ptr())
     else:
         with torch.cuda.device(dev):
-            st = lib.kvc_prompt_attention(*args, _stream_ptr(stream))
+            st = lib.kvc_prompt_attention(*args, _stream_ptr())
     L.check(st, "kvc_prompt_attention")
     return out if sums is None else (out, sums)
 

@@ -479,7 +479,8 @@ kvc_status kvc_prefill_context(kvc_cache* cache, int32_t seq_begin, int32_t batc
  * kvc_prefill_attention_masked and kvc_prefill_context, with every code
  * format and with a bf16 window.  kvc_prefill_workspace_bytes grows while a
  * transform is set.  Enqueues nothing; takes effect with the next call.
- * Capped scores are accurate to 7.2e-7 of softcap, the bias to fp32 rounding.
+ * Capped scores are accurate to 7.2e-7 of softcap (a softcap below sm_scale /
+ * 2^60 to softcap itself), the bias to fp32 rounding.
  * Errors: KVC_ERR_INVALID_ARG for a softcap that is negative or not finite,
  * or a misaligned d_slopes (the transform set before stays). */
 kvc_status kvc_set_score_transform(kvc_cache* cache, float softcap, const float* d_slopes);
@@ -519,7 +520,7 @@ size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t nu
  * makes the rows that see it not finite; a row that sees a key whose V row
  * holds a NaN or an infinity is NaN; rows that do not see them are not
  * touched by them (the status bit KVC_DEV_PREFILL_RANGE is set all the same).
- * Two launches, three with sums; results do not depend on the order of
+ * Outputs and workspace overlap nothing else.  Two launches, three with sums; results do not depend on the order of
  * execution.  Errors, before any launch: KVC_ERR_INVALID_ARG for sizes that
  * are not positive, Hq % Hkv != 0, a null or misaligned pointer, an sm_scale
  * that is not positive and finite, a softcap that is negative or not finite, a
@@ -632,7 +633,7 @@ kvc_status kvc_block_append(kvc_block_cache* cache, int32_t seq_begin, int32_t b
  * another (they share its tickets); two graphs may share a workspace if their
  * replays do not overlap.
  * Errors: KVC_ERR_INVALID_ARG (slice, pointers, sm_scale, softcap, workspace,
- * an empty sequence). */
+ * an empty sequence; one that a replayed graph finds empty gets rows of 0). */
 size_t kvc_block_workspace_bytes(const kvc_block_cache* cache, int32_t batch);
 kvc_status kvc_block_attention(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, const void* d_q, void* d_out,
                                float sm_scale, float softcap, const float* d_slopes, void* d_workspace,
