@@ -424,7 +424,15 @@ __global__ void __launch_bounds__(kReadThreads) block_read_kernel(BlockState s, 
 // bf16 parts (16 significant bits).
 // The CTA that finishes a pair last (an atomic ticket, no CTA waits) joins the
 // pair's partials in CTA order, so the result does not depend on the order of
-// completion.
+// completion.  (A warp per query head, eight rows of 16 bytes a lane in flight:
+// joining a row at a time took 28.7 against 19.4 us for one sequence of 32,000
+// tokens.)
+//
+// PARTS, for few sequences of unequal lengths: a CTA takes a part of one pair,
+// the parts of a sequence in proportion to its length, so that no CTA ends
+// inside a part.  Two CTAs per SM then, with the registers of two; the equal
+// runs take a full wave of three (168 registers; at 216 and two per SM 16 x 32
+// heads of 4,111 capped tokens 94 against 88 us).
 constexpr int kBWarps = 4;
 constexpr int kBThreads = kBWarps * 32;
 constexpr int kBStages = 4;
@@ -452,8 +460,8 @@ __host__ __device__ constexpr int bchunk(int t, int j) {
   return 128 * t + 16 * (j ^ ((2 * ((t >> 2) & 3)) ^ (4 * ((t >> 1) & 1))));
 }
 
-template <bool FP8, int MOD>
-__global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int seq_begin, int batch,
+template <bool FP8, int MOD, bool PARTS>
+__global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(BlockState s, int seq_begin, int batch,
                                                                const uint16_t* __restrict__ q,
                                                                uint16_t* __restrict__ out, BlockAttn a) {
   constexpr bool kCap = (MOD & kBCap) != 0, kBias = (MOD & kBBias) != 0;
@@ -461,6 +469,7 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
   constexpr float kOffK = 128.0f * 0x1p-24f, kOffV = 128.0f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int cum[kMaxCallBatch + 1], len[kMaxCallBatch];
+  __shared__ int parts[PARTS ? kMaxSplitBatch + 1 : 1];  // (split pairs) parts of a head of the sequences before
   __shared__ int sh_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bt = s.bt, ppb = bt / kPage;  // pages per block
@@ -480,6 +489,24 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
       if (i < batch) cum[i + 1] = carry + v;
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
+    if (PARTS) {
+      // every sequence's share of the parts of a head, rounded down (but one at least)
+      const long long per_head = a.parts, total = max(carry, 1);
+      int before = 0;
+      if (lane == 0) parts[0] = 0;
+      for (int base = 0; base < batch; base += 32) {
+        const int i = base + lane;
+        const int nu = i < batch ? block_units(len[i], bt) : 0;
+        int v = nu > 0 ? (int)max(1LL, min((long long)nu, nu * per_head / total)) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        if (i < batch) parts[i + 1] = before + v;
+        before += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
   }
   __syncthreads();
 
@@ -492,8 +519,10 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
     if (len[i] <= 0)
       for (int e = threadIdx.x; e < s.hq * (kHeadDim / 8); e += kBThreads)
         reinterpret_cast<uint4*>(out + (size_t)i * s.hq * kHeadDim)[e] = make_uint4(0u, 0u, 0u, 0u);
-  long long F = (long long)cta * T / N;
-  const long long F1 = (long long)(cta + 1) * T / N;
+  // this CTA's run of units [F, F1), or its parts F, F + N, .. of F1
+  long long F = PARTS ? cta : (long long)cta * T / N;
+  const long long F1 = PARTS ? (long long)hkv * parts[batch] : (long long)(cta + 1) * T / N;
+  const int* first = PARTS ? parts : cum;
   const uint32_t ring_s = smem_u32(smem) + warp * kBStages * kBStage;
   const uint8_t* ring = smem + warp * kBStages * kBStage;
   uint32_t cp_d[4];
@@ -507,22 +536,38 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
   const float qk = kCap ? a.mod.y_scale : a.qk_scale_log2;
 
   while (F < F1) {
-    // ---- the pair of unit F and this CTA's run of its units
+    // ---- the pair of unit (or part) F and the units of it that are this CTA's
     int lo = 0, hi = batch - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((long long)hkv * cum[mid] <= F) lo = mid; else hi = mid - 1;
+      if ((long long)hkv * first[mid] <= F) lo = mid; else hi = mid - 1;
     }
     const int bl = lo, b = seq_begin + bl;
     const int nu = cum[bl + 1] - cum[bl];
-    const long long pbase = (long long)hkv * cum[bl];
-    const int h = (int)((F - pbase) / nu);
-    const long long Pf = pbase + (long long)h * nu;
-    const int u_a = (int)(F - Pf);
-    const int u_e = (int)((F1 < Pf + nu ? F1 : Pf + nu) - Pf);
+    const long long pbase = (long long)hkv * first[bl];
+    const int per_pair = first[bl + 1] - first[bl];
+    const int h = (int)((F - pbase) / per_pair);
+    const long long Pf = pbase + (long long)h * per_pair;
+    int u_a, u_e, cnt;   // units [u_a, u_e); partials of the pair
+    long long slot;      // of this partial; the pair's first
+    long long slot0;
+    if (PARTS) {
+      const int part = (int)(F - Pf);
+      cnt = per_pair;
+      u_a = (int)((long long)nu * part / cnt);
+      u_e = (int)((long long)nu * (part + 1) / cnt);
+      slot = F;
+      slot0 = Pf;
+    } else {
+      u_a = (int)(F - Pf);
+      u_e = (int)((F1 < Pf + nu ? F1 : Pf + nu) - Pf);
+      const int i_first = cta_of_page(Pf, T, N), i_last = cta_of_page(Pf + nu - 1, T, N);
+      cnt = i_last - i_first + 1;
+      slot0 = (long long)bl * hkv + h + i_first;
+      slot = (long long)bl * hkv + h + cta;
+    }
     const int P = len[bl];
     const int closed = block_closed(P, bt), npg = closed * ppb;
-    const int pair = bl * hkv + h;
 
     // ---- this warp's units u_a + warp, + kBWarps, ...: n_my, the first n_pg of them pages
     const int n_my = u_e - u_a > warp ? (u_e - u_a - warp + kBWarps - 1) / kBWarps : 0;
@@ -938,7 +983,6 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
       }
     }
     __syncthreads();
-    const int i_first = cta_of_page(Pf, T, N), i_last = cta_of_page(Pf + nu - 1, T, N);
     const int d = threadIdx.x;  // 128 threads = head_dim
     uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
     for (int g = 0; g < G; ++g) {
@@ -952,10 +996,10 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
         o += wt * sm_o[((size_t)ww * kMaxGroup + g) * kHeadDim + d];
         l += wt * sm_l[ww * kMaxGroup + g];
       }
-      if (i_first == i_last) {
+      if (cnt == 1) {
         orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(l != 0.0f ? o * (1.0f / l) : 0.0f));
       } else {
-        const size_t ps = ((size_t)pair + cta) * G + g;
+        const size_t ps = (size_t)slot * G + g;
         a.part_o[ps * kHeadDim + d] = o;
         if (d == 0) {
           a.part_ml[ps * 2] = M;
@@ -963,12 +1007,12 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
         }
       }
     }
-    if (i_first != i_last) {
+    if (cnt > 1) {
       // the pair's last CTA joins the partials, in CTA order
       __syncthreads();
       if (threadIdx.x == 0) {
         __threadfence();
-        sh_last = atomicAdd(&s.tickets[b * hkv + h], 1) == i_last - i_first;
+        sh_last = atomicAdd(&s.tickets[b * hkv + h], 1) == cnt - 1;
         __threadfence();
       }
       __syncthreads();
@@ -976,9 +1020,8 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
         // a warp per head (several when there are fewer heads than warps, each
         // with every wph-th part): 32 parts' maxima and sums across the lanes,
         // then their rows, eight of 16 bytes a lane in flight
-        const int cnt = i_last - i_first + 1;
         const int wph = G >= kBWarps ? 1 : kBWarps / G, share = warp % wph;
-        const size_t base = ((size_t)pair + i_first) * G;
+        const size_t base = (size_t)slot0 * G;
         float* sm_j = reinterpret_cast<float*>(smem);  // [kBWarps][kHeadDim + 2]
         for (int g = warp / wph; g < G; g += kBWarps / wph) {
           float M = kNegBig, l = 0.0f;
@@ -1040,14 +1083,14 @@ __global__ void __launch_bounds__(kBThreads) block_attn_kernel(BlockState s, int
       }
     }
     __syncthreads();  // shared memory is reused by the next pair
-    F = Pf + u_e;
+    F = PARTS ? F + N : Pf + u_e;
   }
 }
 
-template <bool FP8, int MOD>
+template <bool FP8, int MOD, bool PARTS>
 cudaError_t block_attn_smem() {
   static int done[64] = {0};
-  return opt_in_smem(reinterpret_cast<const void*>(block_attn_kernel<FP8, MOD>), kBSmem, done);
+  return opt_in_smem(reinterpret_cast<const void*>(block_attn_kernel<FP8, MOD, PARTS>), kBSmem, done);
 }
 
 template <bool FP8, int MOD>
@@ -1057,8 +1100,8 @@ int block_attn_ctas() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   if (dev < 64 && cached[dev] > 0) return cached[dev];
   int n = 0;
-  if (block_attn_smem<FP8, MOD>() != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, block_attn_kernel<FP8, MOD>, kBThreads, kBSmem) !=
+  if (block_attn_smem<FP8, MOD, false>() != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, block_attn_kernel<FP8, MOD, false>, kBThreads, kBSmem) !=
           cudaSuccess ||
       n < 1)
     n = 1;
@@ -1071,9 +1114,12 @@ int block_mod(const ScoreMod& m) { return (m.c2 > 0.0f ? kBCap : 0) | (m.slopes 
 template <bool FP8, int MOD>
 cudaError_t launch_block_attn_t(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                 const BlockAttn& w, cudaStream_t st) {
-  const cudaError_t e = block_attn_smem<FP8, MOD>();
+  const cudaError_t e = w.parts ? block_attn_smem<FP8, MOD, true>() : block_attn_smem<FP8, MOD, false>();
   if (e != cudaSuccess) return e;
-  block_attn_kernel<FP8, MOD><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
+  if (w.parts)
+    block_attn_kernel<FP8, MOD, true><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
+  else
+    block_attn_kernel<FP8, MOD, false><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
   return cudaGetLastError();
 }
 

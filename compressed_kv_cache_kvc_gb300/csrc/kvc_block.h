@@ -33,12 +33,18 @@ __host__ __device__ inline int block_units(int P, int bt) {
   return block_closed(P, bt) * (bt / kPage) + (block_exact_rows(P, bt) + kPage - 1) / kPage;
 }
 
+// Sequences of a call that cuts its CTAs to the pairs (their table shares the
+// shared memory with three CTAs' rings).
+constexpr int kMaxSplitBatch = 255;
+
 struct BlockAttn {
-  float* part_o;   // [pairs + ncta][group][128]
+  float* part_o;   // [pairs + ncta][group][128] (at most ncta + pairs parts, however they are cut)
   float* part_ml;  // [pairs + ncta][group][2]
   ScoreMod mod;
   float qk_scale_log2;
   int ncta;
+  int parts;  // 0: equal runs across pairs; else a CTA takes a part of one pair, and the sequences of a head
+                    // have about this many parts together
 };
 
 cudaError_t launch_block_append(const BlockState& s, int seq_begin, int batch, int n_new, const uint16_t* k,
