@@ -18,7 +18,7 @@ struct BlockState {
   int32_t* seq_pos;   // [max_batch]
   int32_t* free_stack;
   int32_t* counters;  // [0] free top, [1] status
-  int32_t* tickets;   // [max_batch * hkv] attention, [max_batch * hkv] append; zero between calls
+  int32_t* tickets;   // [max_batch * hkv] attention, one append; zero between calls
   int32_t hq, hkv, group, bt, num_blocks, max_batch, max_bps, fp8;
 };
 

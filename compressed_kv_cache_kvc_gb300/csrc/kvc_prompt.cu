@@ -16,13 +16,21 @@
 //   prompt_sums_kernel   column sums from the row statistics.
 //
 // prompt_fwd_kernel.  4 * 128 flops per visible pair: bound by the tensor
-// pipe and, with a cap or a bias, by the FMA pipe.  One 576-thread CTA per (256
-// queries, query head, sequence), longest blocks first:
+// pipe and, with a cap or a bias, by the FMA pipe (32 capped heads of 8,192
+// causal tokens in 521 us, 1.06 PFLOP/s), and for short runs of keys by the
+// first and last round trips of a block, about 9 us of latency whatever the
+// block holds.  One 576-thread CTA per (256 queries, query head, sequence), the
+// longest blocks of all heads first (head by head 598 us for that prompt, 271
+// against 228 us for two-way prefixes with sums).  Launched while the prep
+// kernel runs: only V and the masks of its rows are waited for.  Q is loaded
+// while the runs are read; the output goes through Q's shared memory and
+// leaves by TMA (stores of a row a thread and a later Q: 185 against 172 us for
+// packed documents):
 //   * warps 0-7 and 8-15 own one 128-query tile each ("A", "B"), two threads a
 //     query row: of each eight the first four warps take the even key tiles,
 //     the others the odd ones, so that four warps per scheduler hide each
-//     other's latencies (eight warps, a thread a row, took 729 against 597 us for 32
-//     capped heads of 8192 causal tokens);
+//     other's latencies (eight warps, a thread a row, took 729 us where this then
+//     took 597, 32 capped heads of 8,192 causal tokens);
 //   * warp 16 issues the products, warp 17 the TMA loads: K and V tiles of 64
 //     keys into four slots each.  K is read K-major and V in its own layout
 //     (MN-major), both with the 128-byte swizzle, so nothing is transposed.
@@ -36,7 +44,8 @@
 // keys: 4 % slower over prompts of 1 to 8000 tokens and all masks (packed biased
 // documents 213 against 199 us, capped and biased prefixes 167 against 157 us),
 // faster for long causal prompts without a cap (32 heads of 8192 tokens: 454
-// against 561 us plain, 582 against 594 us capped).
+// against 561 us plain, 582 against 594 us capped; all before blocks went longest
+// first).
 // Key tiles go from the last to the first: with a distance bias the nearest
 // keys, which set the maximum, come first.  The running maximum is lazy (O is
 // rescaled when a row's maximum grows by more than 8 in log2 units, after a
@@ -675,7 +684,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 //
 // One 320-thread CTA per (128-key tile, KV head, sequence), two per SM, keys
 // on the TMEM lanes: S^T = K Q^T (M 128, N 128), so thread t of a warpgroup
-// owns key t and adds in registers; no atomics, a fixed order.  Warpgroups 0
+// owns key t and adds in registers; no atomics, a fixed order.  (64 heads of
+// 2,100 tokens, capped and biased: about 95 us, bound by the FMA pipe and the
+// unevenness of the blocks.)  Warpgroups 0
 // and 1 take alternate (query head, query tile) blocks, warp 8 loads the query
 // tiles and stages -m, 1 / l and the run per query, warp 9 issues the products.
 // Two queries go through each instruction (their -m and 1 / l are pairs in
