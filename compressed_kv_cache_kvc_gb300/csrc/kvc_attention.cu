@@ -832,20 +832,23 @@ cudaError_t launch_attention_split(const DevState& s, int seq_begin, int batch, 
 }
 
 cudaError_t launch_attention_merge(const DevState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
-                                   float qk_scale_log2, const AttnWork& w, MergeScores scores, cudaStream_t st) {
-  // Launched while the split's CTAs run (they are one resident wave), so that
-  // its CTAs are in place when the last partial is written: INT4, 32
-  // x 8,192 tokens, five query heads a KV head 73.5 us a call, 75.6 after it;
-  // FP8, 16 ragged sequences of up to 8,192 tokens 43.9 and 46.1.
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
+                                   float qk_scale_log2, const AttnWork& w, MergeScores scores, bool early,
+                                   cudaStream_t st) {
+  // early: launched while the split's CTAs run (they are one resident wave), so
+  // that its CTAs are in place when the last partial is written: INT4, 32 x 8,192
+  // tokens, five query heads a KV head 73.5 us a call, 75.6 after it; FP8, 16 ragged sequences of up to 8,192 tokens 43.9 and 46.1.  Not beside a
+  // second stream's kernels: its waiting CTAs take the room of the eviction that
+  // the overlapped step runs under the next layer's split (48 layers, 32 x 8,192
+  // INT4 tokens: 5.71 against 5.14 ms a step).
+  cudaLaunchAttribute order{};
+  order.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  order.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(s.hkv, batch);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
+  cfg.attrs = &order;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, attn_merge_kernel, s, seq_begin, batch, q, out, qk_scale_log2, w, (int)scores);
 }
 

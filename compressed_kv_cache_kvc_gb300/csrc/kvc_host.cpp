@@ -616,7 +616,8 @@ kvc_status kvc_decode_attention(kvc_cache* c, int32_t seq_begin, int32_t batch, 
   if (st0 != KVC_OK) return st0;
   if (kvc::launch_attention_merge(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
                                   static_cast<uint16_t*>(d_out), qk_scale_log2, w,
-                                  h2o ? kvc::kMergeAllScores : kvc::kMergeNoScores, st) != cudaSuccess)
+                                  h2o ? kvc::kMergeAllScores : kvc::kMergeNoScores, /*early=*/true, st) !=
+      cudaSuccess)
     return KVC_ERR_CUDA;
   ++launches;
   c->last_launches = launches;
@@ -775,7 +776,8 @@ kvc_status decode_step_impl(kvc_cache* c, int32_t seq_begin, int32_t batch, cons
     if (ensure_events(c) != KVC_OK) return KVC_ERR_CUDA;
     if (kvc::launch_attention_merge(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
                                     static_cast<uint16_t*>(d_out), qk_scale_log2, w,
-                                    h2o ? kvc::kMergeSinkScores : kvc::kMergeNoScores, st) != cudaSuccess)
+                                    h2o ? kvc::kMergeSinkScores : kvc::kMergeNoScores, /*early=*/false, st) !=
+        cudaSuccess)
       return KVC_ERR_CUDA;
     ++launches;
     est = static_cast<cudaStream_t>(evict_stream);

@@ -132,7 +132,7 @@ cudaError_t launch_attention_ring(const DevState& s, int seq_begin, int batch, c
 enum MergeScores { kMergeNoScores = 0, kMergeAllScores = 1, kMergeSinkScores = 2 };
 cudaError_t launch_attention_merge(const DevState& s, int seq_begin, int batch, const uint16_t* q,
                                    uint16_t* out, float qk_scale_log2, const AttnWork& w, MergeScores scores,
-                                   cudaStream_t st);
+                                   bool early, cudaStream_t st);
 
 struct SelectArgs {
   int mode, budget, recent, window;
