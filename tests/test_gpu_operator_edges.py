@@ -80,6 +80,48 @@ def test_a_replay_finds_a_sequence_empty():
     assert cache.read_status() == 0
 
 
+@pytest.mark.parametrize("hkv,lengths", [(2, [2000, 37, 700]), (1, [4000, 16, 1, 900, 20]), (8, [60, 3000])])
+def test_a_replay_of_unequal_lengths_at_others(hkv, lengths):
+    """Captured where the grid was cut to the pairs of these lengths, replayed
+    after a release and appends that turn them round."""
+    rng = np.random.default_rng(9)
+    nb, block = len(lengths), 16
+    cache = B._cache(4 * hkv, hkv, [8000] * nb, block, "int8")
+    draw = lambda b, n: T.to_dev_bf16(B._bits(rng, (b, hkv, n, 128)))  # noqa: E731
+    for b, n in enumerate(lengths):
+        cache.append(draw(1, n), draw(1, n), seq_begin=b)
+    q = T.to_dev_bf16(B._bits(rng, (nb, 4 * hkv, 128)))
+    out = torch.empty_like(q)
+    cache.decode_attention(q, softcap=5.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.decode_attention(q, out=out, softcap=5.0)
+
+    def check():
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        held = [b for b in range(nb) if cache.length(b)]
+        for b in range(nb):
+            if b not in held:
+                assert (got[b] == 0).all()
+                continue
+            want = cache.decode_attention(q[b:b + 1].contiguous(), seq_begin=b, softcap=5.0)
+            # (the same values; another grid's order of sums)
+            torch.testing.assert_close(got[b:b + 1].float(), want.float(), rtol=2 ** -7, atol=1e-3)
+
+    check()
+    cache.release(0)
+    check()
+    for b in range(1, nb):
+        n = 3000 // b
+        cache.append(draw(1, n), draw(1, n), seq_begin=b)
+    check()
+    cache.append(draw(1, 5), draw(1, 5))
+    check()
+    assert cache.read_status() == 0
+
+
 @pytest.mark.parametrize("cap", [1e-45, 1e-38, 3.4e38])
 def test_caps_at_the_ends_of_fp32(cap):
     """A cap near 0 leaves every score (and a zero product) at 0: the plain mean
