@@ -231,6 +231,12 @@ class KVCache:
         set to the prompt attention's column sums.  With key_begin or key_end
         (int32 [batch, n]), query i sees the keys [key_begin[i], key_end[i])
         instead (None: from 0, and up to itself)."""
+        if stream is not None:
+            # what is allocated below (a workspace given up on return) then
+            # belongs to that stream, as the kernels do
+            with torch.cuda.stream(stream):
+                return self.prefill(q, k, v, seq_begin, out, sm_scale, accumulate_h2o, workspace, None, key_begin,
+                                    key_end)
         _need(q, torch.bfloat16, "q", self.device)
         _need(k, torch.bfloat16, "k", self.device)
         _need(v, torch.bfloat16, "v", self.device)

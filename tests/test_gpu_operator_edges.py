@@ -214,6 +214,33 @@ def test_reads_on_another_stream():
     assert torch.equal(got_p, want_p) and torch.equal(got_a, want_a)
 
 
+def test_prefills_on_another_stream():
+    """A prefill's workspace is given up on return: it has to belong to the
+    stream that still uses it.  Prefills queued on a side stream, while the
+    current one allocates and fills blocks of the workspace's size, give what
+    they give alone."""
+    from compressed_kv_cache_kvc_gb300.cache import KVCache
+    rng = np.random.default_rng(10)
+    n, hq, hkv, count = 1100, 8, 2, 6
+    q, k, v = (T.to_dev_bf16(B._bits(rng, (1, h, n, 128))) for h in (hq, hkv, hkv))
+    begin = (torch.arange(n, device="cuda", dtype=torch.int32) // 300 * 300).view(1, n)
+    caches = [KVCache(hq, hkv, 8, 72, 1, 72) for _ in range(count + 1)]
+    for c in caches:
+        c.set_score_transform(softcap=20.0)
+    want = caches[-1].prefill(q, k, v, key_begin=begin)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for c in caches[:count]:
+        outs.append(c.prefill(q, k, v, key_begin=begin, stream=side))
+        nbytes = c.lib.kvc_prefill_masked_workspace_bytes(c.handle, 1, n) + 256
+        for _ in range(3):
+            torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for c, o in zip(caches, outs):
+        assert torch.equal(o, want) and c.read_status() == 0
+
+
 def test_one_workspace_call_after_call():
     """Prompts of different values through one workspace, one right behind
     another: no call reads what the one before or after it prepared."""
