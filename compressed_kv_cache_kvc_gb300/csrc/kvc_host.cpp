@@ -911,6 +911,9 @@ kvc_status prefill_transformed(kvc_cache* c, int32_t seq_begin, int32_t batch, i
     a.sums = reinterpret_cast<float*>(ws + w.sums);
     a.stats = reinterpret_cast<float*>(ws + w.stats);
     a.runs = reinterpret_cast<int4*>(ws + w.runs);
+    a.sum_parts = w.sum_parts;
+    a.sum_part = reinterpret_cast<float*>(ws + w.part);
+    a.sum_tickets = reinterpret_cast<int32_t*>(ws + w.tickets);
   }
   a.status = c->dev.counters + kvc::kCtrStatus;
   const bool trace = c->trace_start && c->trace_stop;
@@ -1001,6 +1004,9 @@ kvc_status kvc_prompt_attention(const kvc_prompt_params* p, const void* d_q, con
     a.sums = d_sums;
     a.stats = reinterpret_cast<float*>(ws + w.stats);
     a.runs = reinterpret_cast<int4*>(ws + w.runs);
+    a.sum_parts = w.sum_parts;
+    a.sum_part = reinterpret_cast<float*>(ws + w.part);
+    a.sum_tickets = reinterpret_cast<int32_t*>(ws + w.tickets);
   }
   a.status = d_status;
   return kvc::launch_prompt(a, static_cast<const uint16_t*>(d_q), static_cast<const uint16_t*>(d_k),

@@ -212,10 +212,14 @@ struct PromptArgs {
   uint16_t* v16;             // fp16 [batch][hkv][n][128]
   uint32_t* bad;             // [batch][hkv][tiles][4] keys whose V row is not finite
   int4* runs;                // [batch][tiles] bounds of the runs per 128 queries; null without sums
+  int sum_parts;             // CTAs per key tile and KV head of the column sums, each with some of the query heads
+  float* sum_part;           // [sum_parts][batch][hkv][n] when there are several
+  int32_t* sum_tickets;      // [batch][hkv][tiles]; zeroed by the first kernel
   int32_t* status;           // KVC_DEV_* bits
 };
 struct PromptWs {
-  size_t v16, bad, runs, stats, sums, total;
+  size_t v16, bad, runs, stats, sums, part, tickets, total;
+  int sum_parts;
 };
 PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums);
 cudaError_t launch_prompt(const PromptArgs& a, const uint16_t* q, const uint16_t* k, const uint16_t* v,

@@ -66,6 +66,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kvc_device.h"
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
   }
   __syncthreads();
   if (tid < 4) a.bad[((size_t)plane * tiles + tile) * 4 + tid] = sh_bad[tid];
+  if (tid == 0 && a.sum_parts > 1) a.sum_tickets[(size_t)plane * tiles + tile] = 0;
   if (a.runs != nullptr && plane % a.hkv == 0 && tid == 0)
     a.runs[(size_t)(plane / a.hkv) * tiles + tile] = make_int4(sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
 }
@@ -684,7 +686,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 //
 // One 320-thread CTA per (128-key tile, KV head, sequence), two per SM, keys
 // on the TMEM lanes: S^T = K Q^T (M 128, N 128), so thread t of a warpgroup
-// owns key t and adds in registers; no atomics, a fixed order.  (64 heads of
+// owns key t and adds in registers; a fixed order.  With few key tiles several
+// CTAs share one, each with some of the query heads; the last of them (a ticket)
+// adds their sums in order.  (64 heads of
 // 2,100 tokens, capped and biased: about 95 us, bound by the FMA pipe and the
 // unevenness of the blocks.)  Warpgroups 0
 // and 1 take alternate (query head, query tile) blocks, warp 8 loads the query
@@ -703,6 +707,7 @@ constexpr int kSOffBar = kSOffRed + kTile * 4;
 constexpr int kSBarK = 0, kSBarFull = 1, kSBarEmpty = 3, kSBarS = 5, kSBarSfree = 7, kSBarDone = 9, kSNumBars = 10;
 constexpr int kSumSmem = kSOffBar + 8 * kSNumBars + 16;
 constexpr uint32_t kSumCols = 256;
+constexpr size_t kSumCtas = 608;
 
 // The (query head, query tile) blocks some of whose queries see the keys [k0,
 // k1), in order, for a warp: 32 tiles' bounds are read at a time, one a lane (a
@@ -713,8 +718,8 @@ struct SeenBlocks {
   int g, qt, base;
   uint32_t left, whole;
   bool all;  // every query of the block sees every key
-  __device__ SeenBlocks(const int4* r, int t, int G, int a, int b, int l)
-      : runs(r), tiles(t), heads(G), k0(a), k1(b), lane(l), g(0), qt(0), base(-32), left(0), whole(0), all(false) {}
+  __device__ SeenBlocks(const int4* r, int t, int first, int end, int a, int b, int l)
+      : runs(r), tiles(t), heads(end), k0(a), k1(b), lane(l), g(first), qt(0), base(-32), left(0), whole(0), all(false) {}
   __device__ bool next() {
     while (left == 0) {
       base += 32;
@@ -740,17 +745,19 @@ template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kSumThreads, 2)
     prompt_sums_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
   extern __shared__ __align__(1024) uint8_t ssm[];
+  __shared__ int sh_last;
   const uint32_t base = saddr(ssm);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(ssm + kSOffBar + 8 * kSNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(ssm + kSOffBar + 8 * kSNumBars + 4);
   auto bar = [&](int i) { return base + kSOffBar + 8 * i; };
   const int n = a.n, G = a.group;
-  const int planes = a.hkv * a.batch, plane_kv = blockIdx.x % planes, kt = blockIdx.x / planes;
+  const int planes = a.hkv * a.batch, parts = a.sum_parts, rest = blockIdx.x % (planes * parts);
+  const int kt = blockIdx.x / (planes * parts), plane_kv = rest / parts, part = rest % parts;
   const int h = plane_kv % a.hkv, bl = plane_kv / a.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int k0 = kt * kTile, k1 = min(k0 + kTile, n);
   const int tiles = (n + kTile - 1) / kTile;
-  SeenBlocks blk(a.runs + (size_t)bl * tiles, tiles, G, k0, k1, lane);
+  SeenBlocks blk(a.runs + (size_t)bl * tiles, tiles, G * part / parts, G * (part + 1) / parts, k0, k1, lane);
 
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kSumCols));
@@ -942,9 +949,25 @@ __global__ void __launch_bounds__(kSumThreads, 2)
   float* red = reinterpret_cast<float*>(ssm + kSOffRed);
   if (tid < kTile) red[tid] = sum;
   __syncthreads();
-  if (tid >= kTile && tid < 2 * kTile && !*abort) {
-    const int t = tid - kTile, key = k0 + t;
-    if (key < n) a.sums[((size_t)bl * a.hkv + h) * n + key] = sum + red[t];
+  const bool mine = tid >= kTile && tid < 2 * kTile && k0 + tid - kTile < n && !*abort;
+  const size_t at = (size_t)plane_kv * n + k0 + tid - kTile;
+  if (parts == 1) {
+    if (mine) a.sums[at] = sum + red[tid - kTile];
+  } else {
+    // the last part of the key tile adds them up, in order
+    if (mine) a.sum_part[(size_t)part * planes * n + at] = sum + red[tid - kTile];
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      sh_last = atomicAdd(&a.sum_tickets[(size_t)plane_kv * tiles + kt], 1) == parts - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (sh_last && mine) {
+      float total = 0.0f;
+      for (int e = 0; e < parts; ++e) total += __ldcg(a.sum_part + (size_t)e * planes * n + at);
+      a.sums[at] = total;
+    }
   }
   if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSumCols));
 }
@@ -997,7 +1020,7 @@ cudaError_t launch_sums(const PromptArgs& a, const CUtensorMap& q, const CUtenso
   static int done[64] = {0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(prompt_sums_kernel<CAP, BIAS>), kSumSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((a.n + kTile - 1) / kTile * (a.hkv * a.batch)));
+  const dim3 grid((unsigned)((a.n + kTile - 1) / kTile * (a.hkv * a.batch * a.sum_parts)));
   prompt_sums_kernel<CAP, BIAS><<<grid, kSumThreads, kSumSmem, st>>>(a, q, k);
   return cudaGetLastError();
 }
@@ -1013,7 +1036,17 @@ PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums) {
   w.runs = w.bad + up(planes * tiles * 16);
   w.stats = w.runs + up(sums ? batch * tiles * 16 : 0);
   w.sums = w.stats + up(sums ? (size_t)batch * hq * n * 8 : 0);
-  w.total = w.sums + up(sums ? planes * n * 4 : 0);
+  // column sums with few key tiles and KV heads: several CTAs for each, with some
+  // of its query heads, so that there are about kSumCtas, two full waves (32 heads
+  // on 8 of 8,192 tokens 910 us with the attention, 984 with one CTA each, 981 at
+  // 304, 925 at 1,216; 2 x 14 heads on 2 of 1,529 tokens 68 against 155; every
+  // parts-th block instead of some heads: 926 and 74)
+  const size_t group = (size_t)(hq / hkv), each = planes * tiles;
+  w.sum_parts = sums ? (int)std::min(group, (kSumCtas + each - 1) / each) : 1;
+  const bool split = w.sum_parts > 1;
+  w.part = w.sums + up(sums ? planes * n * 4 : 0);
+  w.tickets = w.part + up(split ? w.sum_parts * planes * n * 4 : 0);
+  w.total = w.tickets + up(split ? each * 4 : 0);
   return w;
 }
 

@@ -505,8 +505,8 @@ typedef struct {
 } kvc_prompt_params;
 
 /* Workspace of kvc_prompt_attention (`sums`: whether d_sums is given): V in
- * fp16, 256 bytes a token and KV head, and with sums 8 bytes a token and query
- * head.  0 for sizes that are not positive. */
+ * fp16, 256 bytes a token and KV head, and with sums up to 12 bytes a token and
+ * query head.  0 for sizes that are not positive. */
 size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t n, int32_t sums);
 
 /*   d_q:   bf16 [batch][Hq][n][128];  d_k, d_v: bf16 [batch][Hkv][n][128];

@@ -260,3 +260,29 @@ def test_one_workspace_call_after_call():
     for i, g in enumerate(got):
         for x, y in zip(g, want[i % 4]):
             assert torch.equal(x.nan_to_num(123.0), y.nan_to_num(123.0)), i
+
+
+@pytest.mark.parametrize("batch,hq,hkv,n", [(1, 7, 1, 900), (2, 12, 2, 300), (1, 3, 1, 5), (1, 8, 8, 700)])
+def test_column_sums_shared_by_several_ctas(batch, hq, hkv, n):
+    """Few key tiles and KV heads: a key tile's sums come from several CTAs.  They
+    are the sum of the calls of one query head a KV head each, within the order
+    of the additions, and the same from call to call."""
+    from compressed_kv_cache_kvc_gb300 import prompt_attention
+    rng = np.random.default_rng(11)
+    q, k, v = (T.to_dev_bf16(B._bits(rng, (batch, h, n, 128))) for h in (hq, hkv, hkv))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, sums = prompt_attention(q, k, v, status=status, softcap=15.0, column_sums=True)
+    for _ in range(3):
+        o, s = prompt_attention(q, k, v, status=status, softcap=15.0, column_sums=True)
+        assert torch.equal(o, out) and torch.equal(s, sums)
+    group = hq // hkv
+    want = torch.zeros_like(sums, dtype=torch.float64)
+    for g in range(group):
+        heads = q[:, g::group].contiguous()
+        o, s = prompt_attention(heads, k, v, status=status, softcap=15.0, column_sums=True)
+        assert torch.equal(o, out[:, g::group])
+        want += s.double()
+    # both sides add up to n fp32 terms in [0, 1] a head: n 2^-24 of the sum each
+    assert ((sums.double() - want).abs() <= 2 * (n + group) * 2.0 ** -24 * want).all()
+    np.testing.assert_allclose(sums.sum().item(), batch * hq * n, rtol=1e-5)
+    assert status.item() == 0
