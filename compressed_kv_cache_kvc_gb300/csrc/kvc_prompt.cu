@@ -689,8 +689,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // owns key t and adds in registers; a fixed order.  With few key tiles several
 // CTAs share one, each with some of the query heads; the last of them (a ticket)
 // adds their sums in order.  (64 heads of
-// 2,100 tokens, capped and biased: about 95 us, bound by the FMA pipe and the
-// unevenness of the blocks.)  Warpgroups 0
+// 2,100 tokens, capped and biased: about 91 us, bound by the FMA pipe and the
+// unevenness of the blocks.)  A block's statistics have places of their own, and
+// its products' place is free once they are read, so that the next Q and S come
+// under a block's sums (40 heads on 8 of 2 x 4,000 tokens: 526 us with the
+// attention, 551 with Q's place held to the block's end).  Warpgroups 0
 // and 1 take alternate (query head, query tile) blocks, warp 8 loads the query
 // tiles and stages -m, 1 / l and the run per query, warp 9 issues the products.
 // Two queries go through each instruction (their -m and 1 / l are pairs in
@@ -700,11 +703,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 constexpr int kSumThreads = 320;
 constexpr int kSOffK = 0;
 constexpr int kSOffQ = kSOffK + kTileB;                    // 2 slots
-constexpr int kSOffStat = kSOffQ + 2 * kTileB;             // 2 x (128 x -m, 128 x 1 / l)
-constexpr int kSOffRun = kSOffStat + 2 * kTile * 8;        // 2 x 128 x (begin, end)
-constexpr int kSOffRed = kSOffRun + 2 * kTile * 8;         // 128 sums
+constexpr int kSStats = 4;                                 // places of a block's statistics and runs
+constexpr int kSOffStat = kSOffQ + 2 * kTileB;             // 4 x (128 x -m, 128 x 1 / l)
+constexpr int kSOffRun = kSOffStat + kSStats * kTile * 8;  // 4 x 128 x (begin, end)
+constexpr int kSOffRed = kSOffRun + kSStats * kTile * 8;   // 128 sums
 constexpr int kSOffBar = kSOffRed + kTile * 4;
-constexpr int kSBarK = 0, kSBarFull = 1, kSBarEmpty = 3, kSBarS = 5, kSBarSfree = 7, kSBarDone = 9, kSNumBars = 10;
+// mbarriers: K landed; a block's Q landed, its place free (per block % 2); S
+// complete, read (% 2); statistics there, read (% 4); all products complete
+constexpr int kSBarK = 0, kSBarFull = 1, kSBarEmpty = 3, kSBarS = 5, kSBarSfree = 7, kSBarStat = 9, kSBarStatfree = 13,
+              kSBarDone = 17, kSNumBars = 18;
 constexpr int kSumSmem = kSOffBar + 8 * kSNumBars + 16;
 constexpr uint32_t kSumCols = 256;
 constexpr size_t kSumCtas = 608;
@@ -765,10 +772,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
   }
   if (tid == 0) {
     for (int i = 0; i < kSNumBars; ++i) {
-      const uint32_t cnt = i >= kSBarFull && i < kSBarFull + 2     ? 2
-                           : i >= kSBarEmpty && i < kSBarEmpty + 2 ? 5
-                           : i >= kSBarSfree && i < kSBarSfree + 2 ? 4
-                                                                   : 1;
+      const uint32_t cnt = (i >= kSBarSfree && i < kSBarSfree + 2) || (i >= kSBarStatfree && i < kSBarStatfree + 4) ? 4 : 1;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(cnt));
     }
     *abort = 0;
@@ -819,8 +823,15 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         tma_load_3d(dst, &tm_q, 0, blk.qt * kTile, plane, b);
         tma_load_3d(dst + kBoxB, &tm_q, 64, blk.qt * kTile, plane, b);
       }
-      float* st = reinterpret_cast<float*>(ssm + kSOffStat) + x * 2 * kTile;
-      int2* rn = reinterpret_cast<int2*>(ssm + kSOffRun) + x * kTile;
+      const int y = it % kSStats;
+      if (it >= kSStats && !__all_sync(0xffffffffu, bar_wait(bar(kSBarStatfree + y),
+                                                             (uint32_t)(((it - kSStats) / kSStats) & 1), abort))) {
+        set_abort(a.status, abort);
+        ++it;  // (its Q is on the way)
+        break;
+      }
+      float* st = reinterpret_cast<float*>(ssm + kSOffStat) + y * 2 * kTile;
+      int2* rn = reinterpret_cast<int2*>(ssm + kSOffRun) + y * kTile;
 #pragma unroll
       for (int e = 0; e < kTile / 32; ++e) {
         const int i = lane + 32 * e;
@@ -830,7 +841,7 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         rn[i] = r[e];
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(bar(kSBarFull + x));
+      if (lane == 0) bar_arrive(bar(kSBarStat + y));
       ++it;
       more = blk.next();
       if (more) read();
@@ -874,8 +885,6 @@ __global__ void __launch_bounds__(kSumThreads, 2)
     // ------------------------------------------------------ sums over the queries
     const int x = warp >> 2, t = tid & (kTile - 1);
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kTile * x;
-    const float* st = reinterpret_cast<const float*>(ssm + kSOffStat) + x * 2 * kTile;
-    const int2* rn = reinterpret_cast<const int2*>(ssm + kSOffRun) + x * kTile;
     const int key = k0 + t;
     int g = -1;
     float slope2 = 0.0f;
@@ -886,7 +895,11 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         slope2 = slope_log2(a.mod, h * G + g);
       }
       const uint32_t par = (uint32_t)((it >> 1) & 1);
-      if (!__all_sync(0xffffffffu, bar_wait(bar(kSBarS + x), par, abort) && bar_wait(bar(kSBarFull + x), par, abort))) {
+      const int y = it % kSStats;
+      const float* st = reinterpret_cast<const float*>(ssm + kSOffStat) + y * 2 * kTile;
+      const int2* rn = reinterpret_cast<const int2*>(ssm + kSOffRun) + y * kTile;
+      if (!__all_sync(0xffffffffu, bar_wait(bar(kSBarS + x), par, abort) &&
+                                       bar_wait(bar(kSBarStat + y), (uint32_t)((it / kSStats) & 1), abort))) {
         set_abort(a.status, abort);
         break;
       }
@@ -898,6 +911,11 @@ __global__ void __launch_bounds__(kSumThreads, 2)
       for (int c0 = 0; c0 < kTile; c0 += 32) {
         float z[32];
         ld32(trow + c0, z);
+        if (c0 == kTile - 32) {  // the products may come over these
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar(kSBarSfree + x));
+        }
         auto nm = [&](int i) { return *reinterpret_cast<const f32x2*>(st + c0 + i); };
         const float d0 = (float)(q0 + c0 - key);
         const bool both = q0 + c0 < key - lane + 31;  // some key of the warp lies after the query
@@ -936,12 +954,8 @@ __global__ void __launch_bounds__(kSumThreads, 2)
       float ax, ay;
       unpack2(add2(acc[0], acc[1]), ax, ay);
       sum += ax + ay;
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
-        bar_arrive(bar(kSBarSfree + x));
-        bar_arrive(bar(kSBarEmpty + x));
-      }
+      if (lane == 0) bar_arrive(bar(kSBarStatfree + y));
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1038,8 +1052,8 @@ PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums) {
   w.sums = w.stats + up(sums ? (size_t)batch * hq * n * 8 : 0);
   // column sums with few key tiles and KV heads: several CTAs for each, with some
   // of its query heads, so that there are about kSumCtas, two full waves (32 heads
-  // on 8 of 8,192 tokens 910 us with the attention, 984 with one CTA each, 981 at
-  // 304, 925 at 1,216; 2 x 14 heads on 2 of 1,529 tokens 68 against 155; every
+  // on 8 of 8,192 tokens then 910 us with the attention, 984 with one CTA each, 981
+  // at 304, 925 at 1,216; 2 x 14 heads on 2 of 1,529 tokens 68 against 155; every
   // parts-th block instead of some heads: 926 and 74)
   const size_t group = (size_t)(hq / hkv), each = planes * tiles;
   w.sum_parts = sums ? (int)std::min(group, (kSumCtas + each - 1) / each) : 1;
