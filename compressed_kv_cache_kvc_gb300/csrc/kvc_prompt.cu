@@ -533,8 +533,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           ld32(t_s + 32 * c, z);
-          if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
-          if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, slope2, dist0 + 32.0f * c, beyond);
+          if (CAP && BIAS && !beyond) {  // (the cap ends in the bias's addition)
+            const f32x2 sl = pack2(slope2, slope2), two = pack2(2.0f, 2.0f);
+            f32x2 d = pack2(dist0 + 32.0f * c, dist0 + 32.0f * c + 1.0f);
+            chunk_cap_plus(a, z, chunk_most(z, 0.0f), [&](int) {
+              const f32x2 add = mul2(d, sl);
+              d = add2(d, two);
+              return add;
+            });
+          } else {
+            if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
+            if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, slope2, dist0 + 32.0f * c, beyond);
+          }
           if (masked) chunk_mask(z, run.x - k0 - 32 * c, run.y - k0 - 32 * c);
           if (BIAS) tmem_st32(t_s + 32 * c, z);
           mx = chunk_max(z, mx);
@@ -689,7 +699,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // owns key t and adds in registers; a fixed order.  With few key tiles several
 // CTAs share one, each with some of the query heads; the last of them (a ticket)
 // adds their sums in order.  (64 heads of
-// 2,100 tokens, capped and biased: about 91 us, bound by the FMA pipe and the
+// 2,100 tokens, capped and biased: about 88 us, bound by the FMA pipe and the
 // unevenness of the blocks.)  A block's statistics have places of their own, and
 // its products' place is free once they are read, so that the next Q and S come
 // under a block's sums (40 heads on 8 of 2 x 4,000 tokens: 526 us with the
@@ -919,16 +929,28 @@ __global__ void __launch_bounds__(kSumThreads, 2)
         auto nm = [&](int i) { return *reinterpret_cast<const f32x2*>(st + c0 + i); };
         const float d0 = (float)(q0 + c0 - key);
         const bool both = q0 + c0 < key - lane + 31;  // some key of the warp lies after the query
-        if (CAP && !BIAS) {
-          chunk_cap_plus(a, z, chunk_most(z, 0.0f), nm);
-        } else {
+        if (BIAS && both) {
           if (CAP) chunk_cap(a, z, chunk_most(z, 0.0f), 0.0f);
-          if (BIAS) chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, -slope2, d0, both);
-          const f32x2 sc = pack2(BIAS ? 1.0f : a.qk_scale_log2, BIAS ? 1.0f : a.qk_scale_log2);
+          chunk_bias(z, CAP ? 1.0f : a.qk_scale_log2, slope2, -slope2, d0, true);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            unpack2(BIAS ? add2(pack2(z[i], z[i + 1]), nm(i)) : fma2(pack2(z[i], z[i + 1]), sc, nm(i)), z[i],
-                    z[i + 1]);
+          for (int i = 0; i < 32; i += 2) unpack2(add2(pack2(z[i], z[i + 1]), nm(i)), z[i], z[i + 1]);
+        } else {
+          // what is added to a pair of scores: -m, less the bias
+          const f32x2 sl = pack2(-slope2, -slope2), two = pack2(2.0f, 2.0f);
+          f32x2 d = pack2(d0, d0 + 1.0f);
+          auto plus = [&](int i) {
+            if (!BIAS) return nm(i);
+            const f32x2 add = fma2(d, sl, nm(i));
+            d = add2(d, two);
+            return add;
+          };
+          if (CAP) {
+            chunk_cap_plus(a, z, chunk_most(z, 0.0f), plus);
+          } else {
+            const f32x2 sc = pack2(a.qk_scale_log2, a.qk_scale_log2);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) unpack2(fma2(pack2(z[i], z[i + 1]), sc, plus(i)), z[i], z[i + 1]);
+          }
         }
         if (whole) {
 #pragma unroll
