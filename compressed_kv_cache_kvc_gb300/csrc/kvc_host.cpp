@@ -614,10 +614,11 @@ kvc_status kvc_decode_attention(kvc_cache* c, int32_t seq_begin, int32_t batch, 
   if (st0 != KVC_OK) return st0;
   st0 = launch_ring(c, seq_begin, batch, d_q, qk_scale_log2, w, st, &launches);
   if (st0 != KVC_OK) return st0;
+  // (not early behind a trace event: the merge then follows the event, not the split)
+  const bool early = !(c->trace_start && c->trace_stop);
   if (kvc::launch_attention_merge(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
                                   static_cast<uint16_t*>(d_out), qk_scale_log2, w,
-                                  h2o ? kvc::kMergeAllScores : kvc::kMergeNoScores, /*early=*/true, st) !=
-      cudaSuccess)
+                                  h2o ? kvc::kMergeAllScores : kvc::kMergeNoScores, early, st) != cudaSuccess)
     return KVC_ERR_CUDA;
   ++launches;
   c->last_launches = launches;

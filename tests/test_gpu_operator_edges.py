@@ -286,3 +286,34 @@ def test_column_sums_shared_by_several_ctas(batch, hq, hkv, n):
     assert ((sums.double() - want).abs() <= 2 * (n + group) * 2.0 ** -24 * want).all()
     np.testing.assert_allclose(sums.sum().item(), batch * hq * n, rtol=1e-5)
     assert status.item() == 0
+
+
+def test_traced_decode_eager_and_captured():
+    """Trace events stand between the split and the merge: the merge is then
+    launched in order, and the results are the untraced ones."""
+    from compressed_kv_cache_kvc_gb300.cache import KVCache
+    rng = np.random.default_rng(12)
+    hq, hkv, n = 8, 2, 900
+    cache = KVCache(hq, hkv, 8, 64, 1, 64)
+    k = T.to_dev_bf16(B._bits(rng, (1, hkv, n, 128)))
+    cache.quantize_append(k, k)
+    cache.set_score_transform(softcap=12.0)
+    q = T.to_dev_bf16(B._bits(rng, (1, hq, 128)))
+    want = cache.decode_attention(q, accumulate_h2o=False)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record(), b.record()
+    cache.set_trace_events(a, b)
+    assert torch.equal(cache.decode_attention(q, accumulate_h2o=False), want)
+    torch.cuda.synchronize()
+    assert a.elapsed_time(b) > 0
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.decode_attention(q, out=out, accumulate_h2o=False)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    cache.set_trace_events(None, None)
+    assert torch.equal(cache.decode_attention(q, accumulate_h2o=False), want)
