@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
   const int G = s.group, hkv = s.hkv;
   const int r = lane >> 2, c = lane & 3;
   const long long T = (long long)hkv * cum[batch];
-  const int N = gridDim.x, cta = blockIdx.x;
+  const int N = PARTS ? (int)gridDim.x : stream_ctas(T, gridDim.x), cta = blockIdx.x;
+  if (cta >= N) return;
   // (a replayed graph may find a sequence empty)
   for (int i = cta; i < batch; i += N)
     if (len[i] <= 0)

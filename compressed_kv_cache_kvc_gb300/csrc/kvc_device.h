@@ -52,7 +52,14 @@ __device__ __forceinline__ void pages_prefix(const DevState& s, int seq_begin, i
   __syncthreads();
 }
 
-// CTA of the stream-K split that holds flattened page F (see AttnWork).
+// CTAs of a stream-K split of T pages (or units) that get some: all N, or, where
+// a graph captured at longer sequences finds fewer pages than its N CTAs, the
+// first T with one each.  (With all N the CTAs between a pair's first and last
+// could be without a page, and their partials never written.)
+__device__ __forceinline__ int stream_ctas(long long T, int N) { return T < N ? max((int)T, 1) : N; }
+
+// CTA of the stream-K split that holds flattened page F (see AttnWork); N =
+// stream_ctas(T, grid).
 __device__ __forceinline__ int cta_of_page(long long F, long long T, int N) {
   return (int)(((F + 1) * (long long)N - 1) / T);
 }
