@@ -228,8 +228,9 @@ __device__ __forceinline__ void merge_phase(const DevState& s, int seq_begin, in
   if (npg > 0) {
     const long long T = (long long)hkv * cum[batch];
     const long long Pf = (long long)hkv * cum[bl] + (long long)h * npg;
-    i_first = cta_of_page(Pf, T, w.ncta);
-    i_last = cta_of_page(Pf + npg - 1, T, w.ncta);
+    const int N = stream_ctas(T, w.ncta);
+    i_first = cta_of_page(Pf, T, N);
+    i_last = cta_of_page(Pf + npg - 1, T, N);
   }
   const uint16_t* sk = s.sink_k + ((size_t)b * hkv + h) * kSinks * kHeadDim;
   const uint16_t* sv = s.sink_v + ((size_t)b * hkv + h) * kSinks * kHeadDim;
