@@ -427,6 +427,12 @@ __global__ void __launch_bounds__(kReadThreads) block_read_kernel(BlockState s, 
 // The exact rows (sinks and open block, up to 3 + bt) are the pair's last
 // units: tiles of 16 bf16 rows read straight into the MMA fragments, P as two
 // bf16 parts (16 significant bits).
+// V may be any finite value, also where blocks and exact rows differ by all of
+// bf16's range: the accumulators are in units of 2^E, which follows the largest V
+// scale (of exact rows 1/128 of the largest |v|) as the maxima follow the scores,
+// and partial results are divided by their sum before they leave units of 2^E,
+// since the sum over a long sequence of values near the top of the range is
+// beyond fp32.
 // The CTA that finishes a pair last (an atomic ticket, no CTA waits) joins the
 // pair's partials in CTA order, so the result does not depend on the order of
 // completion.  (A warp per query head, eight rows of 16 bytes a lane in flight:
@@ -444,7 +450,7 @@ constexpr int kBStages = 4;
 constexpr int kBStage = 4096;  // K page, V page
 constexpr int kBSmem = kBWarps * kBStages * kBStage;
 constexpr float kBLazy = 4.0f;
-constexpr int kJoinRow = kHeadDim + 4;  // one warp's joined row: 128 sums, the maximum, the sum
+constexpr int kJoinRow = kHeadDim + 4;  // one warp's joined row: 128 means, the maximum, the sum
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -668,8 +674,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     float osum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float m0 = kNegBig, m1 = kNegBig, l0 = 0.0f, l1 = 0.0f;
     int E = 0;
-    bool e_set = false;
-    float sv_hi = 0.0f, inv2E = 1.0f;
+    float sv_hi = 0.0f, inv2E = 1.0f;  // (0: E not set yet)
 
     // slots (2r, 2r + 1) x heads (2c, 2c + 1): cap and bias; slot 2r is at
     // distance d0 from the query
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       }
       const float nm0 = fmaxf(m0, tm0), nm1 = fmaxf(m1, tm1);
       const float al0 = fast_exp2(m0 - nm0), al1 = fast_exp2(m1 - nm1);
-      const bool rescale_e = svm > sv_hi || (!e_set && svm > 0.0f);
+      const bool rescale_e = svm > sv_hi;
       const int nE = rescale_e ? min(max(exponent_of(svm), -126), 126) : E;
       const int dE = E - nE;
       const float f = dE >= -126 ? pow2i(min(dE, 127)) : 0.0f;
@@ -715,7 +720,6 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       m1 = nm1;
       if (rescale_e) {
         E = nE;
-        e_set = true;
         sv_hi = pow2i(min(E + 4, 127));
         inv2E = pow2i(-E);
       }
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         tm1 = fmaxf(tm1, fmaxf(acc[pp][1], acc[pp][3]));
         svm = fmaxf(svm, vs[pp]);
       }
-      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi || (!e_set && svm > 0.0f)))
+      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi))
         rescale(tm0, tm1, svm);
       uint32_t pb0[NP], pb1[NP];
 #pragma unroll
@@ -924,14 +928,37 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       }
       if (!on0) acc[0] = acc[1] = -INFINITY;
       if (!on1) acc[2] = acc[3] = -INFINITY;
+      __nv_bfloat162 vm2 = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        vm2 = __hmax2(vm2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i])));
+        vm2 = __hmax2(vm2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i])));
+      }
+      float svm = fmaxf(__low2float(vm2), __high2float(vm2)) * 0x1p-7f;
       const float tm0 = fmaxf(acc[0], acc[2]), tm1 = fmaxf(acc[1], acc[3]);
-      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy)) rescale(tm0, tm1, 0.0f);
+      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi)) {
+        svm = warp_max(svm);
+        rescale(tm0, tm1, svm);
+      }
       const float p0 = fast_exp2(acc[0] - m0), p1 = fast_exp2(acc[1] - m1);
       const float p2 = fast_exp2(acc[2] - m0), p3 = fast_exp2(acc[3] - m1);
       l0 += p0 + p2;
       l1 += p1 + p3;
-      // the P V operand in the accumulators' units (2^24 for offset codes, 2^E)
-      const float unit = pow2i(min(max((kOffset ? -24 : 0) - E, -126), 126));
+      // the P V operands in the accumulators' units (2^24 for offset codes, 2^E),
+      // the power on both where it is large (V that leaves bf16's range by it is
+      // nothing beside 2^E)
+      const int eu = (kOffset ? 24 : 0) + E, ev = eu > 64 ? -64 : eu < -64 ? 64 : 0;
+      if (ev != 0) {
+        const __nv_bfloat162 f = __float2bfloat162_rn(pow2i(ev));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i]), f);
+          __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i]), f);
+          wa[i] = *reinterpret_cast<const uint32_t*>(&x);
+          wc[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      const float unit = pow2i(-eu - ev);
       uint32_t h0, h1, q0, q1;
       split_bf16x2(p0 * unit, p1 * unit, h0, q0);
       split_bf16x2(p2 * unit, p3 * unit, h1, q1);
@@ -954,11 +981,12 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    const float f2E = pow2i(E);
     __syncthreads();  // every warp is done with its ring: reuse shared memory
     float* sm_m = reinterpret_cast<float*>(smem);
     float* sm_l = sm_m + kBWarps * kMaxGroup;
     float* sm_o = sm_l + kBWarps * kMaxGroup;  // [kBWarps][8][128]
+    int* sm_e = reinterpret_cast<int*>(sm_o + kBWarps * kMaxGroup * kHeadDim);
+    if (lane == 0) sm_e[warp] = E;
     if (r == 0) {
       sm_m[warp * kMaxGroup + 2 * c] = m0;
       sm_m[warp * kMaxGroup + 2 * c + 1] = m1;
@@ -973,10 +1001,10 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       float* o1 = o0 + kHeadDim;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o0[2 * j] = (oacc[j][0] * sA - b0) * f2E;
-        o0[2 * j + 1] = (oacc[j][2] * sA - b0) * f2E;
-        o1[2 * j] = (oacc[j][1] * sA - b1) * f2E;
-        o1[2 * j + 1] = (oacc[j][3] * sA - b1) * f2E;
+        o0[2 * j] = oacc[j][0] * sA - b0;
+        o0[2 * j + 1] = oacc[j][2] * sA - b0;
+        o1[2 * j] = oacc[j][1] * sA - b1;
+        o1[2 * j + 1] = oacc[j][3] * sA - b1;
       }
     }
     __syncthreads();
@@ -988,6 +1016,9 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     const long long slot = PARTS ? F : (long long)bl * hkv + h + cta;
     const int d = threadIdx.x;  // 128 threads = head_dim
     uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
+    int e_most = sm_e[0];
+#pragma unroll
+    for (int ww = 1; ww < kBWarps; ++ww) e_most = max(e_most, sm_e[ww]);
     for (int g = 0; g < G; ++g) {
       float M = kNegBig;
 #pragma unroll
@@ -996,11 +1027,12 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
 #pragma unroll
       for (int ww = 0; ww < kBWarps; ++ww) {
         const float wt = fast_exp2(sm_m[ww * kMaxGroup + g] - M);
-        o += wt * sm_o[((size_t)ww * kMaxGroup + g) * kHeadDim + d];
+        o += wt * pow2i(max(sm_e[ww] - e_most, -126)) * sm_o[((size_t)ww * kMaxGroup + g) * kHeadDim + d];
         l += wt * sm_l[ww * kMaxGroup + g];
       }
+      o = l != 0.0f ? o * (1.0f / l) * pow2i(e_most) : 0.0f;
       if (cnt == 1) {
-        orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(l != 0.0f ? o * (1.0f / l) : 0.0f));
+        orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
       } else {
         const size_t ps = (size_t)slot * G + g;
         a.part_o[ps * kHeadDim + d] = o;
@@ -1036,9 +1068,13 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
             const bool on = j0 + lane < mine;
             const float2 x = on ? __ldcg(ml + (size_t)(share + wph * (j0 + lane)) * G) : make_float2(kNegBig, 0.0f);
             const float top = fmaxf(M, warp_max(x.x));
-            const float al = fast_exp2(M - top), wt = on ? fast_exp2(x.x - top) : 0.0f;
+            // the mean so far and the parts' shares of the new one
+            float al = l * fast_exp2(M - top), wt = on ? fast_exp2(x.x - top) * x.y : 0.0f;
             M = top;
-            l = l * al + warp_sum(wt * x.y);
+            l = al + warp_sum(wt);
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            al *= inv;
+            wt *= inv;
             o.x *= al; o.y *= al; o.z *= al; o.w *= al;
             for (int i0 = 0; i0 < min(32, mine - j0); i0 += 8) {
               float4 y[8];
@@ -1061,10 +1097,9 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
               sm_j[warp * kJoinRow + kHeadDim + 1] = l;
             }
           } else {
-            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
             uint2 w;
-            w.x = pack_bf16x2(o.x * inv, o.y * inv);
-            w.y = pack_bf16x2(o.z * inv, o.w * inv);
+            w.x = pack_bf16x2(o.x, o.y);
+            w.y = pack_bf16x2(o.z, o.w);
             *reinterpret_cast<uint2*>(out + ((size_t)bl * s.hq + h * G + g) * kHeadDim + 4 * lane) = w;
           }
         }
@@ -1074,12 +1109,13 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
             const float* row = sm_j + g * wph * kJoinRow;
             float M = kNegBig, o = 0.0f, l = 0.0f;
             for (int i = 0; i < wph; ++i) M = fmaxf(M, row[i * kJoinRow + kHeadDim]);
-            for (int i = 0; i < wph; ++i) {
-              const float wt = fast_exp2(row[i * kJoinRow + kHeadDim] - M);
-              o += wt * row[i * kJoinRow + d];
-              l += wt * row[i * kJoinRow + kHeadDim + 1];
-            }
-            orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(l != 0.0f ? o * (1.0f / l) : 0.0f));
+            for (int i = 0; i < wph; ++i)
+              l += fast_exp2(row[i * kJoinRow + kHeadDim] - M) * row[i * kJoinRow + kHeadDim + 1];
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            for (int i = 0; i < wph; ++i)
+              o += fast_exp2(row[i * kJoinRow + kHeadDim] - M) * row[i * kJoinRow + kHeadDim + 1] * inv *
+                   row[i * kJoinRow + d];
+            orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
           }
         }
         if (threadIdx.x == 0) s.tickets[b * hkv + h] = 0;
