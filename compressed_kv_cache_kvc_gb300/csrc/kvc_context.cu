@@ -121,7 +121,7 @@ constexpr int kRingStage = 2 * 16 * kRingRow * 2;
 // held to 168 registers (three CTAs per SM, as the INT4 and FP8 forms
 // without a window reach unbounded): it is latency-bound, and unbounded it
 // took 239 and 255 registers and ran two CTAs per SM; bounded it spills
-// nothing.  Pass 0 over INT4 codes is held to 96 registers (five CTAs per
+// nothing (INT4 with a window 28 bytes).  Pass 0 over INT4 codes is held to 96 registers (five CTAs per
 // SM instead of four, no spills; over 8-bit codes that was slower).  The
 // other forms keep the compiler's own choice (a minimum of 0 CTAs per SM
 // states none; a minimum of 1 made it spend up to 255 registers on pass 0
@@ -665,6 +665,22 @@ __global__ void __launch_bounds__(kCtxThreads,
       for (int sl = npages * kPage + threadIdx.x; sl < L.S1; sl += kCtxThreads) colsum[kSinks + sl] = 0.0f;
     }
 
+    // a sum over the pool as a plain value: the code offset comes out (INT4: odd
+    // N-tiles carry the 16x high nibbles), 2^E goes in
+    auto plain = [&](int j, int e) {
+      const float sc = kOffset ? (BITS == 4 && (j & 1) ? 0x1p20f : 0x1p24f) : 1.0f;
+      return (oacc[j][e] * sc - (kOffset ? kOffV * osum[2 * (e >> 1)] : 0.0f)) * pow2i(E);
+    };
+    if (PASS == 1 && WIN) {
+      // the window's tokens are added to plain values, whatever their size beside
+      // the pool's (in the accumulators' own units the power of two that brings P
+      // there is out of range next to V of 1e33 and more)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oacc[j][e] = plain(j, e);
+    }
+
     // ---- the bf16 window (hybrid precision): tiles of 16 positions from
     // rlo, K and V exact in bf16 (bf16 MMA; the query rows again as bf16 A
     // fragments, q' = q 2^e being exact in bf16 too)
@@ -696,9 +712,6 @@ __global__ void __launch_bounds__(kCtxThreads,
       }
       const float cr_lo = qk_scale * pow2i(-e_row[0]), cr_hi = qk_scale * pow2i(-e_row[1]);
       const int re_lo = ok_lo ? ctx_ring_end(L, i_lo) : 0, re_hi = ok_hi ? ctx_ring_end(L, i_hi) : 0;
-      // the PV operand of window tokens: p in the units of the pool's
-      // accumulators (their sum is scaled by 2^24 (2^20) and 2^E at the end)
-      const float rscale = pow2i(max((kOffset ? -24 : 0) - E, -126));
       const uint16_t* rk = s.ring_k + ((size_t)b * hkv + h) * W * kHeadDim;
       const uint16_t* rv = s.ring_v + ((size_t)b * hkv + h) * W * kHeadDim;
       auto ring_issue = [&](int u) {
@@ -793,10 +806,10 @@ __global__ void __launch_bounds__(kCtxThreads,
               cs_t[2 * t + 1] = pr[t][1] + pr[t][3];
             }
             uint32_t ph[4], pl[4];
-            split_bf16x2(pr[0][0] * rscale, pr[0][1] * rscale, ph[0], pl[0]);
-            split_bf16x2(pr[0][2] * rscale, pr[0][3] * rscale, ph[1], pl[1]);
-            split_bf16x2(pr[1][0] * rscale, pr[1][1] * rscale, ph[2], pl[2]);
-            split_bf16x2(pr[1][2] * rscale, pr[1][3] * rscale, ph[3], pl[3]);
+            split_bf16x2(pr[0][0], pr[0][1], ph[0], pl[0]);
+            split_bf16x2(pr[0][2], pr[0][3], ph[1], pl[1]);
+            split_bf16x2(pr[1][0], pr[1][1], ph[2], pl[2]);
+            split_bf16x2(pr[1][2], pr[1][3], ph[3], pl[3]);
             // V rows 2tq, 2tq+1, 2tq+8, 2tq+9 at head dims 16g .. 16g+15
             uint32_t xr[4][8];
             const int vr[4] = {2 * tq, 2 * tq + 1, 2 * tq + 8, 2 * tq + 9};
@@ -811,12 +824,8 @@ __global__ void __launch_bounds__(kCtxThreads,
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-              uint32_t b0 = prmt(xr[0][j >> 1], xr[1][j >> 1], sel);
-              uint32_t b1 = prmt(xr[2][j >> 1], xr[3][j >> 1], sel);
-              if (kOffset && BITS == 4 && (j & 1)) {  // these N-tiles hold 16x values (INT4 high nibbles)
-                b0 = bf16x2_times16(b0);
-                b1 = bf16x2_times16(b1);
-              }
+              const uint32_t b0 = prmt(xr[0][j >> 1], xr[1][j >> 1], sel);
+              const uint32_t b1 = prmt(xr[2][j >> 1], xr[3][j >> 1], sel);
               mma16816_bf16(oacc[j], ph[0], ph[1], ph[2], ph[3], b0, b1);
               mma16816_bf16(oacc[j], pl[0], pl[1], pl[2], pl[3], b0, b1);
             }
@@ -897,14 +906,12 @@ __global__ void __launch_bounds__(kCtxThreads,
       if (active) {
         // output rows r_lo / r_hi, head dims 32tq + j (j < 16: N-tile j, column
         // 2tq) and 32tq + 16 + j (column 2tq + 1): 64 contiguous bytes each
-        const float f2E = pow2i(E);
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
           const int row = rr ? r_hi : r_lo;
           if (!(rr ? ok_hi : ok_lo)) continue;
           const int i = row / G, gq = row % G;
           uint16_t* orow = a.out + (((size_t)bl * s.hq + h * G + gq) * n + i) * kHeadDim + 32 * tq;
-          const float bias = kOffset ? kOffV * osum[2 * rr] : 0.0f;
           uint32_t packed[16];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -914,9 +921,7 @@ __global__ void __launch_bounds__(kCtxThreads,
 #pragma unroll
               for (int jj = 0; jj < 2; ++jj) {
                 const int jt = j + jj;
-                // INT4: odd N-tiles carry the 16x high nibbles
-                const float sc = kOffset ? (BITS == 4 && (jt & 1) ? 0x1p20f : 0x1p24f) : 1.0f;
-                float o = (oacc[jt][2 * rr + half] * sc - bias) * f2E;
+                float o = WIN ? oacc[jt][2 * rr + half] : plain(jt, 2 * rr + half);
                 const int d = 32 * tq + 16 * half + jt;
 #pragma unroll
                 for (int sk = 0; sk < kSinks; ++sk)

@@ -100,12 +100,6 @@ __device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uin
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
-// bf16 pair times 16 (exact: a power of two)
-__device__ __forceinline__ uint32_t bf16x2_times16(uint32_t v) {
-  __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&v);
-  x = __hmul2(x, __floats2bfloat162_rn(16.0f, 16.0f));
-  return *reinterpret_cast<uint32_t*>(&x);
-}
 
 // Integer codes enter the MMA as fp16 subnormals: a field of u < 1024 in the
 // low mantissa bits of an fp16 (exponent bits zero) is exactly u * 2^-24.
