@@ -908,6 +908,7 @@ kvc_status prefill_transformed(kvc_cache* c, int32_t seq_begin, int32_t batch, i
   a.out = static_cast<uint16_t*>(d_out);
   a.v16 = reinterpret_cast<uint16_t*>(ws + w.v16);
   a.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+  a.info = reinterpret_cast<uint32_t*>(ws + w.info);
   if (h2o) {
     a.sums = reinterpret_cast<float*>(ws + w.sums);
     a.stats = reinterpret_cast<float*>(ws + w.stats);
@@ -1001,6 +1002,7 @@ kvc_status kvc_prompt_attention(const kvc_prompt_params* p, const void* d_q, con
   a.out = static_cast<uint16_t*>(d_out);
   a.v16 = reinterpret_cast<uint16_t*>(ws + w.v16);
   a.bad = reinterpret_cast<uint32_t*>(ws + w.bad);
+  a.info = reinterpret_cast<uint32_t*>(ws + w.info);
   if (sums) {
     a.sums = d_sums;
     a.stats = reinterpret_cast<float*>(ws + w.stats);

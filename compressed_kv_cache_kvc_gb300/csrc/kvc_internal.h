@@ -209,7 +209,8 @@ struct PromptArgs {
   uint16_t* out;             // bf16 [batch][hq][n][128]
   float* sums;               // [batch][hkv][n] column sums, or null
   float* stats;              // [batch][hq][n][2] row (max, sum); null without sums
-  uint16_t* v16;             // fp16 [batch][hkv][n][128]
+  uint16_t* v16;             // fp16 [batch][hkv][n][128], times a power of two where all are small
+  uint32_t* info;            // [batch][hkv][tiles] what is rare about 128 keys of V, that power
   uint32_t* bad;             // [batch][hkv][tiles][4] keys whose V row is not finite
   int4* runs;                // [batch][tiles] bounds of the runs per 128 queries; null without sums
   int sum_parts;             // CTAs per key tile and KV head of the column sums, each with some of the query heads
@@ -218,7 +219,7 @@ struct PromptArgs {
   int32_t* status;           // KVC_DEV_* bits
 };
 struct PromptWs {
-  size_t v16, bad, runs, stats, sums, part, tickets, total;
+  size_t v16, bad, info, runs, stats, sums, part, tickets, total;
   int sum_parts;
 };
 PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums);

@@ -8,10 +8,10 @@
 // probabilities over the queries and the query heads of its KV head.
 //
 // Three kernels:
-//   prompt_prep_kernel   V from bf16 to fp16 in the workspace (exact below
-//                        2^16 and above the fp16 subnormals), the keys whose V
-//                        row is not finite as bit masks, the runs' bounds per
-//                        128-query tile;
+//   prompt_prep_kernel   V from bf16 to fp16 in the workspace, times a power of
+//                        two where a (sequence, KV head) holds nothing from 2^-6
+//                        on, the keys whose V row is not finite as bit masks, the
+//                        runs' bounds per 128-query tile;
 //   prompt_fwd_kernel    outputs and (for the sums) row statistics;
 //   prompt_sums_kernel   column sums from the row statistics.
 //
@@ -59,6 +59,10 @@
 // a warp sees whole take no mask.  Masked scores are replaced before the
 // maximum, and P is exactly 0 there; V rows that are not finite enter the
 // product as 0 and give NaN only to the rows that see them.
+// V in fp16 is exact from 2^-14 (bf16 has 8 bits) to 2^16 and off by at most 2^-25
+// below.  Where the largest |v| of a (sequence, KV head) lies below 2^-6 all of its
+// V enter times the power of two that brings it to [2^14, 2^15), and O leaves
+// divided by it: a value is off by at most 2^-19 of that largest one.
 //
 // Synchronisation: mbarriers, every wait bounded as in the prefill kernels (a
 // wait that runs out sets KVC_DEV_WAIT_TIMEOUT, all roles leave, the TMEM is
@@ -104,6 +108,8 @@ constexpr int kFwdSmem = kFOffMax + 2 * 2 * kTile * 4;
 constexpr int kNbTile = 1;                           // named barriers of a query tile's warps: 1, 2
 constexpr uint32_t kFwdCols = 512;
 
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
 __device__ __forceinline__ void set_abort(int* status, volatile int* abort) {
   if (!*abort) {
     *abort = 1;
@@ -121,9 +127,14 @@ __device__ __forceinline__ int2 run_of(const PromptArgs& a, int bl, int i) {
 
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
+constexpr float kSmallV = 0x1p-6f;
+// what the forward has to know of a tile of V: whether a row is not finite, and (from
+// bit kInfoShift on) the exponent of its power of two
+constexpr uint32_t kInfoBad = 1;
+constexpr int kInfoShift = 1;
 
 __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a, const uint16_t* __restrict__ v) {
-  __shared__ uint32_t sh_bad[4];
+  __shared__ uint32_t sh_bad[4], sh_top;
   __shared__ int sh_run[4];
   launch_dependents();
   const int tiles = (a.n + kTile - 1) / kTile;
@@ -135,6 +146,7 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
     sh_run[1] = 0;
     sh_run[2] = 0;
     sh_run[3] = INT_MAX;
+    sh_top = 0;
   }
   __syncthreads();
   // 16 bytes a lane, 16 lanes a row, 16 rows a pass
@@ -146,25 +158,32 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
   for (int i = 0; i < 8; ++i)
     if (r0 + 16 * i < rows) w[i] = src[(size_t)(r0 + 16 * i) * 16];
   bool range = false;
+  uint32_t top = 0;  // the largest finite magnitude, as fp32 bits
+  auto convert = [&](float scale) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = r0 + 16 * i;
-    bool bad = false;
-    if (r < rows) {
-      uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 16 * i;
+      bool bad = false;
+      if (r < rows) {
+        uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float lo = bf16f(x[e] & 0xFFFFu), hi = bf16f(x[e] >> 16);
-        range |= !(fabsf(lo) < 65536.0f) || !(fabsf(hi) < 65536.0f);
-        if ((x[e] & 0x7F80u) == 0x7F80u) bad = true, lo = 0.0f;
-        if ((x[e] & 0x7F800000u) == 0x7F800000u) bad = true, hi = 0.0f;
-        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(x[e]) : "f"(hi), "f"(lo));
+        for (int e = 0; e < 4; ++e) {
+          float lo = bf16f(x[e] & 0xFFFFu), hi = bf16f(x[e] >> 16);
+          range |= !(fabsf(lo) < 65536.0f) || !(fabsf(hi) < 65536.0f);
+          if ((x[e] & 0x7F80u) == 0x7F80u) bad = true, lo = 0.0f;
+          if ((x[e] & 0x7F800000u) == 0x7F800000u) bad = true, hi = 0.0f;
+          top = max(top, max(__float_as_uint(fabsf(lo)), __float_as_uint(fabsf(hi))));
+          asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(x[e]) : "f"(hi * scale), "f"(lo * scale));
+        }
+        dst[(size_t)r * 16] = make_uint4(x[0], x[1], x[2], x[3]);
       }
-      dst[(size_t)r * 16] = make_uint4(x[0], x[1], x[2], x[3]);
+      const uint32_t vote = __ballot_sync(0xffffffffu, bad);
+      if (vote != 0 && (lane & 15) == 0 && ((vote >> lane) & 0xFFFFu) != 0) atomicOr(&sh_bad[r >> 5], 1u << (r & 31));
     }
-    const uint32_t vote = __ballot_sync(0xffffffffu, bad);
-    if (vote != 0 && (lane & 15) == 0 && ((vote >> lane) & 0xFFFFu) != 0) atomicOr(&sh_bad[r >> 5], 1u << (r & 31));
-  }
+  };
+  convert(1.0f);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) atomicMax(&sh_top, top);
   if (range) atomicOr(a.status, kDevPrefillRange);
   // bounds of the runs of query tile `tile`, once per sequence
   if (a.runs != nullptr && plane % a.hkv == 0 && tid < kTile && tid < rows) {
@@ -178,7 +197,38 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
     atomicMin(&sh_run[3], any ? run.y : 0);
   }
   __syncthreads();
+  int shift = 0;
+  if (sh_top != 0 && sh_top < __float_as_uint(kSmallV)) {
+    // nothing from 2^-6 on in this tile (rare): is there anywhere in the plane?  The
+    // CTA looks from the next tile on until it finds some; where there is none every
+    // CTA of the plane with other values than zeros comes to the same power
+    const uint4* all = reinterpret_cast<const uint4*>(v + (size_t)plane * a.n * kHeadDim);
+    for (int t = 1; t < tiles && sh_top < __float_as_uint(kSmallV); ++t) {
+      const int other = (tile + t) % tiles;
+      const size_t end = min((size_t)(other + 1) * kTile, (size_t)a.n) * 16;
+      for (size_t i = (size_t)other * kTile * 16 + tid; i < end; i += kPrepThreads) {
+        const uint4 y = all[i];
+        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = (x[e] << 16) & 0x7FFF0000u, hi = x[e] & 0x7FFF0000u;
+          top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      __syncthreads();  // (every thread has read sh_top)
+      if (lane == 0) atomicMax(&sh_top, top);
+      __syncthreads();
+    }
+    if (sh_top < __float_as_uint(kSmallV)) {
+      shift = min(14 - ((int)(sh_top >> 23) - 127), 126);
+      convert(pow2(shift));
+    }
+  }
   if (tid < 4) a.bad[((size_t)plane * tiles + tile) * 4 + tid] = sh_bad[tid];
+  if (tid == 0)
+    a.info[(size_t)plane * tiles + tile] =
+        (sh_bad[0] | sh_bad[1] | sh_bad[2] | sh_bad[3] ? kInfoBad : 0) | (uint32_t)shift << kInfoShift;
   if (tid == 0 && a.sum_parts > 1) a.sum_tickets[(size_t)plane * tiles + tile] = 0;
   if (a.runs != nullptr && plane % a.hkv == 0 && tid == 0)
     a.runs[(size_t)(plane / a.hkv) * tiles + tile] = make_int4(sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
@@ -496,18 +546,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = trow + kTile * x + kKeys * odd, t_o = trow + 256 + kTile * x;
     const float slope2 = BIAS ? slope_log2(a.mod, hqi) : 0.0f;
-    const size_t bad_row = (size_t)plane_kv * ((n + kTile - 1) / kTile) * 4;  // a word per 32 keys
+    const size_t info_row = (size_t)plane_kv * ((n + kTile - 1) / kTile);
     float* sh_m = reinterpret_cast<float*>(fsm + kFOffMax) + x * 2 * kTile + row;
     const int bar_m = kFBarM + 8 * x + (warp & 3);  // + 4 * parity
     const int n_x = hi - lo;
     bool ok = true, poison = false;
-    // whether any V row of the tiles ahead is not finite (under the first loads:
-    // a mask read in the loop would put a global load's latency into every tile)
+    // what is rare about the tiles of V ahead (under the first loads: a word read
+    // in the loop would put a global load's latency into every tile); tiles of a
+    // plane have one power of two, or none where they hold nothing but zeros
     wait_for_previous();
-    uint32_t any_bad = 0;
-    for (int j = 2 * lo + lane; j < 2 * hi; j += 32)
-      if (32 * j < n) any_bad |= a.bad[bad_row + j];
-    any_bad = __reduce_or_sync(0xffffffffu, any_bad);
+    uint32_t rare = 0;
+    for (int j = lo / 2 + lane; j < (hi + 1) / 2; j += 32) rare |= a.info[info_row + j];
+    rare = __reduce_or_sync(0xffffffffu, rare);
     auto wait = [&](int b, uint32_t par) {
       if (!__all_sync(0xffffffffu, bar_try(bar(b), par)) && !__all_sync(0xffffffffu, bar_wait(bar(b), par, abort))) {
         ok = false;
@@ -607,10 +657,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           st16(t_o + c0, t);
         }
       }
-      if (any_bad) {  // V rows that are not finite (rare)
+      if (rare & kInfoBad) {  // V rows that are not finite
 #pragma unroll 1
         for (int e = 0; e < kKeys && k0 + e < n; ++e)
-          if ((a.bad[bad_row + (k0 + e) / 32] >> (e & 31)) & 1u) poison |= k0 + e >= run.x && k0 + e < run.y;
+          if ((a.bad[info_row * 4 + (k0 + e) / 32] >> (e & 31)) & 1u) poison |= k0 + e >= run.x && k0 + e < run.y;
       }
       // P (fp16) over the front of the products: chunk c's 16 columns lie before
       // the products of chunk c + 1
@@ -662,7 +712,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // the output takes Q's place in shared memory (every S of the tile is
       // complete) and leaves by TMA, 32 rows of 64 dims a warp: stores of a row
       // a thread took 2800 cycles of the load-store unit a block
-      const float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a row that sees nothing is 0
+      float inv = total != 0.0f ? 1.0f / total : 0.0f;  // a row that sees nothing is 0
+      // V's power of two comes out, in two steps where 1 / l over it would be subnormal
+      const int shift = (int)(rare >> kInfoShift), down = max(shift - 60, 0);
+      if (shift != 0) inv *= pow2(down - shift);
       uint8_t* orow = fsm + kFOffQ + x * kTileB + odd * kBoxB + row * 128;
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 32) {
@@ -672,6 +725,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) t[e] = 0.0f;
+        }
+        if (down != 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) t[e] *= pow2(-down);
         }
         uint32_t w[16];
 #pragma unroll
@@ -1079,7 +1136,8 @@ PromptWs prompt_ws(int batch, int hq, int hkv, int n, bool sums) {
   PromptWs w{};
   w.v16 = 0;
   w.bad = up(planes * n * kHeadDim * 2);
-  w.runs = w.bad + up(planes * tiles * 16);
+  w.info = w.bad + up(planes * tiles * 16);
+  w.runs = w.info + up(planes * tiles * 4);
   w.stats = w.runs + up(sums ? batch * tiles * 16 : 0);
   w.sums = w.stats + up(sums ? (size_t)batch * hq * n * 8 : 0);
   // column sums with few key tiles and KV heads: several CTAs for each, with some

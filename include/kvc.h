@@ -505,8 +505,8 @@ typedef struct {
 } kvc_prompt_params;
 
 /* Workspace of kvc_prompt_attention (`sums`: whether d_sums is given): V in
- * fp16, 256 bytes a token and KV head, and with sums up to 12 bytes a token and
- * query head.  0 for sizes that are not positive. */
+ * fp16, 256 bytes a token and KV head (and 20 for each 128 of them), and with sums
+ * up to 12 bytes a token and query head.  0 for sizes that are not positive. */
 size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t n, int32_t sums);
 
 /*   d_q:   bf16 [batch][Hq][n][128];  d_k, d_v: bf16 [batch][Hkv][n][128];
@@ -516,7 +516,11 @@ size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t nu
  *   d_status: one i32 on the device; KVC_DEV_* bits are or'ed into it
  *   (KVC_DEV_WAIT_TIMEOUT, KVC_DEV_PREFILL_RANGE), never cleared.
  * Runs are clamped to [0, n); products are bf16 x bf16 (Q K^T, exact) and fp16
- * (P V, P rounded to 11 bits), sums fp32.  A K or Q value that is not finite
+ * (P V, P rounded to 11 bits), sums fp32.  V in fp16 is exact from 2^-14 on and
+ * off by at most 2^-25 below; in a (sequence, KV head) whose |v| all lie below
+ * 2^-6 it enters times a power of two.  So a value is off by at most 2^-19 of the
+ * largest finite |v| of its (sequence, KV head).  Values of 65536 and more
+ * saturate and set KVC_DEV_PREFILL_RANGE.  A K or Q value that is not finite
  * makes the rows that see it not finite; a row that sees a key whose V row
  * holds a NaN or an infinity is NaN; rows that do not see them are not
  * touched by them (the status bit KVC_DEV_PREFILL_RANGE is set all the same).
