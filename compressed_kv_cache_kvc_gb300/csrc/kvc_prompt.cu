@@ -71,6 +71,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kvc_device.h"
@@ -1161,8 +1162,9 @@ cudaError_t launch_prompt_scores(const DevState& s, int seq_begin, int batch, in
 }
 
 // The degree-2 polynomial takes q . k itself: x (c0 + u (c1 + ...)), u = x^2, so
-// its coefficients carry powers of y_scale up to the seventh; a y_scale for which
-// those leave fp32's range (caps no model uses) goes without it.
+// its coefficients carry powers of y_scale up to the seventh times the cap: a
+// y_scale far from 1, or coefficients beyond fp32's normal range (caps no model
+// uses), go without it.
 void prompt_polynomials(PromptArgs* a) {
   a->close_max = a->mid_max = -1.0f;
   const double ys = a->mod.y_scale, c2 = a->mod.c2;
@@ -1171,13 +1173,16 @@ void prompt_polynomials(PromptArgs* a) {
   a->mid[0] = (float)c2;
   for (int i = 0; i < 9; ++i) a->mid[i + 1] = (float)(c2 * kCapP8[i]);
   if (ys < 5e-4 || ys > 1e3) return;
-  a->close_max = (float)(kCapClose / ys);
-  double pw = ys;
-  a->close[0] = (float)(c2 * pw);
+  double pw = ys, c[4] = {c2 * pw};
   for (int i = 0; i < 3; ++i) {
     pw *= ys * ys;
-    a->close[i + 1] = (float)(c2 * kCapP2[i] * pw);
+    c[i + 1] = c2 * kCapP2[i] * pw;
   }
+  for (int i = 0; i < 4; ++i) {
+    if (!(std::abs(c[i]) >= 1e-37 && std::abs(c[i]) <= 1e37)) return;
+    a->close[i] = (float)c[i];
+  }
+  a->close_max = (float)(kCapClose / ys);
 }
 
 cudaError_t launch_prompt(const PromptArgs& args, const uint16_t* q, const uint16_t* k, const uint16_t* v,

@@ -115,3 +115,28 @@ def test_prefill_of_small_values():
     f = O.bf16_bits_to_f32
     sums = P._reference(f(q[0]), f(k[0]), f(v[0]), None, None, 20.0, None)[2]
     _check(f(q[0]), f(k[0]), f(v[0]), None, None, 20.0, None, out, sums)
+
+
+@pytest.mark.parametrize("scale,cap,size", [(5e32, 1e30, 2e-33), (1e34, 3e31, 1e-34)])
+def test_scales_and_caps_far_from_one(scale, cap, size):
+    """Caps and scales whose polynomials' coefficients leave fp32's range: the
+    scores are as for any others.  The polynomials are off by 2^-22 of a score
+    (their fits by 2e-7 and a step's rounding), all scores lie in their
+    interval: |z| (2^-22 + 2e-7) in place of the cap's absolute bound."""
+    from compressed_kv_cache_kvc_gb300 import prompt_attention
+    rng = np.random.default_rng(5)
+    n = 200
+    q, k, v = P._bits(rng, (1, 2, n, 128), size), P._bits(rng, (1, 1, n, 128), 0.1), P._bits(rng, (1, 1, n, 128))
+    out = T.bf16_tensor_to_f32(prompt_attention(*[T.to_dev_bf16(x) for x in (q, k, v)], status=P._status(),
+                                                sm_scale=scale, softcap=cap))[0]
+    f = O.bf16_bits_to_f32
+    at = np.arange(n)
+    see = at[None, :] <= at[:, None]
+    vd = f(v[0, 0]).astype(np.float64)
+    for j in range(2):
+        z = R.scores(f(q[0, j]), f(k[0, 0]), scale, cap, 0.0, at, at)
+        assert 0.1 < np.abs(z).max() < 100
+        p = R.softmax_rows(np.where(see, z, -np.inf))
+        dz = R.score_error(z, 0.0, see) + np.abs(z).max() * R.LOG2E * (2.0 ** -22 + 2e-7)
+        ref = p @ vd
+        assert (np.abs(out[j] - ref) <= R.output_bound(ref, p, vd, dz)).all()
