@@ -36,7 +36,10 @@
 // step, so one's softmax overlaps the other's products and the producer's
 // copies overlap both.  A bf16 P alone missed the output tolerance on rows
 // that see few keys.  V entries beyond fp16's range (|v| >= 65536, or not
-// finite) saturate to +-65504 and set KVC_DEV_PREFILL_RANGE.
+// finite) saturate to +-65504 and set KVC_DEV_PREFILL_RANGE.  V in fp16 is off
+// by at most 2^-25 below 2^-14; where a block's keys hold nothing from 2^-6 on, all
+// of them enter times a power of two, which the output is divided by: the producer
+// looks at the first tile, and further only where that is small.
 //
 // Synchronisation: mbarriers (Q and K/V tiles landed, counted in bytes; S
 // read and P written by the query warpgroups; slot full from the producer;
@@ -76,7 +79,7 @@ constexpr int kOffQ = 0;                                      // 2 x 32 KB: Q_A,
 constexpr int kOffK = kOffQ + 2 * kTcQ * kHeadDim * 2;        // 3 x 16 KB: K ring (TMA, 128-byte swizzle)
 constexpr int kOffVt = kOffK + kSlots * kTileBytes;           // 3 x 16 KB: V^T ring, fp16 (operand layout)
 constexpr int kOffVs = kOffVt + kSlots * kTileBytes;          // 2 x 16 KB: V staging (producer, TMA, 1 KB aligned)
-constexpr int kOffBar = kOffVs + 2 * kTileBytes;              // mbarriers, TMEM base, abort flag
+constexpr int kOffBar = kOffVs + 2 * kTileBytes;              // mbarriers, TMEM base, abort flag, V's shift and largest
 // mbarriers: tile published, slot read by query tile A / B (per slot); S
 // and P V complete, S read, P written, Q loaded (per query tile); TMA bytes
 // landed (per staging tile); each issuing thread's products all complete
@@ -122,6 +125,10 @@ __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
   return r;
 }
 
+constexpr float kSmallV = 0x1p-6f;
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
 // A failed wait: flag it for the host and tell the other warpgroups.
 __device__ __forceinline__ void give_up(const DevState& s, volatile int* abort) {
   if (!*abort) {
@@ -142,6 +149,52 @@ __device__ __forceinline__ bool wg_and(int id, bool v) {
   return r != 0;
 }
 
+// The shift of a block whose first key tile holds nothing from 2^-6 on: 0 where a
+// later one of its n_kt tiles does, else what brings the largest |v| to [2^14,
+// 2^15).  By the producer's threads together.  (Asked before the producer's loop:
+// in it the question took 4 % of the kernel.)
+__device__ __noinline__ int small_shift(const uint16_t* __restrict__ v, int n, int n_kt, int wt, uint32_t* sh_top) {
+  const uint4* rows = reinterpret_cast<const uint4*>(v);
+  volatile uint32_t* most = sh_top;
+  for (int t = 0; t < n_kt && *most < __float_as_uint(kSmallV); ++t) {
+    uint32_t top = 0;
+    const size_t end = (size_t)min((t + 1) * kTcKeys, n) * (kHeadDim / 8);
+    for (size_t i = (size_t)t * kTcKeys * (kHeadDim / 8) + wt; i < end; i += kWg) {
+      const uint4 y = rows[i];
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = (w[e] << 16) & 0x7FFF0000u, hi = w[e] & 0x7FFF0000u;
+        top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    wg_and(kNbProducer, true);  // every thread has read the largest so far
+    if ((wt & 31) == 0) atomicMax(sh_top, top);
+    wg_and(kNbProducer, true);
+  }
+  const uint32_t top = *most;
+  return top != 0 && top < __float_as_uint(kSmallV) ? min(14 - ((int)(top >> 23) - 127), 126) : 0;
+}
+
+// A tile's V^T in fp16 times 2^shift over what the producer's loop wrote (each
+// thread over its own).
+__device__ __noinline__ void transpose_scaled(const uint8_t* sv, uint8_t* svt, int pw, int lane, int shift) {
+  const float scale = pow2(shift);
+#pragma unroll 1
+  for (int bi = 0; bi < 8; ++bi) {
+    const int blk = pw * 32 + bi * 4, kg = blk >> 4, dg = blk & 15;
+    uint32_t tv[4];
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(tv[0]), "=r"(tv[1]), "=r"(tv[2]), "=r"(tv[3])
+                 : "r"(saddr(sv + vstage_off(8 * kg + (lane & 7), dg + (lane >> 3)))));
+#pragma unroll
+    for (int mm = 0; mm < 4; ++mm)
+      *reinterpret_cast<uint32_t*>(svt + core_off(8 * (dg + mm) + (lane >> 2), kg, kTcKeys / 8) + 4 * (lane & 3)) =
+          f16x2_sat(bf16f(tv[mm] & 0xFFFFu) * scale, bf16f(tv[mm] >> 16) * scale);
+  }
+}
+
 // Key tiles a 128-query tile starting at q0 attends to.
 __device__ __forceinline__ int key_tiles(int q0, int n) {
   return min((q0 + kTcQ - 1) / kTcKeys + 1, (n + kTcKeys - 1) / kTcKeys);
@@ -150,11 +203,14 @@ __device__ __forceinline__ int key_tiles(int q0, int n) {
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_fwd_tc_kernel(DevState s, int n, const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          uint16_t* __restrict__ out, float* __restrict__ stats, float qk_scale_log2) {
+                          const uint16_t* __restrict__ v, uint16_t* __restrict__ out, float* __restrict__ stats,
+                          float qk_scale_log2) {
   extern __shared__ __align__(1024) uint8_t tc_smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(tc_smem + kOffBar);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(tc_smem + kOffBar + 8 * kNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tc_smem + kOffBar + 8 * kNumBars + 4);
+  volatile int* sh_shift = abort + 1;  // V enters times 2^shift
+  uint32_t* sh_top = tbase + 3;
   auto bar = [&](int i) { return saddr(bars + i); };
 
   // blocks launch x fastest: a (query head, sequence)'s query blocks run
@@ -178,6 +234,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar(i)));
     *abort = 0;
+    *sh_shift = 0;
+    *sh_top = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -203,6 +261,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tma_load_3d(vdst, &tm_v, 0, jt * kTcKeys, zkv, tb);
       tma_load_3d(vdst + kTileBytes / 2, &tm_v, 64, jt * kTcKeys, zkv, tb);
     };
+    int shift = 0;
     if (wt == 0) {
       // both query tiles first (128-row boxes; rows past n read as zeros)
 #pragma unroll
@@ -215,6 +274,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       load(0);
     }
     issued = 1;
+    // small values alone in the first tile (rare)?
+    if (!bar_wait(bar(kBarTma), 0, abort)) {
+      give_up(s, abort);
+      ok = false;
+    }
+    {
+      __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
+      const uint4* first = reinterpret_cast<const uint4*>(tc_smem + kOffVs) + wt;
+#pragma unroll
+      for (int i = 0; i < kTileBytes / 16 / kWg; ++i) {
+        const uint4 y = first[i * kWg];
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+      }
+      if (wg_and(kNbProducer, ok && fmaxf(__low2float(top), __high2float(top)) < kSmallV)) {
+        shift = small_shift(v + (size_t)zkv * n * kHeadDim, n, n_kt, wt, sh_top);
+        if (wt == 0) *sh_shift = shift;
+      }
+    }
     for (int j = 0; j < n_kt; ++j) {
       // tile j's copies complete
       if (bar_wait(bar(kBarTma + (j & 1)), (uint32_t)((j >> 1) & 1), abort)) {
@@ -246,6 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                        4 * (lane & 3)) = hv;
         }
       }
+      if (shift != 0) transpose_scaled(sv, svt, pw, lane, shift);
       // V^T (written) of tile j to the tensor cores' proxy; K came by TMA
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       if (!wg_and(kNbProducer, !*abort)) break;
@@ -452,12 +532,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // O / l to bf16, and the row's (max, sum); every lane reads (the TMEM
       // load is warp-collective), rows past n store nothing
       const bool row_ok = qi < n;
-      const float inv = row_ok ? 1.0f / l : 0.0f;
+      // V's power of two comes out, in two steps where 1 / l over it would be subnormal
+      const int shift = *sh_shift, down = max(shift - 60, 0);
+      const float inv = (row_ok ? 1.0f / l : 0.0f) * pow2(down - shift);
       uint16_t* orow = out + (qrow0 + (row_ok ? qi : 0)) * kHeadDim;
 #pragma unroll 1
       for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
         float t[16];
         ld16(trow + col_o + c0, t);
+        if (down != 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[e] *= pow2(-down);
+        }
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -728,7 +814,7 @@ cudaError_t launch_prefill_fwd_tc(const DevState& s, int batch, int n, const uin
       !tc::encode_rows_map(&tm_v, v, n, batch * s.hkv, kTcKeys))
     return cudaErrorInvalidValue;
   const int blocks = (n + kTcBlock - 1) / kTcBlock;
-  prefill_fwd_tc_kernel<<<dim3(blocks, s.hq, batch), kTcThreads, kTcSmem, st>>>(s, n, tm_q, tm_k, tm_v, out, stats,
+  prefill_fwd_tc_kernel<<<dim3(blocks, s.hq, batch), kTcThreads, kTcSmem, st>>>(s, n, tm_q, tm_k, tm_v, v, out, stats,
                                                                                 qk_scale_log2);
   return cudaGetLastError();
 }

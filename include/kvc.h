@@ -419,8 +419,8 @@ kvc_status kvc_decode_step_overlap(kvc_cache* cache, int32_t seq_begin, int32_t 
  *   d_out: bf16 [batch][Hq][n][128];  all 16-byte aligned;
  *   d_workspace: kvc_prefill_workspace_bytes(cache, batch, n) bytes, 256-byte
  *   aligned (the row statistics the score pass reads).
- * Two or three launches (append, attention, scores), tensor cores (bf16
- * operands, fp32 accumulation).  Errors: KVC_ERR_STATE unless every sequence
+ * Two or three launches (append, attention, scores), tensor cores (Q K^T in bf16,
+ * P V in fp16, V as in kvc_prompt_attention; fp32 accumulation).  Errors: KVC_ERR_STATE unless every sequence
  * of the slice is empty (no token appended since the last reset);
  * KVC_ERR_CAPACITY as kvc_quantize_append. */
 size_t kvc_prefill_workspace_bytes(const kvc_cache* cache, int32_t batch, int32_t n);
