@@ -147,12 +147,23 @@ class BlockScaledCache:
     def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, status: torch.Tensor, seq_begin: int = 0,
                 stream=None, **attention) -> torch.Tensor:
         """A fresh prompt: append it and return `prompt_attention` of it (over
-        its exact bf16 keys and values; `attention` goes to it unchanged)."""
-        if self.lengths(seq_begin, k.shape[0])[1] != 0:
+        its exact bf16 keys and values; `attention` goes to it unchanged).  A
+        refused call leaves the cache, the outputs and `status` as they were."""
+        _need(q, torch.bfloat16, "q", self.device)
+        if q.dim() != 4 or q.shape[1] != self.num_q_heads or q.shape[3] != HEAD_DIM:
+            raise ValueError("q must be [batch, num_q_heads, n, 128]")
+        batch = q.shape[0]
+        _need(k, torch.bfloat16, "k", self.device, (batch, self.num_kv_heads, q.shape[2], HEAD_DIM))
+        if self.lengths(seq_begin, batch)[1] != 0:
             raise L.KvcError(L.KVC_ERR_STATE, "prefill")
-        got = prompt_attention(q, k, v, status=status, stream=stream, **attention)
+        # the append asks for room before it writes; where the attention then
+        # refuses its arguments the (so far empty) sequences are given up again
         self.append(k, v, seq_begin=seq_begin, stream=stream)
-        return got
+        try:
+            return prompt_attention(q, k, v, status=status, stream=stream, **attention)
+        except Exception:
+            self.release(seq_begin, batch, stream=stream)
+            raise
 
     def read(self, seq_begin: int = 0, batch: int = 1, pos_begin: int = 0, n: int | None = None, out=None,
              stream=None):
