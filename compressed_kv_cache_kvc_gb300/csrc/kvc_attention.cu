@@ -167,11 +167,10 @@ __global__ void __launch_bounds__(kWarps * 32) attn_split_kernel(DevState s, int
   const int r = lane >> 2;
   const int c = lane & 3;
   const long long T = (long long)hkv * cum[batch];
-  const int N = stream_ctas(T, gridDim.x);
   const int cta = blockIdx.x;
-  if (cta >= N) return;
-  long long F = (long long)cta * T / N;
-  const long long F1 = (long long)(cta + 1) * T / N;
+  const PageRun run = cta_pages(cta, T, gridDim.x);
+  long long F = run.first;
+  const long long F1 = run.end;
 
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t ring_s = smem_u32(smem) + warp * STAGES * kStageBytes;

@@ -524,16 +524,16 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
   const int G = s.group, hkv = s.hkv;
   const int r = lane >> 2, c = lane & 3;
   const long long T = (long long)hkv * cum[batch];
-  const int N = PARTS ? (int)gridDim.x : stream_ctas(T, gridDim.x), cta = blockIdx.x;
-  if (cta >= N) return;
+  const int N = gridDim.x, cta = blockIdx.x;
   // (a replayed graph may find a sequence empty)
   for (int i = cta; i < batch; i += N)
     if (len[i] <= 0)
       for (int e = threadIdx.x; e < s.hq * (kHeadDim / 8); e += kBThreads)
         reinterpret_cast<uint4*>(out + (size_t)i * s.hq * kHeadDim)[e] = make_uint4(0u, 0u, 0u, 0u);
   // this CTA's run of units [F, F1), or its parts F, F + N, .. of F1
-  long long F = PARTS ? cta : (long long)cta * T / N;
-  const long long F1 = PARTS ? (long long)hkv * parts[batch] : (long long)(cta + 1) * T / N;
+  const PageRun run = PARTS ? PageRun{cta, (long long)hkv * parts[batch]} : cta_pages(cta, T, N);
+  long long F = run.first;
+  const long long F1 = run.end;
   const int* first = PARTS ? parts : cum;
   const uint32_t ring_s = smem_u32(smem) + warp * kBStages * kBStage;
   const uint8_t* ring = smem + warp * kBStages * kBStage;

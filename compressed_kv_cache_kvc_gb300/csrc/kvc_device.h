@@ -52,16 +52,25 @@ __device__ __forceinline__ void pages_prefix(const DevState& s, int seq_begin, i
   __syncthreads();
 }
 
-// CTAs of a stream-K split of T pages (or units) that get some: all N, or, where
-// a graph captured at longer sequences finds fewer pages than its N CTAs, the
-// first T with one each.  (With all N the CTAs between a pair's first and last
-// could be without a page, and their partials never written.)
-__device__ __forceinline__ int stream_ctas(long long T, int N) { return T < N ? max((int)T, 1) : N; }
+// The pages (or units) of CTA `cta` in a stream-K split of T over N CTAs: equal
+// runs, or, where a graph captured at longer sequences finds fewer pages than its N
+// CTAs, one each for the first T.  (By equal runs the CTAs between a pair's first
+// and last could be without a page, and their partials never written.)
+struct PageRun {
+  long long first, end;
+};
+__device__ __forceinline__ PageRun cta_pages(int cta, long long T, int N) {
+  PageRun r{(long long)cta * T / N, (long long)(cta + 1) * T / N};
+  if (T < N) {
+    r.first = cta;
+    r.end = cta < T ? cta + 1 : cta;
+  }
+  return r;
+}
 
-// CTA of the stream-K split that holds flattened page F (see AttnWork); N =
-// stream_ctas(T, grid).
+// CTA of the stream-K split that holds flattened page F (see AttnWork).
 __device__ __forceinline__ int cta_of_page(long long F, long long T, int N) {
-  return (int)(((F + 1) * (long long)N - 1) / T);
+  return T < N ? (int)F : (int)(((F + 1) * (long long)N - 1) / T);
 }
 
 // Block-wide inclusive sum of one int per thread; returns the thread's
@@ -228,9 +237,8 @@ __device__ __forceinline__ void merge_phase(const DevState& s, int seq_begin, in
   if (npg > 0) {
     const long long T = (long long)hkv * cum[batch];
     const long long Pf = (long long)hkv * cum[bl] + (long long)h * npg;
-    const int N = stream_ctas(T, w.ncta);
-    i_first = cta_of_page(Pf, T, N);
-    i_last = cta_of_page(Pf + npg - 1, T, N);
+    i_first = cta_of_page(Pf, T, w.ncta);
+    i_last = cta_of_page(Pf + npg - 1, T, w.ncta);
   }
   const uint16_t* sk = s.sink_k + ((size_t)b * hkv + h) * kSinks * kHeadDim;
   const uint16_t* sv = s.sink_v + ((size_t)b * hkv + h) * kSinks * kHeadDim;
