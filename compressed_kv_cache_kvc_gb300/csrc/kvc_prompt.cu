@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
   for (int i = 0; i < 8; ++i)
     if (r0 + 16 * i < rows) w[i] = src[(size_t)(r0 + 16 * i) * 16];
   bool range = false;
-  uint32_t top = 0;  // the largest finite magnitude, as fp32 bits
+  float most = 0.0f;  // the largest finite magnitude
   auto convert = [&](float scale) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
           range |= !(fabsf(lo) < 65536.0f) || !(fabsf(hi) < 65536.0f);
           if ((x[e] & 0x7F80u) == 0x7F80u) bad = true, lo = 0.0f;
           if ((x[e] & 0x7F800000u) == 0x7F800000u) bad = true, hi = 0.0f;
-          top = max(top, max(__float_as_uint(fabsf(lo)), __float_as_uint(fabsf(hi))));
+          most = max3_abs(lo, hi, most);
           asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(x[e]) : "f"(hi * scale), "f"(lo * scale));
         }
         dst[(size_t)r * 16] = make_uint4(x[0], x[1], x[2], x[3]);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPrepThreads) prompt_prep_kernel(PromptArgs a,
     }
   };
   convert(1.0f);
-  top = __reduce_max_sync(0xffffffffu, top);
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
   if (lane == 0) atomicMax(&sh_top, top);
   if (range) atomicOr(a.status, kDevPrefillRange);
   // bounds of the runs of query tile `tile`, once per sequence
