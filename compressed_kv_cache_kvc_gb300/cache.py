@@ -150,8 +150,9 @@ class KVCache:
     def set_score_transform(self, softcap: float = 0.0, slopes: torch.Tensor | None = None):
         """Scores of every attention on this cache from now on: capped at
         `softcap` by a tanh (0: not), then lowered by slopes[head] times the
-        distance between query and key (float32 [Hq], kept by the cache; None:
-        not)."""
+        distance between query and key (float32 [Hq]; None: not).  The cache
+        keeps the tensor until the next call of this; work of other streams and
+        captured graphs that still read it need the caller to keep it."""
         if slopes is not None:
             _need(slopes, torch.float32, "slopes", self.device, (self.num_q_heads,))
         L.check(self.lib.kvc_set_score_transform(self.handle, ctypes.c_float(softcap),

@@ -836,8 +836,9 @@ cudaError_t launch_attention_merge(const DevState& s, int seq_begin, int batch, 
                                    cudaStream_t st) {
   // early: launched while the split's CTAs run (they are one resident wave), so
   // that its CTAs are in place when the last partial is written: INT4, 32 x 8,192
-  // tokens, five query heads a KV head 73.5 us a call, 75.6 after it; FP8, 16 ragged sequences of up to 8,192 tokens 43.9 and 46.1.  Not beside a
-  // second stream's kernels: its waiting CTAs take the room of the eviction that
+  // tokens, five query heads a KV head 73.5 us a call, 75.6 after it; FP8, 16 ragged
+  // sequences of up to 8,192 tokens 43.9 and 46.1.  Not beside a second stream's
+  // kernels: its waiting CTAs take the room of the eviction that
   // the overlapped step runs under the next layer's split (48 layers, 32 x 8,192
   // INT4 tokens: 5.71 against 5.14 ms a step).
   cudaLaunchAttribute order{};

@@ -412,10 +412,11 @@ __global__ void __launch_bounds__(kReadThreads) block_read_kernel(BlockState s, 
 // out = softmax(z) . v over everything a sequence holds, z as kvc_score.h says.
 //
 // Bound by DRAM: 256 bytes a token and KV head (16 sequences x 32 heads x 4,111
-// INT8 tokens, capped: 88 us, 6.1 TB/s; one of 8 heads x 517: 8.6 us, latency).
-// As in the per-token cache's kernel, one wave of CTAs shares the units of all (sequence, KV head) pairs
-// end to end (each CTA an equal run, which may span pairs), the four warps of
-// a CTA take a run's units in turn, and each warp streams 16-token pages
+// INT8 tokens, capped: 91 us a call, 5.9 TB/s; one of 8 heads x 517: 8.6 us, latency).
+// As in the per-token cache's kernel, one wave of CTAs shares the units of all
+// (sequence, KV head) pairs end to end (each CTA an equal run, which may span
+// pairs), the four warps of a CTA take a run's units in turn, and each warp streams
+// 16-token pages
 // through its own ring of four shared-memory stages with cp.async (a block of
 // one head is one contiguous run, so a page is 2 KB of K and 2 KB of V).  The
 // codes enter mma.sync m16n8k16 as fp16 (INT8 offset subnormals, E4M3 by the

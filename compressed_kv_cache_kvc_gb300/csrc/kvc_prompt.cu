@@ -17,8 +17,8 @@
 //
 // prompt_fwd_kernel.  4 * 128 flops per visible pair: bound by the tensor
 // pipe and, with a cap or a bias, by the FMA pipe (32 capped heads of 8,192
-// causal tokens in 504 us, 1.09 PFLOP/s), and for short runs of keys by the
-// first and last round trips of a block, about 9 us of latency whatever the
+// causal tokens in 506 us, 1.09 PFLOP/s; half of the issue slots used), and for
+// short runs of keys by the first and last round trips of a block, about 9 us of latency whatever the
 // block holds.  One 576-thread CTA per (256 queries, query head, sequence), the
 // longest blocks of all heads first (head by head 598 us for that prompt, 271
 // against 228 us for two-way prefixes with sums).  Launched while the prep
@@ -792,7 +792,7 @@ constexpr int kSBarK = 0, kSBarFull = 1, kSBarEmpty = 3, kSBarS = 5, kSBarSfree 
               kSBarDone = 17, kSNumBars = 18;
 constexpr int kSumSmem = kSOffBar + 8 * kSNumBars + 16;
 constexpr uint32_t kSumCols = 256;
-constexpr size_t kSumCtas = 608;
+constexpr size_t kSumCtas = 608;  // two waves of two a SM on 152 SMs
 
 // The (query head, query tile) blocks some of whose queries see the keys [k0,
 // k1), in order, for a warp: 32 tiles' bounds are read at a time, one a lane (a

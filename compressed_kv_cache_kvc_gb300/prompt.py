@@ -90,7 +90,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, statu
 def document_runs(lengths, prefix=0, device=None):
     """(key_begin, key_end), int32 [1, n], of documents of the given lengths
     packed end to end: causal inside each document, the first `prefix` tokens
-    of each seeing each other both ways."""
+    of each seeing each other both ways.  One row; rows of a batch are
+    concatenated (or repeated) by the caller."""
     begin, end, at = [], [], 0
     for m in lengths:
         if m < 0 or prefix < 0:

@@ -454,9 +454,9 @@ kvc_status kvc_prefill_attention(kvc_cache* cache, int32_t seq_begin, int32_t ba
  *   column sums over 4 + max_blocks_per_seq * 16 tokens).
  * Errors, before any launch: KVC_ERR_INVALID_ARG (range, n <= 0, flags,
  * sm_scale not positive and finite, pointers, workspace);
- * KVC_ERR_CAPACITY as kvc_quantize_append; KVC_ERR_UNSUPPORTED with a bf16
- * window (bf16_window > 0) or n * Hq > 2^30.  KVC_ERR_CUDA when a launch
- * fails; the lengths then already include the appended prompt. */
+ * KVC_ERR_CAPACITY as kvc_quantize_append; KVC_ERR_UNSUPPORTED for n * Hq >
+ * 2^30.  KVC_ERR_CUDA when a launch fails; the lengths then already include the
+ * appended prompt. */
 size_t kvc_prefill_context_workspace_bytes(const kvc_cache* cache, int32_t batch, int32_t n);
 kvc_status kvc_prefill_context(kvc_cache* cache, int32_t seq_begin, int32_t batch, int32_t n, const void* d_q,
                                const void* d_k, const void* d_v, void* d_out, float sm_scale, int32_t flags,
@@ -471,9 +471,11 @@ kvc_status kvc_prefill_context(kvc_cache* cache, int32_t seq_begin, int32_t batc
  * (and with it the H2O scores) runs over z.  In a decode step p_q is the
  * sequence's newest position; keys have the positions they were appended at,
  * also after evictions.  softcap 0: no cap; d_slopes null: no bias.
- *   d_slopes: f32 [Hq] on the device, any finite values; borrowed until the
- *   next kvc_set_score_transform or kvc_cache_destroy (and by every CUDA graph
- *   captured meanwhile).
+ *   d_slopes: f32 [Hq] on the device, finite, of either sign; borrowed until the
+ *   work enqueued before the next kvc_set_score_transform or kvc_cache_destroy
+ *   has run (and by every CUDA graph captured meanwhile).
+ * Scores are meant to stay below 2^96 in magnitude (a softmax starts from a
+ * maximum of -1e30).
  * Honoured by kvc_decode_attention, kvc_decode_attention_noalloc,
  * kvc_decode_step, kvc_decode_step_overlap, kvc_prefill_attention,
  * kvc_prefill_attention_masked and kvc_prefill_context, with every code
@@ -524,8 +526,8 @@ size_t kvc_prompt_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t nu
  * makes the rows that see it not finite; a row that sees a key whose V row
  * holds a NaN or an infinity is NaN; rows that do not see them are not
  * touched by them (the status bit KVC_DEV_PREFILL_RANGE is set all the same).
- * Outputs and workspace overlap nothing else.  Two launches, three with sums; results do not depend on the order of
- * execution.  Errors, before any launch: KVC_ERR_INVALID_ARG for sizes that
+ * Outputs and workspace overlap nothing else.  Two launches, three with sums;
+ * results do not depend on the order of execution.  Errors, before any launch: KVC_ERR_INVALID_ARG for sizes that
  * are not positive, Hq % Hkv != 0, a null or misaligned pointer, an sm_scale
  * that is not positive and finite, a softcap that is negative or not finite, a
  * short workspace; KVC_ERR_UNSUPPORTED for more than 65535 sequences or query
@@ -629,13 +631,15 @@ kvc_status kvc_block_append(kvc_block_cache* cache, int32_t seq_begin, int32_t b
 /* Single-query attention over everything the slice's sequences hold, the
  * newest token included: d_q, d_out bf16 [batch][Hq][128], 16-byte aligned;
  * scores transformed as kvc_set_score_transform says (softcap 0 and d_slopes
- * null: plain), the query at the newest position.  Accumulated in fp32.
+ * null: plain), the query at the newest position.  Accumulated in fp32; V of any
+ * finite size, blocks and exact rows of different sizes included.
  *   d_workspace: kvc_block_workspace_bytes(cache, batch) bytes, 256-byte
  *   aligned, contents arbitrary.
  * One launch: the CTA that finishes a (sequence, KV head) last joins its
  * partial results, in a fixed order.  Calls on the same cache run one after
  * another (they share its tickets); two graphs may share a workspace if their
- * replays do not overlap.
+ * replays do not overlap.  A captured call replays correctly at any lengths,
+ * longer or shorter than those of the capture.
  * Errors: KVC_ERR_INVALID_ARG (slice, pointers, sm_scale, softcap, workspace,
  * an empty sequence; one that a replayed graph finds empty gets rows of 0). */
 size_t kvc_block_workspace_bytes(const kvc_block_cache* cache, int32_t batch);
