@@ -126,6 +126,7 @@ __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi) {
 }
 
 constexpr float kSmallV = 0x1p-6f;
+constexpr int kLookTiles = 8;  // key tiles looked at between two questions
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
@@ -156,9 +157,10 @@ __device__ __forceinline__ bool wg_and(int id, bool v) {
 __device__ __noinline__ int small_shift(const uint16_t* __restrict__ v, int n, int n_kt, int wt, uint32_t* sh_top) {
   const uint4* rows = reinterpret_cast<const uint4*>(v);
   volatile uint32_t* most = sh_top;
-  for (int t = 0; t < n_kt && *most < __float_as_uint(kSmallV); ++t) {
+  for (int t = 0; t < n_kt && *most < __float_as_uint(kSmallV); t += kLookTiles) {
     uint32_t top = 0;
-    const size_t end = (size_t)min((t + 1) * kTcKeys, n) * (kHeadDim / 8);
+    const size_t end = min((size_t)min(t + kLookTiles, n_kt) * kTcKeys, (size_t)n) * (kHeadDim / 8);
+#pragma unroll 8
     for (size_t i = (size_t)t * kTcKeys * (kHeadDim / 8) + wt; i < end; i += kWg) {
       const uint4 y = rows[i];
       const uint32_t w[4] = {y.x, y.y, y.z, y.w};
