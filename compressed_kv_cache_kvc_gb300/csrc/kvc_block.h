@@ -38,7 +38,8 @@ __host__ __device__ inline int block_units(int P, int bt) {
 constexpr int kMaxSplitBatch = 255;
 
 struct BlockAttn {
-  float* part_o;   // [pairs + ncta][group][128] (at most ncta + pairs parts, however they are cut); divided by their sums
+  // (at most ncta + pairs parts, however they are cut)
+  float* part_o;   // [pairs + ncta][group][128], divided by their sums
   float* part_ml;  // [pairs + ncta][group][2]: maximum, sum
   ScoreMod mod;
   float qk_scale_log2;

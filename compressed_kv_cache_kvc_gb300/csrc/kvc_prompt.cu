@@ -15,13 +15,13 @@
 //   prompt_fwd_kernel    outputs and (for the sums) row statistics;
 //   prompt_sums_kernel   column sums from the row statistics.
 //
-// prompt_fwd_kernel.  4 * 128 flops per visible pair: bound by the tensor
-// pipe and, with a cap or a bias, by the FMA pipe (32 capped heads of 8,192
-// causal tokens in 506 us, 1.09 PFLOP/s; half of the issue slots used), and for
-// short runs of keys by the first and last round trips of a block, about 9 us of latency whatever the
-// block holds.  One 576-thread CTA per (256 queries, query head, sequence), the
-// longest blocks of all heads first (head by head 598 us for that prompt, 271
-// against 228 us for two-way prefixes with sums).  Launched while the prep
+// prompt_fwd_kernel.  4 * 128 flops per visible pair.  Bound by issue and latency,
+// not by one pipe (32 capped heads of 8,192 causal tokens in 506 us, 1.09 PFLOP/s:
+// issue 52 %, tensor pipe 47 %, FMA pipe 39 %), and for short runs of keys by the
+// softmax's own chain, about 9 us a block whatever it holds.  One 576-thread CTA per
+// (256 queries, query head, sequence), the longest blocks of all heads first (head
+// by head 598 us for that prompt, 271 against 228 us for two-way prefixes with
+// sums).  Launched while the prep
 // kernel runs: only V and the masks of its rows are waited for.  Q is loaded
 // while the runs are read; the output goes through Q's shared memory and
 // leaves by TMA (stores of a row a thread and a later Q: 185 against 172 us for
@@ -347,8 +347,9 @@ __device__ __forceinline__ void chunk_shift(float (&z)[32], float scale, float m
 
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
-    prompt_fwd_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o) {
+    prompt_fwd_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_o) {
   extern __shared__ __align__(1024) uint8_t fsm[];
   const uint32_t base = saddr(fsm);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(fsm + kFOffMisc);
@@ -828,7 +829,8 @@ struct SeenBlocks {
 
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kSumThreads, 2)
-    prompt_sums_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
+    prompt_sums_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k) {
   extern __shared__ __align__(1024) uint8_t ssm[];
   __shared__ int sh_last;
   const uint32_t base = saddr(ssm);

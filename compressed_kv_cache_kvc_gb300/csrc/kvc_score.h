@@ -36,7 +36,9 @@ constexpr float kCapClose = 0.4f;  // the one of degree 2
 constexpr float kCapMid = 1.5f;    // and the one of degree 8
 constexpr double kCapP2[3] = {-0.3333190183144874, 0.13278022829794303, -0.047811859768676745};
 constexpr double kCapP3[4] = {-0.3333262160369896, 0.13313520721608138, -0.052231106454585126, 0.01564048021294071};
-constexpr double kCapP8[9] = {-0.3333324241639356, 0.13331582011696386, -0.053850984564149926, 0.021477584226268928, -0.008099126689853861, 0.002642995882885061, -0.000656591311100134, 0.00010466406356551689, -7.770424672509535e-06};
+constexpr double kCapP8[9] = {-0.3333324241639356, 0.13331582011696386, -0.053850984564149926,
+                              0.021477584226268928, -0.008099126689853861, 0.002642995882885061,
+                              -0.000656591311100134, 0.00010466406356551689, -7.770424672509535e-06};
 
 // By value in kernel arguments.
 struct ScoreMod {
