@@ -732,9 +732,9 @@ __global__ void __launch_bounds__(kCtxThreads,
       ring_issue(0);
 #pragma unroll 1
       for (int u = 0; u < nrt; ++u) {
-        ring_issue(u + 1);
-        cp_async_wait<1>();
-        __syncthreads();  // tile u is in; every warp is done with tile u - 1
+        cp_async_wait<0>();
+        __syncthreads();    // tile u is in; every warp is done with tile u - 1
+        ring_issue(u + 1);  // (into the stage of tile u - 1)
         if (PASS == 1 && u > 0 && threadIdx.x < 16) {
           const int e2 = 16 * (u - 1) + threadIdx.x;
           if (L.rlo + e2 < L.P1) {

@@ -127,3 +127,36 @@ def test_value_range_with_a_window(bits, kind, pool, window):
         err = np.abs(out[0, j] - ref)
         assert (err <= bound).all(), (j, float((err / bound).max()))
     assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("bits,kind,hq,hkv,ctx,n,W,bias", [
+    (8, "int", 56, 8, 66, 38, 40, True),
+    (8, "int", 16, 2, 300, 90, 100, True),
+    (4, "int", 40, 8, 200, 33, 130, False),
+    (8, "e4m3", 28, 4, 150, 70, 64, True),
+    (4, "int", 8, 1, 700, 100, 512, True),
+])
+def test_windows_of_several_tiles(bits, kind, hq, hkv, ctx, n, W, bias):
+    """More tiles of the bf16 window than stages for them, the warps of a CTA at
+    different tiles: the formula's outputs and scores, call after call."""
+    from compressed_kv_cache_kvc_gb300 import KVCache
+    rng = np.random.default_rng(W + n)
+    pages = (ctx + n) // 16 + 4
+    cache = KVCache(hq, hkv, bits, pages, 1, pages, bf16_window=W, codes="e4m3" if kind == "e4m3" else "int")
+    slopes = S._slopes(hq) if bias else None
+    cache.set_score_transform(softcap=20.0, slopes=slopes)
+    draw = lambda h, m, size=1.0: S._bits(rng, (1, h, m, 128), size)  # noqa: E731
+    k0, v0, k, v = (T.to_dev_bf16(draw(hkv, m)) for m in (ctx, ctx, n, n))
+    q = draw(hq, n, 1.5)
+    first = None
+    for _ in range(20):
+        cache.release()
+        cache.quantize_append(k0, v0)
+        before = _scores(cache) if first is None else None
+        out = cache.prefill_context(T.to_dev_bf16(q), k, v)
+        if first is None:
+            first = out
+            _check(cache, kind, q, T.bf16_tensor_to_f32(out), before, ctx, 20.0,
+                   slopes.double().cpu().numpy() if bias else None)
+        assert torch.equal(out, first)
+    assert cache.read_status() == 0
