@@ -1,12 +1,12 @@
 """Compressed-KV decode step for GB300 (sm_103a).
 
 The compute lives in the CUDA library ``libkvc.so`` (C ABI: ``include/kvc.h``);
-``KVCache``, ``BlockScaledCache`` and ``prompt_attention`` are thin bindings that
+``KVCache``, ``BlockScaledCache``, ``Rotary`` and ``prompt_attention`` are thin bindings that
 pass device pointers and the torch CUDA stream to it.
 """
 from . import workloads  # noqa: F401
 
-__all__ = ["BlockScaledCache", "KVCache", "document_runs", "prompt_attention", "workloads"]
+__all__ = ["BlockScaledCache", "KVCache", "Rotary", "document_runs", "prompt_attention", "workloads"]
 
 
 def __getattr__(name):
@@ -16,6 +16,9 @@ def __getattr__(name):
     if name == "BlockScaledCache":
         from .block_cache import BlockScaledCache
         return BlockScaledCache
+    if name == "Rotary":
+        from .rotary import Rotary
+        return Rotary
     if name in ("prompt_attention", "document_runs"):
         from . import prompt
         return getattr(prompt, name)

@@ -23,6 +23,7 @@ KVC_CODES_E4M3 = 1
 KVC_EVICT_H2O = 0
 KVC_EVICT_STREAMING = 1
 KVC_EVICT_BLOCK = 2
+KVC_ROTARY_AXES = 4
 KVC_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 BUF = dict(K_CODES=0, V_CODES=1, K_SCALE=2, V_SCALE=3, SLOT_POS=4, SCORE=5, SINK_K=6, SINK_V=7,
@@ -58,6 +59,16 @@ class KvcBlockConfig(ctypes.Structure):
                 ("max_blocks_per_seq", ctypes.c_int32), ("codes", ctypes.c_int32)]
 
 
+class KvcRotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("adjacent", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("freq", ctypes.c_float * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+class KvcRows(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_void_p), ("d_out", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("stride_batch", ctypes.c_int64), ("stride_head", ctypes.c_int64), ("stride_token", ctypes.c_int64)]
+
+
 class KvcError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -87,6 +98,12 @@ _SIGS = {
     "kvc_block_last_launch_count": (_I, [_P]),
     "kvc_block_release": (_I, [_P, _I, _I, _P]),
     "kvc_block_append": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "kvc_block_append_rotary": (_I, [_P, _I, _I, _I, ctypes.POINTER(KvcRotary), ctypes.POINTER(KvcRows),
+                                     ctypes.POINTER(KvcRows), ctypes.POINTER(KvcRows), _P, _I, _P]),
+    "kvc_block_key_bounds_bytes": (_SZ, [_P]),
+    "kvc_block_set_key_bounds": (_I, [_P, _P, _SZ]),
+    "kvc_rotary_rotate": (_I, [ctypes.POINTER(KvcRotary), _I, _I, ctypes.POINTER(KvcRows), ctypes.POINTER(KvcRows), _P,
+                               _I, _P]),
     "kvc_block_workspace_bytes": (_SZ, [_P, _I]),
     "kvc_block_attention": (_I, [_P, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
     "kvc_block_read": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),

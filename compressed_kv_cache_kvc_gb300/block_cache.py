@@ -11,14 +11,16 @@ import torch
 from . import _lib as L
 from .cache import HEAD_DIM, _current_device, _need, _stream_ptr
 from .prompt import _ptr, _slopes, prompt_attention
+from .rotary import Rotary, _out, _rows
 
 
 class BlockScaledCache:
     """One layer's block-scaled cache on a CUDA device."""
 
     def __init__(self, num_q_heads: int, num_kv_heads: int, num_blocks: int, max_batch: int, max_blocks_per_seq: int,
-                 block_tokens: int = 16, codes: str = "int8", device=None):
-        """codes: "int8" or "e4m3"."""
+                 block_tokens: int = 16, codes: str = "int8", device=None, key_bounds: bool = False):
+        """codes: "int8" or "e4m3"; key_bounds: keep the bounds of every block's
+        keys, which `selected_attention` chooses by."""
         if codes not in ("int8", "e4m3"):
             raise ValueError('codes must be "int8" or "e4m3"')
         self.handle = None
@@ -43,6 +45,11 @@ class BlockScaledCache:
                 "kvc_block_cache_create")
         self.handle = h
         self._ws = {}
+        self.bounds = None
+        if key_bounds:
+            nbytes = self.lib.kvc_block_key_bounds_bytes(h)
+            self.bounds = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            L.check(self.lib.kvc_block_set_key_bounds(h, _ptr(self.bounds), nbytes), "kvc_block_set_key_bounds")
         self.reset()
 
     def __del__(self):
@@ -116,6 +123,35 @@ class BlockScaledCache:
             raise ValueError("k, v must be [batch, num_kv_heads, n_new, 128]")
         _need(v, torch.bfloat16, "v", self.device, k.shape)
         self._call("kvc_block_append", seq_begin, k.shape[0], k.shape[2], _ptr(k), _ptr(v), stream=stream)
+
+    def append_rotary(self, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, rotary: Rotary, *,
+                      positions: torch.Tensor | None = None, first: int = 0, seq_begin: int = 0,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+        """Append k, v (bf16 [batch, Hkv, n_new, 128]) with the keys turned on
+        the way, and return the queries q (bf16 [batch, Hq, n_new, 128], or None)
+        turned, packed.  All three may be strided views.  positions: int32
+        [num_axes, batch, n_new], [batch, n_new] with one axis; None: first +
+        the token's index in its sequence on every axis."""
+        if stream is not None:
+            with torch.cuda.stream(stream):  # (what is allocated below belongs to that stream)
+                return self.append_rotary(q, k, v, rotary, positions=positions, first=first, seq_begin=seq_begin,
+                                          out=out)
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k, v must be [batch, num_kv_heads, n_new, 128]")
+        batch, n = k.shape[0], k.shape[2]
+        rk = _rows(k, "k", self.device, batch, n, self.num_kv_heads, None)
+        rv = _rows(v, "v", self.device, batch, n, self.num_kv_heads, None)
+        pos = rotary._positions(positions, batch, n, self.device)
+        rq = None
+        if q is not None:
+            _rows(q, "q", self.device, batch, n, self.num_q_heads, None)
+            out = _out(out, q, "out")
+            if out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+                raise ValueError("out may be q only where q is packed")
+            rq = _rows(q, "q", self.device, batch, n, self.num_q_heads, out)
+        self._call("kvc_block_append_rotary", seq_begin, batch, n, ctypes.byref(rotary.plan),
+                   ctypes.byref(rq) if rq is not None else None, ctypes.byref(rk), ctypes.byref(rv), pos, first)
+        return out if q is not None else None
 
     def decode_attention(self, q: torch.Tensor, out: torch.Tensor | None = None, seq_begin: int = 0,
                          sm_scale: float | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,

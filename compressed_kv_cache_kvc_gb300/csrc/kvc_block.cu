@@ -66,18 +66,51 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
-template <bool FP8>
+// What a form of the append has beside the plain one: keys (and queries) rotated
+// on the way, rows at strides; the bounds of every block's keys.
+struct AppendPlain {
+  static constexpr bool kRot = false, kBounds = false;
+};
+struct AppendBounds {
+  static constexpr bool kRot = false, kBounds = true;
+  KeyBounds bounds;
+};
+struct AppendRotary {
+  static constexpr bool kRot = true, kBounds = false;
+  RotaryArgs rot;  // q's rows, k's input; hk 0
+  RowsIn v;
+  int splits;
+};
+struct AppendRotaryBounds {
+  static constexpr bool kRot = true, kBounds = true;
+  RotaryArgs rot;
+  RowsIn v;
+  int splits;
+  KeyBounds bounds;
+};
+
+template <bool FP8, class Form>
 __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(BlockState s, int seq_begin, int batch, int n_new,
                                                                       int tiles_per_pair,
                                                                       const uint16_t* __restrict__ kin,
-                                                                      const uint16_t* __restrict__ vin) {
+                                                                      const uint16_t* __restrict__ vin,
+                                                                      const __grid_constant__ Form f) {
+  constexpr bool kRot = Form::kRot, kBounds = Form::kBounds;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int before[kMaxCallBatch], held[kMaxCallBatch];  // blocks completed before it; its length
   __shared__ int sh_total, sh_bad, sh_last;
   __shared__ float sh_amax[2][kAppWarps];
+  __shared__ uint64_t sh_turns[kRot ? kRotPairs : 1];
+  __shared__ uint8_t sh_axis[kRot ? kRotPairs : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hkv = s.hkv, bt = s.bt;
   const int top = s.counters[kCtrFreeTop];
+  if constexpr (kRot) {
+    if (threadIdx.x < kRotPairs) {
+      sh_turns[threadIdx.x] = f.rot.table.turns[threadIdx.x];
+      sh_axis[threadIdx.x] = f.rot.table.axis[threadIdx.x];
+    }
+  }
   if (warp == 0) {
     int total = 0, bad = 0;
     for (int base = 0; base < batch; base += 32) {
@@ -141,6 +174,20 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
       cur.bl = (int)(pair / 2 / hkv);
     }
 
+    // row i of the new tokens of a (sequence, KV head), values from one row to the next
+    auto rows_in = [&](int kv, int bl, int h) -> const uint16_t* {
+      if constexpr (kRot) {
+        const RowsIn& r = kv ? f.v : f.rot.k;
+        return r.in + bl * r.sb + h * r.sh;
+      } else {
+        return (kv ? vin : kin) + ((size_t)bl * hkv + h) * n_new * kHeadDim;
+      }
+    };
+    auto step_in = [&](int kv) -> ptrdiff_t {
+      if constexpr (kRot) return kv ? f.v.st : f.rot.k.st;
+      return kHeadDim;
+    };
+
     // the copies of the CTA's next tile
     int i_next = 0, st_next = 0;
     Tile nxt = cur;
@@ -152,8 +199,8 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
         if (row0 < (long long)nb << sh) {
           const size_t pair = (size_t)nxt.bl * hkv + nxt.h;
           const int p0 = kSinks + (c0 << sh) + (int)row0 + (lane >> 4);  // the lane's first row
-          const uint16_t* in =
-              (nxt.kv ? vin : kin) + (pair * n_new + (p0 - P)) * (ptrdiff_t)kHeadDim + 8 * (lane & 15);
+          const ptrdiff_t step = step_in(nxt.kv);
+          const uint16_t* in = rows_in(nxt.kv, nxt.bl, nxt.h) + (p0 - P) * step + 8 * (lane & 15);
           if (nxt.x == 0) {  // may begin in the open block's rows
             const uint16_t* exact = (nxt.kv ? s.v_exact : s.k_exact) +
                                     (((size_t)seq_begin * hkv + pair) * exact_rows + kSinks) * kHeadDim + 8 * (lane & 15);
@@ -161,11 +208,11 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
             for (int i = 0; i < 8; ++i) {
               const int p = p0 + 2 * i;
               cp_async16(ring_s + st_next * kAppStage + 512 * i,
-                         p < P ? exact + (size_t)((p - kSinks) & (bt - 1)) * kHeadDim : in + 2 * i * kHeadDim);
+                         p < P ? exact + (size_t)((p - kSinks) & (bt - 1)) * kHeadDim : in + 2 * i * step);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) cp_async16(ring_s + st_next * kAppStage + 512 * i, in + 2 * i * kHeadDim);
+            for (int i = 0; i < 8; ++i) cp_async16(ring_s + st_next * kAppStage + 512 * i, in + 2 * i * step);
           }
           cp_async4(ring_id_s + st_next * kAppStage, s.free_stack + (top - 1 - (before[nxt.bl] + ((int)row0 >> sh))));
         }
@@ -191,14 +238,69 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
       const int c = live ? (int)row0 >> sh : 0;
       const uint8_t* rows = ring + st * kAppStage;
       float amax = 0.0f;
+      if constexpr (kRot) {
+        // new keys are turned where they lie (a row of the open block was when it came)
+        if (kv == 0 && live) {
+          const int cl = lane & 7;
+          if (rotary::turns_here(f.rot.table, cl)) {
+            const int p0 = kSinks + (c0 << sh) + (int)row0;
+            uint8_t* mine = smem + warp * kAppStages * kAppStage + st * kAppStage;
+            const int ca = 16 * rotary::chunk_a(f.rot.table, cl), cb = 16 * rotary::chunk_b(f.rot.table, cl);
+#pragma unroll 1
+            for (int r = lane >> 3; r < 16; r += 4) {
+              const int p = p0 + r;
+              if (p < P) continue;
+              float cs[8], sn[8];
+              rotary::angles(sh_turns, sh_axis,
+                             rotary::row_pos(f.rot.table, (size_t)bl * n_new + (p - P), (size_t)batch * n_new, p), cl, cs,
+                             sn);
+              uint4* xa = reinterpret_cast<uint4*>(mine + 256 * r + ca);
+              uint4* xb = reinterpret_cast<uint4*>(mine + 256 * r + cb);
+              uint4 x = *xa, y = *xb;
+              rotary::turn16(f.rot.table.adjacent != 0, x, y, cs, sn);
+              *xa = x;
+              *xb = y;
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // (a lane's eight channels, kBounds: the least of them in lanes 0 .. 15, the largest
+      // in the others)
+      uint4 ends = make_uint4(0u, 0u, 0u, 0u);
       if (live) {
         __nv_bfloat162 mx = __floats2bfloat162_rn(0.0f, 0.0f);
+        if (kBounds && kv == 0) {
+          __nv_bfloat162 least[4], most[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(rows + 512 * i);
-          const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+          for (int i = 0; i < 8; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(rows + 512 * i);
+            const uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[e])));
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&y[e]);
+              least[e] = i == 0 ? x : __hmin2(least[e], x);
+              most[e] = i == 0 ? x : __hmax2(most[e], x);
+            }
+          }
+          uint32_t z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 a = __shfl_xor_sync(0xffffffffu, least[e], 16);
+            const __nv_bfloat162 b = __shfl_xor_sync(0xffffffffu, most[e], 16);
+            const __nv_bfloat162 x = lane < 16 ? __hmin2(least[e], a) : __hmax2(most[e], b);
+            mx = __hmax2(mx, __habs2(x));
+            z[e] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          ends = make_uint4(z[0], z[1], z[2], z[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(rows + 512 * i);
+            const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = __hmax2(mx, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[e])));
+          }
         }
         amax = fmaxf(__low2float(mx), __high2float(mx));
 #pragma unroll
@@ -214,18 +316,43 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
         // sinks, and the rows of the block that stays open, now that the first
         // block's rows are in shared memory
         __syncthreads();
-        const uint16_t* in = (kv ? vin : kin) + ((size_t)bl * hkv + h) * n_new * kHeadDim;
+        const uint16_t* in = rows_in(kv, bl, h);
+        const ptrdiff_t step = step_in(kv);
         uint16_t* exact = (kv ? s.v_exact : s.k_exact) + ((size_t)b * hkv + h) * exact_rows * kHeadDim;
         const int open0 = kSinks + ((c0 + nb) << sh);
         const int n_sink = max(0, min(kSinks - P, n_new));
         const int first = min(max(open0 - P, n_sink), n_new);  // first new token of the open block
+        auto new_token = [&](int r) { return r < n_sink ? r : first + (r - n_sink); };
+        auto place = [&](int p) {
+          return exact + (size_t)(p < kSinks ? p : kSinks + ((p - kSinks) & (bt - 1))) * kHeadDim;
+        };
+        if (kRot && kv == 0) {
+          if constexpr (kRot) {
+            const int cl = lane & 7;
+            const int ca = 8 * rotary::chunk_a(f.rot.table, cl), cb = 8 * rotary::chunk_b(f.rot.table, cl);
+#pragma unroll 1
+            for (int r = threadIdx.x >> 3; r < n_sink + (n_new - first); r += kAppThreads / 8) {
+              const int i = new_token(r);
+              uint4 x = *reinterpret_cast<const uint4*>(in + i * step + ca);
+              uint4 y = *reinterpret_cast<const uint4*>(in + i * step + cb);
+              if (rotary::turns_here(f.rot.table, cl)) {
+                float cs[8], sn[8];
+                rotary::angles(
+                    sh_turns, sh_axis,
+                    rotary::row_pos(f.rot.table, (size_t)bl * n_new + i, (size_t)batch * n_new, P + i), cl, cs, sn);
+                rotary::turn16(f.rot.table.adjacent != 0, x, y, cs, sn);
+              }
+              *reinterpret_cast<uint4*>(place(P + i) + ca) = x;
+              *reinterpret_cast<uint4*>(place(P + i) + cb) = y;
+            }
+          }
+        } else {
 #pragma unroll 4
-        for (int r = threadIdx.x >> 4; r < n_sink + (n_new - first); r += kAppThreads / 16) {
-          const int i = r < n_sink ? r : first + (r - n_sink);
-          const int p = P + i;
-          const int row = p < kSinks ? p : kSinks + ((p - kSinks) & (bt - 1));
-          reinterpret_cast<uint4*>(exact + (size_t)row * kHeadDim)[threadIdx.x & 15] =
-              reinterpret_cast<const uint4*>(in + (size_t)i * kHeadDim)[threadIdx.x & 15];
+          for (int r = threadIdx.x >> 4; r < n_sink + (n_new - first); r += kAppThreads / 16) {
+            const int i = new_token(r);
+            reinterpret_cast<uint4*>(place(P + i))[threadIdx.x & 15] =
+                reinterpret_cast<const uint4*>(in + i * step)[threadIdx.x & 15];
+          }
         }
       }
       if (live) {
@@ -246,6 +373,39 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
             (kv ? s.v_scale : s.k_scale)[hblk] = scale;
             if (h == 0 && kv == 0) s.table[(size_t)b * s.max_bps + c0 + c] = blk;
           }
+          if constexpr (kBounds) {
+            if (kv == 0) {
+              // the block's warps meet in the places of their rows, which they have read
+              if (wpb > 1) {
+                uint8_t* met = smem + st * kAppStage + 16 * lane;
+                __syncwarp();
+                *reinterpret_cast<uint4*>(met + warp * kAppStages * kAppStage) = ends;
+                named_sync(1 + w0, 32 * wpb);
+                if (warp == w0) {
+                  uint32_t z[4] = {ends.x, ends.y, ends.z, ends.w};
+                  for (int i = w0 + 1; i < w0 + wpb; ++i) {
+                    const uint4 o = *reinterpret_cast<const uint4*>(met + i * kAppStages * kAppStage);
+                    const uint32_t y[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&z[e]);
+                      const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&y[e]);
+                      const __nv_bfloat162 x = lane < 16 ? __hmin2(a, b) : __hmax2(a, b);
+                      z[e] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+                  }
+                  ends = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+                named_sync(1 + w0, 32 * wpb);
+              }
+              if (warp == w0) {
+                const float t = FP8 ? __fdiv_rn(amax, 127.0f) : scale;
+                *reinterpret_cast<uint2*>(f.bounds.codes + hblk * (2 * kHeadDim) + 8 * lane) = block_codes8<false>(
+                    ends, t, FP8 ? rcp_approx_ftz(t) : inv, !(t >= 0x1p-126f && t < INFINITY));
+                if (lane == 0) f.bounds.scale[hblk] = t;
+              }
+            }
+          }
         } else if (lane == 0) {
           atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
         }
@@ -254,6 +414,13 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
       advance(cur);
     }
     cp_async_wait<0>();
+    if constexpr (kRot) {
+      if (f.rot.hq > 0) {
+        const long long units = ((long long)batch * n_new + 3) / 4 * f.splits;
+        for (long long u = (long long)blockIdx.x * kAppWarps + warp; u < units; u += (long long)gridDim.x * kAppWarps)
+          rotary::rotate_unit(f.rot, sh_turns, sh_axis, u, f.splits, [&](int b) { return held[b]; });
+      }
+    }
   }
   // the last CTA advances the lengths and the stack (every CTA has read them)
   __syncthreads();
@@ -1184,19 +1351,30 @@ int block_attn_ctas_mod(int mod) {
   }
 }
 
-template <bool FP8>
-cudaError_t append_launch(const BlockState& s, int seq_begin, int batch, int n_new, int tpp, long long tiles,
-                          const uint16_t* k, const uint16_t* v, cudaStream_t st) {
+template <bool FP8, class Form>
+cudaError_t append_launch(const BlockState& s, int seq_begin, int batch, int n_new, const uint16_t* k,
+                          const uint16_t* v, const Form& f, cudaStream_t st) {
+  // rows of the most blocks an append of n_new tokens completes (at any state)
+  const long long rows = ((long long)n_new + s.bt - 1) / s.bt * s.bt;
+  const int tpp = (int)((rows + kAppRows - 1) / kAppRows);
+  const long long tiles = 2LL * batch * s.hkv * tpp;
   static int done[64] = {0};
-  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(block_append_kernel<FP8>), kAppSmem, done);
+  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(block_append_kernel<FP8, Form>), kAppSmem, done);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
     sms = 152;
   const int grid = (int)std::min(tiles, (long long)kAppCtas * sms);
-  block_append_kernel<FP8><<<grid, kAppThreads, kAppSmem, st>>>(s, seq_begin, batch, n_new, tpp, k, v);
+  block_append_kernel<FP8, Form><<<grid, kAppThreads, kAppSmem, st>>>(s, seq_begin, batch, n_new, tpp, k, v, f);
   return cudaGetLastError();
+}
+
+template <class Form>
+cudaError_t append_launch(const BlockState& s, int seq_begin, int batch, int n_new, const uint16_t* k,
+                          const uint16_t* v, const Form& f, cudaStream_t st) {
+  return s.fp8 ? append_launch<true>(s, seq_begin, batch, n_new, k, v, f, st)
+               : append_launch<false>(s, seq_begin, batch, n_new, k, v, f, st);
 }
 
 }  // namespace
@@ -1211,14 +1389,18 @@ cudaError_t launch_block_attention(const BlockState& s, int seq_begin, int batch
                : launch_block_attn_mod<false>(s, seq_begin, batch, q, out, w, st);
 }
 
-cudaError_t launch_block_append(const BlockState& s, int seq_begin, int batch, int n_new, const uint16_t* k,
-                                const uint16_t* v, cudaStream_t st) {
-  // rows of the most blocks an append of n_new tokens completes (at any state)
-  const long long rows = ((long long)n_new + s.bt - 1) / s.bt * s.bt;
-  const int tpp = (int)((rows + kAppRows - 1) / kAppRows);
-  const long long tiles = 2LL * batch * s.hkv * tpp;
-  return s.fp8 ? append_launch<true>(s, seq_begin, batch, n_new, tpp, tiles, k, v, st)
-               : append_launch<false>(s, seq_begin, batch, n_new, tpp, tiles, k, v, st);
+cudaError_t launch_block_append(const BlockState& s, const KeyBounds& bounds, int seq_begin, int batch, int n_new,
+                                const uint16_t* k, const uint16_t* v, cudaStream_t st) {
+  return bounds.codes ? append_launch(s, seq_begin, batch, n_new, k, v, AppendBounds{bounds}, st)
+                      : append_launch(s, seq_begin, batch, n_new, k, v, AppendPlain{}, st);
+}
+
+cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bounds, int seq_begin,
+                                       const RotaryArgs& rot, const RowsIn& v, cudaStream_t st) {
+  const int splits = rotary_splits((long long)rot.batch * rot.n, rot.hq);
+  return bounds.codes ? append_launch(s, seq_begin, rot.batch, rot.n, nullptr, nullptr,
+                                      AppendRotaryBounds{rot, v, splits, bounds}, st)
+                      : append_launch(s, seq_begin, rot.batch, rot.n, nullptr, nullptr, AppendRotary{rot, v, splits}, st);
 }
 
 cudaError_t launch_block_release(const BlockState& s, int seq_begin, int batch, cudaStream_t st) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kvc_internal.h"
+#include "kvc_rotary.h"
 
 namespace kvc {
 
@@ -20,6 +21,13 @@ struct BlockState {
   int32_t* counters;  // [0] free top, [1] status
   int32_t* tickets;   // [max_batch * hkv] attention, one append; zero between calls
   int32_t hq, hkv, group, bt, num_blocks, max_batch, max_bps, fp8;
+};
+
+// Bounds of every block's keys (the caller's memory; codes null: none are kept):
+// per channel the least and the largest INT8 code of the block's keys.
+struct KeyBounds {
+  uint8_t* codes;  // [num_blocks][hkv][2][128]
+  float* scale;    // [num_blocks][hkv], amax / 127
 };
 
 // A sequence of P tokens: closed (quantised) blocks, rows held exactly (the
@@ -48,8 +56,10 @@ struct BlockAttn {
                     // have about this many parts together
 };
 
-cudaError_t launch_block_append(const BlockState& s, int seq_begin, int batch, int n_new, const uint16_t* k,
-                                const uint16_t* v, cudaStream_t st);
+cudaError_t launch_block_append(const BlockState& s, const KeyBounds& bounds, int seq_begin, int batch, int n_new,
+                                const uint16_t* k, const uint16_t* v, cudaStream_t st);
+cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bounds, int seq_begin,
+                                       const RotaryArgs& rot, const RowsIn& v, cudaStream_t st);
 cudaError_t launch_block_release(const BlockState& s, int seq_begin, int batch, cudaStream_t st);
 cudaError_t launch_block_read(const BlockState& s, int seq_begin, int batch, int pos_begin, int n, uint16_t* k,
                               uint16_t* v, cudaStream_t st);

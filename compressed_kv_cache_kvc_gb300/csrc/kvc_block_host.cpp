@@ -10,6 +10,7 @@
 
 #include "../../include/kvc.h"
 #include "kvc_block.h"
+#include "kvc_rotary_host.h"
 
 namespace {
 
@@ -78,6 +79,7 @@ struct kvc_block_cache {
   Layout layout;
   uint8_t* base;
   kvc::BlockState dev;
+  kvc::KeyBounds bounds{};
   std::vector<int32_t> pos;  // host mirror: tokens held per sequence
   int32_t last_launches = 0;
   int sm_count = 0;
@@ -87,6 +89,21 @@ namespace {
 
 bool range_ok(const kvc_block_cache* c, int32_t seq_begin, int32_t batch) {
   return seq_begin >= 0 && batch > 0 && (long long)seq_begin + batch <= c->cfg.max_batch;
+}
+
+// Whether n_new more tokens fit into every sequence's table row and the pool.
+bool has_room(const kvc_block_cache* c, int32_t seq_begin, int32_t batch, int32_t n_new) {
+  const int bt = c->cfg.block_tokens;
+  long long used = 0, need = 0;
+  for (int b = 0; b < c->cfg.max_batch; ++b) used += kvc::block_closed(c->pos[b], bt);
+  for (int i = 0; i < batch; ++i) {
+    const int P = c->pos[seq_begin + i];
+    if ((long long)P + n_new > 2000000000LL) return false;
+    const int after = kvc::block_closed(P + n_new, bt);
+    if (after > c->cfg.max_blocks_per_seq) return false;
+    need += after - kvc::block_closed(P, bt);
+  }
+  return need <= c->cfg.num_blocks - used;
 }
 
 struct WsLayout {
@@ -270,22 +287,62 @@ kvc_status kvc_block_append(kvc_block_cache* c, int32_t seq_begin, int32_t batch
   if (!range_ok(c, seq_begin, batch) || n_new < 0) return KVC_ERR_INVALID_ARG;
   if (n_new == 0) return KVC_OK;
   if (!d_k || !d_v || !aligned(d_k, 16) || !aligned(d_v, 16)) return KVC_ERR_INVALID_ARG;
-  const int bt = c->cfg.block_tokens;
-  long long used = 0, need = 0;
-  for (int b = 0; b < c->cfg.max_batch; ++b) used += kvc::block_closed(c->pos[b], bt);
-  for (int i = 0; i < batch; ++i) {
-    const int P = c->pos[seq_begin + i];
-    if ((long long)P + n_new > 2000000000LL) return KVC_ERR_CAPACITY;
-    const int after = kvc::block_closed(P + n_new, bt);
-    if (after > c->cfg.max_blocks_per_seq) return KVC_ERR_CAPACITY;
-    need += after - kvc::block_closed(P, bt);
-  }
-  if (need > c->cfg.num_blocks - used) return KVC_ERR_CAPACITY;
-  if (kvc::launch_block_append(c->dev, seq_begin, batch, n_new, static_cast<const uint16_t*>(d_k),
+  if (!has_room(c, seq_begin, batch, n_new)) return KVC_ERR_CAPACITY;
+  if (kvc::launch_block_append(c->dev, c->bounds, seq_begin, batch, n_new, static_cast<const uint16_t*>(d_k),
                                static_cast<const uint16_t*>(d_v), static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return KVC_ERR_CUDA;
   c->last_launches = 1;
   for (int i = 0; i < batch; ++i) c->pos[seq_begin + i] += n_new;
+  return KVC_OK;
+}
+
+kvc_status kvc_block_append_rotary(kvc_block_cache* c, int32_t seq_begin, int32_t batch, int32_t n_new,
+                                   const kvc_rotary* rotary, const kvc_rows* q, const kvc_rows* k, const kvc_rows* v,
+                                   const int32_t* d_positions, int32_t first, void* stream) {
+  if (!c) return KVC_ERR_INVALID_ARG;
+  c->last_launches = 0;
+  if (!range_ok(c, seq_begin, batch) || n_new < 0) return KVC_ERR_INVALID_ARG;
+  if (n_new == 0) return KVC_OK;
+  kvc::RotaryArgs a{};
+  kvc::RowsIn rows_v{};
+  kvc_status st = kvc::rotary_table(rotary, d_positions, first, &a.table);
+  if (st == KVC_OK) st = kvc::rows_in(k, batch, n_new, false, &a.k);
+  if (st == KVC_OK) st = kvc::rows_in(v, batch, n_new, false, &rows_v);
+  if (st == KVC_OK && q) st = kvc::rows_in(q, batch, n_new, true, &a.q);
+  if (st != KVC_OK) return st;
+  if (k->heads != c->cfg.num_kv_heads || v->heads != c->cfg.num_kv_heads || (q && q->heads != c->cfg.num_q_heads))
+    return KVC_ERR_INVALID_ARG;
+  if (!has_room(c, seq_begin, batch, n_new)) return KVC_ERR_CAPACITY;
+  a.batch = batch;
+  a.n = n_new;
+  a.hq = q ? q->heads : 0;
+  a.q_out = q ? static_cast<uint16_t*>(q->d_out) : nullptr;
+  if (kvc::launch_block_append_rotary(c->dev, c->bounds, seq_begin, a, rows_v, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
+    return KVC_ERR_CUDA;
+  c->last_launches = 1;
+  for (int i = 0; i < batch; ++i) c->pos[seq_begin + i] += n_new;
+  return KVC_OK;
+}
+
+size_t kvc_block_key_bounds_bytes(const kvc_block_cache* c) {
+  if (!c) return 0;
+  const size_t hb = (size_t)c->cfg.num_blocks * c->cfg.num_kv_heads;
+  return align_up(hb * 2 * kvc::kHeadDim) + align_up(hb * 4);
+}
+
+kvc_status kvc_block_set_key_bounds(kvc_block_cache* c, void* d_bounds, size_t bytes) {
+  if (!c) return KVC_ERR_INVALID_ARG;
+  c->last_launches = 0;
+  if (d_bounds && (!aligned(d_bounds, kAlign) || bytes < kvc_block_key_bounds_bytes(c))) return KVC_ERR_INVALID_ARG;
+  for (const int32_t p : c->pos)
+    if (p != 0) return KVC_ERR_STATE;
+  c->bounds = kvc::KeyBounds{};
+  if (d_bounds) {
+    const size_t hb = (size_t)c->cfg.num_blocks * c->cfg.num_kv_heads;
+    c->bounds.codes = static_cast<uint8_t*>(d_bounds);
+    c->bounds.scale = reinterpret_cast<float*>(c->bounds.codes + align_up(hb * 2 * kvc::kHeadDim));
+  }
   return KVC_OK;
 }
 

@@ -1,0 +1,36 @@
+// Queries and keys rotated by their positions, outside any cache.
+//
+// Per row 256 bytes in, 256 out and 128 values turned: bound by DRAM.  The angles
+// of a token serve all of its heads, so a warp takes four tokens (eight lanes a
+// row) and goes through the heads with them in registers.
+#include "kvc_rotary.h"
+
+namespace kvc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, int splits) {
+  __shared__ uint64_t turns[kRotPairs];
+  __shared__ uint8_t axis[kRotPairs];
+  if (threadIdx.x < kRotPairs) {
+    turns[threadIdx.x] = a.table.turns[threadIdx.x];
+    axis[threadIdx.x] = a.table.axis[threadIdx.x];
+  }
+  __syncthreads();
+  rotary::rotate_unit(a, turns, axis, (long long)blockIdx.x * kWarps + (threadIdx.x >> 5), splits,
+                      [](int) { return 0; });
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st) {
+  const long long rows = (long long)a.batch * a.n;
+  const int splits = rotary_splits(rows, a.hq + a.hk);
+  const long long warps = (rows + 3) / 4 * splits;
+  rotary_kernel<<<(unsigned)((warps + kWarps - 1) / kWarps), kThreads, 0, st>>>(a, splits);
+  return cudaGetLastError();
+}
+
+}  // namespace kvc

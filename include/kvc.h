@@ -550,6 +550,47 @@ kvc_status kvc_prefill_attention_masked(kvc_cache* cache, int32_t seq_begin, int
                                         const int32_t* d_key_begin, const int32_t* d_key_end, void* d_workspace,
                                         size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------- rotary positions ---- */
+
+/* Queries and keys turned by their positions: pair i of a row of 128, (x, y),
+ * at position p of the pair's axis becomes
+ *   (x cos t - y sin t, y cos t + x sin t),  t = p * freq[i],
+ * in fp32 (cos and sin off by at most 1e-7 for every 32-bit position), rounded
+ * once to bf16.  Text has one axis; images and video have several (time, height,
+ * width), each pair following one of them.  Host data: set it up once per model. */
+#define KVC_ROTARY_AXES 4
+typedef struct {
+  int32_t rotary_dim; /* values of a row that turn, a multiple of 16 up to 128; the
+                         others pass unchanged                                  */
+  int32_t adjacent;   /* 0: pair i is values (i, i + rotary_dim / 2); 1: (2i, 2i+1) */
+  int32_t axes;       /* 1 to 4                                                 */
+  float freq[64];     /* angle per position of pair i < rotary_dim / 2, |freq| <=
+                         65536                                                  */
+  uint8_t axis[64];   /* axis of pair i, below axes                             */
+} kvc_rotary;
+
+/* Rows of 128 bf16 values at strides (in values, multiples of 8; that of a
+ * dimension of size 1 does not count): element (b, h, i) at d_in + b *
+ * stride_batch + h * stride_head + i * stride_token, so that the slices of a
+ * fused projection need no copy.  d_in and d_out 16-byte aligned. */
+typedef struct {
+  const void* d_in;
+  void* d_out;         /* bf16 [batch][heads][n][128], packed */
+  int32_t heads;
+  int64_t stride_batch, stride_head, stride_token;
+} kvc_rows;
+
+/* Rotate the rows of q and, unless null, of k.
+ *   d_positions: i32 [axes][batch][n], of either sign, or null: first + i on
+ *   every axis for token i.
+ * d_out may be d_in where that is packed; nothing else overlaps.  One launch.
+ * Errors, before any launch: KVC_ERR_INVALID_ARG for sizes that are not positive, a
+ * null or misaligned pointer or stride, an in-place call on rows that are not
+ * packed, a frequency that is not finite or beyond 65536, an axis out of range;
+ * KVC_ERR_UNSUPPORTED for another rotary_dim. */
+kvc_status kvc_rotary_rotate(const kvc_rotary* rotary, int32_t batch, int32_t n, const kvc_rows* q, const kvc_rows* k,
+                             const int32_t* d_positions, int32_t first, void* stream);
+
 /* -------------------------------------------------- block-scaled cache ---- */
 
 /* A second form of the cache: 8-bit codes with ONE scale per block of
@@ -627,6 +668,30 @@ kvc_status kvc_block_release(kvc_block_cache* cache, int32_t seq_begin, int32_t 
  * blocks or the pool has too few (nothing is written). */
 kvc_status kvc_block_append(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t n_new, const void* d_k,
                             const void* d_v, void* stream);
+
+/* The same with the rotation on the way: new keys are turned by their positions
+ * and rounded to bf16 (kvc_rotary_rotate) and then appended as above, to the
+ * same codes as in two calls; the queries q, unless null, are turned into q->d_out.
+ *   k, v: rows at strides, num_kv_heads of them (d_out not used);
+ *   d_positions: i32 [axes][batch][n_new], or null: first + the token's index in
+ *   its sequence on every axis, read on the device (a replayed graph goes on
+ *   counting).
+ * One launch.  Errors as kvc_block_append and kvc_rotary_rotate. */
+kvc_status kvc_block_append_rotary(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t n_new,
+                                   const kvc_rotary* rotary, const kvc_rows* q, const kvc_rows* k, const kvc_rows* v,
+                                   const int32_t* d_positions, int32_t first, void* stream);
+
+/* Bounds of the keys of every closed block, kept from now on by every append: per
+ * KV head and channel the least and the largest INT8 code (scale amax / 127,
+ * whatever codes the cache holds).  d_bounds: kvc_block_key_bounds_bytes(cache)
+ * bytes, 256-byte aligned, the caller's, part of the state when it is saved:
+ *   u8 [num_blocks][Hkv][2][128] codes (least, largest), at the next multiple of
+ *   256 bytes f32 [num_blocks][Hkv] scales.
+ * Null: none are kept (the state a cache is created in).  Enqueues nothing.
+ * Errors: KVC_ERR_STATE unless every sequence is empty; KVC_ERR_INVALID_ARG for a
+ * misaligned pointer or too few bytes. */
+size_t kvc_block_key_bounds_bytes(const kvc_block_cache* cache);
+kvc_status kvc_block_set_key_bounds(kvc_block_cache* cache, void* d_bounds, size_t bytes);
 
 /* Single-query attention over everything the slice's sequences hold, the
  * newest token included: d_q, d_out bf16 [batch][Hq][128], 16-byte aligned;
