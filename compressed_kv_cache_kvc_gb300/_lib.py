@@ -106,6 +106,10 @@ _SIGS = {
                                _I, _P]),
     "kvc_block_workspace_bytes": (_SZ, [_P, _I]),
     "kvc_block_attention": (_I, [_P, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
+    "kvc_block_selected_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "kvc_block_selected_attention": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
+    "kvc_block_prefix_workspace_bytes": (_SZ, [_P, _I]),
+    "kvc_block_prefix_attention": (_I, [_P, _I, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
     "kvc_block_read": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "kvc_version": (_I, []),
     "kvc_status_string": (ctypes.c_char_p, [_I]),

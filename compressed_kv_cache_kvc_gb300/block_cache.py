@@ -153,14 +153,8 @@ class BlockScaledCache:
                    ctypes.byref(rq) if rq is not None else None, ctypes.byref(rk), ctypes.byref(rv), pos, first)
         return out if q is not None else None
 
-    def decode_attention(self, q: torch.Tensor, out: torch.Tensor | None = None, seq_begin: int = 0,
-                         sm_scale: float | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
-                         workspace=None, stream=None) -> torch.Tensor:
-        """q: bf16 [batch, Hq, 128], at the newest position -> bf16 [batch,
-        Hq, 128]; scores transformed as in `prompt_attention`."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
-                return self.decode_attention(q, out, seq_begin, sm_scale, softcap, slopes, workspace)
+    def _attention_args(self, q, out, slopes, sm_scale):
+        """(out, scale) of a single-query attention, its arguments checked."""
         _need(q, torch.bfloat16, "q", self.device)
         if q.dim() != 3 or q.shape[1] != self.num_q_heads or q.shape[2] != HEAD_DIM:
             raise ValueError("q must be [batch, num_q_heads, 128]")
@@ -170,14 +164,88 @@ class BlockScaledCache:
             out = torch.empty_like(q)
         else:
             _need(out, torch.bfloat16, "out", self.device, q.shape)
+        return out, 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
+
+    def _workspace_of(self, workspace, key, nbytes):
+        """`workspace`, or the cache's own for the calls of `key`."""
+        if workspace is not None:
+            _need(workspace, torch.uint8, "workspace", self.device)
+            return workspace
+        ws = self._ws.get(key)
+        if ws is None:
+            ws = self._ws[key] = torch.empty(max(int(nbytes()), 1), dtype=torch.uint8, device=self.device)
+        return ws
+
+    def decode_attention(self, q: torch.Tensor, out: torch.Tensor | None = None, seq_begin: int = 0,
+                         sm_scale: float | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                         workspace=None, stream=None) -> torch.Tensor:
+        """q: bf16 [batch, Hq, 128], at the newest position -> bf16 [batch,
+        Hq, 128]; scores transformed as in `prompt_attention`."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.decode_attention(q, out, seq_begin, sm_scale, softcap, slopes, workspace)
+        out, scale = self._attention_args(q, out, slopes, sm_scale)
         if workspace is None:
             ws = self.workspace(q.shape[0])
         else:
             ws = workspace
             _need(ws, torch.uint8, "workspace", self.device)
-        scale = 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
         self._call("kvc_block_attention", seq_begin, q.shape[0], _ptr(q), _ptr(out), scale,
                    softcap, _ptr(slopes), _ptr(ws), ws.numel())
+        return out
+
+    def selected_attention(self, q: torch.Tensor, top_blocks: int, *, recent_blocks: int = 1,
+                           out: torch.Tensor | None = None, seq_begin: int = 0, sm_scale: float | None = None,
+                           softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                           return_blocks: bool | torch.Tensor = False, workspace=None, stream=None):
+        """`decode_attention` to the sinks, the open block, the `recent_blocks`
+        newest closed blocks and, of the others, the `top_blocks` whose keys'
+        bounds promise the largest products with the query heads of the KV head
+        (a cache made with key_bounds).  return_blocks: True, or an int32 tensor
+        [batch, Hkv, top_blocks + recent_blocks], returns (out, blocks) with the
+        chosen blocks, ascending, -1 behind the last."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.selected_attention(q, top_blocks, recent_blocks=recent_blocks, out=out,
+                                               seq_begin=seq_begin, sm_scale=sm_scale, softcap=softcap, slopes=slopes,
+                                               return_blocks=return_blocks, workspace=workspace)
+        if self.bounds is None:
+            raise ValueError("selected_attention needs a cache made with key_bounds=True")
+        if top_blocks < 1 or recent_blocks < 0 or top_blocks + recent_blocks > 1 << 20:
+            raise ValueError("top_blocks must be positive, recent_blocks not negative, both together at most 2^20")
+        out, scale = self._attention_args(q, out, slopes, sm_scale)
+        batch = q.shape[0]
+        blocks = None
+        if return_blocks is not False:
+            shape = (batch, self.num_kv_heads, top_blocks + recent_blocks)
+            if return_blocks is True:
+                blocks = torch.empty(shape, dtype=torch.int32, device=self.device)
+            else:
+                blocks = return_blocks
+                _need(blocks, torch.int32, "return_blocks", self.device, shape)
+        ws = self._workspace_of(workspace, ("selected", batch, top_blocks, recent_blocks),
+                                lambda: self.lib.kvc_block_selected_workspace_bytes(self.handle, batch, top_blocks,
+                                                                                    recent_blocks))
+        self._call("kvc_block_selected_attention", seq_begin, batch, top_blocks, recent_blocks, _ptr(q), _ptr(out),
+                   _ptr(blocks), scale, softcap, _ptr(slopes), _ptr(ws), ws.numel())
+        return out if blocks is None else (out, blocks)
+
+    def prefix_attention(self, q: torch.Tensor, prefix: int, *, out: torch.Tensor | None = None, seq_begin: int = 0,
+                         sm_scale: float | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                         workspace=None, stream=None) -> torch.Tensor:
+        """`decode_attention` of sequences that share a prefix, held once as the
+        sequence `prefix`: each query sees the prefix and then its own sequence
+        (appended with first = the prefix's length where keys are rotated)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.prefix_attention(q, prefix, out=out, seq_begin=seq_begin, sm_scale=sm_scale,
+                                             softcap=softcap, slopes=slopes, workspace=workspace)
+        out, scale = self._attention_args(q, out, slopes, sm_scale)
+        batch = q.shape[0]
+        ws = self._workspace_of(workspace, ("prefix", batch),
+                                lambda: self.lib.kvc_block_prefix_workspace_bytes(self.handle, batch))
+        self._call("kvc_block_prefix_attention", prefix, seq_begin, batch, _ptr(q), _ptr(out), scale, softcap,
+                   _ptr(slopes), _ptr(ws), ws.numel())
         return out
 
     def prefill(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, status: torch.Tensor, seq_begin: int = 0,

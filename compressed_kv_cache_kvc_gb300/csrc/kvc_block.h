@@ -52,8 +52,23 @@ struct BlockAttn {
   ScoreMod mod;
   float qk_scale_log2;
   int ncta;
+  // the selected form: blocks of every pair in ascending order, `most` places a pair
+  const int32_t* list;
+  int most;
+  // the prefix form: the sequence that holds it, whether its pages are among the
+  // units; partials of its blocks from elsewhere, `more` of [hkv][batch][group]
+  int prefix, prefix_pages, more;
+  const float *more_o, *more_ml;
   int parts;  // 0: equal runs across pairs; else a CTA takes a part of one pair, and the sequences of a head
                     // have about this many parts together
+};
+
+// The choice of blocks: the top_blocks best of the closed ones but the `recent`
+// newest, and these.
+struct BlockChoice {
+  uint32_t* keys;  // [pairs][max_bps], ordered as the scores
+  int32_t* list;   // [pairs][top + recent], ascending, -1 behind the last
+  int top, recent;
 };
 
 cudaError_t launch_block_append(const BlockState& s, const KeyBounds& bounds, int seq_begin, int batch, int n_new,
@@ -67,5 +82,15 @@ cudaError_t launch_block_fill(const BlockState& s, cudaStream_t st);
 int block_attention_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
 cudaError_t launch_block_attention(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                    const BlockAttn& w, cudaStream_t st);
+
+// longest: the most tokens a sequence of the slice holds
+cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, const BlockChoice& ch, int seq_begin,
+                                int batch, int longest, const uint16_t* q, cudaStream_t st);
+int block_selected_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
+cudaError_t launch_block_selected(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
+                                  const BlockAttn& w, cudaStream_t st);
+int block_prefix_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
+cudaError_t launch_block_prefix(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
+                                const BlockAttn& w, cudaStream_t st);
 
 }  // namespace kvc

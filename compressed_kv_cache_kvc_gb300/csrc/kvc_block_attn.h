@@ -1,0 +1,870 @@
+// The single-query attention kernel over the block-scaled cache, instantiated by
+// the translation units of its forms: a sequence whole (kvc_block.cu), its selected
+// blocks (kvc_block_select.cu), a shared prefix and the sequence's own tokens
+// (kvc_block_prefix.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "kvc_block.h"
+#include "kvc_device.h"
+#include "kvc_mma.h"
+
+namespace kvc {
+namespace {
+
+using namespace dev;
+using namespace codes;
+
+__host__ __device__ constexpr int kExactRows(int bt) { return kSinks + bt; }
+
+enum { kPlain = 0, kSelected = 1, kPrefix = 2 };  // forms
+
+// ---------------------------------------------------------------- attention
+// out = softmax(z) . v over everything a sequence holds, z as kvc_score.h says.
+//
+// Bound by DRAM: 256 bytes a token and KV head (16 sequences x 32 heads x 4,111
+// INT8 tokens, capped: 91 us a call, 5.9 TB/s; one of 8 heads x 517: 8.6 us, latency).
+// As in the per-token cache's kernel, one wave of CTAs shares the units of all
+// (sequence, KV head) pairs end to end (each CTA an equal run, which may span
+// pairs), the four warps of a CTA take a run's units in turn, and each warp streams
+// 16-token pages
+// through its own ring of four shared-memory stages with cp.async (a block of
+// one head is one contiguous run, so a page is 2 KB of K and 2 KB of V).  The
+// codes enter mma.sync m16n8k16 as fp16 (INT8 offset subnormals, E4M3 by the
+// conversion instruction), 16 tokens on M and the G <= 8 query heads on N.
+// What the scale per block changes: every page is full and has ONE K scale and
+// ONE V scale, so a logit is acc * (k_scale * cq), the P V operand p *
+// (v_scale 2^-E), the pages need no scale rows, and positions follow from the
+// page index, so the distance bias reads nothing.
+// The exact rows (sinks and open block, up to 3 + bt) are the pair's last
+// units: tiles of 16 bf16 rows read straight into the MMA fragments, P as two
+// bf16 parts (16 significant bits).
+// V may be any finite value, also where blocks and exact rows differ by all of
+// bf16's range: the accumulators are in units of 2^E, which follows the largest V
+// scale (of exact rows 1/128 of the largest |v|) as the maxima follow the scores,
+// and partial results are divided by their sum before they leave units of 2^E,
+// since the sum over a long sequence of values near the top of the range is
+// beyond fp32.
+// The CTA that finishes a pair last (an atomic ticket, no CTA waits) joins the
+// pair's partials in CTA order, so the result does not depend on the order of
+// completion.  (A warp per query head, eight rows of 16 bytes a lane in flight:
+// joining a row at a time took 28.7 against 19.4 us for one sequence of 32,000
+// tokens.)
+//
+// PARTS, for few sequences of unequal lengths: a CTA takes a part of one pair,
+// the parts of a sequence in proportion to its length, so that no CTA ends
+// inside a part.  Two CTAs per SM then, with the registers of two; the equal
+// runs take a full wave of three (168 registers; at 216 and two per SM 16 x 32
+// heads of 4,111 capped tokens 94 against 88 us).
+constexpr int kBWarps = 4;
+constexpr int kBThreads = kBWarps * 32;
+constexpr int kBStages = 4;
+constexpr int kBStage = 4096;  // K page, V page
+constexpr int kBSmem = kBWarps * kBStages * kBStage;
+constexpr float kBLazy = 4.0f;
+constexpr int kJoinRow = kHeadDim + 4;  // one warp's joined row: 128 means, the maximum, the sum
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+constexpr int kBCap = 1, kBBias = 2;
+
+// chunk j (16 bytes) of row t of a page: every copy and read instruction of
+// the kernel touches each bank at most once per 128 bytes
+__host__ __device__ constexpr int bchunk(int t, int j) {
+  return 128 * t + 16 * (j ^ ((2 * ((t >> 2) & 3)) ^ (4 * ((t >> 1) & 1))));
+}
+
+template <int FORM, bool FP8, int MOD, bool PARTS>
+__global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(BlockState s, int seq_begin, int batch,
+                                                               const uint16_t* __restrict__ q,
+                                                               uint16_t* __restrict__ out, BlockAttn a) {
+  constexpr bool kCap = (MOD & kBCap) != 0, kBias = (MOD & kBBias) != 0;
+  constexpr bool kOffset = !FP8;
+  constexpr float kOffK = 128.0f * 0x1p-24f, kOffV = 128.0f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int cum[kMaxCallBatch + 1], len[kMaxCallBatch];
+  __shared__ int parts[PARTS ? kMaxSplitBatch + 1 : 1];  // (split pairs) parts of a head of the sequences before
+  __shared__ int sh_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bt = s.bt, ppb = bt / kPage;  // pages per block
+  // (kPrefix) tokens of the prefix; its pages and tiles of exact rows among the units
+  const int pre_len = FORM == kPrefix ? s.seq_pos[a.prefix] : 0;
+  const int pre_npg = FORM == kPrefix && a.prefix_pages ? block_closed(pre_len, bt) * ppb : 0;
+  const int pre_tiles = FORM == kPrefix ? (block_exact_rows(pre_len, bt) + kPage - 1) / kPage : 0;
+  // closed blocks among the units, and all units, of a sequence that holds n tokens
+  auto blocks_of = [&](int n) { return FORM == kSelected ? min(block_closed(n, bt), a.most) : block_closed(n, bt); };
+  auto units_of = [&](int n) {
+    return pre_npg + pre_tiles + blocks_of(n) * ppb + (block_exact_rows(n, bt) + kPage - 1) / kPage;
+  };
+  if (warp == 0) {
+    int carry = 0;
+    if (lane == 0) cum[0] = 0;
+    for (int base = 0; base < batch; base += 32) {
+      const int i = base + lane;
+      const int held = i < batch ? s.seq_pos[seq_begin + i] : 0;
+      int v = i < batch ? units_of(held) : 0;
+      if (i < batch) len[i] = held;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (i < batch) cum[i + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (PARTS) {
+      // every sequence's share of the parts of a head, rounded down (but one at least)
+      const long long per_head = a.parts, total = max(carry, 1);
+      int before = 0;
+      if (lane == 0) parts[0] = 0;
+      for (int base = 0; base < batch; base += 32) {
+        const int i = base + lane;
+        const int nu = i < batch ? units_of(len[i]) : 0;
+        int v = nu > 0 ? (int)max(1LL, min((long long)nu, nu * per_head / total)) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        if (i < batch) parts[i + 1] = before + v;
+        before += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+  }
+  __syncthreads();
+
+  const int G = s.group, hkv = s.hkv;
+  const int r = lane >> 2, c = lane & 3;
+  const long long T = (long long)hkv * cum[batch];
+  const int N = gridDim.x, cta = blockIdx.x;
+  // (a replayed graph may find a sequence empty)
+  for (int i = cta; i < batch; i += N)
+    if (cum[i + 1] == cum[i])
+      for (int e = threadIdx.x; e < s.hq * (kHeadDim / 8); e += kBThreads)
+        reinterpret_cast<uint4*>(out + (size_t)i * s.hq * kHeadDim)[e] = make_uint4(0u, 0u, 0u, 0u);
+  // this CTA's run of units [F, F1), or its parts F, F + N, .. of F1
+  const PageRun run = PARTS ? PageRun{cta, (long long)hkv * parts[batch]} : cta_pages(cta, T, N);
+  long long F = run.first;
+  const long long F1 = run.end;
+  const int* first = PARTS ? parts : cum;
+  const uint32_t ring_s = smem_u32(smem) + warp * kBStages * kBStage;
+  const uint8_t* ring = smem + warp * kBStages * kBStage;
+  uint32_t cp_d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) cp_d[i] = bchunk((lane + 32 * i) >> 3, (lane + 32 * i) & 7);
+  const int k_off[4] = {bchunk(2 * r, c), bchunk(2 * r, c + 4), bchunk(2 * r + 1, c), bchunk(2 * r + 1, c + 4)};
+  int v_off[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v_off[k] = 2048 + bchunk(4 * c + k, r);
+  const uint64_t pol = l2_evict_first();
+  const float qk = kCap ? a.mod.y_scale : a.qk_scale_log2;
+
+  while (F < F1) {
+    // ---- the pair of unit (or part) F and the units of it that are this CTA's
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)hkv * first[mid] <= F) lo = mid; else hi = mid - 1;
+    }
+    const int bl = lo, b = seq_begin + bl;
+    const int nu = cum[bl + 1] - cum[bl];
+    const long long pbase = (long long)hkv * first[bl];
+    const int per_pair = first[bl + 1] - first[bl];
+    const int h = (int)((F - pbase) / per_pair);
+    const long long Pf = pbase + (long long)h * per_pair;
+    int u_a, u_e;  // units [u_a, u_e)
+    if (PARTS) {
+      const int part = (int)(F - Pf);
+      u_a = (int)((long long)nu * part / per_pair);
+      u_e = (int)((long long)nu * (part + 1) / per_pair);
+    } else {
+      u_a = (int)(F - Pf);
+      u_e = (int)((F1 < Pf + nu ? F1 : Pf + nu) - Pf);
+    }
+    const int P = len[bl];
+    const int closed = block_closed(P, bt), npg = pre_npg + blocks_of(P) * ppb;
+
+    // ---- this warp's units u_a + warp, + kBWarps, ...: n_my, the first n_pg of them pages
+    const int n_my = u_e - u_a > warp ? (u_e - u_a - warp + kBWarps - 1) / kBWarps : 0;
+    const int n_pg = min(u_e, npg) - u_a > warp ? (min(u_e, npg) - u_a - warp + kBWarps - 1) / kBWarps : 0;
+    const int32_t* table = s.table + (size_t)b * s.max_bps;
+    const int32_t* list = FORM == kSelected ? a.list + ((size_t)bl * hkv + h) * a.most : nullptr;
+    // block ids and scales of this warp's pages, 32 at a time across the lanes
+    auto tab_load = [&](int chunk) -> int {
+      const int k = chunk * 32 + lane, u = u_a + warp + kBWarps * k;
+      if (k >= n_pg) return -1;
+      if (FORM == kSelected) return table[list[u / ppb]];
+      if (FORM == kPrefix)
+        return u < pre_npg ? s.table[(size_t)a.prefix * s.max_bps + u / ppb] : table[(u - pre_npg) / ppb];
+      return table[u / ppb];
+    };
+    // (selected, biased) the pages' blocks in the sequence
+    constexpr bool kBlocks = FORM == kSelected && kBias;
+    auto block_load = [&](int chunk) -> int {
+      const int k = chunk * 32 + lane;
+      return kBlocks && k < n_pg ? list[(u_a + warp + kBWarps * k) / ppb] : 0;
+    };
+    int blk_use = block_load(0), blk_nxt = n_pg > 32 ? block_load(1) : 0;
+    int id_cur = tab_load(0), id_nxt = n_pg > 32 ? tab_load(1) : -1;
+    auto scale_of = [&](const float* sc, int id) {
+      return (unsigned)id < (unsigned)s.num_blocks ? sc[(size_t)id * hkv + h] : 0.0f;
+    };
+    float ks_use = scale_of(s.k_scale, id_cur), vs_use = scale_of(s.v_scale, id_cur);
+    float ks_nxt = scale_of(s.k_scale, id_nxt), vs_nxt = scale_of(s.v_scale, id_nxt);
+    uint32_t stage_ok = 0;
+    const uint8_t* kb = s.k_codes + (size_t)h * bt * kHeadDim + 16 * lane;
+    const uint8_t* vb = s.v_codes + (size_t)h * bt * kHeadDim + 16 * lane;
+    const uint32_t stride = (uint32_t)hkv * bt * kHeadDim;
+    auto issue = [&](int k) {
+      if ((k & 31) == 0 && k > 0) {
+        id_cur = id_nxt;
+        id_nxt = tab_load((k >> 5) + 1);
+      }
+      const int id = __shfl_sync(0xffffffffu, id_cur, k & 31);
+      const bool ok = k < n_pg && (unsigned)id < (unsigned)s.num_blocks;
+      const int st = k & (kBStages - 1);
+      stage_ok = (stage_ok & ~(1u << st)) | ((uint32_t)ok << st);
+      if (ok) {
+        const int sub = (u_a + warp + kBWarps * k) % ppb;
+        const size_t off = (size_t)id * stride + (size_t)sub * (kPage * kHeadDim);
+        const uint32_t sb = ring_s + st * kBStage;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(sb + cp_d[i]),
+                       "l"(kb + off + 512 * i), "l"(pol));
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(sb + 2048 + cp_d[i]),
+                       "l"(vb + off + 512 * i), "l"(pol));
+        }
+      }
+      cp_async_commit();
+    };
+    issue(0);
+    issue(1);
+
+    // ---- query fragments (B operand), scaled by 2^e into fp16 range
+    uint32_t bq[8][2];
+    float cq0, cq1, ch0 = 0.0f, ch1 = 0.0f;
+    const uint16_t* qrow = q + ((size_t)bl * s.hq + h * G + (r < G ? r : 0)) * kHeadDim;
+    {
+      float qv[32];
+      const uint4* src_a = reinterpret_cast<const uint4*>(qrow + 16 * c);
+      const uint4* src_b = reinterpret_cast<const uint4*>(qrow + 64 + 16 * c);
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = i < 2 ? src_a[i] : src_b[i - 2];
+        const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qv[8 * i + 2 * j] = r < G ? bf16f(ws[j] & 0xFFFFu) : 0.0f;
+          qv[8 * i + 2 * j + 1] = r < G ? bf16f(ws[j] >> 16) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(qv[i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      int e = 0;
+      if (amax > 0.0f) e = min(max(14 - exponent_of(amax), -100), 100);
+      const float f2e = pow2i(e);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) qv[i] *= f2e;
+      float qs = 0.0f;
+#pragma unroll
+      for (int st = 0; st < 8; ++st) {
+        // INT8 offset codes pair bytes (0, 2) and (1, 3) of a word, E4M3 (0, 1) and (2, 3)
+        bq[st][0] = FP8 ? pack_half2(qv[4 * st], qv[4 * st + 1]) : pack_half2(qv[4 * st], qv[4 * st + 2]);
+        bq[st][1] = FP8 ? pack_half2(qv[4 * st + 2], qv[4 * st + 3]) : pack_half2(qv[4 * st + 1], qv[4 * st + 3]);
+        if (kOffset) {
+          const float2 x = unpack_half2(bq[st][0]), y = unpack_half2(bq[st][1]);
+          qs += (x.x + x.y) + (y.x + y.y);
+        }
+      }
+      if (kOffset) {
+        qs += __shfl_xor_sync(0xffffffffu, qs, 1);
+        qs += __shfl_xor_sync(0xffffffffu, qs, 2);
+        ch0 = kOffK * __shfl_sync(0xffffffffu, qs, 8 * c);
+        ch1 = kOffK * __shfl_sync(0xffffffffu, qs, 8 * c + 4);
+      }
+      cq0 = qk * pow2i((kOffset ? 24 : 0) - __shfl_sync(0xffffffffu, e, 8 * c));
+      cq1 = qk * pow2i((kOffset ? 24 : 0) - __shfl_sync(0xffffffffu, e, 8 * c + 4));
+    }
+    const float sl0 = kBias && 2 * c < G ? slope_log2(a.mod, h * G + 2 * c) : 0.0f;
+    const float sl1 = kBias && 2 * c + 1 < G ? slope_log2(a.mod, h * G + 2 * c + 1) : 0.0f;
+
+    float oacc[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.0f;
+    float osum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float m0 = kNegBig, m1 = kNegBig, l0 = 0.0f, l1 = 0.0f;
+    int E = 0;
+    float sv_hi = 0.0f, inv2E = 1.0f;  // (0: E not set yet)
+
+    // slots (2r, 2r + 1) x heads (2c, 2c + 1): cap and bias; slot 2r is at
+    // distance d0 from the query
+    auto transform = [&](float (&lg)[4], int d0) {
+      if (kCap) cap_scores(a.mod, lg);
+      if (kBias) {
+        const float da = (float)d0, db = (float)(d0 - 1);
+        lg[0] = fmaf(-sl0, da, lg[0]);
+        lg[1] = fmaf(-sl1, da, lg[1]);
+        lg[2] = fmaf(-sl0, db, lg[2]);
+        lg[3] = fmaf(-sl1, db, lg[3]);
+      }
+    };
+    // the running maxima rise to cover tm0, tm1 and the P V scale to cover a V
+    // scale svm > 0 (0: unchanged); O, the sums and l are rescaled
+    auto rescale = [&](float tm0, float tm1, float svm) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        tm0 = fmaxf(tm0, __shfl_xor_sync(0xffffffffu, tm0, o));
+        tm1 = fmaxf(tm1, __shfl_xor_sync(0xffffffffu, tm1, o));
+      }
+      const float nm0 = fmaxf(m0, tm0), nm1 = fmaxf(m1, tm1);
+      const float al0 = fast_exp2(m0 - nm0), al1 = fast_exp2(m1 - nm1);
+      const bool rescale_e = svm > sv_hi;
+      const int nE = rescale_e ? min(max(exponent_of(svm), -126), 126) : E;
+      const int dE = E - nE;
+      const float f = dE >= -126 ? pow2i(min(dE, 127)) : 0.0f;
+      const float f0 = al0 * f, f1 = al1 * f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        oacc[j][0] *= f0;
+        oacc[j][2] *= f0;
+        oacc[j][1] *= f1;
+        oacc[j][3] *= f1;
+      }
+      osum[0] *= f0;
+      osum[2] *= f0;
+      osum[1] *= f1;
+      osum[3] *= f1;
+      l0 *= al0;
+      l1 *= al1;
+      m0 = nm0;
+      m1 = nm1;
+      if (rescale_e) {
+        E = nE;
+        sv_hi = pow2i(min(E + 4, 127));
+        inv2E = pow2i(-E);
+      }
+    };
+
+    // the position of page k's first slot
+    auto page_pos = [&](int k) {
+      const int u = u_a + warp + kBWarps * k;
+      if (kBlocks) return kSinks + __shfl_sync(0xffffffffu, blk_use, k & 31) * bt + u % ppb * kPage;
+      if (FORM == kPrefix) return kSinks + (u < pre_npg ? u * kPage : pre_len + (u - pre_npg) * kPage);
+      return kSinks + u * kPage;
+    };
+    // K and V scale of page k (called once per page, in order)
+    auto scales_at = [&](int k, float& ks, float& vs) {
+      if ((k & 31) == 0 && k > 0) {
+        if (kBlocks) {
+          blk_use = blk_nxt;
+          blk_nxt = block_load((k >> 5) + 1);
+        }
+        ks_use = ks_nxt;
+        vs_use = vs_nxt;
+        const int id = tab_load((k >> 5) + 1);
+        ks_nxt = scale_of(s.k_scale, id);
+        vs_nxt = scale_of(s.v_scale, id);
+      }
+      ks = __shfl_sync(0xffffffffu, ks_use, k & 31);
+      vs = __shfl_sync(0xffffffffu, vs_use, k & 31);
+    };
+
+    // NP consecutive pages of this warp, their instructions interleaved
+    auto pages = [&](auto np_tag, int k) {
+      constexpr int NP = decltype(np_tag)::value;
+      const uint8_t* st[NP];
+      float ks[NP], vs[NP];
+#pragma unroll
+      for (int pp = 0; pp < NP; ++pp) {
+        st[pp] = ring + ((k + pp) & (kBStages - 1)) * kBStage;
+        scales_at(k + pp, ks[pp], vs[pp]);
+      }
+      float acc[NP][4];
+#pragma unroll
+      for (int pp = 0; pp < NP; ++pp) {
+        acc[pp][0] = acc[pp][2] = -ch0;
+        acc[pp][1] = acc[pp][3] = -ch1;
+      }
+      {
+        uint32_t w0[NP][8], w1[NP][8];
+#pragma unroll
+        for (int pp = 0; pp < NP; ++pp) {
+          const uint4 x0 = *reinterpret_cast<const uint4*>(st[pp] + k_off[0]);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(st[pp] + k_off[1]);
+          const uint4 x2 = *reinterpret_cast<const uint4*>(st[pp] + k_off[2]);
+          const uint4 x3 = *reinterpret_cast<const uint4*>(st[pp] + k_off[3]);
+          w0[pp][0] = x0.x; w0[pp][1] = x0.y; w0[pp][2] = x0.z; w0[pp][3] = x0.w;
+          w0[pp][4] = x1.x; w0[pp][5] = x1.y; w0[pp][6] = x1.z; w0[pp][7] = x1.w;
+          w1[pp][0] = x2.x; w1[pp][1] = x2.y; w1[pp][2] = x2.z; w1[pp][3] = x2.w;
+          w1[pp][4] = x3.x; w1[pp][5] = x3.y; w1[pp][6] = x3.z; w1[pp][7] = x3.w;
+        }
+#pragma unroll
+        for (int stp = 0; stp < 8; ++stp) {
+#pragma unroll
+          for (int pp = 0; pp < NP; ++pp) {
+            uint32_t a0, a1, a2, a3;
+            if (FP8) {
+              e4m3x4_to_h2(w0[pp][stp], a0, a2);
+              e4m3x4_to_h2(w1[pp][stp], a1, a3);
+            } else {
+              a0 = u8_even(w0[pp][stp]);
+              a1 = u8_even(w1[pp][stp]);
+              a2 = u8_even(w0[pp][stp] >> 8);
+              a3 = u8_even(w1[pp][stp] >> 8);
+            }
+            mma16816(acc[pp], a0, a1, a2, a3, bq[stp][0], bq[stp][1]);
+          }
+        }
+      }
+      float tm0 = -INFINITY, tm1 = -INFINITY, svm = 0.0f;
+#pragma unroll
+      for (int pp = 0; pp < NP; ++pp) {
+        const float f0 = ks[pp] * cq0, f1 = ks[pp] * cq1;
+        acc[pp][0] *= f0;
+        acc[pp][1] *= f1;
+        acc[pp][2] *= f0;
+        acc[pp][3] *= f1;
+        transform(acc[pp], pre_len + P - 1 - (page_pos(k + pp) + 2 * r));
+        tm0 = fmaxf(tm0, fmaxf(acc[pp][0], acc[pp][2]));
+        tm1 = fmaxf(tm1, fmaxf(acc[pp][1], acc[pp][3]));
+        svm = fmaxf(svm, vs[pp]);
+      }
+      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi))
+        rescale(tm0, tm1, svm);
+      uint32_t pb0[NP], pb1[NP];
+#pragma unroll
+      for (int pp = 0; pp < NP; ++pp) {
+        const float sn = vs[pp] * inv2E;
+        const float p0 = fast_exp2(acc[pp][0] - m0), p1 = fast_exp2(acc[pp][1] - m1);
+        const float p2 = fast_exp2(acc[pp][2] - m0), p3 = fast_exp2(acc[pp][3] - m1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        pb0[pp] = movmatrix_t(pack_half2(p0 * sn, p1 * sn));
+        pb1[pp] = movmatrix_t(pack_half2(p2 * sn, p3 * sn));
+      }
+      // O^T += V_codes^T . P^T (rows: head dims 16r + 2j (+1), columns: query heads)
+#pragma unroll
+      for (int pp = 0; pp < NP; ++pp) {
+        const uint4 r0 = *reinterpret_cast<const uint4*>(st[pp] + v_off[0]);
+        const uint4 r1 = *reinterpret_cast<const uint4*>(st[pp] + v_off[1]);
+        const uint4 r2 = *reinterpret_cast<const uint4*>(st[pp] + v_off[2]);
+        const uint4 r3 = *reinterpret_cast<const uint4*>(st[pp] + v_off[3]);
+        const uint32_t x0[4] = {r0.x, r0.y, r0.z, r0.w};
+        const uint32_t x1[4] = {r1.x, r1.y, r1.z, r1.w};
+        const uint32_t x2[4] = {r2.x, r2.y, r2.z, r2.w};
+        const uint32_t x3[4] = {r3.x, r3.y, r3.z, r3.w};
+#pragma unroll
+        for (int wd = 0; wd < 4; ++wd) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sa = (2 * half) | ((4 + 2 * half) << 8);
+            const uint32_t sb = (2 * half + 1) | ((5 + 2 * half) << 8);
+            uint32_t a0, a1, a2, a3;
+            if (FP8) {
+              a0 = e4m3_pair_to_h2(x0[wd], x2[wd], 2 * half);
+              a1 = e4m3_pair_to_h2(x0[wd], x2[wd], 2 * half + 1);
+              a2 = e4m3_pair_to_h2(x1[wd], x3[wd], 2 * half);
+              a3 = e4m3_pair_to_h2(x1[wd], x3[wd], 2 * half + 1);
+            } else {
+              a0 = u8_even(prmt(x0[wd], x2[wd], sa));
+              a1 = u8_even(prmt(x0[wd], x2[wd], sb));
+              a2 = u8_even(prmt(x1[wd], x3[wd], sa));
+              a3 = u8_even(prmt(x1[wd], x3[wd], sb));
+            }
+            mma16816(oacc[2 * wd + half], a0, a1, a2, a3, pb0[pp], pb1[pp]);
+          }
+        }
+        if (kOffset) {
+          constexpr uint32_t kOne = 0x3C003C00u;  // fp16 (1, 1)
+          mma16816(osum, kOne, kOne, kOne, kOne, pb0[pp], pb1[pp]);
+        }
+      }
+    };
+
+    int k = 0;
+    // two pages an iteration, the copies of the next two in flight
+#pragma unroll 1
+    for (; k + 1 < n_pg; k += 2) {
+      if (((stage_ok >> (k & (kBStages - 1))) & 3u) != 3u) break;  // a bad block id
+      issue(k + 2);
+      issue(k + 3);
+      cp_async_wait<2>();
+      __syncwarp();
+      pages(std::integral_constant<int, 2>{}, k);
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (; k < n_pg; ++k) {
+      // pages k and k + 1 were issued; the rest one at a time
+      cp_async_wait<1>();
+      __syncwarp();
+      if ((stage_ok >> (k & (kBStages - 1))) & 1u) {
+        pages(std::integral_constant<int, 1>{}, k);
+      } else {  // a bad block id: flagged and left out
+        float ks, vs;
+        scales_at(k, ks, vs);
+        if (lane == 0) atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
+      }
+      __syncwarp();
+      issue(k + 2);
+    }
+    cp_async_wait<0>();
+
+    // ---- exact rows: tiles of 16 (mma.sync bf16; the lane's dims are 32c ..
+    // 32c + 31 of its rows, in the order of Q and K alike)
+#pragma unroll 1
+    for (; k < n_my; ++k) {
+      // first exact row of the tile; (kPrefix) the prefix's tiles come before the sequence's
+      const int tile = u_a + warp + kBWarps * k - npg;
+      const bool shared = FORM == kPrefix && tile < pre_tiles;
+      const int e0 = (FORM == kPrefix && !shared ? tile - pre_tiles : tile) * kPage;
+      const int rows = block_exact_rows(shared ? pre_len : P, bt) - e0;
+      const size_t eb = ((size_t)(shared ? a.prefix : b) * hkv + h) * kExactRows(bt) + e0;
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      // MMA rows r and r + 8 hold exact rows 2r and 2r + 1 (as the pages' slots)
+      const bool on0 = 2 * r < rows, on1 = 2 * r + 1 < rows;
+      const uint4* ka = reinterpret_cast<const uint4*>(s.k_exact + (eb + (on0 ? 2 * r : 0)) * kHeadDim + 32 * c);
+      const uint4* kc = reinterpret_cast<const uint4*>(s.k_exact + (eb + (on1 ? 2 * r + 1 : 0)) * kHeadDim + 32 * c);
+      // V rows 2r (first K half) and 2r + 1 (second) of the tile, dims 32c ..:
+      // head dims 16r' + 2j and 16r' + 2j + 1 on the MMA's rows
+      const uint4* va = reinterpret_cast<const uint4*>(s.v_exact + (eb + (on0 ? 2 * r : 0)) * kHeadDim + 32 * c);
+      const uint4* vc = reinterpret_cast<const uint4*>(s.v_exact + (eb + (on1 ? 2 * r + 1 : 0)) * kHeadDim + 32 * c);
+      uint32_t wa[16], wc[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 x = va[i], y = vc[i];
+        if (!on0) x = make_uint4(0u, 0u, 0u, 0u);
+        if (!on1) y = make_uint4(0u, 0u, 0u, 0u);
+        wa[4 * i] = x.x; wa[4 * i + 1] = x.y; wa[4 * i + 2] = x.z; wa[4 * i + 3] = x.w;
+        wc[4 * i] = y.x; wc[4 * i + 1] = y.y; wc[4 * i + 2] = y.z; wc[4 * i + 3] = y.w;
+      }
+      const uint4* qp = reinterpret_cast<const uint4*>(qrow + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = ka[i], y = kc[i];
+        uint4 z = qp[i];
+        if (r >= G) z = make_uint4(0u, 0u, 0u, 0u);
+        mma16816_bf16(acc, x.x, y.x, x.y, y.y, z.x, z.y);
+        mma16816_bf16(acc, x.z, y.z, x.w, y.w, z.z, z.w);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= qk;
+      // position of exact row e: e itself (sinks), then the open block's
+      if (kCap) cap_scores(a.mod, acc);
+      if (kBias) {
+        const int ea = e0 + 2 * r, ec = ea + 1;
+        const int open = (shared ? block_closed(pre_len, bt) : closed) * bt;
+        const int last = pre_len + P - 1 - (FORM == kPrefix && !shared ? pre_len : 0);
+        const float da = (float)(last - (ea < kSinks ? ea : ea + open));
+        const float dc = (float)(last - (ec < kSinks ? ec : ec + open));
+        acc[0] = fmaf(-sl0, da, acc[0]);
+        acc[1] = fmaf(-sl1, da, acc[1]);
+        acc[2] = fmaf(-sl0, dc, acc[2]);
+        acc[3] = fmaf(-sl1, dc, acc[3]);
+      }
+      if (!on0) acc[0] = acc[1] = -INFINITY;
+      if (!on1) acc[2] = acc[3] = -INFINITY;
+      __nv_bfloat162 vm2 = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        vm2 = __hmax2(vm2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i])));
+        vm2 = __hmax2(vm2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i])));
+      }
+      float svm = fmaxf(__low2float(vm2), __high2float(vm2)) * 0x1p-7f;
+      const float tm0 = fmaxf(acc[0], acc[2]), tm1 = fmaxf(acc[1], acc[3]);
+      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi)) {
+        svm = warp_max(svm);
+        rescale(tm0, tm1, svm);
+      }
+      const float p0 = fast_exp2(acc[0] - m0), p1 = fast_exp2(acc[1] - m1);
+      const float p2 = fast_exp2(acc[2] - m0), p3 = fast_exp2(acc[3] - m1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      // the P V operands in the accumulators' units (2^24 for offset codes, 2^E),
+      // the power on both where it is large (V that leaves bf16's range by it is
+      // nothing beside 2^E)
+      const int eu = (kOffset ? 24 : 0) + E, ev = eu > 64 ? -64 : eu < -64 ? 64 : 0;
+      if (ev != 0) {
+        const __nv_bfloat162 f = __float2bfloat162_rn(pow2i(ev));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i]), f);
+          __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i]), f);
+          wa[i] = *reinterpret_cast<const uint32_t*>(&x);
+          wc[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      const float unit = pow2i(-eu - ev);
+      uint32_t h0, h1, q0, q1;
+      split_bf16x2(p0 * unit, p1 * unit, h0, q0);
+      split_bf16x2(p2 * unit, p3 * unit, h1, q1);
+      h0 = movmatrix_t(h0);
+      h1 = movmatrix_t(h1);
+      q0 = movmatrix_t(q0);
+      q1 = movmatrix_t(q1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t a0 = movmatrix_t(prmt(wa[j], wa[8 + j], 0x5410u)), a1 = movmatrix_t(prmt(wa[j], wa[8 + j], 0x7632u));
+        const uint32_t a2 = movmatrix_t(prmt(wc[j], wc[8 + j], 0x5410u)), a3 = movmatrix_t(prmt(wc[j], wc[8 + j], 0x7632u));
+        mma16816_bf16(oacc[j], a0, a1, a2, a3, h0, h1);
+        mma16816_bf16(oacc[j], a0, a1, a2, a3, q0, q1);
+      }
+    }
+
+    // ---- per-warp totals, CTA merge of the warps
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    __syncthreads();  // every warp is done with its ring: reuse shared memory
+    float* sm_m = reinterpret_cast<float*>(smem);
+    float* sm_l = sm_m + kBWarps * kMaxGroup;
+    float* sm_o = sm_l + kBWarps * kMaxGroup;  // [kBWarps][8][128]
+    int* sm_e = reinterpret_cast<int*>(sm_o + kBWarps * kMaxGroup * kHeadDim);
+    if (lane == 0) sm_e[warp] = E;
+    if (r == 0) {
+      sm_m[warp * kMaxGroup + 2 * c] = m0;
+      sm_m[warp * kMaxGroup + 2 * c + 1] = m1;
+      sm_l[warp * kMaxGroup + 2 * c] = l0;
+      sm_l[warp * kMaxGroup + 2 * c + 1] = l1;
+    }
+    {
+      const float sA = kOffset ? 0x1p24f : 1.0f;
+      const float b0 = kOffset ? kOffV * osum[0] : 0.0f;
+      const float b1 = kOffset ? kOffV * osum[1] : 0.0f;
+      float* o0 = sm_o + ((size_t)warp * kMaxGroup + 2 * c) * kHeadDim + 16 * r;
+      float* o1 = o0 + kHeadDim;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o0[2 * j] = oacc[j][0] * sA - b0;
+        o0[2 * j + 1] = oacc[j][2] * sA - b0;
+        o1[2 * j] = oacc[j][1] * sA - b1;
+        o1[2 * j + 1] = oacc[j][3] * sA - b1;
+      }
+    }
+    __syncthreads();
+    // the pair's partials, the slot of this one and of the first (here, not above:
+    // alive across the loops they cost 1 us of 90 for 16 x 32 heads of 4,111 tokens)
+    const int i_first = PARTS ? 0 : cta_of_page(Pf, T, N);
+    const int cnt = PARTS ? per_pair : cta_of_page(Pf + nu - 1, T, N) - i_first + 1;
+    const long long slot0 = PARTS ? Pf : (long long)bl * hkv + h + i_first;
+    const long long slot = PARTS ? F : (long long)bl * hkv + h + cta;
+    const int d = threadIdx.x;  // 128 threads = head_dim
+    uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
+    // (kPrefix) partials of the prefix's blocks, joined after the pair's own
+    const int more = FORM == kPrefix ? a.more : 0;
+    int e_most = sm_e[0];
+#pragma unroll
+    for (int ww = 1; ww < kBWarps; ++ww) e_most = max(e_most, sm_e[ww]);
+    for (int g = 0; g < G; ++g) {
+      float M = kNegBig;
+#pragma unroll
+      for (int ww = 0; ww < kBWarps; ++ww) M = fmaxf(M, sm_m[ww * kMaxGroup + g]);
+      float o = 0.0f, l = 0.0f;
+#pragma unroll
+      for (int ww = 0; ww < kBWarps; ++ww) {
+        const float wt = fast_exp2(sm_m[ww * kMaxGroup + g] - M);
+        o += wt * pow2i(max(sm_e[ww] - e_most, -126)) * sm_o[((size_t)ww * kMaxGroup + g) * kHeadDim + d];
+        l += wt * sm_l[ww * kMaxGroup + g];
+      }
+      o = l != 0.0f ? o * (1.0f / l) * pow2i(e_most) : 0.0f;
+      if (cnt + more == 1) {
+        orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+      } else {
+        const size_t ps = (size_t)slot * G + g;
+        a.part_o[ps * kHeadDim + d] = o;
+        if (d == 0) {
+          a.part_ml[ps * 2] = M;
+          a.part_ml[ps * 2 + 1] = l;
+        }
+      }
+    }
+    if (cnt + more > 1) {
+      // the pair's last CTA joins the partials, in CTA order
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        __threadfence();
+        sh_last = atomicAdd(&s.tickets[b * hkv + h], 1) == cnt - 1;
+        __threadfence();
+      }
+      __syncthreads();
+      if (sh_last) {
+        // a warp per head (several when there are fewer heads than warps, each
+        // with every wph-th part): 32 parts' maxima and sums across the lanes,
+        // then their rows, eight of 16 bytes a lane in flight
+        const int wph = G >= kBWarps ? 1 : kBWarps / G, share = warp % wph;
+        const size_t base = (size_t)slot0 * G;
+        float* sm_j = reinterpret_cast<float*>(smem);  // [kBWarps][kHeadDim + 2]
+        for (int g = warp / wph; g < G; g += kBWarps / wph) {
+          float M = kNegBig, l = 0.0f;
+          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + base + g;
+          const float4* po = reinterpret_cast<const float4*>(a.part_o + (base + g) * kHeadDim) + lane;
+          const int mine = (cnt + more - share + wph - 1) / wph;  // parts share + wph j
+          // part i: the pair's own, then (kPrefix) those of the prefix
+          const size_t more0 = FORM == kPrefix ? ((size_t)h * batch + bl) * G + g : 0;
+          const size_t more_step = FORM == kPrefix ? (size_t)hkv * batch * G : 0;
+          auto part_ml = [&](int i) {
+            if (FORM == kPrefix && i >= cnt)
+              return __ldcg(reinterpret_cast<const float2*>(a.more_ml) + more0 + (i - cnt) * more_step);
+            return __ldcg(ml + (size_t)i * G);
+          };
+          auto part_o = [&](int i) {
+            if (FORM == kPrefix && i >= cnt)
+              return __ldcg(reinterpret_cast<const float4*>(a.more_o + (more0 + (i - cnt) * more_step) * kHeadDim) +
+                            lane);
+            return __ldcg(po + (size_t)i * G * (kHeadDim / 4));
+          };
+          for (int j0 = 0; j0 < mine; j0 += 32) {
+            const bool on = j0 + lane < mine;
+            const float2 x = on ? part_ml(share + wph * (j0 + lane)) : make_float2(kNegBig, 0.0f);
+            const float top = fmaxf(M, warp_max(x.x));
+            // the mean so far and the parts' shares of the new one
+            float al = l * fast_exp2(M - top), wt = on ? fast_exp2(x.x - top) * x.y : 0.0f;
+            M = top;
+            l = al + warp_sum(wt);
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            al *= inv;
+            wt *= inv;
+            o.x *= al; o.y *= al; o.z *= al; o.w *= al;
+            for (int i0 = 0; i0 < min(32, mine - j0); i0 += 8) {
+              float4 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)  // past the end: the last part again, weight 0
+                y[i] = part_o(share + wph * min(j0 + i0 + i, mine - 1));
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float w = __shfl_sync(0xffffffffu, wt, i0 + i);
+                if (j0 + i0 + i < mine) {
+                  o.x += w * y[i].x; o.y += w * y[i].y; o.z += w * y[i].z; o.w += w * y[i].w;
+                }
+              }
+            }
+          }
+          if (wph > 1) {  // (kBWarps >= wph G: every warp with a head comes here once)
+            *reinterpret_cast<float4*>(sm_j + warp * kJoinRow + 4 * lane) = o;
+            if (lane == 0) {
+              sm_j[warp * kJoinRow + kHeadDim] = M;
+              sm_j[warp * kJoinRow + kHeadDim + 1] = l;
+            }
+          } else {
+            uint2 w;
+            w.x = pack_bf16x2(o.x, o.y);
+            w.y = pack_bf16x2(o.z, o.w);
+            *reinterpret_cast<uint2*>(out + ((size_t)bl * s.hq + h * G + g) * kHeadDim + 4 * lane) = w;
+          }
+        }
+        if (wph > 1) {
+          __syncthreads();
+          for (int g = 0; g < G; ++g) {
+            const float* row = sm_j + g * wph * kJoinRow;
+            float M = kNegBig, o = 0.0f, l = 0.0f;
+            for (int i = 0; i < wph; ++i) M = fmaxf(M, row[i * kJoinRow + kHeadDim]);
+            for (int i = 0; i < wph; ++i)
+              l += fast_exp2(row[i * kJoinRow + kHeadDim] - M) * row[i * kJoinRow + kHeadDim + 1];
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            for (int i = 0; i < wph; ++i)
+              o += fast_exp2(row[i * kJoinRow + kHeadDim] - M) * row[i * kJoinRow + kHeadDim + 1] * inv *
+                   row[i * kJoinRow + d];
+            orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+          }
+        }
+        if (threadIdx.x == 0) s.tickets[b * hkv + h] = 0;
+      }
+    }
+    __syncthreads();  // shared memory is reused by the next pair
+    F = PARTS ? F + N : Pf + u_e;
+  }
+}
+
+template <int FORM, bool FP8, int MOD, bool PARTS>
+cudaError_t block_attn_smem() {
+  static int done[64] = {0};
+  return opt_in_smem(reinterpret_cast<const void*>(block_attn_kernel<FORM, FP8, MOD, PARTS>), kBSmem, done);
+}
+
+template <int FORM, bool FP8, int MOD>
+int block_attn_ctas() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev < 64 && cached[dev] > 0) return cached[dev];
+  int n = 0;
+  if (block_attn_smem<FORM, FP8, MOD, false>() != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, block_attn_kernel<FORM, FP8, MOD, false>, kBThreads, kBSmem) !=
+          cudaSuccess ||
+      n < 1)
+    n = 1;
+  if (dev < 64) cached[dev] = n;
+  return n;
+}
+
+int block_mod(const ScoreMod& m) { return (m.c2 > 0.0f ? kBCap : 0) | (m.slopes != nullptr ? kBBias : 0); }
+
+template <int FORM, bool FP8, int MOD>
+cudaError_t launch_block_attn_t(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
+                                const BlockAttn& w, cudaStream_t st) {
+  const cudaError_t e = w.parts ? block_attn_smem<FORM, FP8, MOD, true>() : block_attn_smem<FORM, FP8, MOD, false>();
+  if (e != cudaSuccess) return e;
+  if (w.parts)
+    block_attn_kernel<FORM, FP8, MOD, true><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
+  else
+    block_attn_kernel<FORM, FP8, MOD, false><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
+  return cudaGetLastError();
+}
+
+template <int FORM, bool FP8>
+cudaError_t launch_block_attn_mod(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
+                                  const BlockAttn& w, cudaStream_t st) {
+  switch (block_mod(w.mod)) {
+    case 0: return launch_block_attn_t<FORM, FP8, 0>(s, seq_begin, batch, q, out, w, st);
+    case 1: return launch_block_attn_t<FORM, FP8, 1>(s, seq_begin, batch, q, out, w, st);
+    case 2: return launch_block_attn_t<FORM, FP8, 2>(s, seq_begin, batch, q, out, w, st);
+    default: return launch_block_attn_t<FORM, FP8, 3>(s, seq_begin, batch, q, out, w, st);
+  }
+}
+
+template <int FORM, bool FP8>
+int block_attn_ctas_mod(int mod) {
+  switch (mod) {
+    case 0: return block_attn_ctas<FORM, FP8, 0>();
+    case 1: return block_attn_ctas<FORM, FP8, 1>();
+    case 2: return block_attn_ctas<FORM, FP8, 2>();
+    default: return block_attn_ctas<FORM, FP8, 3>();
+  }
+}
+
+
+template <int FORM>
+int attn_ctas(const BlockState& s, const ScoreMod& mod) {
+  return s.fp8 ? block_attn_ctas_mod<FORM, true>(block_mod(mod)) : block_attn_ctas_mod<FORM, false>(block_mod(mod));
+}
+
+template <int FORM>
+cudaError_t attn_launch(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
+                        const BlockAttn& w, cudaStream_t st) {
+  return s.fp8 ? launch_block_attn_mod<FORM, true>(s, seq_begin, batch, q, out, w, st)
+               : launch_block_attn_mod<FORM, false>(s, seq_begin, batch, q, out, w, st);
+}
+
+}  // namespace
+}  // namespace kvc

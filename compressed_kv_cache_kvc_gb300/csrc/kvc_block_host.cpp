@@ -156,6 +156,48 @@ int sm_count(kvc_block_cache* c) {
   return c->sm_count;
 }
 
+bool attention_args_ok(const void* d_q, const void* d_out, float sm_scale, float softcap, const float* d_slopes) {
+  return d_q && d_out && aligned(d_q, 16) && aligned(d_out, 16) && aligned(d_slopes, 4) && sm_scale > 0.0f &&
+         std::isfinite(sm_scale) && softcap >= 0.0f && std::isfinite(softcap);
+}
+
+kvc::BlockAttn attention_of(const WsLayout& wl, void* d_workspace, float sm_scale, float softcap,
+                            const float* d_slopes) {
+  kvc::BlockAttn a{};
+  a.part_o = static_cast<float*>(d_workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + wl.part_ml);
+  a.mod = kvc::make_score_mod(sm_scale, softcap, d_slopes);
+  a.qk_scale_log2 = sm_scale * kvc::kLog2E;
+  return a;
+}
+
+// The CTAs of an attention, and whether they take parts of pairs.
+void split_attention(kvc_block_cache* c, kvc::BlockAttn* a, int per_sm, int batch, long long units, bool ragged) {
+  const int hkv = c->cfg.num_kv_heads;
+  a->ncta = grid_of(sm_count(c), per_sm, batch * hkv, units);
+  if (ragged && batch <= kvc::kMaxSplitBatch && a->ncta >= batch * hkv * kPartsPerPair) {
+    // (a sequence has one part at least; a CTA without a part ends)
+    a->parts = a->ncta / hkv;
+    a->ncta = std::min((a->parts + batch) * hkv, kvc::kMaxSplitCtas);
+  }
+}
+
+bool choice_ok(int top, int recent) { return top > 0 && recent >= 0 && (long long)top + recent <= 1 << 20; }
+
+struct SelectedLayout {
+  WsLayout ws;
+  size_t keys, list, total;
+};
+SelectedLayout selected_layout(const kvc_block_cache* c, int batch, int top, int recent) {
+  const size_t pairs = (size_t)batch * c->cfg.num_kv_heads;
+  SelectedLayout l{};
+  l.ws = ws_layout(c, batch);
+  l.keys = align_up(l.ws.total);
+  l.list = l.keys + align_up(pairs * c->cfg.max_blocks_per_seq * 4);
+  l.total = l.list + align_up(pairs * ((size_t)top + recent) * 4);
+  return l;
+}
+
 }  // namespace
 
 extern "C" {
@@ -357,9 +399,7 @@ kvc_status kvc_block_attention(kvc_block_cache* c, int32_t seq_begin, int32_t ba
   if (!c) return KVC_ERR_INVALID_ARG;
   c->last_launches = 0;
   if (!range_ok(c, seq_begin, batch)) return KVC_ERR_INVALID_ARG;
-  if (!d_q || !d_out || !aligned(d_q, 16) || !aligned(d_out, 16) || !aligned(d_slopes, 4)) return KVC_ERR_INVALID_ARG;
-  if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale) || !(softcap >= 0.0f) || !std::isfinite(softcap))
-    return KVC_ERR_INVALID_ARG;
+  if (!attention_args_ok(d_q, d_out, sm_scale, softcap, d_slopes)) return KVC_ERR_INVALID_ARG;
   const WsLayout wl = ws_layout(c, batch);
   if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < wl.total) return KVC_ERR_INVALID_ARG;
   long long units = 0;
@@ -370,20 +410,95 @@ kvc_status kvc_block_attention(kvc_block_cache* c, int32_t seq_begin, int32_t ba
     units += (long long)kvc::block_units(P, c->cfg.block_tokens) * c->cfg.num_kv_heads;
     ragged |= P != c->pos[seq_begin];
   }
-  kvc::BlockAttn a{};
-  a.part_o = static_cast<float*>(d_workspace);
-  a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + wl.part_ml);
-  a.mod = kvc::make_score_mod(sm_scale, softcap, d_slopes);
-  a.qk_scale_log2 = sm_scale * kvc::kLog2E;
-  a.ncta = grid_of(sm_count(c), kvc::block_attention_ctas_per_sm(c->dev, a.mod), batch * c->cfg.num_kv_heads, units);
-  const int hkv = c->cfg.num_kv_heads;
-  if (ragged && batch <= kvc::kMaxSplitBatch && a.ncta >= batch * hkv * kPartsPerPair) {
-    // (a sequence has one part at least; a CTA without a part ends)
-    a.parts = a.ncta / hkv;
-    a.ncta = std::min((a.parts + batch) * hkv, kvc::kMaxSplitCtas);
-  }
+  kvc::BlockAttn a = attention_of(wl, d_workspace, sm_scale, softcap, d_slopes);
+  split_attention(c, &a, kvc::block_attention_ctas_per_sm(c->dev, a.mod), batch, units, ragged);
   if (kvc::launch_block_attention(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
                                   static_cast<uint16_t*>(d_out), a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return KVC_ERR_CUDA;
+  c->last_launches = 1;
+  return KVC_OK;
+}
+
+size_t kvc_block_selected_workspace_bytes(const kvc_block_cache* c, int32_t batch, int32_t top_blocks,
+                                          int32_t recent_blocks) {
+  if (!c || batch <= 0 || batch > c->cfg.max_batch || !choice_ok(top_blocks, recent_blocks)) return 0;
+  return selected_layout(c, batch, top_blocks, recent_blocks).total;
+}
+
+kvc_status kvc_block_selected_attention(kvc_block_cache* c, int32_t seq_begin, int32_t batch, int32_t top_blocks,
+                                        int32_t recent_blocks, const void* d_q, void* d_out, int32_t* d_blocks,
+                                        float sm_scale, float softcap, const float* d_slopes, void* d_workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (!c) return KVC_ERR_INVALID_ARG;
+  c->last_launches = 0;
+  if (!range_ok(c, seq_begin, batch) || !choice_ok(top_blocks, recent_blocks)) return KVC_ERR_INVALID_ARG;
+  if (!attention_args_ok(d_q, d_out, sm_scale, softcap, d_slopes) || !aligned(d_blocks, 4)) return KVC_ERR_INVALID_ARG;
+  const SelectedLayout sl = selected_layout(c, batch, top_blocks, recent_blocks);
+  if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < sl.total) return KVC_ERR_INVALID_ARG;
+  if (!c->bounds.codes) return KVC_ERR_STATE;
+  const int bt = c->cfg.block_tokens, most = top_blocks + recent_blocks;
+  long long units = 0;
+  int longest = 0, first = 0;
+  bool ragged = false;
+  for (int i = 0; i < batch; ++i) {
+    const int P = c->pos[seq_begin + i];
+    if (P <= 0) return KVC_ERR_INVALID_ARG;  // nothing to attend to
+    const int u = std::min(kvc::block_closed(P, bt), most) * (bt / kvc::kPage) +
+                  (kvc::block_exact_rows(P, bt) + kvc::kPage - 1) / kvc::kPage;
+    units += (long long)u * c->cfg.num_kv_heads;
+    if (i == 0) first = u;
+    ragged |= u != first;
+    longest = std::max(longest, P);
+  }
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  kvc::BlockChoice ch{};
+  ch.keys = reinterpret_cast<uint32_t*>(ws + sl.keys);
+  ch.list = d_blocks ? d_blocks : reinterpret_cast<int32_t*>(ws + sl.list);
+  ch.top = top_blocks;
+  ch.recent = recent_blocks;
+  kvc::BlockAttn a = attention_of(sl.ws, d_workspace, sm_scale, softcap, d_slopes);
+  a.list = ch.list;
+  a.most = most;
+  split_attention(c, &a, kvc::block_selected_ctas_per_sm(c->dev, a.mod), batch, units, ragged);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const uint16_t* q = static_cast<const uint16_t*>(d_q);
+  if (kvc::launch_block_choice(c->dev, c->bounds, ch, seq_begin, batch, longest, q, st) != cudaSuccess ||
+      kvc::launch_block_selected(c->dev, seq_begin, batch, q, static_cast<uint16_t*>(d_out), a, st) != cudaSuccess)
+    return KVC_ERR_CUDA;
+  c->last_launches = 3;
+  return KVC_OK;
+}
+
+size_t kvc_block_prefix_workspace_bytes(const kvc_block_cache* c, int32_t batch) {
+  if (!c || batch <= 0 || batch > c->cfg.max_batch) return 0;
+  return ws_layout(c, batch).total;
+}
+
+kvc_status kvc_block_prefix_attention(kvc_block_cache* c, int32_t prefix, int32_t seq_begin, int32_t batch,
+                                      const void* d_q, void* d_out, float sm_scale, float softcap,
+                                      const float* d_slopes, void* d_workspace, size_t workspace_bytes, void* stream) {
+  if (!c) return KVC_ERR_INVALID_ARG;
+  c->last_launches = 0;
+  if (!range_ok(c, seq_begin, batch) || !range_ok(c, prefix, 1) || (prefix >= seq_begin && prefix < seq_begin + batch))
+    return KVC_ERR_INVALID_ARG;
+  if (!attention_args_ok(d_q, d_out, sm_scale, softcap, d_slopes)) return KVC_ERR_INVALID_ARG;
+  const WsLayout wl = ws_layout(c, batch);
+  if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < wl.total) return KVC_ERR_INVALID_ARG;
+  const int bt = c->cfg.block_tokens, shared = c->pos[prefix];
+  long long units = 0;
+  bool ragged = false;
+  for (int i = 0; i < batch; ++i) {
+    const int P = c->pos[seq_begin + i];
+    if (P + (long long)shared <= 0 || P + (long long)shared > 2000000000LL) return KVC_ERR_INVALID_ARG;
+    units += (long long)(kvc::block_units(P, bt) + kvc::block_units(shared, bt)) * c->cfg.num_kv_heads;
+    ragged |= P != c->pos[seq_begin];
+  }
+  kvc::BlockAttn a = attention_of(wl, d_workspace, sm_scale, softcap, d_slopes);
+  a.prefix = prefix;
+  a.prefix_pages = 1;
+  split_attention(c, &a, kvc::block_prefix_ctas_per_sm(c->dev, a.mod), batch, units, ragged);
+  if (kvc::launch_block_prefix(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
+                               static_cast<uint16_t*>(d_out), a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return KVC_ERR_CUDA;
   c->last_launches = 1;
   return KVC_OK;

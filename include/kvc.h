@@ -712,6 +712,45 @@ kvc_status kvc_block_attention(kvc_block_cache* cache, int32_t seq_begin, int32_
                                float sm_scale, float softcap, const float* d_slopes, void* d_workspace,
                                size_t workspace_bytes, void* stream);
 
+/* The same over selected blocks of each (sequence, KV head): of the closed blocks
+ * the `recent_blocks` newest and, of the others, the `top_blocks` whose score is
+ * highest (ties to the lower block), beside the sinks and the open block.  Needs
+ * the keys' bounds (kvc_block_set_key_bounds).  A block's score for a query head
+ * bounds its products with the block's keys from above: with q8 the INT8 codes of
+ * the query row and s their scale (as a row of kvc_quantize_append), lo, hi and t the
+ * block's bounds and their scale,
+ *   I = sum over the 128 channels of max(q8 lo, q8 hi),  score = (I s) t,
+ * I exact, both products rounded to fp32; a KV head takes the largest of its query
+ * heads' scores.  Neither softcap (which keeps the order) nor slopes enter the choice;
+ * both enter the attention.
+ *   d_blocks: null, or i32 [batch][Hkv][top_blocks + recent_blocks]: the chosen
+ *   blocks (0 holds positions 4 ..), ascending, -1 behind the last.
+ *   d_workspace: kvc_block_selected_workspace_bytes(cache, batch, top_blocks,
+ *   recent_blocks) bytes, 256-byte aligned.
+ * Three launches.  Replays, order and errors as kvc_block_attention, and
+ * KVC_ERR_INVALID_ARG for top_blocks < 1, recent_blocks < 0 or more than 2^20 of
+ * both together, KVC_ERR_STATE without bounds. */
+size_t kvc_block_selected_workspace_bytes(const kvc_block_cache* cache, int32_t batch, int32_t top_blocks,
+                                          int32_t recent_blocks);
+kvc_status kvc_block_selected_attention(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t top_blocks,
+                                        int32_t recent_blocks, const void* d_q, void* d_out, int32_t* d_blocks,
+                                        float sm_scale, float softcap, const float* d_slopes, void* d_workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* The same for sequences that share a prefix, held once as the sequence `prefix`:
+ * every query attends to the prefix's tokens and to its own sequence's, which
+ * follow them (token i of a sequence that comes after Pp tokens of the prefix is
+ * at position Pp + i for the distances of the transform; kvc_block_append_rotary
+ * with first = Pp for the rotation).
+ *   d_workspace: kvc_block_prefix_workspace_bytes(cache, batch) bytes.
+ * A sequence, or the prefix, may be empty (rows that see nothing at all are
+ * refused, 0 in a replay).  Replays, order and errors as kvc_block_attention, and
+ * KVC_ERR_INVALID_ARG for a prefix outside the cache or inside the slice. */
+size_t kvc_block_prefix_workspace_bytes(const kvc_block_cache* cache, int32_t batch);
+kvc_status kvc_block_prefix_attention(kvc_block_cache* cache, int32_t prefix, int32_t seq_begin, int32_t batch,
+                                      const void* d_q, void* d_out, float sm_scale, float softcap,
+                                      const float* d_slopes, void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* Read the cache back as dense tensors: the values of positions [pos_begin,
  * pos_begin + n) of every sequence of the slice as the attention sees them
  * (code * scale rounded to bf16; sinks and the open block as appended).
