@@ -89,6 +89,17 @@ cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, co
 int block_selected_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
 cudaError_t launch_block_selected(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                   const BlockAttn& w, cudaStream_t st);
+// The products of all query rows with a prefix's closed blocks: `splits` runs of
+// them per KV head, a partial result of every row each.
+struct PrefixTc {
+  float *more_o, *more_ml;  // [splits][hkv][batch][group][128], [..][2]
+  ScoreMod mod;
+  float qk_scale_log2;
+  int prefix, batch, splits;
+};
+constexpr int kPrefixRows = 256, kPrefixTile = 128;  // query rows of a CTA, tokens of a tile
+cudaError_t launch_prefix_tc(const BlockState& s, int seq_begin, const uint16_t* q, const PrefixTc& a,
+                             cudaStream_t st);
 int block_prefix_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
 cudaError_t launch_block_prefix(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                 const BlockAttn& w, cudaStream_t st);

@@ -198,6 +198,39 @@ SelectedLayout selected_layout(const kvc_block_cache* c, int batch, int top, int
   return l;
 }
 
+// Runs of the prefix's tiles per KV head: the number that takes the fewest tiles one
+// after another, over all waves of CTAs, and of those the smallest.
+constexpr int kPrefixCtas = 152;
+int prefix_splits(long long ctas, long long tiles) {
+  const long long most = std::max(1LL, std::min(tiles, kPrefixCtas / std::min<long long>(ctas, kPrefixCtas)));
+  long long best = 1, cost = 0;
+  for (long long k = 1; k <= most; ++k) {
+    const long long c = (ctas * k + kPrefixCtas - 1) / kPrefixCtas * ((tiles + k - 1) / k);
+    if (k == 1 || c < cost) {
+      best = k;
+      cost = c;
+    }
+  }
+  return (int)best;
+}
+
+struct PrefixLayout {
+  WsLayout ws;
+  size_t more_o, more_ml, total;
+};
+PrefixLayout prefix_layout(const kvc_block_cache* c, int batch) {
+  const size_t rows = (size_t)batch * c->dev.group;
+  const size_t ctas = (rows + kvc::kPrefixRows - 1) / kvc::kPrefixRows * c->cfg.num_kv_heads;
+  const size_t parts = std::max<size_t>(1, kPrefixCtas / std::min<size_t>(ctas, kPrefixCtas)) * rows *
+                       c->cfg.num_kv_heads;
+  PrefixLayout l{};
+  l.ws = ws_layout(c, batch);
+  l.more_o = align_up(l.ws.total);
+  l.more_ml = l.more_o + align_up(parts * kvc::kHeadDim * 4);
+  l.total = l.more_ml + align_up(parts * 2 * 4);
+  return l;
+}
+
 }  // namespace
 
 extern "C" {
@@ -471,7 +504,7 @@ kvc_status kvc_block_selected_attention(kvc_block_cache* c, int32_t seq_begin, i
 
 size_t kvc_block_prefix_workspace_bytes(const kvc_block_cache* c, int32_t batch) {
   if (!c || batch <= 0 || batch > c->cfg.max_batch) return 0;
-  return ws_layout(c, batch).total;
+  return prefix_layout(c, batch).total;
 }
 
 kvc_status kvc_block_prefix_attention(kvc_block_cache* c, int32_t prefix, int32_t seq_begin, int32_t batch,
@@ -482,25 +515,46 @@ kvc_status kvc_block_prefix_attention(kvc_block_cache* c, int32_t prefix, int32_
   if (!range_ok(c, seq_begin, batch) || !range_ok(c, prefix, 1) || (prefix >= seq_begin && prefix < seq_begin + batch))
     return KVC_ERR_INVALID_ARG;
   if (!attention_args_ok(d_q, d_out, sm_scale, softcap, d_slopes)) return KVC_ERR_INVALID_ARG;
-  const WsLayout wl = ws_layout(c, batch);
-  if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < wl.total) return KVC_ERR_INVALID_ARG;
-  const int bt = c->cfg.block_tokens, shared = c->pos[prefix];
+  const PrefixLayout pl = prefix_layout(c, batch);
+  if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < pl.total) return KVC_ERR_INVALID_ARG;
+  const int bt = c->cfg.block_tokens, hkv = c->cfg.num_kv_heads, shared = c->pos[prefix];
+  const int tiles = (kvc::block_closed(shared, bt) * bt + kvc::kPrefixTile - 1) / kvc::kPrefixTile;
+  const bool product = batch > 1 && tiles > 3;
+  const long long front = (kvc::block_exact_rows(shared, bt) + kvc::kPage - 1) / kvc::kPage +
+                          (product ? 0LL : (long long)kvc::block_closed(shared, bt) * (bt / kvc::kPage));
   long long units = 0;
   bool ragged = false;
   for (int i = 0; i < batch; ++i) {
     const int P = c->pos[seq_begin + i];
     if (P + (long long)shared <= 0 || P + (long long)shared > 2000000000LL) return KVC_ERR_INVALID_ARG;
-    units += (long long)(kvc::block_units(P, bt) + kvc::block_units(shared, bt)) * c->cfg.num_kv_heads;
+    units += (kvc::block_units(P, bt) + front) * hkv;
     ragged |= P != c->pos[seq_begin];
   }
-  kvc::BlockAttn a = attention_of(wl, d_workspace, sm_scale, softcap, d_slopes);
+  kvc::BlockAttn a = attention_of(pl.ws, d_workspace, sm_scale, softcap, d_slopes);
   a.prefix = prefix;
-  a.prefix_pages = 1;
+  a.prefix_pages = product ? 0 : 1;
   split_attention(c, &a, kvc::block_prefix_ctas_per_sm(c->dev, a.mod), batch, units, ragged);
-  if (kvc::launch_block_prefix(c->dev, seq_begin, batch, static_cast<const uint16_t*>(d_q),
-                               static_cast<uint16_t*>(d_out), a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const uint16_t* q = static_cast<const uint16_t*>(d_q);
+  if (product) {
+    uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+    kvc::PrefixTc t{};
+    t.more_o = reinterpret_cast<float*>(ws + pl.more_o);
+    t.more_ml = reinterpret_cast<float*>(ws + pl.more_ml);
+    t.mod = a.mod;
+    t.qk_scale_log2 = a.qk_scale_log2;
+    t.prefix = prefix;
+    t.batch = batch;
+    t.splits = prefix_splits((long long)(batch * c->dev.group + kvc::kPrefixRows - 1) / kvc::kPrefixRows * hkv, tiles);
+    a.more = t.splits;
+    a.more_o = t.more_o;
+    a.more_ml = t.more_ml;
+    if (kvc::launch_prefix_tc(c->dev, seq_begin, q, t, st) != cudaSuccess) return KVC_ERR_CUDA;
+    c->last_launches = 1;
+  }
+  if (kvc::launch_block_prefix(c->dev, seq_begin, batch, q, static_cast<uint16_t*>(d_out), a, st) != cudaSuccess)
     return KVC_ERR_CUDA;
-  c->last_launches = 1;
+  ++c->last_launches;
   return KVC_OK;
 }
 
