@@ -59,6 +59,8 @@ struct BlockAttn {
   // units; partials of its blocks from elsewhere, `more` of [hkv][batch][group]
   int prefix, prefix_pages, more;
   const float *more_o, *more_ml;
+  int early;       // (those two) launched under the kernel before them
+  int part_units;  // (those two) units of a part at least; `parts` of them at most per pair
   int parts;  // 0: equal runs across pairs; else a CTA takes a part of one pair, and the sequences of a head
                     // have about this many parts together
 };
@@ -86,7 +88,6 @@ cudaError_t launch_block_attention(const BlockState& s, int seq_begin, int batch
 // longest: the most tokens a sequence of the slice holds
 cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, const BlockChoice& ch, int seq_begin,
                                 int batch, int longest, const uint16_t* q, cudaStream_t st);
-int block_selected_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
 cudaError_t launch_block_selected(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                   const BlockAttn& w, cudaStream_t st);
 // The products of all query rows with a prefix's closed blocks: `splits` runs of
@@ -100,7 +101,6 @@ struct PrefixTc {
 constexpr int kPrefixRows = 256, kPrefixTile = 128;  // query rows of a CTA, tokens of a tile
 cudaError_t launch_prefix_tc(const BlockState& s, int seq_begin, const uint16_t* q, const PrefixTc& a,
                              cudaStream_t st);
-int block_prefix_ctas_per_sm(const BlockState& s, const ScoreMod& mod);
 cudaError_t launch_block_prefix(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                 const BlockAttn& w, cudaStream_t st);
 

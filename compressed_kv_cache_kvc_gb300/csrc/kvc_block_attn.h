@@ -23,6 +23,10 @@ using namespace codes;
 __host__ __device__ constexpr int kExactRows(int bt) { return kSinks + bt; }
 
 enum { kPlain = 0, kSelected = 1, kPrefix = 2 };  // forms
+#ifndef KVC_DP
+#define KVC_DP true
+#endif
+constexpr bool kDirectParts = KVC_DP;
 
 // ---------------------------------------------------------------- attention
 // out = softmax(z) . v over everything a sequence holds, z as kvc_score.h says.
@@ -67,6 +71,7 @@ constexpr int kBStages = 4;
 constexpr int kBStage = 4096;  // K page, V page
 constexpr int kBSmem = kBWarps * kBStages * kBStage;
 constexpr float kBLazy = 4.0f;
+constexpr int kMergeRow = kHeadDim + 4;
 constexpr int kJoinRow = kHeadDim + 4;  // one warp's joined row: 128 means, the maximum, the sum
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -94,13 +99,22 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
                                                                uint16_t* __restrict__ out, BlockAttn a) {
   constexpr bool kCap = (MOD & kBCap) != 0, kBias = (MOD & kBBias) != 0;
   constexpr bool kOffset = !FP8;
+  constexpr bool kDirect = FORM != kPlain;  // a CTA has one part of one pair
   constexpr float kOffK = 128.0f * 0x1p-24f, kOffV = 128.0f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int cum[kMaxCallBatch + 1], len[kMaxCallBatch];
-  __shared__ int parts[PARTS ? kMaxSplitBatch + 1 : 1];  // (split pairs) parts of a head of the sequences before
+  __shared__ int cum[kDirect ? 1 : kMaxCallBatch + 1], len[kDirect ? 1 : kMaxCallBatch];
+  __shared__ int parts[PARTS && !kDirect ? kMaxSplitBatch + 1 : 1];  // (split pairs) parts of a head of the sequences before
   __shared__ int sh_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bt = s.bt, ppb = bt / kPage;  // pages per block
+  const int G = s.group, hkv = s.hkv;
+  int bl = 0, h = 0, P = 0, part = 0;  // the pair, its sequence's length, the part
+  if (kDirect) {
+    part = blockIdx.x % a.parts;
+    h = blockIdx.x / a.parts % hkv;
+    bl = blockIdx.x / a.parts / hkv;
+    P = s.seq_pos[seq_begin + bl];
+  }
   // (kPrefix) tokens of the prefix; its pages and tiles of exact rows among the units
   const int pre_len = FORM == kPrefix ? s.seq_pos[a.prefix] : 0;
   const int pre_npg = FORM == kPrefix && a.prefix_pages ? block_closed(pre_len, bt) * ppb : 0;
@@ -110,7 +124,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
   auto units_of = [&](int n) {
     return pre_npg + pre_tiles + blocks_of(n) * ppb + (block_exact_rows(n, bt) + kPage - 1) / kPage;
   };
-  if (warp == 0) {
+  if (!kDirect && warp == 0) {
     int carry = 0;
     if (lane == 0) cum[0] = 0;
     for (int base = 0; base < batch; base += 32) {
@@ -145,22 +159,30 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       }
     }
   }
-  __syncthreads();
+  if (!kDirect) __syncthreads();
 
-  const int G = s.group, hkv = s.hkv;
   const int r = lane >> 2, c = lane & 3;
-  const long long T = (long long)hkv * cum[batch];
   const int N = gridDim.x, cta = blockIdx.x;
-  // (a replayed graph may find a sequence empty)
-  for (int i = cta; i < batch; i += N)
-    if (cum[i + 1] == cum[i])
-      for (int e = threadIdx.x; e < s.hq * (kHeadDim / 8); e += kBThreads)
-        reinterpret_cast<uint4*>(out + (size_t)i * s.hq * kHeadDim)[e] = make_uint4(0u, 0u, 0u, 0u);
   // this CTA's run of units [F, F1), or its parts F, F + N, .. of F1
-  const PageRun run = PARTS ? PageRun{cta, (long long)hkv * parts[batch]} : cta_pages(cta, T, N);
-  long long F = run.first;
-  const long long F1 = run.end;
+  long long T = 0, F = 0, F1 = 1;
+  int direct_nu = 0, direct_parts = 0;  // units of the pair and the parts they make
   const int* first = PARTS ? parts : cum;
+  if (kDirect) {
+    direct_nu = units_of(P);
+    direct_parts = max(1, min(a.parts, direct_nu / a.part_units));
+    if (direct_nu == 0 && part == 0 && threadIdx.x < G * (kHeadDim / 8))  // (a replayed graph may find a sequence empty)
+      reinterpret_cast<uint4*>(out + ((size_t)bl * s.hq + h * G) * kHeadDim)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    if (direct_nu == 0 || part >= direct_parts) return;
+  } else {
+    T = (long long)hkv * cum[batch];
+    for (int i = cta; i < batch; i += N)
+      if (cum[i + 1] == cum[i])
+        for (int e = threadIdx.x; e < s.hq * (kHeadDim / 8); e += kBThreads)
+          reinterpret_cast<uint4*>(out + (size_t)i * s.hq * kHeadDim)[e] = make_uint4(0u, 0u, 0u, 0u);
+    const PageRun run = PARTS ? PageRun{cta, (long long)hkv * parts[batch]} : cta_pages(cta, T, N);
+    F = run.first;
+    F1 = run.end;
+  }
   const uint32_t ring_s = smem_u32(smem) + warp * kBStages * kBStage;
   const uint8_t* ring = smem + warp * kBStages * kBStage;
   uint32_t cp_d[4];
@@ -175,33 +197,39 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
 
   while (F < F1) {
     // ---- the pair of unit (or part) F and the units of it that are this CTA's
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((long long)hkv * first[mid] <= F) lo = mid; else hi = mid - 1;
+    int nu = direct_nu, per_pair = direct_parts;
+    long long Pf = 0;
+    if (!kDirect) {
+      int lo = 0, hi = batch - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)hkv * first[mid] <= F) lo = mid; else hi = mid - 1;
+      }
+      bl = lo;
+      nu = cum[bl + 1] - cum[bl];
+      const long long pbase = (long long)hkv * first[bl];
+      per_pair = first[bl + 1] - first[bl];
+      h = (int)((F - pbase) / per_pair);
+      Pf = pbase + (long long)h * per_pair;
+      part = (int)(F - Pf);
+      P = len[bl];
     }
-    const int bl = lo, b = seq_begin + bl;
-    const int nu = cum[bl + 1] - cum[bl];
-    const long long pbase = (long long)hkv * first[bl];
-    const int per_pair = first[bl + 1] - first[bl];
-    const int h = (int)((F - pbase) / per_pair);
-    const long long Pf = pbase + (long long)h * per_pair;
+    const int b = seq_begin + bl;
     int u_a, u_e;  // units [u_a, u_e)
-    if (PARTS) {
-      const int part = (int)(F - Pf);
+    if (PARTS || kDirect) {
       u_a = (int)((long long)nu * part / per_pair);
       u_e = (int)((long long)nu * (part + 1) / per_pair);
     } else {
       u_a = (int)(F - Pf);
       u_e = (int)((F1 < Pf + nu ? F1 : Pf + nu) - Pf);
     }
-    const int P = len[bl];
     const int closed = block_closed(P, bt), npg = pre_npg + blocks_of(P) * ppb;
 
     // ---- this warp's units u_a + warp, + kBWarps, ...: n_my, the first n_pg of them pages
     const int n_my = u_e - u_a > warp ? (u_e - u_a - warp + kBWarps - 1) / kBWarps : 0;
     const int n_pg = min(u_e, npg) - u_a > warp ? (min(u_e, npg) - u_a - warp + kBWarps - 1) / kBWarps : 0;
     const int32_t* table = s.table + (size_t)b * s.max_bps;
+    if (FORM == kSelected) wait_for_previous();  // the list
     const int32_t* list = FORM == kSelected ? a.list + ((size_t)bl * hkv + h) * a.most : nullptr;
     // block ids and scales of this warp's pages, 32 at a time across the lanes
     auto tab_load = [&](int chunk) -> int {
@@ -499,39 +527,9 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       }
     };
 
-    int k = 0;
-    // two pages an iteration, the copies of the next two in flight
-#pragma unroll 1
-    for (; k + 1 < n_pg; k += 2) {
-      if (((stage_ok >> (k & (kBStages - 1))) & 3u) != 3u) break;  // a bad block id
-      issue(k + 2);
-      issue(k + 3);
-      cp_async_wait<2>();
-      __syncwarp();
-      pages(std::integral_constant<int, 2>{}, k);
-      __syncwarp();
-    }
-#pragma unroll 1
-    for (; k < n_pg; ++k) {
-      // pages k and k + 1 were issued; the rest one at a time
-      cp_async_wait<1>();
-      __syncwarp();
-      if ((stage_ok >> (k & (kBStages - 1))) & 1u) {
-        pages(std::integral_constant<int, 1>{}, k);
-      } else {  // a bad block id: flagged and left out
-        float ks, vs;
-        scales_at(k, ks, vs);
-        if (lane == 0) atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
-      }
-      __syncwarp();
-      issue(k + 2);
-    }
-    cp_async_wait<0>();
-
     // ---- exact rows: tiles of 16 (mma.sync bf16; the lane's dims are 32c ..
     // 32c + 31 of its rows, in the order of Q and K alike)
-#pragma unroll 1
-    for (; k < n_my; ++k) {
+    auto exact_tile = [&](int k) {
       // first exact row of the tile; (kPrefix) the prefix's tiles come before the sequence's
       const int tile = u_a + warp + kBWarps * k - npg;
       const bool shared = FORM == kPrefix && tile < pre_tiles;
@@ -627,6 +625,47 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         mma16816_bf16(oacc[j], a0, a1, a2, a3, h0, h1);
         mma16816_bf16(oacc[j], a0, a1, a2, a3, q0, q1);
       }
+    };
+
+    // the other forms' come before them, while the first pages are on their way
+    if (kDirect) {
+#pragma unroll 1
+      for (int k = n_pg; k < n_my; ++k) exact_tile(k);
+    }
+
+    int k = 0;
+    // two pages an iteration, the copies of the next two in flight
+#pragma unroll 1
+    for (; k + 1 < n_pg; k += 2) {
+      if (((stage_ok >> (k & (kBStages - 1))) & 3u) != 3u) break;  // a bad block id
+      issue(k + 2);
+      issue(k + 3);
+      cp_async_wait<2>();
+      __syncwarp();
+      pages(std::integral_constant<int, 2>{}, k);
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (; k < n_pg; ++k) {
+      // pages k and k + 1 were issued; the rest one at a time
+      cp_async_wait<1>();
+      __syncwarp();
+      if ((stage_ok >> (k & (kBStages - 1))) & 1u) {
+        pages(std::integral_constant<int, 1>{}, k);
+      } else {  // a bad block id: flagged and left out
+        float ks, vs;
+        scales_at(k, ks, vs);
+        if (lane == 0) atomicOr(&s.counters[kCtrStatus], kDevBadBlockId);
+      }
+      __syncwarp();
+      issue(k + 2);
+    }
+    cp_async_wait<0>();
+
+    // the plain form's exact rows come after its pages
+    if (!kDirect) {
+#pragma unroll 1
+      for (; k < n_my; ++k) exact_tile(k);
     }
 
     // ---- per-warp totals, CTA merge of the warps
@@ -638,8 +677,8 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     __syncthreads();  // every warp is done with its ring: reuse shared memory
     float* sm_m = reinterpret_cast<float*>(smem);
     float* sm_l = sm_m + kBWarps * kMaxGroup;
-    float* sm_o = sm_l + kBWarps * kMaxGroup;  // [kBWarps][8][128]
-    int* sm_e = reinterpret_cast<int*>(sm_o + kBWarps * kMaxGroup * kHeadDim);
+    float* sm_o = sm_l + kBWarps * kMaxGroup;  // [kBWarps][8][kMergeRow]
+    int* sm_e = reinterpret_cast<int*>(sm_o + kBWarps * kMaxGroup * kMergeRow);
     if (lane == 0) sm_e[warp] = E;
     if (r == 0) {
       sm_m[warp * kMaxGroup + 2 * c] = m0;
@@ -651,23 +690,24 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       const float sA = kOffset ? 0x1p24f : 1.0f;
       const float b0 = kOffset ? kOffV * osum[0] : 0.0f;
       const float b1 = kOffset ? kOffV * osum[1] : 0.0f;
-      float* o0 = sm_o + ((size_t)warp * kMaxGroup + 2 * c) * kHeadDim + 16 * r;
-      float* o1 = o0 + kHeadDim;
+      // dim 16 r + i of a head at 8 i + r, rows of 132: each bank once a store
+      float* o0 = sm_o + ((size_t)warp * kMaxGroup + 2 * c) * kMergeRow + r;
+      float* o1 = o0 + kMergeRow;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o0[2 * j] = oacc[j][0] * sA - b0;
-        o0[2 * j + 1] = oacc[j][2] * sA - b0;
-        o1[2 * j] = oacc[j][1] * sA - b1;
-        o1[2 * j + 1] = oacc[j][3] * sA - b1;
+        o0[16 * j] = oacc[j][0] * sA - b0;
+        o0[16 * j + 8] = oacc[j][2] * sA - b0;
+        o1[16 * j] = oacc[j][1] * sA - b1;
+        o1[16 * j + 8] = oacc[j][3] * sA - b1;
       }
     }
     __syncthreads();
     // the pair's partials, the slot of this one and of the first (here, not above:
     // alive across the loops they cost 1 us of 90 for 16 x 32 heads of 4,111 tokens)
-    const int i_first = PARTS ? 0 : cta_of_page(Pf, T, N);
-    const int cnt = PARTS ? per_pair : cta_of_page(Pf + nu - 1, T, N) - i_first + 1;
-    const long long slot0 = PARTS ? Pf : (long long)bl * hkv + h + i_first;
-    const long long slot = PARTS ? F : (long long)bl * hkv + h + cta;
+    const int i_first = PARTS || kDirect ? 0 : cta_of_page(Pf, T, N);
+    const int cnt = PARTS || kDirect ? per_pair : cta_of_page(Pf + nu - 1, T, N) - i_first + 1;
+    const long long slot0 = kDirect ? ((long long)bl * hkv + h) * a.parts : PARTS ? Pf : (long long)bl * hkv + h + i_first;
+    const long long slot = kDirect ? slot0 + part : PARTS ? F : (long long)bl * hkv + h + cta;
     const int d = threadIdx.x;  // 128 threads = head_dim
     uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
     // (kPrefix) partials of the prefix's blocks, joined after the pair's own
@@ -683,7 +723,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
 #pragma unroll
       for (int ww = 0; ww < kBWarps; ++ww) {
         const float wt = fast_exp2(sm_m[ww * kMaxGroup + g] - M);
-        o += wt * pow2i(max(sm_e[ww] - e_most, -126)) * sm_o[((size_t)ww * kMaxGroup + g) * kHeadDim + d];
+        o += wt * pow2i(max(sm_e[ww] - e_most, -126)) * sm_o[((size_t)ww * kMaxGroup + g) * kMergeRow + 8 * (d & 15) + (d >> 4)];
         l += wt * sm_l[ww * kMaxGroup + g];
       }
       o = l != 0.0f ? o * (1.0f / l) * pow2i(e_most) : 0.0f;
@@ -701,13 +741,16 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     if (cnt + more > 1) {
       // the pair's last CTA joins the partials, in CTA order
       __syncthreads();
-      if (threadIdx.x == 0) {
-        __threadfence();
-        sh_last = atomicAdd(&s.tickets[b * hkv + h], 1) == cnt - 1;
-        __threadfence();
+      if (!kDirect || cnt > 1) {
+        if (threadIdx.x == 0) {
+          __threadfence();
+          sh_last = atomicAdd(&s.tickets[b * hkv + h], 1) == cnt - 1;
+          __threadfence();
+        }
+        __syncthreads();
       }
-      __syncthreads();
-      if (sh_last) {
+      if ((kDirect && cnt == 1) || sh_last) {
+        if (FORM == kPrefix && more > 0) wait_for_previous();  // the prefix's partials
         // a warp per head (several when there are fewer heads than warps, each
         // with every wph-th part): 32 parts' maxima and sums across the lanes,
         // then their rows, eight of 16 bytes a lane in flight
@@ -746,13 +789,14 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
             al *= inv;
             wt *= inv;
             o.x *= al; o.y *= al; o.z *= al; o.w *= al;
-            for (int i0 = 0; i0 < min(32, mine - j0); i0 += 8) {
-              float4 y[8];
+            constexpr int kAtOnce = FORM == kPrefix ? 16 : 8;
+            for (int i0 = 0; i0 < min(32, mine - j0); i0 += kAtOnce) {
+              float4 y[kAtOnce];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)  // past the end: the last part again, weight 0
+              for (int i = 0; i < kAtOnce; ++i)  // past the end: the last part again, weight 0
                 y[i] = part_o(share + wph * min(j0 + i0 + i, mine - 1));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < kAtOnce; ++i) {
                 const float w = __shfl_sync(0xffffffffu, wt, i0 + i);
                 if (j0 + i0 + i < mine) {
                   o.x += w * y[i].x; o.y += w * y[i].y; o.z += w * y[i].z; o.w += w * y[i].w;
@@ -788,11 +832,11 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
             orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
           }
         }
-        if (threadIdx.x == 0) s.tickets[b * hkv + h] = 0;
+        if (threadIdx.x == 0 && (!kDirect || cnt > 1)) s.tickets[b * hkv + h] = 0;
       }
     }
     __syncthreads();  // shared memory is reused by the next pair
-    F = PARTS ? F + N : Pf + u_e;
+    F = kDirect ? F1 : PARTS ? F + N : Pf + u_e;
   }
 }
 
@@ -823,13 +867,30 @@ int block_mod(const ScoreMod& m) { return (m.c2 > 0.0f ? kBCap : 0) | (m.slopes 
 template <int FORM, bool FP8, int MOD>
 cudaError_t launch_block_attn_t(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                 const BlockAttn& w, cudaStream_t st) {
-  const cudaError_t e = w.parts ? block_attn_smem<FORM, FP8, MOD, true>() : block_attn_smem<FORM, FP8, MOD, false>();
-  if (e != cudaSuccess) return e;
-  if (w.parts)
-    block_attn_kernel<FORM, FP8, MOD, true><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
-  else
-    block_attn_kernel<FORM, FP8, MOD, false><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
-  return cudaGetLastError();
+  if constexpr (FORM != kPlain) {
+    const cudaError_t e = block_attn_smem<FORM, FP8, MOD, kDirectParts>();
+    if (e != cudaSuccess) return e;
+    // may start under the kernel before it (wait_for_previous)
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(w.ncta);
+    cfg.blockDim = dim3(kBThreads);
+    cfg.dynamicSmemBytes = kBSmem;
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = w.early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, block_attn_kernel<FORM, FP8, MOD, kDirectParts>, s, seq_begin, batch, q, out, w);
+  } else {
+    const cudaError_t e = w.parts ? block_attn_smem<FORM, FP8, MOD, true>() : block_attn_smem<FORM, FP8, MOD, false>();
+    if (e != cudaSuccess) return e;
+    if (w.parts)
+      block_attn_kernel<FORM, FP8, MOD, true><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
+    else
+      block_attn_kernel<FORM, FP8, MOD, false><<<w.ncta, kBThreads, kBSmem, st>>>(s, seq_begin, batch, q, out, w);
+    return cudaGetLastError();
+  }
 }
 
 template <int FORM, bool FP8>

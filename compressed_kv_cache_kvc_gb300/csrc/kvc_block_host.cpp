@@ -23,6 +23,7 @@ constexpr int kMinUnitsPerCta = 16;  // 16-token units: a CTA's share of a pair
 // against 42.7; of equal lengths the runs end with the pairs by themselves and
 // need no spare CTAs: 3 x 8 of 8,000 15.8 against 16.4).
 constexpr int kPartsPerPair = 2;
+constexpr int kCtasPerSm = 2;
 constexpr int kWholePairUnits = 64;  // pairs up to this long are not cut to even out a wave
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -180,6 +181,15 @@ void split_attention(kvc_block_cache* c, kvc::BlockAttn* a, int per_sm, int batc
     a->parts = a->ncta / hkv;
     a->ncta = std::min((a->parts + batch) * hkv, kvc::kMaxSplitCtas);
   }
+}
+
+// The parts of pairs of the selected and the prefix form: up to `parts` CTAs for every
+// pair, of at least part_units units each.
+void split_pairs(kvc_block_cache* c, kvc::BlockAttn* a, int batch, long long units) {
+  const long long pairs = (long long)batch * c->cfg.num_kv_heads, slots = kCtasPerSm * sm_count(c);
+  a->part_units = (int)std::max<long long>(kMinUnitsPerCta, (units + slots - 1) / slots);
+  a->parts = (int)std::max<long long>(1, std::min<long long>(kvc::kMaxSplitCtas / pairs, 2 * slots / pairs));
+  a->ncta = (int)(pairs * a->parts);
 }
 
 bool choice_ok(int top, int recent) { return top > 0 && recent >= 0 && (long long)top + recent <= 1 << 20; }
@@ -471,16 +481,13 @@ kvc_status kvc_block_selected_attention(kvc_block_cache* c, int32_t seq_begin, i
   if (!c->bounds.codes) return KVC_ERR_STATE;
   const int bt = c->cfg.block_tokens, most = top_blocks + recent_blocks;
   long long units = 0;
-  int longest = 0, first = 0;
-  bool ragged = false;
+  int longest = 0;
   for (int i = 0; i < batch; ++i) {
     const int P = c->pos[seq_begin + i];
     if (P <= 0) return KVC_ERR_INVALID_ARG;  // nothing to attend to
     const int u = std::min(kvc::block_closed(P, bt), most) * (bt / kvc::kPage) +
                   (kvc::block_exact_rows(P, bt) + kvc::kPage - 1) / kvc::kPage;
     units += (long long)u * c->cfg.num_kv_heads;
-    if (i == 0) first = u;
-    ragged |= u != first;
     longest = std::max(longest, P);
   }
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
@@ -492,7 +499,8 @@ kvc_status kvc_block_selected_attention(kvc_block_cache* c, int32_t seq_begin, i
   kvc::BlockAttn a = attention_of(sl.ws, d_workspace, sm_scale, softcap, d_slopes);
   a.list = ch.list;
   a.most = most;
-  split_attention(c, &a, kvc::block_selected_ctas_per_sm(c->dev, a.mod), batch, units, ragged);
+  split_pairs(c, &a, batch, units);
+  a.early = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const uint16_t* q = static_cast<const uint16_t*>(d_q);
   if (kvc::launch_block_choice(c->dev, c->bounds, ch, seq_begin, batch, longest, q, st) != cudaSuccess ||
@@ -523,17 +531,16 @@ kvc_status kvc_block_prefix_attention(kvc_block_cache* c, int32_t prefix, int32_
   const long long front = (kvc::block_exact_rows(shared, bt) + kvc::kPage - 1) / kvc::kPage +
                           (product ? 0LL : (long long)kvc::block_closed(shared, bt) * (bt / kvc::kPage));
   long long units = 0;
-  bool ragged = false;
   for (int i = 0; i < batch; ++i) {
     const int P = c->pos[seq_begin + i];
     if (P + (long long)shared <= 0 || P + (long long)shared > 2000000000LL) return KVC_ERR_INVALID_ARG;
     units += (kvc::block_units(P, bt) + front) * hkv;
-    ragged |= P != c->pos[seq_begin];
   }
   kvc::BlockAttn a = attention_of(pl.ws, d_workspace, sm_scale, softcap, d_slopes);
   a.prefix = prefix;
   a.prefix_pages = product ? 0 : 1;
-  split_attention(c, &a, kvc::block_prefix_ctas_per_sm(c->dev, a.mod), batch, units, ragged);
+  split_pairs(c, &a, batch, units);
+  a.early = product ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const uint16_t* q = static_cast<const uint16_t*>(d_q);
   if (product) {

@@ -39,7 +39,9 @@ using namespace tc;
 
 constexpr int kTile = 128;  // query rows and tokens per tile
 constexpr int kRows = 2 * kTile;
-constexpr int kThreads = 544;
+constexpr int kSoftWarps = 16, kLoadWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kScoutWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kScoutWarp + 1);
 constexpr int kTileB = kTile * kHeadDim * 2;  // 32 KB, two boxes of 64 dims
 constexpr int kBoxB = kTileB / 2;
 constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kTileB, kOffV = kOffK + 2 * kTileB;
@@ -49,10 +51,13 @@ constexpr int kOffScale = kOffV + 2 * kTileB;  // [4][2][8] f32
 constexpr int kOffMask = kOffScale + 4 * 2 * 8 * 4;
 constexpr int kOffBar = kOffMask + 4 * 4;
 constexpr int kBarQ = 0, kBarK = 1, kBarV = 3, kBarKFree = 5, kBarVFree = 7, kBarS = 9, kBarP = 11, kBarO = 13,
-              kBarScale = 15, kBarDone = 19, kNumBars = 20;
+              kBarScale = 15, kBarRead = 19, kBarDone = 27, kNumBars = 28;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort flag, largest V scale
-constexpr int kSmem = kOffMisc + 16;
+constexpr int kOffMax = kOffMisc + 16;            // [2][2 halves][256] what a row's two threads exchange
+constexpr int kSmem = kOffMax + 4 * kRows * 4;
+constexpr int kNbPair = 1;  // named barriers 1 .. 8 of the two warps that share 32 rows
 constexpr float kLazyMax = 8.0f;
+constexpr int kAhead = 4;  // tiles whose codes are on their way to L2
 constexpr uint32_t kCols = 512;
 
 __device__ __forceinline__ float group_max(const float* z, float m) {
@@ -122,14 +127,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* table = s.table + (size_t)a.prefix * s.max_bps;
   launch_dependents();
 
-  // this thread's row (softmax warps)
-  const int x = warp >> 2, row = tid & (kTile - 1);
+  // this thread's row (softmax warps), and which half of a tile's tokens it has
+  const int x = warp >> 3, half = (warp >> 2) & 1, row = tid & (kTile - 1);
   const int rr = rb * kRows + x * kTile + row;  // among the rows of the KV head
-  const bool on = warp < 8 && x * kTile + row < rows;
+  const bool on = warp < kSoftWarps && x * kTile + row < rows;
   const int bl = on ? rr / G : 0, g = on ? rr % G : 0;
   const size_t part = (((size_t)split * hkv + h) * a.batch + bl) * G + g;
   if (n_t == 0) {  // (a graph replayed with a shorter prefix: nothing to add)
-    if (on) {
+    if (on && half == 0) {
       for (int e = 0; e < kHeadDim / 4; ++e)
         reinterpret_cast<float4*>(a.more_o + part * kHeadDim)[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       *reinterpret_cast<float2*>(a.more_ml + part * 2) = make_float2(kNegBig, 0.0f);
@@ -137,16 +142,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kBarQ) count = 4 * nq;
-      if (i >= kBarK && i < kBarKFree) count = 8;
-      if (i >= kBarP && i < kBarO) count = 4;
+      if (i == kBarQ) count = 8 * nq;
+      if (i >= kBarK && i < kBarKFree) count = kLoadWarps;
+      if (i >= kBarP && i < kBarO) count = 8;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(count));
     }
     *abort = 0;
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     // -------------------------------------------------------------- products
     const bool el = elect_one();
     const uint32_t id_s = instr_desc(kTile, kTile, false), id_o = instr_desc(kTile, kHeadDim, false) | kInstrTransB;
@@ -228,10 +233,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (el) mma_commit(bar(kBarDone));
     bar_wait(bar(kBarDone), 0, nullptr);
     __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp == kScoutWarp) {
+    // ------------------------- scales, and the codes of the tiles ahead into L2
+    // lanes 0 .. 7 have the K, 8 .. 15 the V of a 16-token page
+    const int page = lane & 7;
+    const bool v = lane & 8;
+    const uint8_t* codes = (v ? s.v_codes : s.k_codes) + (size_t)h * bt * kHeadDim;
+    const float* scales = v ? s.v_scale : s.k_scale;
+    auto id_of = [&](int i) {
+      const int tok = (t1 - 1 - i) * kTile + 16 * page;
+      if (lane >= 16 || i >= n_t || tok >= n_tok) return -1;
+      const int id = table[tok >> sh];
+      return (unsigned)id < (unsigned)s.num_blocks ? id : -2;
+    };
+    auto scale_of = [&](int id) { return id >= 0 ? scales[(size_t)id * hkv + h] : 0.0f; };
+    auto fetch = [&](int i, int id) {
+      if (id < 0) return;
+      const int tok = (t1 - 1 - i) * kTile + 16 * page;
+      const uint8_t* at = codes + (size_t)id * hkv * bt * kHeadDim + (size_t)(tok & (bt - 1)) * kHeadDim;
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(16 * kHeadDim) : "memory");
+    };
+    int ids[kAhead + 1];  // of tiles i .. i + kAhead
+#pragma unroll
+    for (int e = 0; e <= kAhead; ++e) ids[e] = id_of(e);
+    float sc = scale_of(ids[0]);
+#pragma unroll
+    for (int e = 1; e < kAhead; ++e) fetch(e, ids[e]);
+#pragma unroll 1
+    for (int i = 0; i < n_t; ++i) {
+      const int id = ids[0], next = id_of(i + kAhead + 1);
+      fetch(i + kAhead, ids[kAhead]);
+      const float sc_next = scale_of(ids[1]);
+      if (i >= 2) wait(kBarKFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
+      if (!ok) break;
+      float* to = reinterpret_cast<float*>(sm + kOffScale) + (i & 3) * 16;
+      if (lane < 8) to[lane] = sc;
+      if (lane >= 8 && lane < 16) to[lane] = vmax > 0.0f ? __fdiv_rn(sc, vmax) * 128.0f : 0.0f;
+      if (id == -2 && lane < 8) atomicOr(status, kDevBadBlockId);
+      const uint32_t pages = __ballot_sync(0xffffffffu, id >= 0) & 0xFFu;
+      if (lane == 0) reinterpret_cast<uint32_t*>(sm + kOffMask)[i & 3] = pages;
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(kBarScale + (i & 3)));
+      sc = sc_next;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) ids[e] = ids[e + 1];
+      ids[kAhead] = next;
+    }
+  } else if (warp >= kSoftWarps) {
     // ----------------------------------------------------- codes -> fp16 tiles
     // a thread has 16 codes (column ch) of rows r0, r0 + 32, .. of K and of V
-    const int pt = tid - 256, r0 = pt >> 3, ch = pt & 7;
+    const int pt = tid - 32 * kSoftWarps, r0 = pt >> 3, ch = pt & 7;
     const size_t head = (size_t)h * bt * kHeadDim + 16 * ch;
     const size_t stride = (size_t)hkv * bt * kHeadDim;
     auto load_ids = [&](int i, int (&id)[4]) {
@@ -281,41 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async();
       __syncwarp();
     };
-    // (lanes 0 .. 7 of warp 8) the scales of a 16-token page
-    const bool scaler = warp == 8 && lane < 8;
-    float ks = 0.0f, vs = 0.0f;
-    bool valid = false;
-    auto load_scales = [&](int i) {
-      if (!scaler || i >= n_t) return;
-      const int tok = (t1 - 1 - i) * kTile + 16 * lane;
-      const int id = tok < n_tok ? table[tok >> sh] : -1;
-      valid = (unsigned)id < (unsigned)s.num_blocks;
-      if (!valid && tok < n_tok) atomicOr(status, kDevBadBlockId);
-      ks = valid ? s.k_scale[(size_t)id * hkv + h] : 0.0f;
-      vs = valid ? s.v_scale[(size_t)id * hkv + h] : 0.0f;
-    };
     int id[4], id_next[4];
     uint4 wk[4], wv[4];
     load_ids(0, id);
-    load_scales(0);
     load_codes(s.k_codes, 0, id, wk);
     load_codes(s.v_codes, 0, id, wv);
     load_ids(1, id_next);
     for (int i = 0; i < n_t; ++i) {
       if (i >= 2) wait(kBarKFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
       if (!ok) break;
-      if (warp == 8) {
-        float* to = reinterpret_cast<float*>(sm + kOffScale) + (i & 3) * 16;
-        if (lane < 8) {
-          to[lane] = ks;
-          to[8 + lane] = vmax > 0.0f ? __fdiv_rn(vs, vmax) * 128.0f : 0.0f;
-        }
-        const uint32_t pages = __ballot_sync(0xffffffffu, scaler && valid);
-        if (lane == 0) reinterpret_cast<uint32_t*>(sm + kOffMask)[i & 3] = pages;
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(kBarScale + (i & 3)));
-        load_scales(i + 1);
-      }
       store(sm + kOffK + (i & 1) * kTileB, wk);
       if (lane == 0) bar_arrive(bar(kBarK + (i & 1)));
       load_codes(s.k_codes, i + 1, id_next, wk);
@@ -328,60 +353,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (x < nq) {
     // ----------------------------------------------------------- query rows
+    // the value of the row's other thread (two places in turn, so that one barrier
+    // of the two warps is enough)
+    float* sh_x = reinterpret_cast<float*>(sm + kOffMax) + x * kTile + row;
+    const int pair = 4 * x + (warp & 3);
+    int turn = 0;
+    auto exchange = [&](float v) {
+      sh_x[turn * 2 * kRows + half * kRows] = v;
+      asm volatile("bar.sync %0, 64;" ::"r"(kNbPair + pair) : "memory");
+      const float o = sh_x[turn * 2 * kRows + (half ^ 1) * kRows];
+      turn ^= 1;
+      return o;
+    };
     float cq;
     int dist = 0;  // (BIAS) from the query to position 4 of the prefix
     {
       const uint16_t* src = q + ((size_t)bl * s.hq + h * G + g) * kHeadDim;
       if (BIAS && on) dist = pre_len + s.seq_pos[seq_begin + bl] - 1 - kSinks;
       float amax = 0.0f;
-#pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (on) w = reinterpret_cast<const uint4*>(src)[c];
-        const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+      uint4 mine[8];  // (the thread's half of the row)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        mine[c] = on ? reinterpret_cast<const uint4*>(src)[8 * half + c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t y[4] = {mine[c].x, mine[c].y, mine[c].z, mine[c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) amax = max3_abs(amax, bf16f(y[e] & 0xFFFFu), bf16f(y[e] >> 16));
       }
+      amax = fmaxf(amax, exchange(amax));
       int e2 = 0;
       if (amax > 0.0f) e2 = min(max(14 - exponent_of(amax), -100), 100);
       const float up = pow2i(e2);
       cq = (CAP ? a.mod.y_scale : a.qk_scale_log2) * pow2i(-e2);
-      uint8_t* dst = sm + kOffQ + x * kTileB + row * 128;
-#pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (on) w = reinterpret_cast<const uint4*>(src)[c];
-        const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+      uint8_t* dst = sm + kOffQ + x * kTileB + half * kBoxB + row * 128;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t y[4] = {mine[c].x, mine[c].y, mine[c].z, mine[c].w};
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = pack_half2(bf16f(y[e] & 0xFFFFu) * up, bf16f(y[e] >> 16) * up);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kBoxB + (((c & 7) ^ (row & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       fence_async();
       __syncwarp();
       if (lane == 0) bar_arrive(bar(kBarQ));
     }
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = trow + kTile * x, t_o = trow + 256 + kTile * x;
+    const uint32_t t_s = trow + kTile * x, t_o = trow + 256 + kTile * x + 64 * half;
     const float slope2 = BIAS && on ? slope_log2(a.mod, h * G + g) : 0.0f;
     float m = kNegBig, l = 0.0f;
 #pragma unroll 1
     for (int i = 0; i < n_t; ++i) {
       wait(kBarScale + (i & 3), (uint32_t)((i >> 2) & 1));
       if (ok) wait(kBarS + x, (uint32_t)(i & 1));
-      if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const float* sk = reinterpret_cast<const float*>(sm + kOffScale) + (i & 3) * 16;
-      const uint32_t pages = reinterpret_cast<const uint32_t*>(sm + kOffMask)[i & 3];
-      const int d0 = dist - (t1 - 1 - i) * kTile;  // distance to the tile's first token
+      const float* sk = reinterpret_cast<const float*>(sm + kOffScale) + (i & 3) * 16 + 4 * half;
+      const uint32_t pages = reinterpret_cast<const uint32_t*>(sm + kOffMask)[i & 3] >> (4 * half) & 15u;
+      const int d0 = dist - (t1 - 1 - i) * kTile - 64 * half;  // distance to the half's first token
       float z[32];
       // the maximum: over the products (scales and a cap keep their order), with a
       // bias over the scores, which then take the products' place
       float mx = -INFINITY, most = 0.0f;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        ld32(t_s + 32 * c, z);
+      for (int c = 0; c < 2; ++c) {
+        ld32(t_s + 64 * half + 32 * c, z);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float* zz = z + 16 * e;
@@ -400,8 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = group_max(zz, mx);
           }
         }
-        if (BIAS) tmem_st32(t_s + 32 * c, z);
+        if (BIAS) tmem_st32(t_s + 64 * half + 32 * c, z);
       }
+      // (no maximum is a NaN: it says that a wait ran out, and both warps leave here)
+      const float mine = ok ? mx : __int_as_float(0x7FFFFFFF), other = exchange(mine);
+      ok = __all_sync(0xffffffffu, mine == mine && other == other);
+      if (!ok) break;
+      mx = fmaxf(mx, other);
       if (CAP && !BIAS && mx > -INFINITY) mx = cap_score(a.mod, mx);
       const bool grow = mx > m + kLazyMax;
       if (__any_sync(0xffffffffu, grow)) {
@@ -411,10 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= alpha;
         if (i > 0) {
           wait(kBarO + x, (uint32_t)((i - 1) & 1));  // the product before
-          if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-          for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
+          for (int c0 = 0; c0 < 64; c0 += 16) {
             float t[16];
             ld16(t_o + c0, t);
 #pragma unroll
@@ -423,18 +463,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // P (fp16) over the front of the products
+      // P (fp16) over the front of the products: the second half's goes where the
+      // first half's products 32 .. 63 were, once these are read
       f32x2 ls[2] = {0, 0};
       if (BIAS) tmem_st_wait();
       const f32x2 nm = pack2(-m, -m);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         uint32_t pw[16];
-        ld32(t_s + 32 * c, z);
+        ld32(t_s + 64 * half + 32 * c, z);
+        if (half == 0 && c == 1) {
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar(kBarRead + pair));
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float* zz = z + 16 * e;
-          const bool counts = (pages >> (2 * c + e)) & 1u;
           const float f = BIAS ? 1.0f : sk[2 * c + e] * cq, v = sk[8 + 2 * c + e];
           const f32x2 f2 = pack2(f, f), v2 = pack2(v, v);
           if (CAP && !BIAS) {
@@ -443,17 +488,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; j += 2) unpack2(fma2(pack2(zz[j], zz[j + 1]), f2, nm), zz[j], zz[j + 1]);
           }
+          if (!BIAS && !((pages >> (2 * c + e)) & 1u)) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) zz[j] = -INFINITY;
+          }
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            f32x2 p = pack2(fast_exp2(zz[j]), fast_exp2(zz[j + 1]));
-            if (!BIAS && !counts) p = 0;
+            const f32x2 p = pack2(fast_exp2(zz[j]), fast_exp2(zz[j + 1]));
             ls[(j >> 1) & 1] = add2(ls[(j >> 1) & 1], p);
             float lo, hi;
             unpack2(mul2(p, v2), lo, hi);
             pw[8 * e + (j >> 1)] = pack_half2(lo, hi);
           }
         }
-        tmem_st16(t_s + 16 * c, pw);
+        if (half == 1 && c == 0) {
+          wait(kBarRead + pair, (uint32_t)(i & 1));
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
+        tmem_st16(t_s + 32 * half + 16 * c, pw);
       }
       float lx, ly;
       unpack2(add2(ls[0], ls[1]), lx, ly);
@@ -464,28 +516,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) bar_arrive(bar(kBarP + x));
     }
     if (ok) wait(kBarO + x, (uint32_t)((n_t - 1) & 1));
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const float l_other = exchange(l);
+    l = half == 0 ? l + l_other : l_other + l;
     if (ok) {
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const float inv = l != 0.0f ? 1.0f / l : 0.0f, unit = vmax * 0x1p-7f;
-      float* to = a.more_o + part * kHeadDim;
+      float* to = a.more_o + part * kHeadDim + 64 * half;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
-        float z_out[32];
-        ld32(t_o + c0, z_out);
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        float o[32];
+        ld32(t_o + c0, o);
         if (on) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(to + c0 + e) =
-                make_float4(z_out[e] * inv * unit, z_out[e + 1] * inv * unit, z_out[e + 2] * inv * unit,
-                            z_out[e + 3] * inv * unit);
+                make_float4(o[e] * inv * unit, o[e + 1] * inv * unit, o[e + 2] * inv * unit, o[e + 3] * inv * unit);
         }
       }
-      if (on) *reinterpret_cast<float2*>(a.more_ml + part * 2) = make_float2(m, l);
+      if (on && half == 0) *reinterpret_cast<float2*>(a.more_ml + part * 2) = make_float2(m, l);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
 }
 
 template <bool FP8, bool CAP, bool BIAS>
@@ -509,8 +562,6 @@ cudaError_t launch_tc_mod(const BlockState& s, int seq_begin, const uint16_t* q,
 }
 
 }  // namespace
-
-int block_prefix_ctas_per_sm(const BlockState& s, const ScoreMod& mod) { return attn_ctas<kPrefix>(s, mod); }
 
 cudaError_t launch_prefix_tc(const BlockState& s, int seq_begin, const uint16_t* q, const PrefixTc& a,
                              cudaStream_t st) {

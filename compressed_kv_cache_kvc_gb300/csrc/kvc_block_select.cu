@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(BlockState s
   const int pair = blockIdx.x / chunks, bl = pair / hkv, h = pair % hkv, b = seq_begin + bl;
   const int closed = block_closed(s.seq_pos[b], s.bt);
   const int n = closed - ch.recent;
+  launch_dependents();
   if (closed <= ch.top + ch.recent) return;  // all are chosen
   if (warp < G) {
     const uint2 w = reinterpret_cast<const uint2*>(q + ((size_t)bl * s.hq + h * G + warp) * kHeadDim)[lane];
@@ -104,6 +105,8 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
   const int pair = blockIdx.x, b = seq_begin + pair / s.hkv, most = ch.top + ch.recent;
   const int closed = block_closed(s.seq_pos[b], s.bt);
   int32_t* list = ch.list + (size_t)pair * most;
+  launch_dependents();
+  wait_for_previous();  // the keys (and, for a list that stays, the call before)
   if (closed <= most) {
     for (int i = threadIdx.x; i < most; i += kChooseThreads) list[i] = i < closed ? i : -1;
     return;
@@ -155,8 +158,6 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
 
 }  // namespace
 
-int block_selected_ctas_per_sm(const BlockState& s, const ScoreMod& mod) { return attn_ctas<kSelected>(s, mod); }
-
 cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, const BlockChoice& ch, int seq_begin,
                                 int batch, int longest, const uint16_t* q, cudaStream_t st) {
   const int pairs = batch * s.hkv, n = block_closed(longest, s.bt) - ch.recent;
@@ -166,8 +167,17 @@ cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, co
   block_score_kernel<<<pairs * chunks, kScoreThreads, 0, st>>>(s, bounds, ch, seq_begin, chunks, q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  block_choose_kernel<<<pairs, kChooseThreads, 0, st>>>(s, ch, seq_begin);
-  return cudaGetLastError();
+  // may start under the scores (wait_for_previous)
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(pairs);
+  cfg.blockDim = dim3(kChooseThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_choose_kernel, s, ch, seq_begin);
 }
 
 cudaError_t launch_block_selected(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
