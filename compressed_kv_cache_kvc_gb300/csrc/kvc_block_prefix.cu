@@ -9,25 +9,32 @@
 // block_attn_kernel, which has the sequences' own tokens and everything held
 // exactly, joins its partial results.
 //
-// prefix_tc_kernel.  One 544-thread CTA per (up to 256 rows, KV head, run of
-// 128-token tiles):
-//   * warps 0-3 and 4-7: the softmax of one 128-row query tile each, a thread a row;
-//   * warps 8-15: codes from global memory (the next tile's on their way in
+// prefix_tc_kernel.  One 640-thread CTA per (up to 256 rows, KV head, run of
+// 128-token tiles), in two streams: the two 128-row query tiles, or (up to 128 rows)
+// every other tile of tokens for the same rows, joined in the end.
+//   * warps 4-7 and 8-11: the softmax of one stream each, a thread a row;
+//   * warps 12-19: codes from global memory (the next tile's on their way in
 //     registers) to fp16 in shared memory, K and V alike [128 tokens][128 dims] in
 //     two boxes of 64 dims with the 128-byte swizzle; every code is exact in fp16;
-//   * warp 16 issues the products: S = Q K^T (Q fp16 times a power of two per
+//   * warp 1: the scales, and the codes of the tiles ahead into L2;
+//   * warps 0 and 2 issue the products of a query tile each (one warp for both spent
+//     half of its time between them): S = Q K^T (Q fp16 times a power of two per
 //     row, which is exact for everything within 2^-28 of the row's largest value),
 //     O += P V with P from tensor memory.
-// TMEM columns: S_x at 128 x, O_x at 256 + 128 x; P (fp16) takes the front half of
-// its S.  Per tile PV_0(i - 1), S_0(i), PV_1(i - 1), S_1(i): the pipe runs them in
-// order, so S(i) may overwrite P(i - 1), and each query tile's softmax runs under the
-// other's products.
+// A step is 64 tokens.  TMEM columns: S_x of step j at 128 x + 64 (j % 2), O_x at
+// 256 + 128 x; P (fp16) takes the back half of its S.  In step j the MMA warp of query
+// tile x issues PV_x(j - 2), S_x(j): the pipe runs one thread's products in order, so
+// S(j) may overwrite P(j - 2), and a softmax finds the scores of its next step ready.
 // A block's K scale multiplies its scores, its V scale over the largest of the
-// run (times 2^7) its probabilities, which so keep 11 bits down to 2^-21 of what
-// the largest value would contribute at p = 1; O leaves times that scale.  The
-// running maximum is lazy (O is rescaled when it grows by more than 8 in log2
-// units: p <= 2^8, so P stays below 2^15), the sums add the unrounded p in fp32.
-// Tiles go from the last to the first: with a distance bias the nearest come first.
+// run (as a power of two, so that the quotient lies in [1/2, 1)) its probabilities: P
+// keeps 11 bits down to 2^-14 of what the largest value would contribute at p = 1 and
+// is off by 2^-25 of it below; O leaves times that power.  The running maximum is
+// lazy: p is formed with the one so far, and only where 32 of them sum to more than
+// 2^15 is the maximum looked for and O rescaled, so that P fits fp16 and most steps read their scores once and compare nothing
+// (with the maximum of every step first 43 us where this takes 37, 64 x 32 heads
+// after 32,768 tokens).  The sums add the unrounded p in fp32.
+// Tiles, and the steps and chunks inside, go from the last to the first: with a
+// distance bias the nearest come first, and the maximum hardly ever rises again.
 // Synchronisation: mbarriers, every wait bounded, as in the prompt kernels.
 #include "kvc_block_attn.h"
 #include "kvc_tc.h"
@@ -38,10 +45,12 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;  // query rows and tokens per tile
+constexpr int kStep = 64;   // tokens per step of the softmax
 constexpr int kRows = 2 * kTile;
-constexpr int kSoftWarps = 16, kLoadWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kScoutWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kScoutWarp + 1);
+constexpr int kSoftWarps = 8, kLoadWarps = 8;
+// (the first warps are the ones the schedulers prefer: what the others wait for goes first)
+constexpr int kMmaWarp = 0, kScoutWarp = 1, kMmaWarp2 = 2, kSoft0 = 4, kLoad0 = kSoft0 + kSoftWarps;
+constexpr int kThreads = 32 * (kLoad0 + kLoadWarps);
 constexpr int kTileB = kTile * kHeadDim * 2;  // 32 KB, two boxes of 64 dims
 constexpr int kBoxB = kTileB / 2;
 constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kTileB, kOffV = kOffK + 2 * kTileB;
@@ -50,13 +59,12 @@ constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kTileB, kOffV = kOffK + 2 * kTileB;
 constexpr int kOffScale = kOffV + 2 * kTileB;  // [4][2][8] f32
 constexpr int kOffMask = kOffScale + 4 * 2 * 8 * 4;
 constexpr int kOffBar = kOffMask + 4 * 4;
-constexpr int kBarQ = 0, kBarK = 1, kBarV = 3, kBarKFree = 5, kBarVFree = 7, kBarS = 9, kBarP = 11, kBarO = 13,
-              kBarScale = 15, kBarRead = 19, kBarDone = 27, kNumBars = 28;
-constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort flag, largest V scale
-constexpr int kOffMax = kOffMisc + 16;            // [2][2 halves][256] what a row's two threads exchange
-constexpr int kSmem = kOffMax + 4 * kRows * 4;
-constexpr int kNbPair = 1;  // named barriers 1 .. 8 of the two warps that share 32 rows
-constexpr float kLazyMax = 8.0f;
+constexpr int kBarQ = 0, kBarK = 1, kBarV = 3, kBarKFree = 5, kBarVFree = 7, kBarS = 9, kBarP = 13, kBarO = 17,
+              kBarScale = 21, kBarDone = 25, kNumBars = 27;  // (S, P, O: 2 x + step parity)
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort flag, the power of two of the V scales
+constexpr int kOffMl = kOffMisc + 32;  // [2][128][2] the rows' maxima and sums
+constexpr int kSmem = kOffMl + 2 * kTile * 8;
+constexpr float kMostSum = 32768.0f;
 constexpr int kAhead = 4;  // tiles whose codes are on their way to L2
 constexpr uint32_t kCols = 512;
 
@@ -109,72 +117,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = saddr(sm);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kOffMisc + 4);
-  uint32_t* sh_vmax = reinterpret_cast<uint32_t*>(sm + kOffMisc + 8);
+  uint32_t* sh_vmax = reinterpret_cast<uint32_t*>(sm + kOffMisc + 16);
   auto bar = [&](int i) { return base + kOffBar + 8 * i; };
   auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   int* status = s.counters + kCtrStatus;
 
-  const int G = s.group, hkv = s.hkv, bt = s.bt, sh = __ffs(bt) - 1;
-  const int rows_all = a.batch * G, row_blocks = (rows_all + kRows - 1) / kRows;
-  const int rb = blockIdx.x % row_blocks, split = blockIdx.x / row_blocks % a.splits, h = blockIdx.x / row_blocks / a.splits;
-  const int pre_len = s.seq_pos[a.prefix];
-  const int n_tok = block_closed(pre_len, bt) << sh;
-  const int tiles = (n_tok + kTile - 1) / kTile;
-  const int t0 = (int)((long long)tiles * split / a.splits), t1 = (int)((long long)tiles * (split + 1) / a.splits);
-  const int n_t = t1 - t0;  // tile i of the loops is t1 - 1 - i
-  const int rows = min(rows_all - rb * kRows, kRows), nq = rows > kTile ? 2 : 1;
-  const int32_t* table = s.table + (size_t)a.prefix * s.max_bps;
   launch_dependents();
-
-  // this thread's row (softmax warps), and which half of a tile's tokens it has
-  const int x = warp >> 3, half = (warp >> 2) & 1, row = tid & (kTile - 1);
-  const int rr = rb * kRows + x * kTile + row;  // among the rows of the KV head
-  const bool on = warp < kSoftWarps && x * kTile + row < rows;
-  const int bl = on ? rr / G : 0, g = on ? rr % G : 0;
-  const size_t part = (((size_t)split * hkv + h) * a.batch + bl) * G + g;
-  if (n_t == 0) {  // (a graph replayed with a shorter prefix: nothing to add)
-    if (on && half == 0) {
-      for (int e = 0; e < kHeadDim / 4; ++e)
-        reinterpret_cast<float4*>(a.more_o + part * kHeadDim)[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      *reinterpret_cast<float2*>(a.more_ml + part * 2) = make_float2(kNegBig, 0.0f);
-    }
-    return;
-  }
-
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tbase)), "r"(kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (tid == 0) {
+  const int G = s.group, hkv = s.hkv, bt = s.bt, sh = __ffs(bt) - 1;
+  const int rows_all = a.batch * G, row_blocks = (rows_all + kRows - 1) / kRows;
+  const int rb = blockIdx.x % row_blocks, split = blockIdx.x / row_blocks % a.splits, h = blockIdx.x / row_blocks / a.splits;
+  // up to 128 rows: both streams have them, every other tile each
+  const int rows = min(rows_all - rb * kRows, kRows), nq = rows > kTile ? 2 : 1;
+  const bool single = nq == 1;
+  if (tid == 32) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i == kBarQ) count = 8 * nq;
+      if (i == kBarQ) count = 4 * nq;
       if (i >= kBarK && i < kBarKFree) count = kLoadWarps;
-      if (i >= kBarP && i < kBarO) count = 8;
+      if (i >= kBarKFree && i < kBarS) count = nq;
+      if (i >= kBarP && i < kBarO) count = 4;  // (warps of a query tile)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(count));
     }
     *abort = 0;
-    *sh_vmax = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
   }
-  __syncthreads();
-  {  // the largest V scale of the run's blocks
-    const int b0 = (t0 * kTile) >> sh, b1 = min(n_tok, t1 * kTile) >> sh;
-    uint32_t most = 0;
-    for (int i = b0 + tid; i < b1; i += kThreads) {
-      const int id = table[i];
-      if ((unsigned)id < (unsigned)s.num_blocks) most = max(most, __float_as_uint(s.v_scale[(size_t)id * hkv + h]));
-    }
-    most = __reduce_max_sync(0xffffffffu, most);  // (scales are not negative: their order is their bits')
-    if (lane == 0 && most != 0) atomicMax(sh_vmax, most);
-  }
+  const int pre_len = s.seq_pos[a.prefix];
+  const int n_tok = block_closed(pre_len, bt) << sh;
+  const int tiles = (n_tok + kTile - 1) / kTile;
+  const int t0 = (int)((long long)tiles * split / a.splits), t1 = (int)((long long)tiles * (split + 1) / a.splits);
+  const int n_t = t1 - t0;  // tile i of the loops is t1 - 1 - i (none: a graph replayed with a shorter prefix)
+  const int32_t* table = s.table + (size_t)a.prefix * s.max_bps;
+  // this thread's row (softmax warps)
+  const bool soft = warp >= kSoft0 && warp < kLoad0;
+  const int x = (warp - kSoft0) >> 2, row = tid & (kTile - 1);
+  const int in_block = (single ? 0 : x * kTile) + row, rr = rb * kRows + in_block;  // among the rows of the KV head
+  const bool on = soft && in_block < rows;
+  const int bl = on ? rr / G : 0, g = on ? rr % G : 0;
+  const size_t part = (((size_t)split * hkv + h) * a.batch + bl) * G + g;
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = (uint32_t)uniform((int)*tbase);
-  const float vmax = __uint_as_float(*sh_vmax);
 
   bool ok = true;
   auto wait = [&](int b, uint32_t par) {
@@ -187,51 +176,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  if (warp == kMmaWarp) {
-    // -------------------------------------------------------------- products
+  // stream x's tiles, the one of its index i, its slot of K and V and the slot's use
+  auto tiles_of = [&](int x) { return single ? (n_t + 1 - x) >> 1 : n_t; };
+  auto tile_of = [&](int x, int i) { return single ? 2 * i + x : i; };
+
+  if (n_t == 0) {
+    if (on && (x == 0 || !single)) {
+      for (int e = 0; e < kHeadDim / 4; ++e)
+        reinterpret_cast<float4*>(a.more_o + part * kHeadDim)[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      *reinterpret_cast<float2*>(a.more_ml + part * 2) = make_float2(kNegBig, 0.0f);
+    }
+  } else if (warp == kMmaWarp || warp == kMmaWarp2) {
+    // ------------------------------------- products of one stream
     const bool el = elect_one();
-    const uint32_t id_s = instr_desc(kTile, kTile, false), id_o = instr_desc(kTile, kHeadDim, false) | kInstrTransB;
+    const int y = warp == kMmaWarp2;
+    const uint32_t id_s = instr_desc(kTile, kStep, false), id_o = instr_desc(kTile, kHeadDim, false) | kInstrTransB;
     const uint64_t dq = op_desc_sw128(base + kOffQ), dk = op_desc_sw128(base + kOffK),
                    dv = op_desc_mn_sw128(base + kOffV, kBoxB);
+    const int n_y = tiles_of(y);
+    auto slot = [&](int i) { return tile_of(y, i) & 1; };
+    auto use = [&](int i) { return (uint32_t)(tile_of(y, i) >> 1 & 1); };
     wait(kBarQ, 0);
-    for (int i = 0; ok && i <= n_t; ++i) {
-      if (i < n_t) wait(kBarK + (i & 1), (uint32_t)((i >> 1) & 1));
-      if (ok && i > 0) wait(kBarV + ((i - 1) & 1), (uint32_t)(((i - 1) >> 1) & 1));
-      if (!ok) break;
-      for (int y = 0; y < nq; ++y) {
-        const uint32_t t_s = tmem + kTile * y, t_o = tmem + 256 + kTile * y;
-        if (i > 0) {
-          wait(kBarP + y, (uint32_t)((i - 1) & 1));
-          if (!ok) break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (i > 0 && el) {
-          const uint64_t d = dv + (uint64_t)((((i - 1) & 1) * kTileB) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_f16_ts(t_o, t_s + 8 * ks, d + (uint64_t)((ks * 2048) >> 4), id_o, i > 1 || ks > 0);
-          mma_commit(bar(kBarO + y));
-        }
-        if (i < n_t && el) {
-          const uint64_t d = dk + (uint64_t)(((i & 1) * kTileB) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < kHeadDim / 16; ++ks)
-            mma_f16(t_s, dq + (uint64_t)((y * kTileB + (ks >> 2) * kBoxB + (ks & 3) * 32) >> 4),
-                    d + (uint64_t)(((ks >> 2) * kBoxB + (ks & 3) * 32) >> 4), id_s, ks > 0);
-          mma_commit(bar(kBarS + y));
-        }
-        __syncwarp();
+    for (int j = 0; ok && j < 2 * n_y + 2; ++j) {
+      const int i = j >> 1, e = i - 1;  // the tiles of this step's S and P V
+      if (!(j & 1)) {
+        if (i < n_y) wait(kBarK + slot(i), use(i));
+        if (ok && e >= 0) wait(kBarV + slot(e), use(e));
+        if (!ok) break;
       }
-      if (!ok) break;
-      if (el) {
-        if (i > 0) mma_commit(bar(kBarVFree + ((i - 1) & 1)));
-        if (i < n_t) mma_commit(bar(kBarKFree + (i & 1)));
+      if (e >= 0) {
+        wait(kBarP + 2 * y + (j & 1), (uint32_t)(e & 1));
+        if (!ok) break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t t_s = tmem + kTile * y + kStep * (j & 1), t_o = tmem + 256 + kTile * y;
+      if (e >= 0 && el) {
+        const uint64_t d = dv + (uint64_t)((slot(e) * kTileB + (~j & 1) * (kStep * 128)) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kStep / 16; ++ks)
+          mma_f16_ts(t_o, t_s + kStep / 2 + 8 * ks, d + (uint64_t)((ks * 2048) >> 4), id_o, j > 2 || ks > 0);
+        mma_commit(bar(kBarO + 2 * y + (j & 1)));
+      }
+      if (i < n_y && el) {
+        const uint64_t d = dk + (uint64_t)((slot(i) * kTileB + (~j & 1) * (kStep * 128)) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kHeadDim / 16; ++ks)
+          mma_f16(t_s, dq + (uint64_t)(((single ? 0 : y * kTileB) + (ks >> 2) * kBoxB + (ks & 3) * 32) >> 4),
+                  d + (uint64_t)(((ks >> 2) * kBoxB + (ks & 3) * 32) >> 4), id_s, ks > 0);
+        mma_commit(bar(kBarS + 2 * y + (j & 1)));
+      }
+      if (el && (j & 1)) {
+        if (e >= 0) mma_commit(bar(kBarVFree + slot(e)));
+        if (i < n_y) mma_commit(bar(kBarKFree + slot(i)));
       }
       __syncwarp();
     }
     // every product complete before the tensor memory goes back
-    if (el) mma_commit(bar(kBarDone));
-    bar_wait(bar(kBarDone), 0, nullptr);
+    if (el) mma_commit(bar(kBarDone + y));
+    bar_wait(bar(kBarDone + y), 0, nullptr);
     __syncwarp();
   } else if (warp == kScoutWarp) {
     // ------------------------- scales, and the codes of the tiles ahead into L2
@@ -256,9 +258,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ids[kAhead + 1];  // of tiles i .. i + kAhead
 #pragma unroll
     for (int e = 0; e <= kAhead; ++e) ids[e] = id_of(e);
-    float sc = scale_of(ids[0]);
 #pragma unroll
     for (int e = 1; e < kAhead; ++e) fetch(e, ids[e]);
+    float sc = scale_of(ids[0]);
+    // the power of two E of the run's largest V scale: P takes a block's V scale times
+    // 2^(-1 - E), in two steps that no exponent leaves fp32's range by
+    uint32_t most = 0;
+    const int b0 = (t0 * kTile) >> sh, b1 = min(n_tok, t1 * kTile) >> sh;
+#pragma unroll 4
+    for (int k = b0 + lane; k < b1; k += 32) {
+      const int id = table[k];
+      if ((unsigned)id < (unsigned)s.num_blocks) most = max(most, __float_as_uint(s.v_scale[(size_t)id * hkv + h]));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);  // (scales are not negative: their order is their bits')
+    const int E = min(max((int)(most >> 23) - 127, -126), 126);
+    const float down0 = v ? pow2i((-1 - E) / 2) : 1.0f, down1 = v ? pow2i(-1 - E - (-1 - E) / 2) : 1.0f;
+    if (lane == 0) *reinterpret_cast<volatile int*>(sm + kOffMisc + 16) = E;
 #pragma unroll 1
     for (int i = 0; i < n_t; ++i) {
       const int id = ids[0], next = id_of(i + kAhead + 1);
@@ -267,8 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= 2) wait(kBarKFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
       if (!ok) break;
       float* to = reinterpret_cast<float*>(sm + kOffScale) + (i & 3) * 16;
-      if (lane < 8) to[lane] = sc;
-      if (lane >= 8 && lane < 16) to[lane] = vmax > 0.0f ? __fdiv_rn(sc, vmax) * 128.0f : 0.0f;
+      if (lane < 16) to[lane] = sc * down0 * down1;
       if (id == -2 && lane < 8) atomicOr(status, kDevBadBlockId);
       const uint32_t pages = __ballot_sync(0xffffffffu, id >= 0) & 0xFFu;
       if (lane == 0) reinterpret_cast<uint32_t*>(sm + kOffMask)[i & 3] = pages;
@@ -279,28 +293,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < kAhead; ++e) ids[e] = ids[e + 1];
       ids[kAhead] = next;
     }
-  } else if (warp >= kSoftWarps) {
+  } else if (warp >= kLoad0) {
     // ----------------------------------------------------- codes -> fp16 tiles
     // a thread has 16 codes (column ch) of rows r0, r0 + 32, .. of K and of V
-    const int pt = tid - 32 * kSoftWarps, r0 = pt >> 3, ch = pt & 7;
-    const size_t head = (size_t)h * bt * kHeadDim + 16 * ch;
+    const int pt = tid - 32 * kLoad0, r0 = pt >> 3, ch = pt & 7;
     const size_t stride = (size_t)hkv * bt * kHeadDim;
+    uint32_t at[4];  // (of a row in its block's bytes: blocks do not cross tiles, so it stays)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) at[e] = (uint32_t)(h * bt + ((r0 + 32 * e) & (bt - 1))) * kHeadDim + 16 * ch;
     auto load_ids = [&](int i, int (&id)[4]) {
+      const int tok = (t1 - 1 - i) * kTile + r0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int tok = (t1 - 1 - i) * kTile + r0 + 32 * e;
-        id[e] = i < n_t && tok < n_tok ? table[tok >> sh] : -1;
-      }
+      for (int e = 0; e < 4; ++e) id[e] = i < n_t && tok + 32 * e < n_tok ? table[(tok + 32 * e) >> sh] : -1;
     };
-    auto load_codes = [&](const uint8_t* from, int i, const int (&id)[4], uint4 (&w)[4]) {
+    auto load_codes = [&](const uint8_t* from, const int (&id)[4], uint4 (&w)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int tok = (t1 - 1 - i) * kTile + r0 + 32 * e;
         w[e] = make_uint4(0u, 0u, 0u, 0u);  // (the code 0 in both formats)
         if ((unsigned)id[e] < (unsigned)s.num_blocks)
-          w[e] = *reinterpret_cast<const uint4*>(from + id[e] * stride + head + (size_t)(tok & (bt - 1)) * kHeadDim);
+          w[e] = *reinterpret_cast<const uint4*>(from + (uint32_t)id[e] * stride + at[e]);
       }
     };
+    // 16-byte chunks 2 (ch & 3) and the next of a row; the second box's lanes write
+    // them in the other order (each bank once per 8 lanes)
+    const int c0 = 2 * (ch & 3) + (ch >> 2);
+    const uint32_t to0 = (ch >> 2) * kBoxB + r0 * 128 + ((c0 ^ (r0 & 7)) << 4), to1 = to0 ^ 16;
     auto to_halves = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
       if (FP8) {
         e4m3x4_to_h2(c, lo, hi);
@@ -316,18 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto store = [&](uint8_t* tile, const uint4 (&w)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = r0 + 32 * e;
         uint4 y0, y1;
         to_halves(w[e].x, y0.x, y0.y);
         to_halves(w[e].y, y0.z, y0.w);
         to_halves(w[e].z, y1.x, y1.y);
         to_halves(w[e].w, y1.z, y1.w);
-        // 16-byte chunks 2 (ch & 3) and the next of the row; the second box's lanes
-        // write them in the other order (each bank once per 8 lanes)
-        uint8_t* dst = tile + (ch >> 2) * kBoxB + r * 128;
-        const int c0 = 2 * (ch & 3) + (ch >> 2), c1 = c0 ^ 1;
-        *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = ch >> 2 ? y1 : y0;
-        *reinterpret_cast<uint4*>(dst + ((c1 ^ (r & 7)) << 4)) = ch >> 2 ? y0 : y1;
+        *reinterpret_cast<uint4*>(tile + to0 + e * 4096) = ch >> 2 ? y1 : y0;
+        *reinterpret_cast<uint4*>(tile + to1 + e * 4096) = ch >> 2 ? y0 : y1;
       }
       fence_async();
       __syncwarp();
@@ -335,205 +347,292 @@ __global__ void __launch_bounds__(kThreads, 1)
     int id[4], id_next[4];
     uint4 wk[4], wv[4];
     load_ids(0, id);
-    load_codes(s.k_codes, 0, id, wk);
-    load_codes(s.v_codes, 0, id, wv);
+    load_codes(s.k_codes, id, wk);
+    load_codes(s.v_codes, id, wv);
     load_ids(1, id_next);
     for (int i = 0; i < n_t; ++i) {
       if (i >= 2) wait(kBarKFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
       if (!ok) break;
       store(sm + kOffK + (i & 1) * kTileB, wk);
       if (lane == 0) bar_arrive(bar(kBarK + (i & 1)));
-      load_codes(s.k_codes, i + 1, id_next, wk);
+      load_codes(s.k_codes, id_next, wk);
       if (i >= 2) wait(kBarVFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
       if (!ok) break;
       store(sm + kOffV + (i & 1) * kTileB, wv);
       if (lane == 0) bar_arrive(bar(kBarV + (i & 1)));
-      load_codes(s.v_codes, i + 1, id_next, wv);
+      load_codes(s.v_codes, id_next, wv);
       load_ids(i + 2, id_next);
     }
-  } else if (x < nq) {
+  } else if (soft) {
     // ----------------------------------------------------------- query rows
-    // the value of the row's other thread (two places in turn, so that one barrier
-    // of the two warps is enough)
-    float* sh_x = reinterpret_cast<float*>(sm + kOffMax) + x * kTile + row;
-    const int pair = 4 * x + (warp & 3);
-    int turn = 0;
-    auto exchange = [&](float v) {
-      sh_x[turn * 2 * kRows + half * kRows] = v;
-      asm volatile("bar.sync %0, 64;" ::"r"(kNbPair + pair) : "memory");
-      const float o = sh_x[turn * 2 * kRows + (half ^ 1) * kRows];
-      turn ^= 1;
-      return o;
-    };
     float cq;
     int dist = 0;  // (BIAS) from the query to position 4 of the prefix
+    if (BIAS && on) dist = pre_len + s.seq_pos[seq_begin + bl] - 1 - kSinks;
     {
-      const uint16_t* src = q + ((size_t)bl * s.hq + h * G + g) * kHeadDim;
-      if (BIAS && on) dist = pre_len + s.seq_pos[seq_begin + bl] - 1 - kSinks;
+      // the warp's rows as they are into their places (whole rows a copy), then each
+      // thread its own, times a power of two, in fp16
+      const uint32_t mine = (uint32_t)(bl * s.hq + h * G + g);
+      const uint32_t to = base + kOffQ + (single ? 0 : x * kTileB);
+      if (x < nq) {
+#pragma unroll 8
+        for (int i = 0; i < 16; ++i) {
+          const int src_lane = 2 * i + (lane >> 4), r = (row & ~31) + src_lane, c = lane & 15;
+          const uint32_t from = __shfl_sync(0xffffffffu, mine, src_lane);
+          const uint32_t dst = to + (c >> 3) * kBoxB + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst),
+                       "l"(q + (size_t)from * kHeadDim + 8 * c), "r"((in_block & ~31) + src_lane < rows ? 16 : 0)
+                       : "memory");
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+      }
+      if (single) {  // (both streams' warps read the rows)
+        asm volatile("bar.sync 1, %0;" ::"r"(32 * kSoftWarps) : "memory");
+      } else {
+        __syncwarp();
+      }
+      uint8_t* own = sm + kOffQ + (single ? 0 : x * kTileB) + row * 128;
+      auto chunk = [&](int c) { return reinterpret_cast<uint4*>(own + (c >> 3) * kBoxB + (((c & 7) ^ (row & 7)) << 4)); };
       float amax = 0.0f;
-      uint4 mine[8];  // (the thread's half of the row)
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        mine[c] = on ? reinterpret_cast<const uint4*>(src)[8 * half + c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t y[4] = {mine[c].x, mine[c].y, mine[c].z, mine[c].w};
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        const uint4 w = *chunk(c);
+        const uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) amax = max3_abs(amax, bf16f(y[e] & 0xFFFFu), bf16f(y[e] >> 16));
       }
-      amax = fmaxf(amax, exchange(amax));
       int e2 = 0;
       if (amax > 0.0f) e2 = min(max(14 - exponent_of(amax), -100), 100);
       const float up = pow2i(e2);
       cq = (CAP ? a.mod.y_scale : a.qk_scale_log2) * pow2i(-e2);
-      uint8_t* dst = sm + kOffQ + x * kTileB + half * kBoxB + row * 128;
+      if (single) asm volatile("bar.sync 1, %0;" ::"r"(32 * kSoftWarps) : "memory");
+      if (x < nq) {
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          const uint4 w = *chunk(c);
+          const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+          uint32_t o[4];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t y[4] = {mine[c].x, mine[c].y, mine[c].z, mine[c].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = pack_half2(bf16f(y[e] & 0xFFFFu) * up, bf16f(y[e] >> 16) * up);
-        *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int e = 0; e < 4; ++e) o[e] = pack_half2(bf16f(y[e] & 0xFFFFu) * up, bf16f(y[e] >> 16) * up);
+          *chunk(c) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(kBarQ));
       }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bar(kBarQ));
     }
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = trow + kTile * x, t_o = trow + 256 + kTile * x + 64 * half;
+    const uint32_t t_x = trow + kTile * x, t_o = trow + 256 + kTile * x;
     const float slope2 = BIAS && on ? slope_log2(a.mod, h * G + g) : 0.0f;
+    const int n_x = tiles_of(x);
     float m = kNegBig, l = 0.0f;
 #pragma unroll 1
-    for (int i = 0; i < n_t; ++i) {
-      wait(kBarScale + (i & 3), (uint32_t)((i >> 2) & 1));
-      if (ok) wait(kBarS + x, (uint32_t)(i & 1));
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const float* sk = reinterpret_cast<const float*>(sm + kOffScale) + (i & 3) * 16 + 4 * half;
-      const uint32_t pages = reinterpret_cast<const uint32_t*>(sm + kOffMask)[i & 3] >> (4 * half) & 15u;
-      const int d0 = dist - (t1 - 1 - i) * kTile - 64 * half;  // distance to the half's first token
-      float z[32];
-      // the maximum: over the products (scales and a cap keep their order), with a
-      // bias over the scores, which then take the products' place
-      float mx = -INFINITY, most = 0.0f;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        ld32(t_s + 64 * half + 32 * c, z);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float* zz = z + 16 * e;
-          const float f = sk[2 * c + e] * cq;
-          const bool counts = (pages >> (2 * c + e)) & 1u;
-          if (!BIAS) {
-            if (counts) {
-              mx = fmaxf(mx, group_max(zz, -INFINITY) * f);
-              if (CAP) most = fmaxf(most, group_most(zz, 0.0f) * f);
-            }
-          } else {
-            if (CAP) group_cap(a.mod, zz, f, group_most(zz, 0.0f) * f, 0.0f);
-            const float fz = CAP ? 1.0f : f, first = (float)(d0 - 32 * c - 16 * e);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) zz[j] = counts ? fmaf(-slope2, first - (float)j, zz[j] * fz) : -INFINITY;
-            mx = group_max(zz, mx);
-          }
-        }
-        if (BIAS) tmem_st32(t_s + 64 * half + 32 * c, z);
-      }
-      // (no maximum is a NaN: it says that a wait ran out, and both warps leave here)
-      const float mine = ok ? mx : __int_as_float(0x7FFFFFFF), other = exchange(mine);
-      ok = __all_sync(0xffffffffu, mine == mine && other == other);
+    for (int j = 0; j < 2 * n_x; ++j) {
+      const int i = tile_of(x, j >> 1), first = kStep * (~j & 1);  // the tile, the step's first token in it
+      const uint32_t t_s = t_x + kStep * (j & 1);
+      if (!(j & 1)) wait(kBarScale + (i & 3), (uint32_t)((i >> 2) & 1));
+      if (ok) wait(kBarS + 2 * x + (j & 1), (uint32_t)(j >> 1 & 1));
       if (!ok) break;
-      mx = fmaxf(mx, other);
-      if (CAP && !BIAS && mx > -INFINITY) mx = cap_score(a.mod, mx);
-      const bool grow = mx > m + kLazyMax;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float m_old = m;
-        if (grow) m = mx;
-        const float alpha = fast_exp2(m_old - m);
-        l *= alpha;
-        if (i > 0) {
-          wait(kBarO + x, (uint32_t)((i - 1) & 1));  // the product before
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll 1
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            float t[16];
-            ld16(t_o + c0, t);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const float* scales = reinterpret_cast<const float*>(sm + kOffScale) + (i & 3) * 16 + (first >> 4);
+      const float4 sk = *reinterpret_cast<const float4*>(scales), sv = *reinterpret_cast<const float4*>(scales + 8);
+      const uint32_t pages = reinterpret_cast<const uint32_t*>(sm + kOffMask)[i & 3] >> (first >> 4) & 15u;
+      // (a page that does not count has scores of -inf)
+      const float f[4] = {pages & 1u ? sk.x * cq : 1.0f, pages & 2u ? sk.y * cq : 1.0f, pages & 4u ? sk.z * cq : 1.0f,
+                          pages & 8u ? sk.w * cq : 1.0f};
+      const float v[4] = {sv.x, sv.y, sv.z, sv.w};
+      // P (fp16) over the back half of the products, 32 of which have been read when the
+      // first 16 columns of P come there.  The probabilities are formed with the maximum so far;
+      // only where their sum says that one of them may exceed 2^9 is the maximum
+      // itself looked for
 #pragma unroll
-            for (int e = 0; e < 16; ++e) t[e] *= alpha;
-            st16(t_o + c0, t);
-          }
-        }
-      }
-      // P (fp16) over the front of the products: the second half's goes where the
-      // first half's products 32 .. 63 were, once these are read
-      f32x2 ls[2] = {0, 0};
-      if (BIAS) tmem_st_wait();
-      const f32x2 nm = pack2(-m, -m);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 1; c >= 0; --c) {
+        float z[32];
         uint32_t pw[16];
-        ld32(t_s + 64 * half + 32 * c, z);
-        if (half == 0 && c == 1) {
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) bar_arrive(bar(kBarRead + pair));
-        }
+        f32x2 sum;
+        // scores less the maximum -> P, and the unrounded sum
+        auto probabilities = [&]() {
+          f32x2 ls[2] = {0, 0};
+          const f32x2 nm = pack2(-m, -m);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float* zz = z + 16 * e;
-          const float f = BIAS ? 1.0f : sk[2 * c + e] * cq, v = sk[8 + 2 * c + e];
-          const f32x2 f2 = pack2(f, f), v2 = pack2(v, v);
-          if (CAP && !BIAS) {
-            group_cap(a.mod, zz, f, most, -m);
-          } else {
+          for (int e = 0; e < 2; ++e) {
+            float* zz = z + 16 * e;
+            const float fe = f[2 * c + e];
+            const f32x2 f2 = pack2(fe, fe), v2 = pack2(v[2 * c + e], v[2 * c + e]);
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) unpack2(fma2(pack2(zz[j], zz[j + 1]), f2, nm), zz[j], zz[j + 1]);
+            for (int k = 0; k < 16; k += 2) {
+              const f32x2 zp = pack2(zz[k], zz[k + 1]);
+              float y0, y1;
+              unpack2(CAP || BIAS ? add2(zp, nm) : fma2(zp, f2, nm), y0, y1);
+              const f32x2 p = pack2(fast_exp2(y0), fast_exp2(y1));
+              ls[(k >> 1) & 1] = add2(ls[(k >> 1) & 1], p);
+              unpack2(mul2(p, v2), y0, y1);
+              pw[8 * e + (k >> 1)] = pack_half2(y0, y1);
+            }
           }
-          if (!BIAS && !((pages >> (2 * c + e)) & 1u)) {
+          sum = add2(ls[0], ls[1]);
+        };
+        // products -> capped and biased scores (without either they stay products);
+        // pages that do not count become -inf
+        auto scores = [&]() {
+          ld32(t_s + 32 * c, z);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) zz[j] = -INFINITY;
-          }
+          for (int e = 0; e < 2; ++e) {
+            float* zz = z + 16 * e;
+            const float fe = f[2 * c + e];
+            if (CAP) group_cap(a.mod, zz, fe, group_most(zz, 0.0f) * fe, 0.0f);
+            if (BIAS) {
+              const float d0 = (float)(dist - (t1 - 1 - i) * kTile - first - 32 * c - 16 * e);
+              const f32x2 fz = CAP ? pack2(1.0f, 1.0f) : pack2(fe, fe), ns = pack2(-slope2, -slope2);
+              f32x2 d = pack2(d0, d0 - 1.0f);
+              const f32x2 two = pack2(-2.0f, -2.0f);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const f32x2 p = pack2(fast_exp2(zz[j]), fast_exp2(zz[j + 1]));
-            ls[(j >> 1) & 1] = add2(ls[(j >> 1) & 1], p);
-            float lo, hi;
-            unpack2(mul2(p, v2), lo, hi);
-            pw[8 * e + (j >> 1)] = pack_half2(lo, hi);
+              for (int k = 0; k < 16; k += 2) {
+                const f32x2 zp = pack2(zz[k], zz[k + 1]);
+                unpack2(fma2(ns, d, CAP ? zp : mul2(zp, fz)), zz[k], zz[k + 1]);
+                d = add2(d, two);
+              }
+            }
+            if (pages != 15u && !((pages >> (2 * c + e)) & 1u)) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) zz[k] = -INFINITY;
+            }
           }
+        };
+        scores();
+        float lx = INFINITY, ly = 0.0f;
+        if (j > 0 || c == 0) {
+          probabilities();
+          unpack2(sum, lx, ly);
         }
-        if (half == 1 && c == 0) {
-          wait(kBarRead + pair, (uint32_t)(i & 1));
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const bool ask = !(lx + ly <= kMostSum);  // (a row's results do not depend on the others')
+        if (__any_sync(0xffffffffu, ask)) {
+          if (j > 0 || c == 0) scores();  // (P has taken none of this chunk's products yet)
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mx = fmaxf(mx, group_max(z + 16 * e, -INFINITY) * (CAP || BIAS ? 1.0f : f[2 * c + e]));
+          // the maximum rises by a whole number, so that what has been rounded is
+          // scaled without a second rounding
+          float alpha = 1.0f;
+          if (ask && mx > m) {
+            const float up = m > kNegBig ? ceilf(mx - m) : INFINITY;
+            alpha = up < 127.0f ? pow2i(-(int)up) : 0.0f;
+            m = up < 127.0f ? m + up : mx;
+          }
+          l *= alpha;
+          if (c == 0) {  // the other chunk's P
+            uint32_t w[16];
+            tmem_st_wait();
+            ld16u(t_s + kStep * 3 / 4, w);
+            const __half2 a2 = __float2half2_rn(alpha);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), a2);
+              w[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tmem_st16(t_s + kStep * 3 / 4, w);
+          }
+          if (j > 0) {
+            wait(kBarO + 2 * x + ((j - 1) & 1), (uint32_t)((j - 1) >> 1 & 1));  // the product before
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+            for (int c0 = 0; c0 < kHeadDim; c0 += 16) {
+              float t[16];
+              ld16(t_o + c0, t);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) t[e] *= alpha;
+              st16(t_o + c0, t);
+            }
+          }
+          probabilities();
+          unpack2(sum, lx, ly);
         }
-        tmem_st16(t_s + 32 * half + 16 * c, pw);
+        l += lx + ly;
+        tmem_st16(t_s + kStep / 2 + 16 * c, pw);
       }
-      float lx, ly;
-      unpack2(add2(ls[0], ls[1]), lx, ly);
-      l += lx + ly;
+      if (!ok) break;
       tmem_st_wait();
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(bar(kBarP + x));
+      if (lane == 0) bar_arrive(bar(kBarP + 2 * x + (j & 1)));
     }
-    if (ok) wait(kBarO + x, (uint32_t)((n_t - 1) & 1));
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const float l_other = exchange(l);
-    l = half == 0 ? l + l_other : l_other + l;
+    if (ok && n_x > 0) wait(kBarO + 2 * x + 1, (uint32_t)((n_x - 1) & 1));
+    // through shared memory (32 rows of 512 bytes a warp, over the Q and K tiles, which
+    // no product of the stream reads any more; 16-byte chunk e of row i at e ^ i), so
+    // that a warp stores whole rows
+    uint8_t* box = sm + (row < kTile / 2 ? kOffQ : kOffK) + (row >> 5 & 1) * kBoxB;
     if (ok) {
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f, unit = vmax * 0x1p-7f;
-      float* to = a.more_o + part * kHeadDim + 64 * half;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      // (the scales of some tile came after the power was written)
+      const int E = *reinterpret_cast<volatile int*>(sm + kOffMisc + 16);
+      const float up0 = pow2i((E + 1) / 2), up1 = pow2i(E + 1 - (E + 1) / 2);
 #pragma unroll 1
-      for (int c0 = 0; c0 < 64; c0 += 32) {
+      for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
         float o[32];
-        ld32(t_o + c0, o);
-        if (on) {
+        if (n_x > 0) {
+          ld32(t_o + c0, o);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(to + c0 + e) =
-                make_float4(o[e] * inv * unit, o[e + 1] * inv * unit, o[e + 2] * inv * unit, o[e + 3] * inv * unit);
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(box + x * kTileB + lane * 512 + (((c0 + e) >> 2 ^ lane) << 4)) =
+              make_float4(o[e] * inv * up0 * up1, o[e + 1] * inv * up0 * up1, o[e + 2] * inv * up0 * up1,
+                          o[e + 3] * inv * up0 * up1);
+      }
+    }
+    float2* sh_ml = reinterpret_cast<float2*>(sm + kOffMl);  // [2 streams][128]
+    sh_ml[x * kTile + row] = make_float2(m, l);
+    if (single)
+      asm volatile("bar.sync 1, %0;" ::"r"(32 * kSoftWarps) : "memory");
+    else
+      __syncwarp();
+    if (ok && !*abort) {
+      const int first = in_block & ~31;  // the warp's first row; the rows' places follow one another
+      float* to = a.more_o + (((size_t)split * hkv + h) * rows_all + rb * kRows + first) * kHeadDim;
+      float* to_ml = a.more_ml + (((size_t)split * hkv + h) * rows_all + rb * kRows + first) * 2;
+      if (!single) {
+#pragma unroll
+        for (int i0 = 0; i0 < 32; i0 += 8) {
+          float4 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = *reinterpret_cast<const float4*>(box + x * kTileB + (i0 + i) * 512 + ((lane ^ (i0 + i)) << 4));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (first + i0 + i < rows) reinterpret_cast<float4*>(to + (size_t)(i0 + i) * kHeadDim)[lane] = y[i];
+        }
+        if (on) reinterpret_cast<float2*>(to_ml)[lane] = make_float2(m, l);
+      } else {  // each stream stores every other row, joined
+        const float2 ml = sh_ml[row], o = sh_ml[kTile + row];
+        const float top = fmaxf(ml.x, o.x);
+        float wy = fast_exp2(ml.x - top) * ml.y, wz = fast_exp2(o.x - top) * o.y;
+        const float sum = wy + wz, inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+        if (on && x == 0) reinterpret_cast<float2*>(to_ml)[lane] = make_float2(top, sum);
+        wy *= inv;
+        wz *= inv;
+#pragma unroll
+        for (int i0 = x; i0 < 32; i0 += 8) {
+          float4 y[4], z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i0 + 2 * i;
+            y[i] = *reinterpret_cast<const float4*>(box + r * 512 + ((lane ^ r) << 4));
+            z[i] = *reinterpret_cast<const float4*>(box + kTileB + r * 512 + ((lane ^ r) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float u = __shfl_sync(0xffffffffu, wy, i0 + 2 * i), w = __shfl_sync(0xffffffffu, wz, i0 + 2 * i);
+            if (first + i0 + 2 * i < rows)
+              reinterpret_cast<float4*>(to + (size_t)(i0 + 2 * i) * kHeadDim)[lane] =
+                  make_float4(u * y[i].x + w * z[i].x, u * y[i].y + w * z[i].y, u * y[i].z + w * z[i].z,
+                              u * y[i].w + w * z[i].w);
+          }
         }
       }
-      if (on && half == 0) *reinterpret_cast<float2*>(a.more_ml + part * 2) = make_float2(m, l);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
