@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
       if (i == kBarQ) count = 4 * nq;
-      if (i >= kBarK && i < kBarKFree) count = kLoadWarps;
+      if (i >= kBarK && i < kBarKFree) count = kLoadWarps / 2;
       if (i >= kBarKFree && i < kBarS) count = nq;
       if (i >= kBarP && i < kBarO) count = 4;  // (warps of a query tile)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(count));
@@ -295,29 +295,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kLoad0) {
     // ----------------------------------------------------- codes -> fp16 tiles
-    // a thread has 16 codes (column ch) of rows r0, r0 + 32, .. of K and of V
-    const int pt = tid - 32 * kLoad0, r0 = pt >> 3, ch = pt & 7;
+    // four warps have K, four V (so that neither waits for the other's slot); a thread
+    // has 16 codes (column ch) of the rows r0, r0 + 16, ..
+    const bool v = warp >= kLoad0 + kLoadWarps / 2;
+    const int pt = tid - 32 * (kLoad0 + (v ? kLoadWarps / 2 : 0)), r0 = pt >> 3, ch = pt & 7;
     const size_t stride = (size_t)hkv * bt * kHeadDim;
-    uint32_t at[4];  // (of a row in its block's bytes: blocks do not cross tiles, so it stays)
+    // (a row's place in its block: blocks do not cross tiles)
+    const uint8_t* from = (v ? s.v_codes : s.k_codes) + (size_t)(h * bt + r0) * kHeadDim + 16 * ch;
+    auto load_ids = [&](int i, int (&id)[8]) {
+      const int tok = (t1 - 1 - i) * kTile;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) at[e] = (uint32_t)(h * bt + ((r0 + 32 * e) & (bt - 1))) * kHeadDim + 16 * ch;
-    auto load_ids = [&](int i, int (&id)[4]) {
-      const int tok = (t1 - 1 - i) * kTile + r0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) id[e] = i < n_t && tok + 32 * e < n_tok ? table[(tok + 32 * e) >> sh] : -1;
+      for (int e = 0; e < 8; ++e) id[e] = i < n_t && tok + 16 * e < n_tok ? table[(tok + 16 * e) >> sh] : -1;
     };
-    auto load_codes = [&](const uint8_t* from, const int (&id)[4], uint4 (&w)[4]) {
+    auto load_codes = [&](const int (&id)[8], uint4 (&w)[8]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 8; ++e) {
         w[e] = make_uint4(0u, 0u, 0u, 0u);  // (the code 0 in both formats)
         if ((unsigned)id[e] < (unsigned)s.num_blocks)
-          w[e] = *reinterpret_cast<const uint4*>(from + (uint32_t)id[e] * stride + at[e]);
+          w[e] = *reinterpret_cast<const uint4*>(from + (uint32_t)id[e] * stride + (16 * e & (bt - 1)) * kHeadDim);
       }
     };
-    // 16-byte chunks 2 (ch & 3) and the next of a row; the second box's lanes write
-    // them in the other order (each bank once per 8 lanes)
-    const int c0 = 2 * (ch & 3) + (ch >> 2);
-    const uint32_t to0 = (ch >> 2) * kBoxB + r0 * 128 + ((c0 ^ (r0 & 7)) << 4), to1 = to0 ^ 16;
     auto to_halves = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
       if (FP8) {
         e4m3x4_to_h2(c, lo, hi);
@@ -330,38 +327,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         hi = *reinterpret_cast<const uint32_t*>(&x1);
       }
     };
-    auto store = [&](uint8_t* tile, const uint4 (&w)[4]) {
+    // 16-byte chunks 2 (ch & 3) and the next of a row; the second box's lanes write
+    // them in the other order (each bank once per 8 lanes)
+    const int c0 = 2 * (ch & 3) + (ch >> 2);
+    uint8_t* to0 = sm + (v ? kOffV : kOffK) + (ch >> 2) * kBoxB + r0 * 128 + ((c0 ^ (r0 & 7)) << 4);
+    uint8_t* to1 = sm + (v ? kOffV : kOffK) + (ch >> 2) * kBoxB + r0 * 128 + ((c0 ^ 1 ^ (r0 & 7)) << 4);
+    int id[8];
+    uint4 w[8];
+    load_ids(0, id);
+    load_codes(id, w);
+    load_ids(1, id);
+    for (int i = 0; i < n_t; ++i) {
+      if (i >= 2) wait((v ? kBarVFree : kBarKFree) + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
+      if (!ok) break;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 8; ++e) {
         uint4 y0, y1;
         to_halves(w[e].x, y0.x, y0.y);
         to_halves(w[e].y, y0.z, y0.w);
         to_halves(w[e].z, y1.x, y1.y);
         to_halves(w[e].w, y1.z, y1.w);
-        *reinterpret_cast<uint4*>(tile + to0 + e * 4096) = ch >> 2 ? y1 : y0;
-        *reinterpret_cast<uint4*>(tile + to1 + e * 4096) = ch >> 2 ? y0 : y1;
+        *reinterpret_cast<uint4*>(to0 + (i & 1) * kTileB + e * 2048) = ch >> 2 ? y1 : y0;
+        *reinterpret_cast<uint4*>(to1 + (i & 1) * kTileB + e * 2048) = ch >> 2 ? y0 : y1;
       }
       fence_async();
       __syncwarp();
-    };
-    int id[4], id_next[4];
-    uint4 wk[4], wv[4];
-    load_ids(0, id);
-    load_codes(s.k_codes, id, wk);
-    load_codes(s.v_codes, id, wv);
-    load_ids(1, id_next);
-    for (int i = 0; i < n_t; ++i) {
-      if (i >= 2) wait(kBarKFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
-      if (!ok) break;
-      store(sm + kOffK + (i & 1) * kTileB, wk);
-      if (lane == 0) bar_arrive(bar(kBarK + (i & 1)));
-      load_codes(s.k_codes, id_next, wk);
-      if (i >= 2) wait(kBarVFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
-      if (!ok) break;
-      store(sm + kOffV + (i & 1) * kTileB, wv);
-      if (lane == 0) bar_arrive(bar(kBarV + (i & 1)));
-      load_codes(s.v_codes, id_next, wv);
-      load_ids(i + 2, id_next);
+      if (lane == 0) bar_arrive(bar((v ? kBarV : kBarK) + (i & 1)));
+      load_codes(id, w);
+      load_ids(i + 2, id);
     }
   } else if (soft) {
     // ----------------------------------------------------------- query rows
