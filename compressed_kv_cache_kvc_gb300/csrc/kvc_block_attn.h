@@ -701,6 +701,31 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         o1[16 * j + 8] = oacc[j][3] * sA - b1;
       }
     }
+    // (kPrefix) partials of the prefix's blocks, joined with the pair's own.  Where the
+    // pair has one CTA, a warp's first rows of them come under the merge of the warps
+    const int more = FORM == kPrefix ? a.more : 0;
+    constexpr int kFirstRows = FORM == kPrefix ? 20 : 1;
+    const bool quick = FORM == kPrefix && more > 0 && more <= 32 && per_pair == 1;
+    const size_t more_step = FORM == kPrefix ? (size_t)hkv * batch * G : 0;
+    float2 more_ml = make_float2(kNegBig, 0.0f);
+    float4 more_rows[kFirstRows];
+    auto more_at = [&](int g) { return ((size_t)h * batch + bl) * G + g; };
+    auto load_more = [&](int g, int i0) {
+#pragma unroll
+      for (int i = 0; i < kFirstRows; ++i)  // past the end: the last part again, weight 0
+        more_rows[i] = __ldcg(
+            reinterpret_cast<const float4*>(a.more_o + (more_at(g) + min(i0 + i, more - 1) * more_step) * kHeadDim) + lane);
+    };
+    auto load_more_ml = [&](int g) {
+      if (lane < more) more_ml = __ldcg(reinterpret_cast<const float2*>(a.more_ml) + more_at(g) + lane * more_step);
+    };
+    if (FORM == kPrefix && quick) {
+      wait_for_previous();
+      if (warp < G) {
+        load_more_ml(warp);
+        load_more(warp, 0);
+      }
+    }
     __syncthreads();
     // the pair's partials, the slot of this one and of the first (here, not above:
     // alive across the loops they cost 1 us of 90 for 16 x 32 heads of 4,111 tokens)
@@ -710,8 +735,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     const long long slot = kDirect ? slot0 + part : PARTS ? F : (long long)bl * hkv + h + cta;
     const int d = threadIdx.x;  // 128 threads = head_dim
     uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
-    // (kPrefix) partials of the prefix's blocks, joined after the pair's own
-    const int more = FORM == kPrefix ? a.more : 0;
+    float* sm_own = sm_o + kBWarps * kMaxGroup * kMergeRow + kBWarps;  // (quick) [8][kMergeRow]: o, M, l
     int e_most = sm_e[0];
 #pragma unroll
     for (int ww = 1; ww < kBWarps; ++ww) e_most = max(e_most, sm_e[ww]);
@@ -727,7 +751,13 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         l += wt * sm_l[ww * kMaxGroup + g];
       }
       o = l != 0.0f ? o * (1.0f / l) * pow2i(e_most) : 0.0f;
-      if (cnt + more == 1) {
+      if (FORM == kPrefix && quick) {
+        sm_own[g * kMergeRow + d] = o;
+        if (d == 0) {
+          sm_own[g * kMergeRow + kHeadDim] = M;
+          sm_own[g * kMergeRow + kHeadDim + 1] = l;
+        }
+      } else if (cnt + more == 1) {
         orow[(size_t)g * kHeadDim] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
       } else {
         const size_t ps = (size_t)slot * G + g;
@@ -738,7 +768,38 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         }
       }
     }
-    if (cnt + more > 1) {
+    if (FORM == kPrefix && quick) {
+      __syncthreads();
+      for (int g = warp; g < G; g += kBWarps) {
+        if (g != warp) {
+          load_more_ml(g);
+          load_more(g, 0);
+        }
+        const float* own = sm_own + g * kMergeRow;
+        const float M = own[kHeadDim], top = fmaxf(M, warp_max(more_ml.x));
+        float wt = lane < more ? fast_exp2(more_ml.x - top) * more_ml.y : 0.0f;
+        float wo = fast_exp2(M - top) * own[kHeadDim + 1];
+        const float sum = warp_sum(wt) + wo, inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+        wt *= inv;
+        wo *= inv;
+        float4 o = *reinterpret_cast<const float4*>(own + 4 * lane);
+        o = make_float4(wo * o.x, wo * o.y, wo * o.z, wo * o.w);
+        for (int i0 = 0; i0 < more; i0 += kFirstRows) {
+          if (i0 > 0) load_more(g, i0);
+#pragma unroll
+          for (int i = 0; i < kFirstRows; ++i) {
+            const float w = __shfl_sync(0xffffffffu, wt, (i0 + i) & 31);
+            if (i0 + i < more) {
+              o.x += w * more_rows[i].x; o.y += w * more_rows[i].y; o.z += w * more_rows[i].z; o.w += w * more_rows[i].w;
+            }
+          }
+        }
+        uint2 w;
+        w.x = pack_bf16x2(o.x, o.y);
+        w.y = pack_bf16x2(o.z, o.w);
+        *reinterpret_cast<uint2*>(out + ((size_t)bl * s.hq + h * G + g) * kHeadDim + 4 * lane) = w;
+      }
+    } else if (cnt + more > 1) {
       // the pair's last CTA joins the partials, in CTA order
       __syncthreads();
       if (!kDirect || cnt > 1) {
@@ -764,8 +825,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
           const float4* po = reinterpret_cast<const float4*>(a.part_o + (base + g) * kHeadDim) + lane;
           const int mine = (cnt + more - share + wph - 1) / wph;  // parts share + wph j
           // part i: the pair's own, then (kPrefix) those of the prefix
-          const size_t more0 = FORM == kPrefix ? ((size_t)h * batch + bl) * G + g : 0;
-          const size_t more_step = FORM == kPrefix ? (size_t)hkv * batch * G : 0;
+          const size_t more0 = more_at(g);
           auto part_ml = [&](int i) {
             if (FORM == kPrefix && i >= cnt)
               return __ldcg(reinterpret_cast<const float2*>(a.more_ml) + more0 + (i - cnt) * more_step);
