@@ -60,51 +60,28 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
-// What a form of the append has beside the plain one: keys (and queries) rotated
-// on the way, rows at strides; the bounds of every block's keys.
+// What a form of the append has beside the plain one: the bounds of every block's keys.
 struct AppendPlain {
-  static constexpr bool kRot = false, kBounds = false;
+  static constexpr bool kBounds = false;
 };
 struct AppendBounds {
-  static constexpr bool kRot = false, kBounds = true;
+  static constexpr bool kBounds = true;
   KeyBounds bounds;
 };
-struct AppendRotary {
-  static constexpr bool kRot = true, kBounds = false;
-  RotaryArgs rot;  // q's rows, k's input; hk 0
-  RowsIn v;
-  int splits;
-};
-struct AppendRotaryBounds {
-  static constexpr bool kRot = true, kBounds = true;
-  RotaryArgs rot;
-  RowsIn v;
-  int splits;
-  KeyBounds bounds;
-};
-
 template <bool FP8, class Form>
 __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(BlockState s, int seq_begin, int batch, int n_new,
                                                                       int tiles_per_pair,
                                                                       const uint16_t* __restrict__ kin,
                                                                       const uint16_t* __restrict__ vin,
                                                                       const __grid_constant__ Form f) {
-  constexpr bool kRot = Form::kRot, kBounds = Form::kBounds;
+  constexpr bool kBounds = Form::kBounds;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int before[kMaxCallBatch], held[kMaxCallBatch];  // blocks completed before it; its length
   __shared__ int sh_total, sh_bad, sh_last;
   __shared__ float sh_amax[2][kAppWarps];
-  __shared__ uint64_t sh_turns[kRot ? kRotPairs : 1];
-  __shared__ uint8_t sh_axis[kRot ? kRotPairs : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hkv = s.hkv, bt = s.bt;
   const int top = s.counters[kCtrFreeTop];
-  if constexpr (kRot) {
-    if (threadIdx.x < kRotPairs) {
-      sh_turns[threadIdx.x] = f.rot.table.turns[threadIdx.x];
-      sh_axis[threadIdx.x] = f.rot.table.axis[threadIdx.x];
-    }
-  }
   if (warp == 0) {
     int total = 0, bad = 0;
     for (int base = 0; base < batch; base += 32) {
@@ -168,19 +145,8 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
       cur.bl = (int)(pair / 2 / hkv);
     }
 
-    // row i of the new tokens of a (sequence, KV head), values from one row to the next
-    auto rows_in = [&](int kv, int bl, int h) -> const uint16_t* {
-      if constexpr (kRot) {
-        const RowsIn& r = kv ? f.v : f.rot.k;
-        return r.in + bl * r.sb + h * r.sh;
-      } else {
-        return (kv ? vin : kin) + ((size_t)bl * hkv + h) * n_new * kHeadDim;
-      }
-    };
-    auto step_in = [&](int kv) -> ptrdiff_t {
-      if constexpr (kRot) return kv ? f.v.st : f.rot.k.st;
-      return kHeadDim;
-    };
+    // the new rows of a (sequence, KV head)
+    auto rows_in = [&](int kv, int bl, int h) { return (kv ? vin : kin) + ((size_t)bl * hkv + h) * n_new * kHeadDim; };
 
     // the copies of the CTA's next tile
     int i_next = 0, st_next = 0;
@@ -193,8 +159,7 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
         if (row0 < (long long)nb << sh) {
           const size_t pair = (size_t)nxt.bl * hkv + nxt.h;
           const int p0 = kSinks + (c0 << sh) + (int)row0 + (lane >> 4);  // the lane's first row
-          const ptrdiff_t step = step_in(nxt.kv);
-          const uint16_t* in = rows_in(nxt.kv, nxt.bl, nxt.h) + (p0 - P) * step + 8 * (lane & 15);
+          const uint16_t* in = rows_in(nxt.kv, nxt.bl, nxt.h) + (p0 - P) * (ptrdiff_t)kHeadDim + 8 * (lane & 15);
           if (nxt.x == 0) {  // may begin in the open block's rows
             const uint16_t* exact = (nxt.kv ? s.v_exact : s.k_exact) +
                                     (((size_t)seq_begin * hkv + pair) * exact_rows + kSinks) * kHeadDim + 8 * (lane & 15);
@@ -202,11 +167,11 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
             for (int i = 0; i < 8; ++i) {
               const int p = p0 + 2 * i;
               cp_async16(ring_s + st_next * kAppStage + 512 * i,
-                         p < P ? exact + (size_t)((p - kSinks) & (bt - 1)) * kHeadDim : in + 2 * i * step);
+                         p < P ? exact + (size_t)((p - kSinks) & (bt - 1)) * kHeadDim : in + 2 * i * kHeadDim);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) cp_async16(ring_s + st_next * kAppStage + 512 * i, in + 2 * i * step);
+            for (int i = 0; i < 8; ++i) cp_async16(ring_s + st_next * kAppStage + 512 * i, in + 2 * i * kHeadDim);
           }
           cp_async4(ring_id_s + st_next * kAppStage, s.free_stack + (top - 1 - (before[nxt.bl] + ((int)row0 >> sh))));
         }
@@ -232,33 +197,6 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
       const int c = live ? (int)row0 >> sh : 0;
       const uint8_t* rows = ring + st * kAppStage;
       float amax = 0.0f;
-      if constexpr (kRot) {
-        // new keys are turned where they lie (a row of the open block was when it came)
-        if (kv == 0 && live) {
-          const int cl = lane & 7;
-          if (rotary::turns_here(f.rot.table, cl)) {
-            const int p0 = kSinks + (c0 << sh) + (int)row0;
-            uint8_t* mine = smem + warp * kAppStages * kAppStage + st * kAppStage;
-            const int ca = 16 * rotary::chunk_a(f.rot.table, cl), cb = 16 * rotary::chunk_b(f.rot.table, cl);
-#pragma unroll 1
-            for (int r = lane >> 3; r < 16; r += 4) {
-              const int p = p0 + r;
-              if (p < P) continue;
-              float cs[8], sn[8];
-              rotary::angles(sh_turns, sh_axis,
-                             rotary::row_pos(f.rot.table, (size_t)bl * n_new + (p - P), (size_t)batch * n_new, p), cl, cs,
-                             sn);
-              uint4* xa = reinterpret_cast<uint4*>(mine + 256 * r + ca);
-              uint4* xb = reinterpret_cast<uint4*>(mine + 256 * r + cb);
-              uint4 x = *xa, y = *xb;
-              rotary::turn16(f.rot.table.adjacent != 0, x, y, cs, sn);
-              *xa = x;
-              *xb = y;
-            }
-          }
-          __syncwarp();
-        }
-      }
       // (a lane's eight channels, kBounds: the least of them in lanes 0 .. 15, the largest
       // in the others)
       uint4 ends = make_uint4(0u, 0u, 0u, 0u);
@@ -311,42 +249,17 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
         // block's rows are in shared memory
         __syncthreads();
         const uint16_t* in = rows_in(kv, bl, h);
-        const ptrdiff_t step = step_in(kv);
         uint16_t* exact = (kv ? s.v_exact : s.k_exact) + ((size_t)b * hkv + h) * exact_rows * kHeadDim;
         const int open0 = kSinks + ((c0 + nb) << sh);
         const int n_sink = max(0, min(kSinks - P, n_new));
         const int first = min(max(open0 - P, n_sink), n_new);  // first new token of the open block
-        auto new_token = [&](int r) { return r < n_sink ? r : first + (r - n_sink); };
-        auto place = [&](int p) {
-          return exact + (size_t)(p < kSinks ? p : kSinks + ((p - kSinks) & (bt - 1))) * kHeadDim;
-        };
-        if (kRot && kv == 0) {
-          if constexpr (kRot) {
-            const int cl = lane & 7;
-            const int ca = 8 * rotary::chunk_a(f.rot.table, cl), cb = 8 * rotary::chunk_b(f.rot.table, cl);
-#pragma unroll 1
-            for (int r = threadIdx.x >> 3; r < n_sink + (n_new - first); r += kAppThreads / 8) {
-              const int i = new_token(r);
-              uint4 x = *reinterpret_cast<const uint4*>(in + i * step + ca);
-              uint4 y = *reinterpret_cast<const uint4*>(in + i * step + cb);
-              if (rotary::turns_here(f.rot.table, cl)) {
-                float cs[8], sn[8];
-                rotary::angles(
-                    sh_turns, sh_axis,
-                    rotary::row_pos(f.rot.table, (size_t)bl * n_new + i, (size_t)batch * n_new, P + i), cl, cs, sn);
-                rotary::turn16(f.rot.table.adjacent != 0, x, y, cs, sn);
-              }
-              *reinterpret_cast<uint4*>(place(P + i) + ca) = x;
-              *reinterpret_cast<uint4*>(place(P + i) + cb) = y;
-            }
-          }
-        } else {
 #pragma unroll 4
-          for (int r = threadIdx.x >> 4; r < n_sink + (n_new - first); r += kAppThreads / 16) {
-            const int i = new_token(r);
-            reinterpret_cast<uint4*>(place(P + i))[threadIdx.x & 15] =
-                reinterpret_cast<const uint4*>(in + i * step)[threadIdx.x & 15];
-          }
+        for (int r = threadIdx.x >> 4; r < n_sink + (n_new - first); r += kAppThreads / 16) {
+          const int i = r < n_sink ? r : first + (r - n_sink);
+          const int p = P + i;
+          const int row = p < kSinks ? p : kSinks + ((p - kSinks) & (bt - 1));
+          reinterpret_cast<uint4*>(exact + (size_t)row * kHeadDim)[threadIdx.x & 15] =
+              reinterpret_cast<const uint4*>(in + (size_t)i * kHeadDim)[threadIdx.x & 15];
         }
       }
       if (live) {
@@ -408,13 +321,6 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) block_append_kernel(Blo
       advance(cur);
     }
     cp_async_wait<0>();
-    if constexpr (kRot) {
-      if (f.rot.hq > 0) {
-        const long long units = ((long long)batch * n_new + 3) / 4 * f.splits;
-        for (long long u = (long long)blockIdx.x * kAppWarps + warp; u < units; u += (long long)gridDim.x * kAppWarps)
-          rotary::rotate_unit(f.rot, sh_turns, sh_axis, u, f.splits, [&](int b) { return held[b]; });
-      }
-    }
   }
   // the last CTA advances the lengths and the stack (every CTA has read them)
   __syncthreads();
@@ -608,14 +514,6 @@ cudaError_t launch_block_append(const BlockState& s, const KeyBounds& bounds, in
                                 const uint16_t* k, const uint16_t* v, cudaStream_t st) {
   return bounds.codes ? append_launch(s, seq_begin, batch, n_new, k, v, AppendBounds{bounds}, st)
                       : append_launch(s, seq_begin, batch, n_new, k, v, AppendPlain{}, st);
-}
-
-cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bounds, int seq_begin,
-                                       const RotaryArgs& rot, const RowsIn& v, cudaStream_t st) {
-  const int splits = rotary_splits((long long)rot.batch * rot.n, rot.hq);
-  return bounds.codes ? append_launch(s, seq_begin, rot.batch, rot.n, nullptr, nullptr,
-                                      AppendRotaryBounds{rot, v, splits, bounds}, st)
-                      : append_launch(s, seq_begin, rot.batch, rot.n, nullptr, nullptr, AppendRotary{rot, v, splits}, st);
 }
 
 cudaError_t launch_block_release(const BlockState& s, int seq_begin, int batch, cudaStream_t st) {

@@ -75,6 +75,7 @@ struct BlockChoice {
 
 cudaError_t launch_block_append(const BlockState& s, const KeyBounds& bounds, int seq_begin, int batch, int n_new,
                                 const uint16_t* k, const uint16_t* v, cudaStream_t st);
+int block_append_rotary_launches(const RotaryArgs& rot);
 cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bounds, int seq_begin,
                                        const RotaryArgs& rot, const RowsIn& v, cudaStream_t st);
 cudaError_t launch_block_release(const BlockState& s, int seq_begin, int batch, cudaStream_t st);

@@ -405,7 +405,7 @@ kvc_status kvc_block_append_rotary(kvc_block_cache* c, int32_t seq_begin, int32_
   if (kvc::launch_block_append_rotary(c->dev, c->bounds, seq_begin, a, rows_v, static_cast<cudaStream_t>(stream)) !=
       cudaSuccess)
     return KVC_ERR_CUDA;
-  c->last_launches = 1;
+  c->last_launches = kvc::block_append_rotary_launches(a);
   for (int i = 0; i < batch; ++i) c->pos[seq_begin + i] += n_new;
   return KVC_OK;
 }

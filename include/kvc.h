@@ -676,7 +676,8 @@ kvc_status kvc_block_append(kvc_block_cache* cache, int32_t seq_begin, int32_t b
  *   d_positions: i32 [axes][batch][n_new], or null: first + the token's index in
  *   its sequence on every axis, read on the device (a replayed graph goes on
  *   counting).
- * One launch.  Errors as kvc_block_append and kvc_rotary_rotate. */
+ * One launch, two where the queries are many rows.  Errors as kvc_block_append and
+ * kvc_rotary_rotate. */
 kvc_status kvc_block_append_rotary(kvc_block_cache* cache, int32_t seq_begin, int32_t batch, int32_t n_new,
                                    const kvc_rotary* rotary, const kvc_rows* q, const kvc_rows* k, const kvc_rows* v,
                                    const int32_t* d_positions, int32_t first, void* stream);
