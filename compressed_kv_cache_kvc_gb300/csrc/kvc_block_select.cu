@@ -21,8 +21,18 @@
 namespace kvc {
 namespace {
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreStep = kScoreThreads / 4;  // blocks a CTA takes at once
+constexpr int kScoreThreads = 128, kScoreCtas = 6 * 152;
+constexpr int kScoreStep = kScoreThreads / 32 * 16;  // blocks a CTA takes at once
+
+// c += A (16 rows of 32 codes) x B (32 x 8): of lane l, a holds four codes of the
+// rows l / 4 and l / 4 + 8 at two places, b of column l / 4 at the same two.
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 __device__ __forceinline__ uint32_t order_key(float z) {  // NaN (never of finite inputs) lowest
   const uint32_t u = __float_as_uint(z + 0.0f);           // (-0 is 0)
@@ -32,7 +42,7 @@ __device__ __forceinline__ uint32_t order_key(float z) {  // NaN (never of finit
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(BlockState s, KeyBounds bounds, BlockChoice ch,
                                                                     int seq_begin, int chunks,
                                                                     const uint16_t* __restrict__ q) {
-  __shared__ uint32_t sh_q[kMaxGroup][2][32];  // four codes a word: min(q8, 0), max(q8, 0)
+  __shared__ __align__(16) uint32_t sh_q[kMaxGroup][2][32];  // four codes a word: min(q8, 0), max(q8, 0)
   __shared__ float sh_s[kMaxGroup];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = s.group, hkv = s.hkv;
   const int pair = blockIdx.x / chunks, bl = pair / hkv, h = pair % hkv, b = seq_begin + bl;
@@ -40,57 +50,89 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(BlockState s
   const int n = closed - ch.recent;
   launch_dependents();
   if (closed <= ch.top + ch.recent) return;  // all are chosen
-  if (warp < G) {
-    const uint2 w = reinterpret_cast<const uint2*>(q + ((size_t)bl * s.hq + h * G + warp) * kHeadDim)[lane];
-    const float x[4] = {bf16f(w.x & 0xFFFFu), bf16f(w.x >> 16), bf16f(w.y & 0xFFFFu), bf16f(w.y >> 16)};
+  // a warp's 16 blocks are the rows of A, the group's query rows the columns of B;
+  // block ids are loaded two steps ahead, bounds one
+  const int j = lane & 3, row = lane >> 2, step = chunks * kScoreStep;
+  const int32_t* table = s.table + (size_t)b * s.max_bps;
+  uint32_t* keys = ch.keys + (size_t)pair * s.max_bps;
+  int c = (int)(blockIdx.x % chunks) * kScoreStep + warp * 16 + row;
+  int blk[2], next[2];
+  uint4 w[2][4];
+  float t[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[r][i] = make_uint4(0u, 0u, 0u, 0u);
+  auto ids = [&](int (&to)[2], int c) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) to[r] = c + 8 * r < n ? table[c + 8 * r] : -1;
+  };
+  auto load = [&] {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if ((unsigned)blk[r] < (unsigned)s.num_blocks) {
+        const size_t at = (size_t)blk[r] * hkv + h;
+        const uint4* src = reinterpret_cast<const uint4*>(bounds.codes + at * (2 * kHeadDim)) + j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[r][i] = src[4 * i];
+        t[r] = bounds.scale[at];
+      }
+  };
+  ids(blk, c);
+  ids(next, c + step);
+  load();
+  for (int g = warp; g < G; g += kScoreThreads / 32) {
+    const uint2 v = reinterpret_cast<const uint2*>(q + ((size_t)bl * s.hq + h * G + g) * kHeadDim)[lane];
+    const float x[4] = {bf16f(v.x & 0xFFFFu), bf16f(v.x >> 16), bf16f(v.y & 0xFFFFu), bf16f(v.y >> 16)};
     const float amax = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
     const float scale = __fdiv_rn(amax, 127.0f);
     uint32_t neg = 0, pos = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int c = scale > 0.0f ? min(max(__float2int_rn(__fdiv_rn(x[e], scale)), -127), 127) : 0;
-      neg |= (uint32_t)(min(c, 0) & 0xFF) << (8 * e);
-      pos |= (uint32_t)max(c, 0) << (8 * e);
+      const int code = scale > 0.0f ? min(max(__float2int_rn(__fdiv_rn(x[e], scale)), -127), 127) : 0;
+      neg |= (uint32_t)(min(code, 0) & 0xFF) << (8 * e);
+      pos |= (uint32_t)max(code, 0) << (8 * e);
     }
-    sh_q[warp][0][lane] = neg;
-    sh_q[warp][1][lane] = pos;
-    if (lane == 0) sh_s[warp] = scale;
+    sh_q[g][0][lane] = neg;
+    sh_q[g][1][lane] = pos;
+    if (lane == 0) sh_s[g] = scale;
   }
   __syncthreads();
-  const int j = threadIdx.x & 3;
-  const int32_t* table = s.table + (size_t)b * s.max_bps;
-  uint32_t* keys = ch.keys + (size_t)pair * s.max_bps;
-  for (int c0 = (int)(blockIdx.x % chunks) * kScoreStep; c0 < n; c0 += chunks * kScoreStep) {
-    const int c = c0 + (threadIdx.x >> 2);
-    const int blk = c < n ? table[c] : -1;
-    uint4 w[4];
-    float t = 0.0f;
-    const bool ok = (unsigned)blk < (unsigned)s.num_blocks;
-    if (ok) {
-      const uint4* src = reinterpret_cast<const uint4*>(bounds.codes + ((size_t)blk * hkv + h) * (2 * kHeadDim)) + j;
+  uint4 y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = src[4 * i];
-      t = bounds.scale[(size_t)blk * hkv + h];
-    } else {
+  for (int i = 0; i < 4; ++i)
+    y[i] = row < G ? *reinterpret_cast<const uint4*>(&sh_q[row][i >> 1][4 * (j + 4 * (i & 1))])
+                   : make_uint4(0u, 0u, 0u, 0u);
+  const bool has[2] = {2 * j < G, 2 * j + 1 < G};
+  const float scale[2] = {has[0] ? sh_s[2 * j] : 0.0f, has[1] ? sh_s[2 * j + 1] : 0.0f};
+#pragma unroll 1
+  for (; c - row < n; c += step) {  // (a warp's blocks all or none)
+    int dot[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 4; ++i) {
+      mma_s8(dot, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, y[i].x, y[i].y);
+      mma_s8(dot, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, y[i].z, y[i].w);
     }
-    float best = -INFINITY;
-    for (int g = 0; g < G; ++g) {
-      int dot = 0;
+    float best[2];
+    bool ok[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(&sh_q[g][i >> 1][4 * (j + 4 * (i & 1))]);
-        dot = __dp4a((int)x.x, (int)w[i].x, dot);
-        dot = __dp4a((int)x.y, (int)w[i].y, dot);
-        dot = __dp4a((int)x.z, (int)w[i].z, dot);
-        dot = __dp4a((int)x.w, (int)w[i].w, dot);
-      }
-      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-      best = fmaxf(best, __fmul_rn(__fmul_rn((float)dot, sh_s[g]), t));
+    for (int r = 0; r < 2; ++r) {
+      best[r] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (has[e]) best[r] = fmaxf(best[r], __fmul_rn(__fmul_rn((float)dot[2 * r + e], scale[e]), t[r]));
+      ok[r] = (unsigned)blk[r] < (unsigned)s.num_blocks;
+      blk[r] = next[r];
     }
-    if (j == 0 && c < n) keys[c] = ok ? order_key(best) : 0u;  // (a bad block id is flagged by the attention)
+    ids(next, c + 2 * step);
+    load();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+      // (a bad block id is flagged by the attention)
+      if (j == r && c + 8 * r < n) keys[c + 8 * r] = ok[r] ? order_key(best[r]) : 0u;
+    }
   }
 }
 
@@ -163,7 +205,7 @@ cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, co
   const int pairs = batch * s.hkv, n = block_closed(longest, s.bt) - ch.recent;
   const int steps = (n + kScoreStep - 1) / kScoreStep;
   // (a graph replayed at longer sequences takes more steps a CTA)
-  const int chunks = std::max(1, std::min(steps, (8 * 152 + pairs - 1) / pairs));
+  const int chunks = std::max(1, std::min(steps, kScoreCtas / pairs));
   block_score_kernel<<<pairs * chunks, kScoreThreads, 0, st>>>(s, bounds, ch, seq_begin, chunks, q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
