@@ -144,11 +144,11 @@ class BlockScaledCache:
         pos = rotary._positions(positions, batch, n, self.device)
         rq = None
         if q is not None:
-            _rows(q, "q", self.device, batch, n, self.num_q_heads, None)
+            rq = _rows(q, "q", self.device, batch, n, self.num_q_heads, None)
             out = _out(out, q, "out")
-            if out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            rq.d_out = out.data_ptr()
+            if rq.d_out == rq.d_in and not q.is_contiguous():
                 raise ValueError("out may be q only where q is packed")
-            rq = _rows(q, "q", self.device, batch, n, self.num_q_heads, out)
         self._call("kvc_block_append_rotary", seq_begin, batch, n, ctypes.byref(rotary.plan),
                    ctypes.byref(rq) if rq is not None else None, ctypes.byref(rk), ctypes.byref(rv), pos, first)
         return out if q is not None else None

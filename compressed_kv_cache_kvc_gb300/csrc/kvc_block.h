@@ -53,7 +53,7 @@ struct BlockAttn {
   float qk_scale_log2;
   int ncta;
   // the selected form: blocks of every pair in ascending order, `most` places a pair
-  const int32_t* list;
+  const int32_t* list, *ids;
   int most;
   // the prefix form: the sequence that holds it, whether its pages are among the
   // units; partials of its blocks from elsewhere, `more` of [hkv][batch][group]
@@ -70,6 +70,7 @@ struct BlockAttn {
 struct BlockChoice {
   uint32_t* keys;  // [pairs][max_bps], ordered as the scores
   int32_t* list;   // [pairs][top + recent], ascending, -1 behind the last
+  int32_t* ids;    // their blocks in the pool
   int top, recent;
 };
 

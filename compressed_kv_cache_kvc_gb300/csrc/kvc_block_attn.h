@@ -23,10 +23,6 @@ using namespace codes;
 __host__ __device__ constexpr int kExactRows(int bt) { return kSinks + bt; }
 
 enum { kPlain = 0, kSelected = 1, kPrefix = 2 };  // forms
-#ifndef KVC_DP
-#define KVC_DP true
-#endif
-constexpr bool kDirectParts = KVC_DP;
 
 // ---------------------------------------------------------------- attention
 // out = softmax(z) . v over everything a sequence holds, z as kvc_score.h says.
@@ -229,13 +225,12 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     const int n_my = u_e - u_a > warp ? (u_e - u_a - warp + kBWarps - 1) / kBWarps : 0;
     const int n_pg = min(u_e, npg) - u_a > warp ? (min(u_e, npg) - u_a - warp + kBWarps - 1) / kBWarps : 0;
     const int32_t* table = s.table + (size_t)b * s.max_bps;
-    if (FORM == kSelected) wait_for_previous();  // the list
     const int32_t* list = FORM == kSelected ? a.list + ((size_t)bl * hkv + h) * a.most : nullptr;
     // block ids and scales of this warp's pages, 32 at a time across the lanes
     auto tab_load = [&](int chunk) -> int {
       const int k = chunk * 32 + lane, u = u_a + warp + kBWarps * k;
       if (k >= n_pg) return -1;
-      if (FORM == kSelected) return table[list[u / ppb]];
+      if (FORM == kSelected) return a.ids[((size_t)bl * hkv + h) * a.most + u / ppb];
       if (FORM == kPrefix)
         return u < pre_npg ? s.table[(size_t)a.prefix * s.max_bps + u / ppb] : table[(u - pre_npg) / ppb];
       return table[u / ppb];
@@ -246,13 +241,11 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       const int k = chunk * 32 + lane;
       return kBlocks && k < n_pg ? list[(u_a + warp + kBWarps * k) / ppb] : 0;
     };
-    int blk_use = block_load(0), blk_nxt = n_pg > 32 ? block_load(1) : 0;
-    int id_cur = tab_load(0), id_nxt = n_pg > 32 ? tab_load(1) : -1;
+    int blk_use = 0, blk_nxt = 0, id_cur = -1, id_nxt = -1;
     auto scale_of = [&](const float* sc, int id) {
       return (unsigned)id < (unsigned)s.num_blocks ? sc[(size_t)id * hkv + h] : 0.0f;
     };
-    float ks_use = scale_of(s.k_scale, id_cur), vs_use = scale_of(s.v_scale, id_cur);
-    float ks_nxt = scale_of(s.k_scale, id_nxt), vs_nxt = scale_of(s.v_scale, id_nxt);
+    float ks_use = 0.0f, vs_use = 0.0f, ks_nxt = 0.0f, vs_nxt = 0.0f;
     uint32_t stage_ok = 0;
     const uint8_t* kb = s.k_codes + (size_t)h * bt * kHeadDim + 16 * lane;
     const uint8_t* vb = s.v_codes + (size_t)h * bt * kHeadDim + 16 * lane;
@@ -280,8 +273,21 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       }
       cp_async_commit();
     };
-    issue(0);
-    issue(1);
+    auto first_pages = [&] {
+      blk_use = block_load(0);
+      id_cur = tab_load(0);
+      if (n_pg > 32) {
+        blk_nxt = block_load(1);
+        id_nxt = tab_load(1);
+      }
+      ks_use = scale_of(s.k_scale, id_cur);
+      vs_use = scale_of(s.v_scale, id_cur);
+      ks_nxt = scale_of(s.k_scale, id_nxt);
+      vs_nxt = scale_of(s.v_scale, id_nxt);
+      issue(0);
+      issue(1);
+    };
+    if (FORM != kSelected) first_pages();
 
     // ---- query fragments (B operand), scaled by 2^e into fp16 range
     uint32_t bq[8][2];
@@ -628,9 +634,14 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     };
 
     // the other forms' come before them, while the first pages are on their way
+    // (kSelected: while they are chosen)
     if (kDirect) {
 #pragma unroll 1
       for (int k = n_pg; k < n_my; ++k) exact_tile(k);
+    }
+    if (FORM == kSelected) {
+      wait_for_previous();
+      first_pages();
     }
 
     int k = 0;
@@ -928,7 +939,7 @@ template <int FORM, bool FP8, int MOD>
 cudaError_t launch_block_attn_t(const BlockState& s, int seq_begin, int batch, const uint16_t* q, uint16_t* out,
                                 const BlockAttn& w, cudaStream_t st) {
   if constexpr (FORM != kPlain) {
-    const cudaError_t e = block_attn_smem<FORM, FP8, MOD, kDirectParts>();
+    const cudaError_t e = block_attn_smem<FORM, FP8, MOD, true>();
     if (e != cudaSuccess) return e;
     // may start under the kernel before it (wait_for_previous)
     cudaLaunchAttribute early{};
@@ -941,7 +952,7 @@ cudaError_t launch_block_attn_t(const BlockState& s, int seq_begin, int batch, c
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = w.early ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, block_attn_kernel<FORM, FP8, MOD, kDirectParts>, s, seq_begin, batch, q, out, w);
+    return cudaLaunchKernelEx(&cfg, block_attn_kernel<FORM, FP8, MOD, true>, s, seq_begin, batch, q, out, w);
   } else {
     const cudaError_t e = w.parts ? block_attn_smem<FORM, FP8, MOD, true>() : block_attn_smem<FORM, FP8, MOD, false>();
     if (e != cudaSuccess) return e;

@@ -196,7 +196,7 @@ bool choice_ok(int top, int recent) { return top > 0 && recent >= 0 && (long lon
 
 struct SelectedLayout {
   WsLayout ws;
-  size_t keys, list, total;
+  size_t keys, list, ids, total;
 };
 SelectedLayout selected_layout(const kvc_block_cache* c, int batch, int top, int recent) {
   const size_t pairs = (size_t)batch * c->cfg.num_kv_heads;
@@ -204,7 +204,8 @@ SelectedLayout selected_layout(const kvc_block_cache* c, int batch, int top, int
   l.ws = ws_layout(c, batch);
   l.keys = align_up(l.ws.total);
   l.list = l.keys + align_up(pairs * c->cfg.max_blocks_per_seq * 4);
-  l.total = l.list + align_up(pairs * ((size_t)top + recent) * 4);
+  l.ids = l.list + align_up(pairs * ((size_t)top + recent) * 4);
+  l.total = l.ids + align_up(pairs * ((size_t)top + recent) * 4);
   return l;
 }
 
@@ -494,10 +495,12 @@ kvc_status kvc_block_selected_attention(kvc_block_cache* c, int32_t seq_begin, i
   kvc::BlockChoice ch{};
   ch.keys = reinterpret_cast<uint32_t*>(ws + sl.keys);
   ch.list = d_blocks ? d_blocks : reinterpret_cast<int32_t*>(ws + sl.list);
+  ch.ids = reinterpret_cast<int32_t*>(ws + sl.ids);
   ch.top = top_blocks;
   ch.recent = recent_blocks;
   kvc::BlockAttn a = attention_of(sl.ws, d_workspace, sm_scale, softcap, d_slopes);
   a.list = ch.list;
+  a.ids = ch.ids;
   a.most = most;
   split_pairs(c, &a, batch, units);
   a.early = 1;

@@ -142,15 +142,22 @@ constexpr int kKeysStaged = 4096;
 
 __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState s, BlockChoice ch, int seq_begin) {
   __shared__ uint32_t sh_keys[kKeysStaged];
+  __shared__ int32_t sh_table[kKeysStaged];
   __shared__ int hist[kRadixBins], sh_warp[32], sh_sel[3], sh_more[kChooseWarps], sh_same[kChooseWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pair = blockIdx.x, b = seq_begin + pair / s.hkv, most = ch.top + ch.recent;
   const int closed = block_closed(s.seq_pos[b], s.bt);
   int32_t* list = ch.list + (size_t)pair * most;
+  int32_t* ids = ch.ids + (size_t)pair * most;
+  const int32_t* table = s.table + (size_t)b * s.max_bps;
   launch_dependents();
+  for (int i = threadIdx.x; i < min(closed, kKeysStaged); i += kChooseThreads) sh_table[i] = table[i];
   wait_for_previous();  // the keys (and, for a list that stays, the call before)
   if (closed <= most) {
-    for (int i = threadIdx.x; i < most; i += kChooseThreads) list[i] = i < closed ? i : -1;
+    for (int i = threadIdx.x; i < most; i += kChooseThreads) {
+      list[i] = i < closed ? i : -1;
+      if (i < closed) ids[i] = table[i];
+    }
     return;
   }
   const int n = closed - ch.recent;
@@ -184,6 +191,10 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
     same += sh_same[i];
   }
   const uint32_t below = (1u << lane) - 1u;
+  auto put = [&](int at, int block) {
+    list[at] = block;
+    ids[at] = block < kKeysStaged ? sh_table[block] : table[block];
+  };
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const uint32_t k = i0 + lane < hi ? key(i0 + lane) : 0u;
     const uint32_t up = __ballot_sync(0xffffffffu, i0 + lane < hi && k > limit);
@@ -191,11 +202,11 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
     // blocks at the limit are taken from the lowest on
     const int same_before = same + __popc(at & below);
     const bool take = ((up >> lane) & 1u) || (((at >> lane) & 1u) && same_before < same_left);
-    if (take) list[more + __popc(up & below) + min(same_before, same_left)] = i0 + lane;
+    if (take) put(more + __popc(up & below) + min(same_before, same_left), i0 + lane);
     more += __popc(up);
     same += __popc(at);
   }
-  for (int i = threadIdx.x; i < ch.recent; i += kChooseThreads) list[ch.top + i] = n + i;
+  for (int i = threadIdx.x; i < ch.recent; i += kChooseThreads) put(ch.top + i, n + i);
 }
 
 }  // namespace

@@ -2,6 +2,7 @@
 // of a turn, the launch.
 #include "kvc_rotary_host.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -14,10 +15,10 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 // (kept from its 64th bit behind the point on, the lower ones added in) is off by
 // less than one unit of the last place before it is rounded.
 uint64_t turns_of(float f) {
-  int e = 0;
-  const double m = std::ldexp(std::frexp((double)std::fabs(f), &e), 24);
-  e -= 24;
-  const uint64_t mi = (uint64_t)m;
+  uint32_t bits;
+  std::memcpy(&bits, &f, 4);
+  const int field = bits >> 23 & 0xFF, e = std::max(field, 1) - 150;
+  const uint64_t mi = (bits & 0x7FFFFF) | (field ? 0x800000u : 0u);
   constexpr uint64_t hi = 0x28BE60DB9391054Aull, lo = 0x7F09D5F47D4D3770ull;
   unsigned __int128 t = (unsigned __int128)mi * hi + (((unsigned __int128)mi * lo) >> 64);
   if (mi == 0 || -e >= 120) return 0;

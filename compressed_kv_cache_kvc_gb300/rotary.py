@@ -20,9 +20,10 @@ def _rows(t, name, device, batch, n, heads, out):
     if t.shape != (batch, heads, n, HEAD_DIM):
         raise ValueError(f"{name} must be [batch, heads, n, 128] = {(batch, heads, n, HEAD_DIM)}, not {tuple(t.shape)}")
     sb, sh, st, sd = t.stride()
-    if sd != 1 or any(s % 8 for s, size in ((sb, batch), (sh, heads), (st, n)) if size > 1) or t.data_ptr() % 16:
+    ptr = t.data_ptr()
+    if (sd != 1 or ptr % 16 or (sb % 8 and batch > 1) or (sh % 8 and heads > 1) or (st % 8 and n > 1)):
         raise ValueError(f"the rows of {name} must be of 128 adjacent values and start on 16-byte boundaries")
-    return L.KvcRows(t.data_ptr(), None if out is None else out.data_ptr(), heads, sb, sh, st)
+    return L.KvcRows(ptr, None if out is None else out.data_ptr(), heads, sb, sh, st)
 
 
 def _out(out, t, name):
