@@ -55,17 +55,19 @@ constexpr int kTileB = kTile * kHeadDim * 2;  // 32 KB, two boxes of 64 dims
 constexpr int kBoxB = kTileB / 2;
 constexpr int kOffQ = 0, kOffK = kOffQ + 2 * kTileB, kOffV = kOffK + 2 * kTileB;
 // a tile's K and V scales and which of its eight 16-token pages count, four tiles deep
-// (a slot is written again when the tile four before is through its softmax)
+// (a slot is written again when the softmax of the tile four before has read it: the
+// scout has a barrier of its own for that, since one that also completes without its
+// scales could complete twice before it looks)
 constexpr int kOffScale = kOffV + 2 * kTileB;  // [4][2][8] f32
 constexpr int kOffMask = kOffScale + 4 * 2 * 8 * 4;
 constexpr int kOffBar = kOffMask + 4 * 4;
 constexpr int kBarQ = 0, kBarK = 1, kBarV = 3, kBarKFree = 5, kBarVFree = 7, kBarS = 9, kBarP = 13, kBarO = 17,
-              kBarScale = 21, kBarDone = 25, kNumBars = 27;  // (S, P, O: 2 x + step parity)
+              kBarScale = 21, kBarDone = 25, kBarScaleFree = 27, kNumBars = 31;  // (S, P, O: 2 x + step parity)
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort flag, the power of two of the V scales
 constexpr int kOffMl = kOffMisc + 32;  // [2][128][2] the rows' maxima and sums
 constexpr int kSmem = kOffMl + 2 * kTile * 8;
 constexpr float kMostSum = 32768.0f;
-constexpr int kAhead = 4;  // tiles whose codes are on their way to L2
+constexpr int kAhead = 1;  // (before the scout's own up to four) tiles whose codes are on their way to L2
 constexpr uint32_t kCols = 512;
 
 __device__ __forceinline__ float group_max(const float* z, float m) {
@@ -117,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = saddr(sm);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(sm + kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + kOffMisc + 4);
-  uint32_t* sh_vmax = reinterpret_cast<uint32_t*>(sm + kOffMisc + 16);
   auto bar = [&](int i) { return base + kOffBar + 8 * i; };
   auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= kBarK && i < kBarKFree) count = kLoadWarps / 2;
       if (i >= kBarKFree && i < kBarS) count = nq;
       if (i >= kBarP && i < kBarO) count = 4;  // (warps of a query tile)
+      if (i >= kBarScaleFree) count = 4 * nq;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(count));
     }
     *abort = 0;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int id = ids[0], next = id_of(i + kAhead + 1);
       fetch(i + kAhead, ids[kAhead]);
       const float sc_next = scale_of(ids[1]);
-      if (i >= 2) wait(kBarKFree + (i & 1), (uint32_t)((i >> 1) & 1) ^ 1u);
+      if (i >= 4) wait(kBarScaleFree + (i & 3), (uint32_t)((i >> 2) & 1) ^ 1u);
       if (!ok) break;
       float* to = reinterpret_cast<float*>(sm + kOffScale) + (i & 3) * 16;
       if (lane < 16) to[lane] = sc * down0 * down1;
@@ -548,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(bar(kBarP + 2 * x + (j & 1)));
+      if (lane == 0) {
+        bar_arrive(bar(kBarP + 2 * x + (j & 1)));
+        if (j & 1) bar_arrive(bar(kBarScaleFree + (i & 3)));
+      }
     }
     if (ok && n_x > 0) wait(kBarO + 2 * x + 1, (uint32_t)((n_x - 1) & 1));
     // through shared memory (32 rows of 512 bytes a warp, over the Q and K tiles, which

@@ -76,6 +76,14 @@ PREFIX = [
     (7, 1, 4100, list(range(0, 40)), 64, "int8", 0.0, False, 2.0),
     (8, 2, 6000, [5 + 13 * i for i in range(33)], 16, "e4m3", 30.0, True, 1.0),
     (8, 1, 900, [3 * i for i in range(70)], 16, "int8", 0.0, True, 1.0),
+    # (many rows of much: the prefix as a product)
+    (7, 1, 8200, list(range(0, 40)), 64, "int8", 0.0, False, 2.0),
+    (8, 1, 4100, [3 * i for i in range(70)], 16, "int8", 0.0, True, 1.0),
+    (10, 2, 6000, [33, 2, 90] * 8, 32, "int8", 20.0, True, 2.0),
+    (16, 16, 2117, [150] * 20, 128, "int8", 4.0, True, 3.0),
+    (12, 6, 1501, [5, 0, 31] * 15, 64, "e4m3", 3.0, False, 6.0),
+    (3, 1, 40000, [1] * 9, 16, "e4m3", 0.0, True, 1.0),
+    (16, 8, 900, [3 * i for i in range(40)], 16, "e4m3", 0.0, False, 1.0),
 ]
 
 
@@ -108,11 +116,33 @@ def test_prefix_against_formula(hq, hkv, prefix, own, block, codes, cap, bias, m
     assert (cache.buffer("TICKETS").view(torch.int32) == 0).all()
 
 
-def test_prefix_values_of_any_size():
+@pytest.mark.parametrize("hq,hkv,batch,prefix", [(32, 32, 2, 9000), (8, 1, 3, 150000), (128, 16, 17, 9000)])
+def test_prefix_long_runs(hq, hkv, batch, prefix):
+    """Many tiles for every CTA, in one stream of rows and in two, call after call."""
+    rng = np.random.default_rng(hq + batch)
+    own = [7 + b for b in range(batch)]
+    cache = _cache(hq, hkv, [prefix] + own, 32, "int8")
+    kv = [(_bits(rng, (hkv, n, 128)), _bits(rng, (hkv, n, 128))) for n in [prefix] + own]
+    _fill(cache, kv)
+    q = _bits(rng, (batch, hq, 128), 1.5)
+    dq = T.to_dev_bf16(q)
+    first = cache.prefix_attention(dq, 0, seq_begin=1)
+    outs = [cache.prefix_attention(dq, 0, seq_begin=1) for _ in range(20)]
+    assert all(torch.equal(first, o) for o in outs)
+    assert cache.read_status() == 0
+    got = T.bf16_tensor_to_f32(first)
+    for b, j in ((0, 0), (batch - 1, hq - 1), (1, hq // 2)):
+        h = j * hkv // hq
+        kd, vd = (np.concatenate([_held(kv[0][i][h], 32, "int8"), _held(kv[1 + b][i][h], 32, "int8")]) for i in (0, 1))
+        _check(got[b, j], q[b, j], kd, vd, 0.0, 0.0, prefix + own[b] - 1, np.arange(prefix + own[b]))
+
+
+@pytest.mark.parametrize("prefix", [4 + 16 * 40 + 9, 4 + 16 * 480 + 9])
+def test_prefix_values_of_any_size(prefix):
     """V of very different sizes in the prefix's blocks, its exact rows and the
     sequences' own: every value keeps its bits relative to the largest that counts."""
     rng = np.random.default_rng(8)
-    hq, hkv, block, prefix, own = 8, 1, 16, 4 + 16 * 40 + 9, [50, 2, 21] * 12
+    hq, hkv, block, own = 8, 1, 16, [50, 2, 21] * 12
     for big, small in ((1e30, 1e-30), (3e37, 1.0), (1e-30, 1e-36), (1.0, 1e-9)):
         mult = np.full((hkv, prefix, 1), small)
         mult[:, 20:52] = big
@@ -139,19 +169,20 @@ def test_prefix_values_of_any_size():
         assert cache.read_status() == 0
 
 
-def test_prefix_replays_streams_and_slices():
+@pytest.mark.parametrize("hkv,B", [(2, 5), (8, 90)])
+def test_prefix_replays_streams_and_slices(hkv, B):
     """A captured step (append, attention) replayed while the sequences and the
     prefix grow equals the eager calls; another stream; two graphs that share a
     workspace, one after the other."""
     rng = np.random.default_rng(5)
-    hq, hkv, block, B = 8, 2, 16, 5
+    hq, block, few = 8, 16, B // 2
     caches = [_cache(hq, hkv, [2000] + [200] * B, block, "e4m3") for _ in range(2)]
     k, v = (T.to_dev_bf16(_bits(rng, (1, hkv, 1000, 128))) for _ in range(2))
     for c in caches:
         c.append(k, v, seq_begin=0)
     kn, vn, q = (torch.zeros(B, h, *x, 128, device="cuda", dtype=torch.bfloat16)
                  for h, x in ((hkv, (1,)), (hkv, (1,)), (hq, ())))
-    out, other = torch.empty_like(q), torch.empty_like(q[:2])
+    out, other = torch.empty_like(q), torch.empty_like(q[:few])
     c = caches[0]
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -168,7 +199,7 @@ def test_prefix_replays_streams_and_slices():
                 c.append(kn, vn, seq_begin=1)
                 c.prefix_attention(q, 0, seq_begin=1, out=out, workspace=ws)
             else:
-                c.prefix_attention(q[1:3], 0, seq_begin=2, out=other, workspace=ws)
+                c.prefix_attention(q[1:1 + few], 0, seq_begin=2, out=other, workspace=ws)
         graphs.append(g)
     c.sync_host()
     for step in range(45):
@@ -184,7 +215,7 @@ def test_prefix_replays_streams_and_slices():
         want = caches[1].prefix_attention(z, 0, seq_begin=1) if step not in (20, 30) else None
         if want is not None:
             torch.testing.assert_close(out.float(), want.float(), rtol=2 ** -7, atol=1e-3)
-            torch.testing.assert_close(other.float(), want[1:3].float(), rtol=2 ** -7, atol=1e-3)
+            torch.testing.assert_close(other.float(), want[1:1 + few].float(), rtol=2 ** -7, atol=1e-3)
     # nothing left: rows of 0
     c.sync_host()
     c.release(0, B + 1)
@@ -322,6 +353,19 @@ def test_bad_block_ids_are_flagged():
     assert out.isfinite().all() and not ((blocks == 2) | (blocks == 3)).any() and cache.read_status() == 0
     assert cache.selected_attention(q, 100).isfinite().all() and cache.read_status() == 0x2
     assert cache.prefix_attention(q, 0, seq_begin=1).isfinite().all() and cache.read_status() == 0x2
+    cache = _cache(8, 8, [2000] + [30] * 20, 16, "int8")
+    kv = [(_bits(rng, (8, n, 128)), _bits(rng, (8, n, 128))) for n in [2000] + [30] * 20]
+    _fill(cache, kv)
+    table = cache.buffer("TABLE").view(torch.int32)
+    kept = table[2:4].clone()
+    table[2], table[3] = 1 << 20, -5
+    q = _bits(rng, (20, 8, 128))
+    out = cache.prefix_attention(T.to_dev_bf16(q), 0, seq_begin=1)
+    assert out.isfinite().all() and cache.read_status() == 0x2
+    table[2:4] = kept
+    cut = np.r_[0:4 + 32, 4 + 64:2000]  # the two blocks left out
+    kd, vd = (np.concatenate([_held(kv[0][i][3], 16, "int8")[cut], _held(kv[2][i][3], 16, "int8")]) for i in (0, 1))
+    _check(T.bf16_tensor_to_f32(out)[1, 3], q[1, 3], kd, vd, 0.0, 0.0, 0, np.zeros(len(kd)))
 
 
 def test_refusals():
