@@ -530,7 +530,14 @@ kvc_status kvc_block_prefix_attention(kvc_block_cache* c, int32_t prefix, int32_
   if (!d_workspace || !aligned(d_workspace, kAlign) || workspace_bytes < pl.total) return KVC_ERR_INVALID_ARG;
   const int bt = c->cfg.block_tokens, hkv = c->cfg.num_kv_heads, shared = c->pos[prefix];
   const int tiles = (kvc::block_closed(shared, bt) * bt + kvc::kPrefixTile - 1) / kvc::kPrefixTile;
-  const bool product = batch > 1 && tiles > 3;
+  // The product costs a launch and the join of its parts, the other form takes the
+  // prefix's codes from L2 once per sequence (6.9 TB/s).  200 own tokens a sequence:
+  // 8 x 32 heads after 260 / 2,050 / 8,200 tokens direct 10.1 / 15.8 / 29.9, product
+  // 13.8 / 18.5 / 21.5 us; 64 x 32 after 520 / 1,030 direct 22.2 / 31.5, product 23.2 /
+  // 26.0; 4 x 32 of 32 KV heads after 2,050 / 4,100 direct 20.3 / 29.7, product 21.2 /
+  // 25.3.  Two sequences read it faster than it is converted: 2 x 32 of 32 KV heads
+  // after 16,400 direct 49, product 60.
+  const bool product = batch > 2 && (long long)batch * tiles * hkv > 2048;
   const long long front = (kvc::block_exact_rows(shared, bt) + kvc::kPage - 1) / kvc::kPage +
                           (product ? 0LL : (long long)kvc::block_closed(shared, bt) * (bt / kvc::kPage));
   long long units = 0;
