@@ -166,8 +166,11 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
   if (kDirect) {
     direct_nu = units_of(P);
     direct_parts = max(1, min(a.parts, direct_nu / a.part_units));
-    if (direct_nu == 0 && part == 0 && threadIdx.x < G * (kHeadDim / 8))  // (a replayed graph may find a sequence empty)
-      reinterpret_cast<uint4*>(out + ((size_t)bl * s.hq + h * G) * kHeadDim)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    if (direct_nu == 0 && part == 0) {  // (a replayed graph may find a sequence empty)
+      if (threadIdx.x < G * (kHeadDim / 8))
+        reinterpret_cast<uint4*>(out + ((size_t)bl * s.hq + h * G) * kHeadDim)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+      wait_for_previous();  // (this kernel does not end before the one under which it runs)
+    }
     if (direct_nu == 0 || part >= direct_parts) return;
   } else {
     T = (long long)hkv * cum[batch];
