@@ -138,11 +138,79 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(BlockState s
 
 constexpr int kChooseThreads = 512;
 constexpr int kChooseWarps = kChooseThreads / 32;
-constexpr int kKeysStaged = 4096;
+constexpr int kKeysHeld = 8;  // keys a thread holds
+constexpr int kKeysStaged = kKeysHeld * kChooseThreads;
+constexpr int kDigit = 9;  // bits of a digit: a bin per thread
+
+struct ChooseShared {
+  uint2 ends[kChooseWarps];
+  int hist[2][kChooseThreads], sums[2][kChooseWarps], found[2][3];
+};
+
+// A limit for the `want` largest of n keys (0 < want < n), a thread's own
+// (threadIdx.x + 512 k) in `own`: all keys above it are taken, and of those at it the
+// *same first.  Radix select from the highest bit in which the keys differ (a head's
+// scores are of one size: their first digits would all meet in a few bins), until the
+// rest of the want is all of a bin.
+__device__ uint32_t choose_limit(const uint32_t (&own)[kKeysHeld], int n, int want, ChooseShared& sh, int* same) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+  for (int k = 0; k < kKeysHeld; ++k)
+    if (tid + k * kChooseThreads < n) {
+      lo = min(lo, own[k]);
+      hi = max(hi, own[k]);
+    }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) sh.ends[warp] = make_uint2(lo, hi);
+  sh.hist[0][tid] = 0;
+  __syncthreads();
+  const uint2 e = sh.ends[lane & (kChooseWarps - 1)];
+  lo = __reduce_min_sync(0xffffffffu, e.x);
+  hi = __reduce_max_sync(0xffffffffu, e.y);
+  int bits = 32 - __clz(lo ^ hi);  // below these all keys are as v
+  uint32_t v = bits < 32 ? lo >> bits << bits : 0u;
+  for (int round = 0; bits > 0; round ^= 1) {
+    const int shift = max(bits - kDigit, 0);
+    const uint32_t digit = (1u << (bits - shift)) - 1u, rest = bits < 32 ? 0xffffffffu << bits : 0u;
+#pragma unroll
+    for (int k = 0; k < kKeysHeld; ++k)
+      if (tid + k * kChooseThreads < n && ((own[k] ^ v) & rest) == 0) atomicAdd(&sh.hist[round][own[k] >> shift & digit], 1);
+    sh.hist[round ^ 1][tid] = 0;
+    __syncthreads();
+    const int bin = kChooseThreads - 1 - tid, count = sh.hist[round][bin];  // (from the largest on)
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) sh.sums[round][warp] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(0xffffffffu, lane < warp ? sh.sums[round][lane] : 0);
+    if (upto >= want && upto - count < want) {
+      sh.found[round][0] = bin;
+      sh.found[round][1] = want - (upto - count);
+      sh.found[round][2] = count;
+    }
+    __syncthreads();
+    v |= (uint32_t)sh.found[round][0] << shift;
+    want = sh.found[round][1];
+    bits = shift;
+    if (want == sh.found[round][2] && v > 0) {
+      *same = 0;
+      return v - 1;
+    }
+  }
+  *same = want;
+  return v;
+}
 
 __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState s, BlockChoice ch, int seq_begin) {
   __shared__ uint32_t sh_keys[kKeysStaged];
   __shared__ int32_t sh_table[kKeysStaged];
+  __shared__ ChooseShared sh;
   __shared__ int hist[kRadixBins], sh_warp[32], sh_sel[3], sh_more[kChooseWarps], sh_same[kChooseWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pair = blockIdx.x, b = seq_begin + pair / s.hkv, most = ch.top + ch.recent;
@@ -163,14 +231,23 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
   const int n = closed - ch.recent;
   const uint32_t* keys = ch.keys + (size_t)pair * s.max_bps;
   const bool staged = n <= kKeysStaged;
-  if (staged) {
-    for (int i = threadIdx.x; i < n; i += kChooseThreads) sh_keys[i] = __ldcg(keys + i);
-    __syncthreads();
-  }
   auto key = [&](int i) { return staged ? sh_keys[i] : __ldcg(keys + i); };
-  int same_left, ties;
-  const uint32_t limit = radix_select<kChooseThreads>(n, ch.top, true, [](int) { return true; }, key, hist, sh_warp, sh_sel,
-                                                      &same_left, &ties);
+  int same_left;
+  uint32_t limit;
+  if (staged) {
+    uint32_t own[kKeysHeld];
+#pragma unroll
+    for (int k = 0; k < kKeysHeld; ++k) {
+      const int i = threadIdx.x + k * kChooseThreads;
+      own[k] = i < n ? __ldcg(keys + i) : 0u;
+      if (i < n) sh_keys[i] = own[k];
+    }
+    limit = choose_limit(own, n, ch.top, sh, &same_left);
+  } else {
+    int ties;
+    limit = radix_select<kChooseThreads>(n, ch.top, true, [](int) { return true; }, key, hist, sh_warp, sh_sel, &same_left,
+                                         &ties);
+  }
   // a warp has a run of blocks: those above the limit, and at it
   const int run = ((n + kChooseWarps - 1) / kChooseWarps + 31) / 32 * 32;
   const int lo = min(warp * run, n), hi = min(lo + run, n);
