@@ -52,8 +52,9 @@ struct BlockAttn {
   ScoreMod mod;
   float qk_scale_log2;
   int ncta;
-  // the selected form: blocks of every pair in ascending order, `most` places a pair
-  const int32_t* list, *ids;
+  // the selected form: blocks of every pair in ascending order and where they lie in the
+  // pool, `most` places a pair
+  const int32_t *list, *ids;
   int most;
   // the prefix form: the sequence that holds it, whether its pages are among the
   // units; partials of its blocks from elsewhere, `more` of [hkv][batch][group]
@@ -61,8 +62,9 @@ struct BlockAttn {
   const float *more_o, *more_ml;
   int early;       // (those two) launched under the kernel before them
   int part_units;  // (those two) units of a part at least; `parts` of them at most per pair
-  int parts;  // 0: equal runs across pairs; else a CTA takes a part of one pair, and the sequences of a head
-                    // have about this many parts together
+  // 0: equal runs across pairs; else a CTA takes a part of one pair, and the sequences of
+  // a head have about this many parts together
+  int parts;
 };
 
 // The choice of blocks: the top_blocks best of the closed ones but the `recent`

@@ -61,13 +61,25 @@ enum { kPlain = 0, kSelected = 1, kPrefix = 2 };  // forms
 // inside a part.  Two CTAs per SM then, with the registers of two; the equal
 // runs take a full wave of three (168 registers; at 216 and two per SM 16 x 32
 // heads of 4,111 capped tokens 94 against 88 us).
+//
+// The forms of selected blocks and of a prefix always take parts, one CTA each: the
+// pair follows from the CTA's number, nothing is summed over the sequences, and the
+// exact rows go first, under the first pages' copies or the choice of the blocks (with
+// the launches overlapped and the merge without bank conflicts 64 x 32 heads after a
+// prefix of 32,768 tokens 119 -> 73 us, 16 x 32 heads of selected blocks 71 -> 60).
+// 16 x 32 heads with 128 of 2,048 blocks of 32 tokens each: 31 us, 3.7 TB/s, at two or
+// three CTAs per SM and four or six pages of ring alike: blocks of 4 KB in no order,
+// and the round trips and joins that one sequence's 11 us are made of.
+// kPrefix joins the partials of the prefix's product with the pair's own.  Where the
+// pair has one CTA a warp has up to 20 rows of them on their way under the merge of the
+// warps, and nothing goes through memory (64 x 32 heads: 65.6 -> 61.4 us a call).
 constexpr int kBWarps = 4;
 constexpr int kBThreads = kBWarps * 32;
 constexpr int kBStages = 4;
 constexpr int kBStage = 4096;  // K page, V page
 constexpr int kBSmem = kBWarps * kBStages * kBStage;
 constexpr float kBLazy = 4.0f;
-constexpr int kMergeRow = kHeadDim + 4;
+constexpr int kMergeRow = kHeadDim + 4;  // one warp's row of a head before the merge
 constexpr int kJoinRow = kHeadDim + 4;  // one warp's joined row: 128 means, the maximum, the sum
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -99,7 +111,8 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
   constexpr float kOffK = 128.0f * 0x1p-24f, kOffV = 128.0f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int cum[kDirect ? 1 : kMaxCallBatch + 1], len[kDirect ? 1 : kMaxCallBatch];
-  __shared__ int parts[PARTS && !kDirect ? kMaxSplitBatch + 1 : 1];  // (split pairs) parts of a head of the sequences before
+  // (split pairs) parts of a head of the sequences before
+  __shared__ int parts[PARTS && !kDirect ? kMaxSplitBatch + 1 : 1];
   __shared__ int sh_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bt = s.bt, ppb = bt / kPage;  // pages per block
@@ -167,8 +180,8 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     direct_nu = units_of(P);
     direct_parts = max(1, min(a.parts, direct_nu / a.part_units));
     if (direct_nu == 0 && part == 0) {  // (a replayed graph may find a sequence empty)
-      if (threadIdx.x < G * (kHeadDim / 8))
-        reinterpret_cast<uint4*>(out + ((size_t)bl * s.hq + h * G) * kHeadDim)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+      uint4* rows = reinterpret_cast<uint4*>(out + ((size_t)bl * s.hq + h * G) * kHeadDim);
+      if (threadIdx.x < G * (kHeadDim / 8)) rows[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
       wait_for_previous();  // (this kernel does not end before the one under which it runs)
     }
     if (direct_nu == 0 || part >= direct_parts) return;
@@ -726,9 +739,10 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     auto more_at = [&](int g) { return ((size_t)h * batch + bl) * G + g; };
     auto load_more = [&](int g, int i0) {
 #pragma unroll
-      for (int i = 0; i < kFirstRows; ++i)  // past the end: the last part again, weight 0
-        more_rows[i] = __ldcg(
-            reinterpret_cast<const float4*>(a.more_o + (more_at(g) + min(i0 + i, more - 1) * more_step) * kHeadDim) + lane);
+      for (int i = 0; i < kFirstRows; ++i) {  // past the end: the last part again, weight 0
+        const float* from = a.more_o + (more_at(g) + min(i0 + i, more - 1) * more_step) * kHeadDim;
+        more_rows[i] = __ldcg(reinterpret_cast<const float4*>(from) + lane);
+      }
     };
     auto load_more_ml = [&](int g) {
       if (lane < more) more_ml = __ldcg(reinterpret_cast<const float2*>(a.more_ml) + more_at(g) + lane * more_step);
@@ -745,8 +759,9 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     // alive across the loops they cost 1 us of 90 for 16 x 32 heads of 4,111 tokens)
     const int i_first = PARTS || kDirect ? 0 : cta_of_page(Pf, T, N);
     const int cnt = PARTS || kDirect ? per_pair : cta_of_page(Pf + nu - 1, T, N) - i_first + 1;
-    const long long slot0 = kDirect ? ((long long)bl * hkv + h) * a.parts : PARTS ? Pf : (long long)bl * hkv + h + i_first;
-    const long long slot = kDirect ? slot0 + part : PARTS ? F : (long long)bl * hkv + h + cta;
+    const long long pair = (long long)bl * hkv + h;
+    const long long slot0 = kDirect ? pair * a.parts : PARTS ? Pf : pair + i_first;
+    const long long slot = kDirect ? slot0 + part : PARTS ? F : pair + cta;
     const int d = threadIdx.x;  // 128 threads = head_dim
     uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
     float* sm_own = sm_o + kBWarps * kMaxGroup * kMergeRow + kBWarps;  // (quick) [8][kMergeRow]: o, M, l

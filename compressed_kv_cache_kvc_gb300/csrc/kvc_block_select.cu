@@ -12,10 +12,16 @@
 // the same bits wherever they are computed, and the choice (ties to the lower
 // block) is too.
 //
-// block_score_kernel: 256 bytes of bounds per block and KV head, integer dot
-// products of four (dp4a); four lanes a block, so that a load instruction takes
-// 64 bytes of each of eight blocks.  block_choose_kernel: one CTA per (sequence, KV
-// head): radix select of the top_blocks-th key, then the blocks in ascending order.
+// block_score_kernel: 264 bytes of bounds per block and KV head: bound by DRAM (16 x 8
+// KV heads of 65,536 tokens in blocks of 32, 69 MB: 11.5 us, 6.0 TB/s).  Integer
+// matrix instructions, 16 blocks on M, the group's query rows on N, 256 codes on K,
+// fed from registers: four lanes a block, so that a load instruction takes 64 bytes of
+// each of eight blocks (with dot products of four codes and the query rows in shared
+// memory 17 us; all KV heads of a block in one CTA, 2 KB in a run, 22).
+// block_choose_kernel: one CTA per (sequence, KV head): the top_blocks-th key, then the
+// blocks in ascending order, and their places in the pool beside (128 pairs 6.3 us, 8
+// pairs 5: barriers).  The attention over them runs block_attn_kernel's form kSelected;
+// each of the three is launched under the one before it.
 #include "kvc_block_attn.h"
 
 namespace kvc {
@@ -176,7 +182,8 @@ __device__ uint32_t choose_limit(const uint32_t (&own)[kKeysHeld], int n, int wa
     const uint32_t digit = (1u << (bits - shift)) - 1u, rest = bits < 32 ? 0xffffffffu << bits : 0u;
 #pragma unroll
     for (int k = 0; k < kKeysHeld; ++k)
-      if (tid + k * kChooseThreads < n && ((own[k] ^ v) & rest) == 0) atomicAdd(&sh.hist[round][own[k] >> shift & digit], 1);
+      if (tid + k * kChooseThreads < n && ((own[k] ^ v) & rest) == 0)
+        atomicAdd(&sh.hist[round][own[k] >> shift & digit], 1);
     sh.hist[round ^ 1][tid] = 0;
     __syncthreads();
     const int bin = kChooseThreads - 1 - tid, count = sh.hist[round][bin];  // (from the largest on)
@@ -245,8 +252,8 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
     limit = choose_limit(own, n, ch.top, sh, &same_left);
   } else {
     int ties;
-    limit = radix_select<kChooseThreads>(n, ch.top, true, [](int) { return true; }, key, hist, sh_warp, sh_sel, &same_left,
-                                         &ties);
+    limit = radix_select<kChooseThreads>(n, ch.top, true, [](int) { return true; }, key, hist, sh_warp, sh_sel,
+                                         &same_left, &ties);
   }
   // a warp has a run of blocks: those above the limit, and at it
   const int run = ((n + kChooseWarps - 1) / kChooseWarps + 31) / 32 * 32;
@@ -292,7 +299,7 @@ cudaError_t launch_block_choice(const BlockState& s, const KeyBounds& bounds, co
                                 int batch, int longest, const uint16_t* q, cudaStream_t st) {
   const int pairs = batch * s.hkv, n = block_closed(longest, s.bt) - ch.recent;
   const int steps = (n + kScoreStep - 1) / kScoreStep;
-  // (a graph replayed at longer sequences takes more steps a CTA)
+  // one wave of CTAs (a graph replayed at longer sequences takes more steps a CTA)
   const int chunks = std::max(1, std::min(steps, kScoreCtas / pairs));
   block_score_kernel<<<pairs * chunks, kScoreThreads, 0, st>>>(s, bounds, ch, seq_begin, chunks, q);
   cudaError_t e = cudaGetLastError();

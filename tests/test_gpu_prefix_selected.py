@@ -116,7 +116,8 @@ def test_prefix_against_formula(hq, hkv, prefix, own, block, codes, cap, bias, m
     assert (cache.buffer("TICKETS").view(torch.int32) == 0).all()
 
 
-@pytest.mark.parametrize("hq,hkv,batch,prefix", [(32, 32, 2, 9000), (8, 1, 3, 150000), (128, 16, 17, 9000)])
+@pytest.mark.parametrize("hq,hkv,batch,prefix", [(32, 32, 5, 9000), (8, 1, 3, 150000), (128, 16, 17, 9000),
+                                                 (32, 16, 13, 15669), (96, 32, 5, 7035), (24, 8, 33, 36883)])
 def test_prefix_long_runs(hq, hkv, batch, prefix):
     """Many tiles for every CTA, in one stream of rows and in two, call after call."""
     rng = np.random.default_rng(hq + batch)
@@ -126,10 +127,12 @@ def test_prefix_long_runs(hq, hkv, batch, prefix):
     _fill(cache, kv)
     q = _bits(rng, (batch, hq, 128), 1.5)
     dq = T.to_dev_bf16(q)
-    first = cache.prefix_attention(dq, 0, seq_begin=1)
-    outs = [cache.prefix_attention(dq, 0, seq_begin=1) for _ in range(20)]
-    assert all(torch.equal(first, o) for o in outs)
-    assert cache.read_status() == 0
+    slopes = _slopes(hq)
+    for bias in (slopes, None):  # (the two streams of a CTA do not keep step)
+        first = cache.prefix_attention(dq, 0, seq_begin=1, slopes=bias)
+        outs = [cache.prefix_attention(dq, 0, seq_begin=1, slopes=bias) for _ in range(300)]
+        assert all(torch.equal(first, o) for o in outs)
+        assert cache.read_status() == 0
     got = T.bf16_tensor_to_f32(first)
     for b, j in ((0, 0), (batch - 1, hq - 1), (1, hq // 2)):
         h = j * hkv // hq
