@@ -11,7 +11,7 @@ import torch
 from . import _lib as L
 from .cache import HEAD_DIM, _current_device, _need, _stream_ptr
 from .prompt import _ptr, _slopes, prompt_attention
-from .rotary import Rotary, _out, _rows
+from .rotary import Rotary, _first, _out, _rows
 
 
 class BlockScaledCache:
@@ -150,7 +150,8 @@ class BlockScaledCache:
             if rq.d_out == rq.d_in and not q.is_contiguous():
                 raise ValueError("out may be q only where q is packed")
         self._call("kvc_block_append_rotary", seq_begin, batch, n, ctypes.byref(rotary.plan),
-                   ctypes.byref(rq) if rq is not None else None, ctypes.byref(rk), ctypes.byref(rv), pos, first)
+                   ctypes.byref(rq) if rq is not None else None, ctypes.byref(rk), ctypes.byref(rv), pos,
+                   _first(first))
         return out if q is not None else None
 
     def _attention_args(self, q, out, slopes, sm_scale):

@@ -401,6 +401,9 @@ kvc_status kvc_block_append_rotary(kvc_block_cache* c, int32_t seq_begin, int32_
   if (st != KVC_OK) return st;
   if (k->heads != c->cfg.num_kv_heads || v->heads != c->cfg.num_kv_heads || (q && q->heads != c->cfg.num_q_heads))
     return KVC_ERR_INVALID_ARG;
+  if (!d_positions)
+    for (int i = 0; i < batch; ++i)
+      if ((int64_t)first + c->pos[seq_begin + i] + n_new - 1 > INT32_MAX) return KVC_ERR_INVALID_ARG;
   if (!has_room(c, seq_begin, batch, n_new)) return KVC_ERR_CAPACITY;
   a.batch = batch;
   a.n = n_new;

@@ -12,16 +12,16 @@
 // the same bits wherever they are computed, and the choice (ties to the lower
 // block) is too.
 //
-// block_score_kernel: 264 bytes of bounds per block and KV head: bound by DRAM (16 x 8
-// KV heads of 65,536 tokens in blocks of 32, 69 MB: 11.5 us, 6.0 TB/s).  Integer
-// matrix instructions, 16 blocks on M, the group's query rows on N, 256 codes on K,
+// block_score_kernel: 260 bytes of bounds per block and KV head: 16 x 8 KV heads of up to
+// 65,536 tokens in blocks of 32, 48 MB: 11.5 us, 4.2 TB/s, the integer matrix pipe 46 %
+// busy (a group of 4 fills half of N).  Integer matrix instructions, 16 blocks on M, the group's query rows on N, 256 codes on K,
 // fed from registers: four lanes a block, so that a load instruction takes 64 bytes of
 // each of eight blocks (with dot products of four codes and the query rows in shared
 // memory 17 us; all KV heads of a block in one CTA, 2 KB in a run, 22).
 // block_choose_kernel: one CTA per (sequence, KV head): the top_blocks-th key, then the
 // blocks in ascending order, and their places in the pool beside (128 pairs 6.3 us, 8
-// pairs 5: barriers).  The attention over them runs block_attn_kernel's form kSelected;
-// each of the three is launched under the one before it.
+// pairs 5: barriers).  The attention over them runs block_attn_kernel's form kSelected.
+// The second and the third are launched under the one before.
 #include "kvc_block_attn.h"
 
 namespace kvc {

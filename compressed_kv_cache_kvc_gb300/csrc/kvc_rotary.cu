@@ -1,7 +1,7 @@
 // Queries and keys rotated by their positions, outside any cache.
 //
 // Per row 256 bytes in, 256 out and 128 values turned: bound by DRAM (4 x 40 heads x
-// 4,099 tokens 60.4 us a call, 5.6 TB/s, 82 % of a copy's rate; one token of 40 heads
+// 4,099 tokens 60.4 us a call, 5.6 TB/s, 82 % of a copy's rate; one token of 16 heads
 // 4.5 us, the host's 16 before it).  The angles of a token serve all of its heads,
 // so a warp takes four tokens (eight lanes a row) and goes through heads with them in
 // registers, four rows of each lane in flight.

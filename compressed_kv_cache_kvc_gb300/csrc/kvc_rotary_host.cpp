@@ -65,7 +65,7 @@ kvc_status rows_in(const kvc_rows* r, int32_t batch, int32_t n, bool out, RowsIn
 
 extern "C" kvc_status kvc_rotary_rotate(const kvc_rotary* rotary, int32_t batch, int32_t n, const kvc_rows* q,
                                         const kvc_rows* k, const int32_t* d_positions, int32_t first, void* stream) {
-  if (batch <= 0 || n <= 0) return KVC_ERR_INVALID_ARG;
+  if (batch <= 0 || n <= 0 || (!d_positions && (int64_t)first + n - 1 > INT32_MAX)) return KVC_ERR_INVALID_ARG;
   kvc::RotaryArgs a{};
   kvc_status st = kvc::rotary_table(rotary, d_positions, first, &a.table);
   if (st == KVC_OK) st = kvc::rows_in(q, batch, n, true, &a.q);

@@ -26,6 +26,12 @@ def _rows(t, name, device, batch, n, heads, out):
     return L.KvcRows(ptr, None if out is None else out.data_ptr(), heads, sb, sh, st)
 
 
+def _first(first):
+    if not -1 << 31 <= first < 1 << 31:
+        raise ValueError("first must be a 32-bit position")
+    return first
+
+
 def _out(out, t, name):
     """The packed output of rows t: `out`, or a new tensor."""
     if out is None:
@@ -103,7 +109,7 @@ class Rotary:
             if k_out.data_ptr() == k.data_ptr() and not k.is_contiguous():
                 raise ValueError("k_out may be k only where k is packed")
         args = (ctypes.byref(self.plan), batch, n, ctypes.byref(rq), ctypes.byref(rk) if rk is not None else None, pos,
-                first)
+                _first(first))
         if _current_device() == dev.index:
             st = L.lib().kvc_rotary_rotate(*args, _stream_ptr())
         else:

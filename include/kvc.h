@@ -586,8 +586,9 @@ typedef struct {
  * d_out may be d_in where that is packed; nothing else overlaps.  One launch.
  * Errors, before any launch: KVC_ERR_INVALID_ARG for sizes that are not positive, a
  * null or misaligned pointer or stride, an in-place call on rows that are not
- * packed, a frequency that is not finite or beyond 65536, an axis out of range;
- * KVC_ERR_UNSUPPORTED for another rotary_dim. */
+ * packed, a frequency that is not finite or beyond 65536, an axis out of range,
+ * positions counted from `first` that leave 32 bits; KVC_ERR_UNSUPPORTED for
+ * another rotary_dim. */
 kvc_status kvc_rotary_rotate(const kvc_rotary* rotary, int32_t batch, int32_t n, const kvc_rows* q, const kvc_rows* k,
                              const int32_t* d_positions, int32_t first, void* stream);
 
@@ -743,9 +744,12 @@ kvc_status kvc_block_selected_attention(kvc_block_cache* cache, int32_t seq_begi
  * follow them (token i of a sequence that comes after Pp tokens of the prefix is
  * at position Pp + i for the distances of the transform; kvc_block_append_rotary
  * with first = Pp for the rotation).
- *   d_workspace: kvc_block_prefix_workspace_bytes(cache, batch) bytes.
- * A sequence, or the prefix, may be empty (rows that see nothing at all are
- * refused, 0 in a replay).  Replays, order and errors as kvc_block_attention, and
+ *   d_workspace: kvc_block_prefix_workspace_bytes(cache, batch) bytes, 256-byte
+ *   aligned.
+ * One launch, two where a long prefix serves several sequences (its closed blocks
+ * are then one matrix product for all of them).  A sequence, or the prefix, may be
+ * empty (rows that see nothing at all are refused, 0 in a replay).  Replays (at any
+ * lengths of the prefix too), order and errors as kvc_block_attention, and
  * KVC_ERR_INVALID_ARG for a prefix outside the cache or inside the slice. */
 size_t kvc_block_prefix_workspace_bytes(const kvc_block_cache* cache, int32_t batch);
 kvc_status kvc_block_prefix_attention(kvc_block_cache* cache, int32_t prefix, int32_t seq_begin, int32_t batch,

@@ -261,7 +261,8 @@ def test_refused():
                  lambda: rot.rotate(q, positions=pos[:, :4].contiguous()), lambda: two.rotate(q, positions=pos),
                  lambda: rot.rotate(q, out=q[:1]), lambda: rot.rotate(q.cpu()), lambda: rot.rotate(q[:0]),
                  lambda: rot.rotate(q, q[:1]), lambda: rot.rotate(_rows(0, 2, 4, 8, 132)[..., :128]),
-                 lambda: rot.rotate(q.transpose(0, 1), out=q.transpose(0, 1))):
+                 lambda: rot.rotate(q.transpose(0, 1), out=q.transpose(0, 1)), lambda: rot.rotate(q, first=1 << 31),
+                 lambda: rot.rotate(q, first=-(1 << 31) - 1)):
         with pytest.raises(ValueError):
             call()
     c = _cache(4, 2, [20] * 2, 16, "int8")

@@ -89,6 +89,12 @@ def test_append_rotary_refuses(lib):
     for kw in (dict(begin=-1), dict(begin=1), dict(batch=0), dict(n_new=-1), dict(p=None), dict(heads=(2, 2, 2)),
                dict(heads=(4, 1, 2)), dict(heads=(4, 2, 4)), dict(k_in=None), dict(k_in=room + 2)):
         assert call(**kw) == bad, kw
+    for first in (2 ** 31 - 8, 2 ** 31 - 1):  # the last of eight positions has 32 bits at most
+        r = [lib.KvcRows(room, room + 32768, m, 8192, 1024, 128) for m in (4, 2, 2)]
+        got = L.kvc_block_append_rotary(h, 0, 1, 9, ctypes.byref(plan), None, ctypes.byref(r[1]), ctypes.byref(r[2]), None,
+                                        first, None)
+        assert got == bad
+        assert L.kvc_rotary_rotate(ctypes.byref(plan), 2, 9, ctypes.byref(r[0]), None, None, first, None) == bad
     assert call(n_new=36) == lib.KVC_ERR_CAPACITY and call(batch=1, n_new=52) == lib.KVC_ERR_CAPACITY
     assert call(n_new=0) == lib.KVC_OK
     assert L.kvc_block_append_rotary(None, 0, 1, 1, None, None, None, None, None, 0, None) == bad
