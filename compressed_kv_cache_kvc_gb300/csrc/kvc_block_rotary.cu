@@ -48,8 +48,10 @@ constexpr int kTableRows = kUnitRows + kSinks;   // (the exact rows: at most 4 +
 constexpr int kTableRow = kRotPairs * 8;
 constexpr int kOffTable = kWarps * kStages * kStage;
 constexpr int kSmem = kOffTable + kTableRows * kTableRow;
-// rows of queries from which they are turned by a launch of their own beside the
-// append's (168 us for 8 x 32 heads x 8,192 tokens, at DRAM's rate)
+// rows of queries from which they are turned by a launch of their own before the
+// append's, which starts under it (1 x 32 heads x 512 / 1,024 / 8,192 tokens 25.2 / 29.3
+// / 55.9 us in the append's CTAs, 26.2 / 27.3 / 53.9 apart; 64 x 8 x 41 31.4 both, for a
+// launch more)
 constexpr long long kManyQueryRows = 1 << 15;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {

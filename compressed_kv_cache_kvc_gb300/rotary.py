@@ -35,7 +35,7 @@ def _first(first):
 def _out(out, t, name):
     """The packed output of rows t: `out`, or a new tensor."""
     if out is None:
-        return torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+        return torch.empty_like(t, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
     _need(out, torch.bfloat16, name, t.device, t.shape)
     return out
 
@@ -90,9 +90,10 @@ class Rotary:
         if stream is not None:
             with torch.cuda.stream(stream):  # (what is allocated below belongs to that stream)
                 return self.rotate(q, k, positions=positions, first=first, out=out, k_out=k_out)
-        for t, name in ((q, "q"), (k, "k")):
-            if (t is not None or name == "q") and (not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.numel()):
-                raise ValueError(f"{name} must be [batch, heads, n, 128]")
+        if not isinstance(q, torch.Tensor) or q.dim() != 4 or not q.numel():
+            raise ValueError("q must be [batch, heads, n, 128]")
+        if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4 or not k.numel()):
+            raise ValueError("k must be [batch, heads, n, 128]")
         batch, hq, n, _ = q.shape
         dev = q.device
         if not q.is_cuda:
