@@ -7,9 +7,9 @@
 // it is quantised, 8 x 8 heads x 8,192 tokens took 203 us where the plain append takes
 // 78.  So the work is units of 128 body rows (128 / bt blocks) of one sequence for
 // some of its KV heads: the CTA (one per SM) makes a table of the rows' cosines and
-// sines in shared memory, 512 bytes a row, and two groups of eight warps go through the
-// unit's (head, K or V) pairs with it, a warp 16 rows of each, the rows of the next ones
-// on their way (cp.async, two stages).  The rows that stay exact (sinks, the
+// sines in shared memory, 512 bytes a row, and two groups of eight warps (more of fewer,
+// where an append has few rows) go through the unit's (head, K or V) pairs with it, a
+// warp 16 rows of each, the rows of the next ones on their way (cp.async, two stages).  The rows that stay exact (sinks, the
 // block that stays open) follow at the end of the sequence's first unit, once its
 // tiles, which may hold rows of the open block so far, are in shared memory.
 //
@@ -40,8 +40,7 @@ using namespace quant;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroupWarps = 8;
-constexpr int kUnitRows = 16 * kGroupWarps;
+constexpr int kUnitRows = 128;  // of a unit at most
 constexpr int kStages = 2;
 constexpr int kStage = 16 * kHeadDim * 2 + 128;  // a warp's rows, and a lane's copy of the block's id
 constexpr int kTableRows = kUnitRows + kSinks;   // (the exact rows: at most 4 + 127)
@@ -71,9 +70,11 @@ struct RotaryAppend {
   int splits;      // warps that share a query row's heads
   int tiles;       // units of a sequence and share of its heads
   int shares;      // shares of the KV heads
+  int group;       // warps that have a (head, K or V) together, 16 rows each
 };
 
-template <bool FP8, bool BOUNDS>
+// FULL: groups of eight warps
+template <bool FP8, bool BOUNDS, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1)
     append_rotary_kernel(BlockState s, int seq_begin, const __grid_constant__ RotaryAppend a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -117,9 +118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const bool ok = sh_bad == 0;  // the same for every CTA
   if (ok) {
-    const int group = warp / kGroupWarps, gw = warp % kGroupWarps;
-    const int wpb = bt / 16, w0 = gw & ~(wpb - 1);  // warps per block, the block's first of the group
-    const int block_bar = 1 + 4 * group + w0 / 2;   // (blocks of one warp need none)
+    const int gsz = FULL ? kUnitRows / 16 : a.group, groups = kWarps / gsz, group = warp / gsz, gw = warp % gsz, unit_rows = 16 * gsz;
+    const int wpb = bt / 16, w0 = gw & ~(wpb - 1);     // warps per block, the block's first of the group
+    const int block_bar = 1 + (group * gsz + w0) / 2;  // (blocks of one warp need none)
     const size_t exact_rows = kSinks + bt;
     const bool adjacent = a.rot.table.adjacent != 0;
     const int cl = lane & 7, ca = rotary::chunk_a(a.rot.table, cl), cb = rotary::chunk_b(a.rot.table, cl);
@@ -153,12 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto live_rows = [&](const Unit& t) {  // body rows of the unit's tile
       const int P = held[t.bl];
       const long long rows = (long long)(closed_at(P + n_new) - closed_at(P)) << sh;
-      return (int)max(0LL, min(rows - (long long)t.x * kUnitRows, (long long)kUnitRows));
+      return (int)max(0LL, min(rows - (long long)t.x * unit_rows, (long long)unit_rows));
     };
-    // item q of a unit: (h0 + q / 2, K or V); a group takes every other head, of a
-    // single one K or V
+    // item q of a unit: (h0 + q / 2, K or V); the groups take heads in turn, of fewer
+    // heads than groups K and V
     auto items = [&](const Unit& t) { return 2 * (t.h1 - t.h0); };
-    auto mine = [&](const Unit& t, int q) { return (t.h1 - t.h0 == 1 ? q & 1 : (q >> 1) & 1) == group; };
+    auto mine = [&](const Unit& t, int q) {
+      return (t.h1 - t.h0 < groups ? q : q >> 1) % groups == group;
+    };
 
     // the copies of the group's next item
     uint8_t* ring = smem + warp * kStages * kStage;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue = [&]() {
       if (nu.u < units) {
         const int P = held[nu.bl], c0 = closed_at(P), h = nu.h0 + (nq >> 1), kv = nq & 1;
-        const int row0 = nu.x * kUnitRows + gw * 16;
+        const int row0 = nu.x * unit_rows + gw * 16;
         if (16 * gw < live_rows(nu)) {
           const int p0 = kSinks + (c0 << sh) + row0 + (lane >> 4);  // the lane's first row
           const ptrdiff_t step = step_in(kv);
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_of(u);
       const int bl = t.bl, P = held[bl], c0 = closed_at(P), nb = closed_at(P + n_new) - c0, live = live_rows(t);
-      const int p_tile = kSinks + (c0 << sh) + t.x * kUnitRows;
+      const int p_tile = kSinks + (c0 << sh) + t.x * unit_rows;
       if (live > 0) {
         make_table(bl, live, [&](int r) { return p_tile + r >= P ? p_tile + r - P : -1; });
         __syncthreads();
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (wpb > 1) {
             if (lane == 0) sh_amax[flip][warp] = amax;
             bar_sync(block_bar, 32 * wpb);
-            for (int i = w0; i < w0 + wpb; ++i) amax = fmaxf(amax, sh_amax[flip][group * kGroupWarps + i]);
+            for (int i = w0; i < w0 + wpb; ++i) amax = fmaxf(amax, sh_amax[flip][group * gsz + i]);
             flip ^= 1;  // the next maxima go beside these, which a slower warp may still read
           }
           const float scale = __fdiv_rn(amax, FP8 ? 448.0f : 127.0f);
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (in_block == 0 && lane == 0) {
             (kv ? s.v_scale : s.k_scale)[hblk] = scale;
             if (h == 0 && kv == 0)
-              s.table[(size_t)(seq_begin + bl) * s.max_bps + c0 + ((t.x * kUnitRows + 16 * gw) >> sh)] = blk;
+              s.table[(size_t)(seq_begin + bl) * s.max_bps + c0 + ((t.x * unit_rows + 16 * gw) >> sh)] = blk;
           }
           if (BOUNDS && kv == 0) {
             if (wpb > 1) {  // the block's warps meet in the places of their rows, which they have read
@@ -435,10 +438,10 @@ __global__ void __launch_bounds__(256) append_queries_kernel(BlockState s, int s
                       [&](int b) { return s.seq_pos[seq_begin + b]; });
 }
 
-template <bool FP8, bool BOUNDS>
-cudaError_t launch(const BlockState& s, int seq_begin, const RotaryAppend& a, bool early, cudaStream_t st) {
+template <bool FP8, bool BOUNDS, bool FULL>
+cudaError_t launch_t(const BlockState& s, int seq_begin, const RotaryAppend& a, bool early, cudaStream_t st) {
   static int done[64] = {0};
-  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(append_rotary_kernel<FP8, BOUNDS>), kSmem, done);
+  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(append_rotary_kernel<FP8, BOUNDS, FULL>), kSmem, done);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -455,7 +458,13 @@ cudaError_t launch(const BlockState& s, int seq_begin, const RotaryAppend& a, bo
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, append_rotary_kernel<FP8, BOUNDS>, s, seq_begin, a);
+  return cudaLaunchKernelEx(&cfg, append_rotary_kernel<FP8, BOUNDS, FULL>, s, seq_begin, a);
+}
+
+template <bool FP8, bool BOUNDS>
+cudaError_t launch(const BlockState& s, int seq_begin, const RotaryAppend& a, bool early, cudaStream_t st) {
+  return a.group == kUnitRows / 16 ? launch_t<FP8, BOUNDS, true>(s, seq_begin, a, early, st)
+                                   : launch_t<FP8, BOUNDS, false>(s, seq_begin, a, early, st);
 }
 
 }  // namespace
@@ -483,7 +492,7 @@ int block_append_rotary_launches(const RotaryArgs& rot) {
 
 cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bounds, int seq_begin,
                                        const RotaryArgs& rot, const RowsIn& v, cudaStream_t st) {
-  RotaryAppend a{rot, v, bounds, 1, 1, 1};
+  RotaryAppend a{rot, v, bounds, 1, 1, 1, 1};
   const bool apart = block_append_rotary_launches(rot) > 1;
   const long long rows = (long long)rot.batch * rot.n;
   if (rot.hq > 0) a.splits = rotary_splits(rows, rot.hq);
@@ -496,7 +505,11 @@ cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bou
   }
   // rows of the most blocks an append of n tokens completes (at any state)
   const long long body = ((long long)rot.n + s.bt - 1) / s.bt * s.bt;
-  a.tiles = (int)((body + kUnitRows - 1) / kUnitRows);
+  // few rows: more groups of fewer warps (64 x 41 tokens of
+  // 8 heads 24.6 us with eight warps, 22.5)
+  a.group = kUnitRows / 16;
+  while (a.group > s.bt / 16 && 8 * a.group >= body) a.group /= 2;
+  a.tiles = (int)((body + 16 * a.group - 1) / (16 * a.group));
   a.shares = head_shares((long long)rot.batch * a.tiles, s.hkv);
   const bool kept = bounds.codes != nullptr;
   if (s.fp8) return kept ? launch<true, true>(s, seq_begin, a, apart, st) : launch<true, false>(s, seq_begin, a, apart, st);
