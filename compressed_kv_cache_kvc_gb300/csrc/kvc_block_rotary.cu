@@ -47,10 +47,9 @@ constexpr int kTableRows = kUnitRows + kSinks;   // (the exact rows: at most 4 +
 constexpr int kTableRow = kRotPairs * 8;
 constexpr int kOffTable = kWarps * kStages * kStage;
 constexpr int kSmem = kOffTable + kTableRows * kTableRow;
-// rows of queries from which they are turned by a launch of their own before the
-// append's, which starts under it (1 x 32 heads x 512 / 1,024 / 8,192 tokens 25.2 / 29.3
-// / 55.9 us in the append's CTAs, 26.2 / 27.3 / 53.9 apart; 64 x 8 x 41 31.4 both, for a
-// launch more)
+// rows of queries from which they are turned by a launch of their own (1 x 32 heads x
+// 512 / 1,024 / 8,192 tokens 25.2 / 29.3 / 55.9 us in the append's CTAs, 26.2 / 27.3 /
+// 53.9 apart, before the append; 64 x 8 x 41 31.4 both, for a launch more)
 constexpr long long kManyQueryRows = 1 << 15;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -71,7 +70,31 @@ struct RotaryAppend {
   int tiles;       // units of a sequence and share of its heads
   int shares;      // shares of the KV heads
   int group;       // warps that have a (head, K or V) together, 16 rows each
+  int advance;     // the lengths and the stack too (else the queries' launch does)
 };
+
+// The last CTA's step, by one warp: the lengths and the stack of free blocks.
+__device__ void advance(const BlockState& s, int seq_begin, int batch, int n_new) {
+  const int lane = threadIdx.x & 31, top = s.counters[kCtrFreeTop];
+  int total = 0, bad = 0;
+  for (int i = lane; i < batch; i += 32) {
+    const int P = s.seq_pos[seq_begin + i], c1 = block_closed(P + n_new, s.bt);
+    total += c1 - block_closed(P, s.bt);
+    bad |= c1 > s.max_bps;
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  bad = __any_sync(0xffffffffu, bad);
+  const int flags = (bad ? kDevTableOverflow : 0) | (total > top || top > s.num_blocks ? kDevOutOfBlocks : 0);
+  if (flags == 0)
+    for (int i = lane; i < batch; i += 32) s.seq_pos[seq_begin + i] += n_new;
+  if (lane == 0) {
+    s.tickets[s.max_batch * s.hkv] = 0;
+    if (flags == 0)
+      s.counters[kCtrFreeTop] = top - total;
+    else
+      atomicOr(&s.counters[kCtrStatus], flags);
+  }
+}
 
 // FULL: groups of eight warps
 template <bool FP8, bool BOUNDS, bool FULL>
@@ -86,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = s.hkv, bt = s.bt, sh = __ffs(bt) - 1, batch = a.rot.batch, n_new = a.rot.n;
   const int top = s.counters[kCtrFreeTop];
+  launch_dependents();
   if (tid < kRotPairs) {
     sh_turns[tid] = a.rot.table.turns[tid];
     sh_axis[tid] = a.rot.table.axis[tid];
@@ -398,48 +422,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.rot.hq > 0) {
       const long long n_q = ((long long)batch * n_new + 3) / 4 * a.splits;
       for (long long k = (long long)blockIdx.x * kWarps + warp; k < n_q; k += (long long)gridDim.x * kWarps)
-        rotary::rotate_unit(a.rot, sh_turns, sh_axis, k, a.splits, [&](int b) { return held[b]; });
+        rotary::rotate_unit<4>(a.rot, sh_turns, sh_axis, k, a.splits, [&](int b) { return held[b]; });
     }
   }
-  // the last CTA advances the lengths and the stack (every CTA has read them, and so
-  // has the queries' launch)
-  wait_for_previous();
+  if (!a.advance) return;
+  // the last CTA advances the lengths and the stack (every CTA has read them)
   __syncthreads();
-  int32_t* ticket = s.tickets + s.max_batch * hkv;
   if (tid == 0) {
     __threadfence();
-    sh_last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+    sh_last = atomicAdd(s.tickets + s.max_batch * hkv, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
-  if (!sh_last) return;
-  if (ok)
-    for (int i = tid; i < batch; i += kThreads) s.seq_pos[seq_begin + i] += n_new;
-  if (tid == 0) {
-    *ticket = 0;
-    if (ok)
-      s.counters[kCtrFreeTop] = top - sh_total;
-    else
-      atomicOr(&s.counters[kCtrStatus], sh_bad);
-  }
+  if (sh_last && warp == 0) advance(s, seq_begin, batch, n_new);
 }
 
-// The queries of a long append (positions counted from what the sequences hold).
-__global__ void __launch_bounds__(256) append_queries_kernel(BlockState s, int seq_begin,
-                                                             const __grid_constant__ RotaryArgs a, int splits) {
+// The queries of a long append (positions counted from what the sequences hold), started
+// under the append, which is bound by issue where they are by DRAM: a CTA of four warps
+// with 64 registers, three rows of a lane in flight, fits beside the append's, more of
+// them come as those end (before the append, with all of an SM, and the append under
+// their end: 8 x 32 heads on 8 x 8,192 tokens with release and read-back 380 us, 4 x 32
+// x 4,001 E4M3 287; so 378 and 258.  Room for two or three such CTAs, the append's
+// threads kept to 104 or 80 registers, 366 and 273, 361 and 275).  The last one of them
+// advances the lengths.
+constexpr int kQueryThreads = 128;
+__global__ void __launch_bounds__(kQueryThreads, 8)
+    append_queries_kernel(BlockState s, int seq_begin, const __grid_constant__ RotaryArgs a, int splits) {
   __shared__ uint64_t turns[kRotPairs];
   __shared__ uint8_t axis[kRotPairs];
-  launch_dependents();
+  __shared__ int sh_last;
   if (threadIdx.x < kRotPairs) {
     turns[threadIdx.x] = a.table.turns[threadIdx.x];
     axis[threadIdx.x] = a.table.axis[threadIdx.x];
   }
   __syncthreads();
-  rotary::rotate_unit(a, turns, axis, (long long)blockIdx.x * 8 + (threadIdx.x >> 5), splits,
+  rotary::rotate_unit<3>(a, turns, axis, (long long)blockIdx.x * (kQueryThreads / 32) + (threadIdx.x >> 5), splits,
                       [&](int b) { return s.seq_pos[seq_begin + b]; });
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    sh_last = atomicAdd(s.tickets + s.max_batch * s.hkv, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!sh_last || threadIdx.x >= 32) return;
+  wait_for_previous();  // the append
+  advance(s, seq_begin, a.batch, a.n);
 }
 
 template <bool FP8, bool BOUNDS, bool FULL>
-cudaError_t launch_t(const BlockState& s, int seq_begin, const RotaryAppend& a, bool early, cudaStream_t st) {
+cudaError_t launch_t(const BlockState& s, int seq_begin, const RotaryAppend& a, cudaStream_t st) {
   static int done[64] = {0};
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(append_rotary_kernel<FP8, BOUNDS, FULL>), kSmem, done);
   if (e != cudaSuccess) return e;
@@ -448,23 +478,15 @@ cudaError_t launch_t(const BlockState& s, int seq_begin, const RotaryAppend& a, 
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
     sms = 152;
   const long long units = (long long)a.rot.batch * a.tiles * a.shares;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.rot.hq > 0 ? sms : std::min<long long>(units, sms)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, append_rotary_kernel<FP8, BOUNDS, FULL>, s, seq_begin, a);
+  const unsigned grid = (unsigned)(a.rot.hq > 0 ? sms : std::min<long long>(units, sms));
+  append_rotary_kernel<FP8, BOUNDS, FULL><<<grid, kThreads, kSmem, st>>>(s, seq_begin, a);
+  return cudaGetLastError();
 }
 
 template <bool FP8, bool BOUNDS>
-cudaError_t launch(const BlockState& s, int seq_begin, const RotaryAppend& a, bool early, cudaStream_t st) {
-  return a.group == kUnitRows / 16 ? launch_t<FP8, BOUNDS, true>(s, seq_begin, a, early, st)
-                                   : launch_t<FP8, BOUNDS, false>(s, seq_begin, a, early, st);
+cudaError_t launch(const BlockState& s, int seq_begin, const RotaryAppend& a, cudaStream_t st) {
+  return a.group == kUnitRows / 16 ? launch_t<FP8, BOUNDS, true>(s, seq_begin, a, st)
+                                   : launch_t<FP8, BOUNDS, false>(s, seq_begin, a, st);
 }
 
 }  // namespace
@@ -492,28 +514,36 @@ int block_append_rotary_launches(const RotaryArgs& rot) {
 
 cudaError_t launch_block_append_rotary(const BlockState& s, const KeyBounds& bounds, int seq_begin,
                                        const RotaryArgs& rot, const RowsIn& v, cudaStream_t st) {
-  RotaryAppend a{rot, v, bounds, 1, 1, 1, 1};
   const bool apart = block_append_rotary_launches(rot) > 1;
+  RotaryAppend a{rot, v, bounds, 1, 1, 1, 1, !apart};
   const long long rows = (long long)rot.batch * rot.n;
   if (rot.hq > 0) a.splits = rotary_splits(rows, rot.hq);
-  if (apart) {
-    const long long warps = (rows + 3) / 4 * a.splits;
-    append_queries_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(s, seq_begin, rot, a.splits);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    a.rot.hq = 0;
-  }
+  if (apart) a.splits = std::max(a.splits, (rot.hq + 7) / 8);  // (eight heads a warp, as without a cache)
+  if (apart) a.rot.hq = 0;
   // rows of the most blocks an append of n tokens completes (at any state)
   const long long body = ((long long)rot.n + s.bt - 1) / s.bt * s.bt;
-  // few rows: more groups of fewer warps (64 x 41 tokens of
-  // 8 heads 24.6 us with eight warps, 22.5)
+  // few rows: more groups of fewer warps (64 x 41 tokens of 8 heads 24.6 us with eight
+  // warps, 22.5)
   a.group = kUnitRows / 16;
   while (a.group > s.bt / 16 && 8 * a.group >= body) a.group /= 2;
   a.tiles = (int)((body + 16 * a.group - 1) / (16 * a.group));
   a.shares = head_shares((long long)rot.batch * a.tiles, s.hkv);
   const bool kept = bounds.codes != nullptr;
-  if (s.fp8) return kept ? launch<true, true>(s, seq_begin, a, apart, st) : launch<true, false>(s, seq_begin, a, apart, st);
-  return kept ? launch<false, true>(s, seq_begin, a, apart, st) : launch<false, false>(s, seq_begin, a, apart, st);
+  const cudaError_t e = s.fp8 ? kept ? launch<true, true>(s, seq_begin, a, st) : launch<true, false>(s, seq_begin, a, st)
+                        : kept ? launch<false, true>(s, seq_begin, a, st)
+                               : launch<false, false>(s, seq_begin, a, st);
+  if (e != cudaSuccess || !apart) return e;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  constexpr int kWarpsQ = kQueryThreads / 32;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(((rows + 3) / 4 * a.splits + kWarpsQ - 1) / kWarpsQ));
+  cfg.blockDim = dim3(kQueryThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, append_queries_kernel, s, seq_begin, rot, a.splits);
 }
 
 }  // namespace kvc

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     axis[threadIdx.x] = a.table.axis[threadIdx.x];
   }
   __syncthreads();
-  rotary::rotate_unit(a, turns, axis, (long long)blockIdx.x * kWarps + (threadIdx.x >> 5), splits,
+  rotary::rotate_unit<4>(a, turns, axis, (long long)blockIdx.x * kWarps + (threadIdx.x >> 5), splits,
                       [](int) { return 0; });
 }
 

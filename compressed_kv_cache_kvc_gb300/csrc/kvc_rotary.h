@@ -50,9 +50,7 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st);
 
-// Warps that share a token's heads: enough of them for every SM to have 16 (more have
-// a token's angles computed more often: 4 x 32 heads x 4,001 queries beside an append
-// 290 us with one warp a token, 299 with four, 312 with eight).
+// Warps that share a token's heads: enough of them for every SM to have 16.
 inline int rotary_splits(long long rows, int heads) {
   const long long groups = (rows + 3) / 4, want = (152 * 16 + groups - 1) / groups;
   return (int)(want < 1 ? 1 : want < heads ? want : heads);
@@ -168,8 +166,7 @@ __device__ __forceinline__ void turn16(bool adjacent, uint4& a, uint4& b, const 
 
 // One warp: four tokens (8 lanes a row) and their share of the heads, kAtOnce rows
 // of each lane in flight.  token0(b): index of sequence b's first row.
-constexpr int kAtOnce = 4;
-template <class Token0>
+template <int kAtOnce, class Token0>
 __device__ __forceinline__ void rotate_unit(const RotaryArgs& a, const uint64_t* turns, const uint8_t* axis,
                                             long long unit, int splits, Token0 token0) {
   const int lane = threadIdx.x & 31, c = lane & 7;
