@@ -18,10 +18,10 @@
 // K and V of 8 x 8 heads x 8,192 tokens (INT8) 147 us, of 4 x 32 x 4,001 (E4M3) 172,
 // where the plain append, bound by DRAM, takes 80 and 97.  Bound by latency: 88
 // instructions a row (16 of them its share of the table), issue 57 %, four warps a
-// scheduler, one fifth of their time at barriers.  Tried and slower: the rows in
-// registers without the ring, at three CTAs of eight warps (80 registers, spilled)
-// and at two (391 and 328 us where the two calls with queries and read-back take 380
-// and 290).
+// scheduler (ring and table leave no shared memory for more), one fifth of their time at
+// barriers.  Tried and slower: the rows in registers without the ring, at three CTAs of
+// eight warps (80 registers, spilled) and at two (391 and 328 us where the two calls with
+// queries and read-back took 380 and 290).
 #include <cuda_bf16.h>
 
 #include <algorithm>
