@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     append_rotary_kernel(BlockState s, int seq_begin, const __grid_constant__ RotaryAppend a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int before[kMaxCallBatch], held[kMaxCallBatch];  // blocks completed before it; its length
-  __shared__ int sh_total, sh_bad, sh_last;
+  __shared__ int sh_bad, sh_last;
   __shared__ float sh_amax[2][kWarps];
   __shared__ uint64_t sh_turns[kRotPairs];
   __shared__ uint8_t sh_axis[kRotPairs];
@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-      sh_total = total;
       sh_bad = (bad ? kDevTableOverflow : 0) | (total > top || top > s.num_blocks ? kDevOutOfBlocks : 0);
     }
   }

@@ -251,6 +251,38 @@ def test_replays_and_streams():
         assert torch.equal(x, y)
 
 
+def test_replays_of_long_appends():
+    """Queries of many rows, turned by a launch of their own that also advances the
+    lengths: captured, replayed, and replayed once more than there is room for."""
+    from compressed_kv_cache_kvc_gb300 import Rotary
+    rot = Rotary(64, adjacent=True)
+    b, hq, hkv, n, block = 2, 16, 2, 1100, 32
+    a, ref = (_cache(hq, hkv, [3 * n] * b, block, "e4m3") for _ in range(2))
+    q, k, v = _fused(6, b, n, hq, hkv, hkv)
+    out = torch.empty(b, hq, n, D, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.append_rotary(q, k, v, rot, first=7, out=out)
+    assert a.lib.kvc_block_last_launch_count(a.handle) == 2
+    for i in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, rot.rotate(q, first=7 + i * n))
+        ref.append(rot.rotate(k, first=7 + i * n), v.contiguous())
+    a.sync_host()
+    assert a.lengths(0, b) == (3 * n, 3 * n) and a.read_status() == 0
+    for x, y in zip(a.read(0, b, 0, 3 * n), ref.read(0, b, 0, 3 * n)):
+        assert torch.equal(x, y)
+    graph.replay()  # no room: flagged, nothing appended
+    assert a.read_status() != 0
+    a.sync_host()
+    assert a.lengths(0, b) == (3 * n, 3 * n)
+    assert (a.buffer("TICKETS").view(torch.int32) == 0).all()
+    for x, y in zip(a.read(0, b, 0, 3 * n), ref.read(0, b, 0, 3 * n)):
+        assert torch.equal(x, y)
+
+
 def test_refused():
     from compressed_kv_cache_kvc_gb300 import Rotary
     rot, two = Rotary(), Rotary(axes=_axes(64, 2))
