@@ -45,11 +45,11 @@ enum { kPlain = 0, kSelected = 1, kPrefix = 2 };  // forms
 // units: tiles of 16 bf16 rows read straight into the MMA fragments, P as two
 // bf16 parts (16 significant bits).
 // V may be any finite value, also where blocks and exact rows differ by all of
-// bf16's range: the accumulators are in units of 2^E, which follows the largest V
-// scale (of exact rows 1/128 of the largest |v|) as the maxima follow the scores,
-// and partial results are divided by their sum before they leave units of 2^E,
-// since the sum over a long sequence of values near the top of the range is
-// beyond fp32.
+// bf16's range: a head's accumulators are in units of 2^E, which follows the largest
+// p V scale (of exact rows p |v| / 128) as the maxima follow the scores: V of
+// any size and no weight costs the others no bits.  Partial results are divided by
+// their sum before they leave units of 2^E, since the sum over a long sequence of
+// values near the top of the range is beyond fp32.
 // The CTA that finishes a pair last (an atomic ticket, no CTA waits) joins the
 // pair's partials in CTA order, so the result does not depend on the order of
 // completion.  (A warp per query head, eight rows of 16 bytes a lane in flight:
@@ -361,8 +361,9 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     for (int j = 0; j < 8; ++j) oacc[j][0] = oacc[j][1] = oacc[j][2] = oacc[j][3] = 0.0f;
     float osum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float m0 = kNegBig, m1 = kNegBig, l0 = 0.0f, l1 = 0.0f;
-    int E = 0;
-    float sv_hi = 0.0f, inv2E = 1.0f;  // (0: E not set yet)
+    // the two heads' E (kNegBig: not set yet) and 2^-E, the largest V scale that leaves
+    // the units as they are
+    float E0 = kNegBig, E1 = kNegBig, inv2E0 = 1.0f, inv2E1 = 1.0f, sv_hi = 0.0f;
 
     // slots (2r, 2r + 1) x heads (2c, 2c + 1): cap and bias; slot 2r is at
     // distance d0 from the query
@@ -376,21 +377,46 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         lg[3] = fmaf(-sl1, db, lg[3]);
       }
     };
-    // the running maxima rise to cover tm0, tm1 and the P V scale to cover a V
-    // scale svm > 0 (0: unchanged); O, the sums and l are rescaled
-    auto rescale = [&](float tm0, float tm1, float svm) {
+    // A head's E once its maximum has risen from m to nm, of V scales below 2^(ex + 1)
+    // and products of exp2(score) and V scale below 2^(tw + 1): it stays while that fits
+    // both the scales and the largest product so far, to 2^4; scales of no weight do not
+    // raise it, and where the maximum leaves what set it behind it falls.
+    auto next_unit = [&](float m, float nm, float tw, float ex, float E) {
+      const float e = ex < E + 4.0f ? E : ex, top = fmaxf(m - nm + E, tw - nm);
+      return fminf(fmaxf(top < e - 4.0f ? ceilf(top) : e, -126.0f), 126.0f);
+    };
+    // Exact rows' accumulators are in units of 2^E within 2^+-40: P carries the power
+    // alone, V enters as it is, and neither leaves bf16's range, nor the products fp32's,
+    // for any V.
+    auto exact_unit = [](float E) { return fminf(fmaxf(E, -40.0f), 40.0f); };
+    auto exact_power = [](float x) { return fminf(fmaxf(x, 0x1p-40f), 0x1p40f); };
+    // the running maxima rise to cover tm0, tm1 and, if `units`, the units follow V
+    // scales and products as in next_unit; O, the sums and l are rescaled
+    auto rescale = [&](auto exact_tag, float tm0, float tm1, bool units, float tw0, float tw1, float ex) {
+      constexpr bool kExact = decltype(exact_tag)::value;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         tm0 = fmaxf(tm0, __shfl_xor_sync(0xffffffffu, tm0, o));
         tm1 = fmaxf(tm1, __shfl_xor_sync(0xffffffffu, tm1, o));
+        if (units) {
+          tw0 = fmaxf(tw0, __shfl_xor_sync(0xffffffffu, tw0, o));
+          tw1 = fmaxf(tw1, __shfl_xor_sync(0xffffffffu, tw1, o));
+        }
       }
       const float nm0 = fmaxf(m0, tm0), nm1 = fmaxf(m1, tm1);
       const float al0 = fast_exp2(m0 - nm0), al1 = fast_exp2(m1 - nm1);
-      const bool rescale_e = svm > sv_hi;
-      const int nE = rescale_e ? min(max(exponent_of(svm), -126), 126) : E;
-      const int dE = E - nE;
-      const float f = dE >= -126 ? pow2i(min(dE, 127)) : 0.0f;
-      const float f0 = al0 * f, f1 = al1 * f;
+      float f0 = al0, f1 = al1;
+      if (units) {
+        const float n0 = next_unit(m0, nm0, tw0, ex, E0), n1 = next_unit(m1, nm1, tw1, ex, E1);
+        f0 = fast_exp2(m0 - nm0 + (kExact ? exact_unit(E0) - exact_unit(n0) : E0 - n0));
+        f1 = fast_exp2(m1 - nm1 + (kExact ? exact_unit(E1) - exact_unit(n1) : E1 - n1));
+        const int i0 = (int)n0, i1 = (int)n1;
+        sv_hi = pow2i(min(min(i0, i1) + 4, 127));
+        inv2E0 = pow2i(-i0);
+        inv2E1 = pow2i(-i1);
+        E0 = n0;
+        E1 = n1;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         oacc[j][0] *= f0;
@@ -406,10 +432,27 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       l1 *= al1;
       m0 = nm0;
       m1 = nm1;
-      if (rescale_e) {
-        E = nE;
-        sv_hi = pow2i(min(E + 4, 127));
-        inv2E = pow2i(-E);
+    };
+    // the accumulators from the pages' units (2^24 more for offset codes) to the exact
+    // rows' or back
+    auto to_units = [&](bool exact) {
+      constexpr float kCodes = kOffset ? 0x1p24f : 1.0f;
+      // (2^E from 2^-E by their exponent fields)
+      const float p0 = __int_as_float(0x7F000000 - __float_as_int(inv2E0));
+      const float p1 = __int_as_float(0x7F000000 - __float_as_int(inv2E1));
+      const float a0 = exact ? exact_power(inv2E0) * p0 : exact_power(p0) * inv2E0;
+      const float a1 = exact ? exact_power(inv2E1) * p1 : exact_power(p1) * inv2E1;
+      const float f0 = a0 * (exact ? kCodes : 1.0f / kCodes), f1 = a1 * (exact ? kCodes : 1.0f / kCodes);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        oacc[j][0] *= f0;
+        oacc[j][2] *= f0;
+        oacc[j][1] *= f1;
+        oacc[j][3] *= f1;
+      }
+      if (kOffset && exact) {
+        osum[0] *= a0;
+        osum[1] *= a1;
       }
     };
 
@@ -497,18 +540,31 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
         tm1 = fmaxf(tm1, fmaxf(acc[pp][1], acc[pp][3]));
         svm = fmaxf(svm, vs[pp]);
       }
-      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi))
-        rescale(tm0, tm1, svm);
+      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi)) {
+        float tw0 = -INFINITY, tw1 = -INFINITY, least = INFINITY, ex = -INFINITY;
+#pragma unroll
+        for (int pp = 0; pp < NP; ++pp) {
+          const float e = (float)exponent_of(vs[pp]);
+          tw0 = fmaxf(tw0, fmaxf(acc[pp][0], acc[pp][2]) + e);
+          tw1 = fmaxf(tw1, fmaxf(acc[pp][1], acc[pp][3]) + e);
+          least = fminf(least, e);
+          ex = fmaxf(ex, e);
+        }
+        // (whatever raises a maximum has a scale that keeps the unit, else)
+        const bool units = __any_sync(0xffffffffu, svm > sv_hi || least < fmaxf(E0, E1) - 4.0f);
+        rescale(std::false_type{}, tm0, tm1, units, tw0, tw1, ex);
+      }
       uint32_t pb0[NP], pb1[NP];
 #pragma unroll
       for (int pp = 0; pp < NP; ++pp) {
-        const float sn = vs[pp] * inv2E;
+        // (beyond fp32 only where every p is 0)
+        const float sn0 = fminf(vs[pp] * inv2E0, 0x1p127f), sn1 = fminf(vs[pp] * inv2E1, 0x1p127f);
         const float p0 = fast_exp2(acc[pp][0] - m0), p1 = fast_exp2(acc[pp][1] - m1);
         const float p2 = fast_exp2(acc[pp][2] - m0), p3 = fast_exp2(acc[pp][3] - m1);
         l0 += p0 + p2;
         l1 += p1 + p3;
-        pb0[pp] = movmatrix_t(pack_half2(p0 * sn, p1 * sn));
-        pb1[pp] = movmatrix_t(pack_half2(p2 * sn, p3 * sn));
+        pb0[pp] = movmatrix_t(pack_half2(p0 * sn0, p1 * sn1));
+        pb1[pp] = movmatrix_t(pack_half2(p2 * sn0, p3 * sn1));
       }
       // O^T += V_codes^T . P^T (rows: head dims 16r + 2j (+1), columns: query heads)
 #pragma unroll
@@ -602,40 +658,42 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
       }
       if (!on0) acc[0] = acc[1] = -INFINITY;
       if (!on1) acc[2] = acc[3] = -INFINITY;
-      __nv_bfloat162 vm2 = __floats2bfloat162_rn(0.0f, 0.0f);
+      // the largest magnitudes of the lane's two V rows
+      __nv_bfloat162 va2 = __floats2bfloat162_rn(0.0f, 0.0f), vc2 = va2;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        vm2 = __hmax2(vm2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i])));
-        vm2 = __hmax2(vm2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i])));
+        va2 = __hmax2(va2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i])));
+        vc2 = __hmax2(vc2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i])));
       }
-      float svm = fmaxf(__low2float(vm2), __high2float(vm2)) * 0x1p-7f;
+      float sva = fmaxf(__low2float(va2), __high2float(va2)) * 0x1p-7f;
+      float svc = fmaxf(__low2float(vc2), __high2float(vc2)) * 0x1p-7f;
       const float tm0 = fmaxf(acc[0], acc[2]), tm1 = fmaxf(acc[1], acc[3]);
-      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || svm > sv_hi)) {
-        svm = warp_max(svm);
-        rescale(tm0, tm1, svm);
+      if (__any_sync(0xffffffffu, tm0 > m0 + kBLazy || tm1 > m1 + kBLazy || fmaxf(sva, svc) > sv_hi)) {
+        // (four lanes have a row: a quarter of it is enough to say that it may not be small)
+        int xa = exponent_of(sva), xc = exponent_of(svc);
+        float ea = (float)xa, ec = (float)xc;
+        const float lo = fmaxf(E0, E1) - 4.0f;
+        const bool units =
+            __any_sync(0xffffffffu, fmaxf(sva, svc) > sv_hi || (on0 && ea < lo) || (on1 && ec < lo));
+        float ex = 0.0f;
+        if (units) {
+          ex = (float)__reduce_max_sync(0xffffffffu, max(xa, xc));
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            ea = fmaxf(ea, __shfl_xor_sync(0xffffffffu, ea, o));
+            ec = fmaxf(ec, __shfl_xor_sync(0xffffffffu, ec, o));
+          }
+        }
+        rescale(std::true_type{}, tm0, tm1, units, fmaxf(acc[0] + ea, acc[2] + ec), fmaxf(acc[1] + ea, acc[3] + ec), ex);
       }
       const float p0 = fast_exp2(acc[0] - m0), p1 = fast_exp2(acc[1] - m1);
       const float p2 = fast_exp2(acc[2] - m0), p3 = fast_exp2(acc[3] - m1);
       l0 += p0 + p2;
       l1 += p1 + p3;
-      // the P V operands in the accumulators' units (2^24 for offset codes, 2^E),
-      // the power on both where it is large (V that leaves bf16's range by it is
-      // nothing beside 2^E)
-      const int eu = (kOffset ? 24 : 0) + E, ev = eu > 64 ? -64 : eu < -64 ? 64 : 0;
-      if (ev != 0) {
-        const __nv_bfloat162 f = __float2bfloat162_rn(pow2i(ev));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&wa[i]), f);
-          __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&wc[i]), f);
-          wa[i] = *reinterpret_cast<const uint32_t*>(&x);
-          wc[i] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-      }
-      const float unit = pow2i(-eu - ev);
+      const float unit0 = exact_power(inv2E0), unit1 = exact_power(inv2E1);
       uint32_t h0, h1, q0, q1;
-      split_bf16x2(p0 * unit, p1 * unit, h0, q0);
-      split_bf16x2(p2 * unit, p3 * unit, h1, q1);
+      split_bf16x2(p0 * unit0, p1 * unit1, h0, q0);
+      split_bf16x2(p2 * unit0, p3 * unit1, h1, q1);
       h0 = movmatrix_t(h0);
       h1 = movmatrix_t(h1);
       q0 = movmatrix_t(q0);
@@ -654,6 +712,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     if (kDirect) {
 #pragma unroll 1
       for (int k = n_pg; k < n_my; ++k) exact_tile(k);
+      if (0 < n_pg && n_pg < n_my) to_units(false);
     }
     if (FORM == kSelected) {
       wait_for_previous();
@@ -691,6 +750,7 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
 
     // the plain form's exact rows come after its pages
     if (!kDirect) {
+      if (0 < n_pg && n_pg < n_my) to_units(true);
 #pragma unroll 1
       for (; k < n_my; ++k) exact_tile(k);
     }
@@ -705,16 +765,18 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     float* sm_m = reinterpret_cast<float*>(smem);
     float* sm_l = sm_m + kBWarps * kMaxGroup;
     float* sm_o = sm_l + kBWarps * kMaxGroup;  // [kBWarps][8][kMergeRow]
-    int* sm_e = reinterpret_cast<int*>(sm_o + kBWarps * kMaxGroup * kMergeRow);
-    if (lane == 0) sm_e[warp] = E;
+    float* sm_e = sm_o + kBWarps * kMaxGroup * kMergeRow;
+    const bool page_units = kDirect ? n_pg > 0 : n_pg == n_my;
     if (r == 0) {
+      sm_e[warp * kMaxGroup + 2 * c] = page_units ? E0 : exact_unit(E0);
+      sm_e[warp * kMaxGroup + 2 * c + 1] = page_units ? E1 : exact_unit(E1);
       sm_m[warp * kMaxGroup + 2 * c] = m0;
       sm_m[warp * kMaxGroup + 2 * c + 1] = m1;
       sm_l[warp * kMaxGroup + 2 * c] = l0;
       sm_l[warp * kMaxGroup + 2 * c + 1] = l1;
     }
     {
-      const float sA = kOffset ? 0x1p24f : 1.0f;
+      const float sA = kOffset && page_units ? 0x1p24f : 1.0f;
       const float b0 = kOffset ? kOffV * osum[0] : 0.0f;
       const float b1 = kOffset ? kOffV * osum[1] : 0.0f;
       // dim 16 r + i of a head at 8 i + r, rows of 132: each bank once a store
@@ -764,22 +826,31 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     const long long slot = kDirect ? slot0 + part : PARTS ? F : pair + cta;
     const int d = threadIdx.x;  // 128 threads = head_dim
     uint16_t* orow = out + ((size_t)bl * s.hq + h * G) * kHeadDim + d;
-    float* sm_own = sm_o + kBWarps * kMaxGroup * kMergeRow + kBWarps;  // (quick) [8][kMergeRow]: o, M, l
-    int e_most = sm_e[0];
+    float* sm_own = sm_o + kBWarps * kMaxGroup * kMergeRow + kBWarps * kMaxGroup;  // (quick) [8][kMergeRow]: o, M, l
+    // lane 4 g + w has warp w's weights of head g: exp2(m_w - M) for the sums, for O the
+    // same times 2^(E_w - e), e the unit of the largest
+    static_assert(kBWarps == 4 && kMaxGroup == 8, "a lane per warp and head");
+    const int at_w = (lane & 3) * kMaxGroup + (lane >> 2);
+    float M_g = sm_m[at_w], top_g = M_g + sm_e[at_w], l_g = 0.0f;
 #pragma unroll
-    for (int ww = 1; ww < kBWarps; ++ww) e_most = max(e_most, sm_e[ww]);
+    for (int o = 1; o < kBWarps; o <<= 1) {
+      M_g = fmaxf(M_g, __shfl_xor_sync(0xffffffffu, M_g, o));
+      top_g = fmaxf(top_g, __shfl_xor_sync(0xffffffffu, top_g, o));
+    }
+    const float e_g = fminf(fmaxf(floorf(top_g - M_g), -126.0f), 126.0f), de = sm_e[at_w] - e_g;
+    const float less = sm_m[at_w] - M_g, wt_l = fast_exp2(less), o_g = pow2i((int)e_g);
+    const float wt_o = fabsf(de) < 64.0f ? wt_l * pow2i((int)de) : fast_exp2(less + de);
+#pragma unroll
+    for (int ww = 0; ww < kBWarps; ++ww)
+      l_g = fmaf(__shfl_sync(0xffffffffu, wt_l, (lane & ~3) + ww), sm_l[ww * kMaxGroup + (lane >> 2)], l_g);
     for (int g = 0; g < G; ++g) {
-      float M = kNegBig;
+      const float M = __shfl_sync(0xffffffffu, M_g, 4 * g), l = __shfl_sync(0xffffffffu, l_g, 4 * g);
+      float o = 0.0f;
 #pragma unroll
-      for (int ww = 0; ww < kBWarps; ++ww) M = fmaxf(M, sm_m[ww * kMaxGroup + g]);
-      float o = 0.0f, l = 0.0f;
-#pragma unroll
-      for (int ww = 0; ww < kBWarps; ++ww) {
-        const float wt = fast_exp2(sm_m[ww * kMaxGroup + g] - M);
-        o += wt * pow2i(max(sm_e[ww] - e_most, -126)) * sm_o[((size_t)ww * kMaxGroup + g) * kMergeRow + 8 * (d & 15) + (d >> 4)];
-        l += wt * sm_l[ww * kMaxGroup + g];
-      }
-      o = l != 0.0f ? o * (1.0f / l) * pow2i(e_most) : 0.0f;
+      for (int ww = 0; ww < kBWarps; ++ww)
+        o = fmaf(__shfl_sync(0xffffffffu, wt_o, 4 * g + ww),
+                 sm_o[((size_t)ww * kMaxGroup + g) * kMergeRow + 8 * (d & 15) + (d >> 4)], o);
+      o = l != 0.0f ? o * (1.0f / l) * __shfl_sync(0xffffffffu, o_g, 4 * g) : 0.0f;
       if (FORM == kPrefix && quick) {
         sm_own[g * kMergeRow + d] = o;
         if (d == 0) {

@@ -698,8 +698,11 @@ kvc_status kvc_block_set_key_bounds(kvc_block_cache* cache, void* d_bounds, size
 /* Single-query attention over everything the slice's sequences hold, the
  * newest token included: d_q, d_out bf16 [batch][Hq][128], 16-byte aligned;
  * scores transformed as kvc_set_score_transform says (softcap 0 and d_slopes
- * null: plain), the query at the newest position.  Accumulated in fp32; V of any
- * finite size, blocks and exact rows of different sizes included.
+ * null: plain), the query at the newest position.  Scores, softmax statistics and
+ * sums are fp32.  A probability enters its product with V's codes times the V scale
+ * and in fp16: 11 bits down to 2^-14 of the largest such product of its query head, off
+ * by 2^-25 of it below (with V held exactly in 16 bits).  V of any finite size, blocks
+ * and exact rows of different sizes included: what has no weight costs no bits.
  *   d_workspace: kvc_block_workspace_bytes(cache, batch) bytes, 256-byte
  *   aligned, contents arbitrary.
  * One launch: the CTA that finishes a (sequence, KV head) last joins its
