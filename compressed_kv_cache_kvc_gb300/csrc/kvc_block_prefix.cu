@@ -25,20 +25,20 @@
 // 256 + 128 x; P (fp16) takes the back half of its S.  In step j the MMA warp of query
 // tile x issues PV_x(j - 2), S_x(j): the pipe runs one thread's products in order, so
 // S(j) may overwrite P(j - 2), and a softmax finds the scores of its next step ready.
-// A block's K scale multiplies its scores, its V scale over the largest of the
-// run (as a power of two, so that the quotient lies in [1/2, 1)) its probabilities: P
-// keeps 11 bits down to 2^-14 of what the largest value would contribute at p = 1 and
-// is off by 2^-25 of it below; O leaves times that power.  The running maximum is
-// lazy: p is formed with the one so far, and only where 32 of them sum to more than
-// 2^15 is the maximum looked for and O rescaled, so that P fits fp16 and most steps
-// read their scores once and compare nothing (with the maximum of every step first
-// 43 us where this takes 37, 64 x 32 heads after 32,768 tokens).  The sums add the
-// unrounded p in fp32.
+// A block's K scale multiplies its scores, its V scale over a power of two its
+// probabilities (P, fp16).  That power is the row's own and follows the largest product
+// of p and V scale that the row has met, so that P keeps 11 bits down to 2^-14 of it
+// and is off by 2^-25 of it below, whatever the V of tokens without weight; O leaves
+// times that power.  Maximum and power are lazy: P is formed with those so far, and only
+// where 32 p, or they times their V scales, sum to more than 2^15 are they looked for
+// and O rescaled, so that P fits fp16 and most steps read their scores once and compare
+// nothing (with the maximum of every step first 43 us where this takes 37, 64 x 32
+// heads after 32,768 tokens).  The sums add the unrounded p in fp32.
 // Tiles, and the steps and chunks inside, go from the last to the first: with a
 // distance bias the nearest come first, and the maximum hardly ever rises again.
 // Synchronisation: mbarriers, every wait bounded, as in the prompt kernels.
 //
-// 64 x 32 heads on 8 after 32,768 tokens 37 us, 0.93 PFLOP/s (49 % of a library product's
+// 64 x 32 heads on 8 after 32,768 tokens 38 us, 0.91 PFLOP/s (47 % of a library product's
 // rate, which counts the conversion of the codes, exp2 and the first and last 4 us of a
 // CTA); 24 x 40 heads, capped, biased E4M3, after 16,001 25 us: the softmax of 120 rows.
 // The sequences' own tokens and the join after them 24 and 21 us: one and a half and
@@ -71,7 +71,7 @@ constexpr int kOffMask = kOffScale + 4 * 2 * 8 * 4;
 constexpr int kOffBar = kOffMask + 4 * 4;
 constexpr int kBarQ = 0, kBarK = 1, kBarV = 3, kBarKFree = 5, kBarVFree = 7, kBarS = 9, kBarP = 13, kBarO = 17,
               kBarScale = 21, kBarDone = 25, kBarScaleFree = 27, kNumBars = 31;  // (S, P, O: 2 x + step parity)
-constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort flag, the power of two of the V scales
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // TMEM base, abort flag
 constexpr int kOffMl = kOffMisc + 32;  // [2][128][2] the rows' maxima and sums
 constexpr int kSmem = kOffMl + 2 * kTile * 8;
 constexpr float kMostSum = 32768.0f;
@@ -272,19 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int e = 1; e < kAhead; ++e) fetch(e, ids[e]);
     float sc = scale_of(ids[0]);
-    // the power of two E of the run's largest V scale: P takes a block's V scale times
-    // 2^(-1 - E), in two steps that no exponent leaves fp32's range by
-    uint32_t most = 0;
-    const int b0 = (t0 * kTile) >> sh, b1 = min(n_tok, t1 * kTile) >> sh;
-#pragma unroll 4
-    for (int k = b0 + lane; k < b1; k += 32) {
-      const int id = table[k];
-      if ((unsigned)id < (unsigned)s.num_blocks) most = max(most, __float_as_uint(s.v_scale[(size_t)id * hkv + h]));
-    }
-    most = __reduce_max_sync(0xffffffffu, most);  // (scales are not negative: their order is their bits')
-    const int E = min(max((int)(most >> 23) - 127, -126), 126);
-    const float down0 = v ? pow2i((-1 - E) / 2) : 1.0f, down1 = v ? pow2i(-1 - E - (-1 - E) / 2) : 1.0f;
-    if (lane == 0) *reinterpret_cast<volatile int*>(sm + kOffMisc + 16) = E;
 #pragma unroll 1
     for (int i = 0; i < n_t; ++i) {
       const int id = ids[0], next = id_of(i + kAhead + 1);
@@ -293,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= 4) wait(kBarScaleFree + (i & 3), (uint32_t)((i >> 2) & 1) ^ 1u);
       if (!ok) break;
       float* to = reinterpret_cast<float*>(sm + kOffScale) + (i & 3) * 16;
-      if (lane < 16) to[lane] = sc * down0 * down1;
+      if (lane < 16) to[lane] = sc;
       if (id == -2 && lane < 8) atomicOr(status, kDevBadBlockId);
       const uint32_t pages = __ballot_sync(0xffffffffu, id >= 0) & 0xFFu;
       if (lane == 0) reinterpret_cast<uint32_t*>(sm + kOffMask)[i & 3] = pages;
@@ -431,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_x = trow + kTile * x, t_o = trow + 256 + kTile * x;
     const float slope2 = BIAS && on ? slope_log2(a.mod, h * G + g) : 0.0f;
     const int n_x = tiles_of(x);
-    float m = kNegBig, l = 0.0f;
+    float m = kNegBig, l = 0.0f, per_unit = 1.0f;  // O is in units of 1 / per_unit, a power of two
 #pragma unroll 1
     for (int j = 0; j < 2 * n_x; ++j) {
       const int i = tile_of(x, j >> 1), first = kStep * (~j & 1);  // the tile, the step's first token in it
@@ -448,14 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                           pages & 8u ? sk.w * cq : 1.0f};
       const float v[4] = {sv.x, sv.y, sv.z, sv.w};
       // P (fp16) over the back half of the products, 32 of which have been read when the
-      // first 16 columns of P come there.  The probabilities are formed with the maximum so far;
-      // only where their sum says that one of them may exceed 2^9 is the maximum
-      // itself looked for
+      // first 16 columns of P come there.  P is formed with the maximum and the unit so
+      // far; only where the sums say that a p or an element of P may exceed 2^9 are these
+      // themselves looked for
 #pragma unroll
       for (int c = 1; c >= 0; --c) {
         float z[32];
         uint32_t pw[16];
         f32x2 sum;
+        float vu[2];
+        unpack2(mul2(pack2(v[2 * c], v[2 * c + 1]), pack2(per_unit, per_unit)), vu[0], vu[1]);
         // scores less the maximum -> P, and the unrounded sum
         auto probabilities = [&]() {
           f32x2 ls[2] = {0, 0};
@@ -464,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             float* zz = z + 16 * e;
             const float fe = f[2 * c + e];
-            const f32x2 f2 = pack2(fe, fe), v2 = pack2(v[2 * c + e], v[2 * c + e]);
+            const f32x2 f2 = pack2(fe, fe), v2 = pack2(vu[e], vu[e]);
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               const f32x2 zp = pack2(zz[k], zz[k + 1]);
@@ -506,36 +495,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         scores();
-        float lx = INFINITY, ly = 0.0f;
+        float lx, ly;
+        bool ask = true;
         if (j > 0 || c == 0) {
           probabilities();
           unpack2(sum, lx, ly);
+          // (a row's results do not depend on the others'; a unit that takes the V scale
+          // beyond fp32 asks too)
+          ask = !((lx + ly) * max3(vu[0], vu[1], 1.0f) <= kMostSum);
         }
-        const bool ask = !(lx + ly <= kMostSum);  // (a row's results do not depend on the others')
         if (__any_sync(0xffffffffu, ask)) {
           if (j > 0 || c == 0) scores();  // (P has taken none of this chunk's products yet)
-          float mx = -INFINITY;
+          float mx = -INFINITY, top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            mx = fmaxf(mx, group_max(z + 16 * e, -INFINITY) * (CAP || BIAS ? 1.0f : f[2 * c + e]));
-          // the maximum rises by a whole number, so that what has been rounded is
-          // scaled without a second rounding
-          float alpha = 1.0f;
-          if (ask && mx > m) {
-            const float up = m > kNegBig ? ceilf(mx - m) : INFINITY;
-            alpha = up < 127.0f ? pow2i(-(int)up) : 0.0f;
-            m = up < 127.0f ? m + up : mx;
+          for (int e = 0; e < 2; ++e) {
+            const float y = group_max(z + 16 * e, -INFINITY) * (CAP || BIAS ? 1.0f : f[2 * c + e]);
+            mx = fmaxf(mx, y);
+            top = fmaxf(top, y + (float)exponent_of(v[2 * c + e]));
           }
-          l *= alpha;
+          // the maximum rises by a whole number, so that what has been rounded is
+          // scaled without a second rounding while it stays in fp16's normal range
+          float alpha = 1.0f;
+          if (ask && mx > -INFINITY) {
+            const bool none = m <= kNegBig;
+            const int unit = -exponent_of(per_unit), up = none || mx - m > 4096.0f ? 4096 : max((int)ceilf(mx - m), 0);
+            m = up < 4096 ? m + (float)up : mx;
+            const int to = min(max(none ? -126 : unit - up, (int)ceilf(fmaxf(top - m, -126.0f))), 126);
+            const int by = none ? -4096 : unit - up - to;
+            alpha = by >= -126 ? pow2i(by) : 0.0f;
+            l *= up <= 126 ? pow2i(-up) : 0.0f;
+            per_unit = pow2i(-to);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) vu[e] = fminf(v[2 * c + e] * per_unit, 0x1p127f);  // (beyond it p is 0)
           if (c == 0) {  // the other chunk's P
             uint32_t w[16];
             tmem_st_wait();
             ld16u(t_s + kStep * 3 / 4, w);
-            const __half2 a2 = __float2half2_rn(alpha);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), a2);
-              w[e] = *reinterpret_cast<const uint32_t*>(&y);
+              const float2 y = unpack_half2(w[e]);
+              w[e] = pack_half2(y.x * alpha, y.y * alpha);
             }
             tmem_st16(t_s + kStep * 3 / 4, w);
           }
@@ -576,9 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-      // (the scales of some tile came after the power was written)
-      const int E = *reinterpret_cast<volatile int*>(sm + kOffMisc + 16);
-      const float up0 = pow2i((E + 1) / 2), up1 = pow2i(E + 1 - (E + 1) / 2);
+      const float up = pow2i(-exponent_of(per_unit));
 #pragma unroll 1
       for (int c0 = 0; c0 < kHeadDim; c0 += 32) {
         float o[32];
@@ -591,8 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
           *reinterpret_cast<float4*>(box + x * kTileB + lane * 512 + (((c0 + e) >> 2 ^ lane) << 4)) =
-              make_float4(o[e] * inv * up0 * up1, o[e + 1] * inv * up0 * up1, o[e + 2] * inv * up0 * up1,
-                          o[e + 3] * inv * up0 * up1);
+              make_float4(o[e] * inv * up, o[e + 1] * inv * up, o[e + 2] * inv * up, o[e + 3] * inv * up);
       }
     }
     float2* sh_ml = reinterpret_cast<float2*>(sm + kOffMl);  // [2 streams][128]

@@ -92,7 +92,8 @@ def _marked(where, n):
 SIZES = [(2.0 ** 24, 1.0, 250.0), (1.0, 2.0 ** -45, 250.0), (3e37, 1e-30, 250.0), (2.0 ** 40, 1.0, 28.0),
          (2.0 ** 18, 1.0, 12.0), (2.0 ** 30, 1.0, 0.0), (1e-33, 1e-37, 250.0)]
 FORMS = {  # sequences, tokens of the first and of the others
-    "whole": (2, 1493, 900), "selected": (2, 1493, 900), "direct": (3, 1493, 95),
+    "whole": (2, 1493, 900), "selected": (2, 1493, 900), "direct": (3, 1493, 95), "product": (40, 3853, 95),
+    "product, one stream": (15, 9997, 95),
 }
 WHERE = ["blocks", "newest", "every other", "sinks", "open", "a sink and a block", "own"]
 
