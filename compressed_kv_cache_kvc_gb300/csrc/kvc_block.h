@@ -52,10 +52,10 @@ struct BlockAttn {
   ScoreMod mod;
   float qk_scale_log2;
   int ncta;
-  // the selected form: blocks of every pair in ascending order and where they lie in the
-  // pool, `most` places a pair
+  // the selected form: up to `most` blocks of every pair in ascending order and where they
+  // lie in the pool, list_row and ids_row places a pair
   const int32_t *list, *ids;
-  int most;
+  int most, list_row, ids_row;
   // the prefix form: the sequence that holds it, whether its pages are among the
   // units; partials of its blocks from elsewhere, `more` of [hkv][batch][group]
   int prefix, prefix_pages, more;
@@ -71,9 +71,9 @@ struct BlockAttn {
 // newest, and these.
 struct BlockChoice {
   uint32_t* keys;  // [pairs][max_bps], ordered as the scores
-  int32_t* list;   // [pairs][top + recent], ascending, -1 behind the last
-  int32_t* ids;    // their blocks in the pool
-  int top, recent;
+  int32_t* list;   // [pairs][list_row], ascending, -1 behind the last
+  int32_t* ids;    // [pairs][ids_row] their blocks in the pool
+  int top, recent, list_row, ids_row;
 };
 
 cudaError_t launch_block_append(const BlockState& s, const KeyBounds& bounds, int seq_begin, int batch, int n_new,

@@ -241,12 +241,12 @@ __global__ void __launch_bounds__(kBThreads, PARTS ? 2 : 3) block_attn_kernel(Bl
     const int n_my = u_e - u_a > warp ? (u_e - u_a - warp + kBWarps - 1) / kBWarps : 0;
     const int n_pg = min(u_e, npg) - u_a > warp ? (min(u_e, npg) - u_a - warp + kBWarps - 1) / kBWarps : 0;
     const int32_t* table = s.table + (size_t)b * s.max_bps;
-    const int32_t* list = FORM == kSelected ? a.list + ((size_t)bl * hkv + h) * a.most : nullptr;
+    const int32_t* list = FORM == kSelected ? a.list + ((size_t)bl * hkv + h) * a.list_row : nullptr;
     // block ids and scales of this warp's pages, 32 at a time across the lanes
     auto tab_load = [&](int chunk) -> int {
       const int k = chunk * 32 + lane, u = u_a + warp + kBWarps * k;
       if (k >= n_pg) return -1;
-      if (FORM == kSelected) return a.ids[((size_t)bl * hkv + h) * a.most + u / ppb];
+      if (FORM == kSelected) return a.ids[((size_t)bl * hkv + h) * a.ids_row + u / ppb];
       if (FORM == kPrefix)
         return u < pre_npg ? s.table[(size_t)a.prefix * s.max_bps + u / ppb] : table[(u - pre_npg) / ppb];
       return table[u / ppb];

@@ -200,15 +200,17 @@ bool choice_ok(int top, int recent) { return top > 0 && recent >= 0 && (long lon
 struct SelectedLayout {
   WsLayout ws;
   size_t keys, list, ids, total;
+  int places;  // of a pair's list: the blocks it may hold at most
 };
 SelectedLayout selected_layout(const kvc_block_cache* c, int batch, int top, int recent) {
   const size_t pairs = (size_t)batch * c->cfg.num_kv_heads;
   SelectedLayout l{};
   l.ws = ws_layout(c, batch);
+  l.places = std::min(top + recent, c->cfg.max_blocks_per_seq);
   l.keys = align_up(l.ws.total);
   l.list = l.keys + align_up(pairs * c->cfg.max_blocks_per_seq * 4);
-  l.ids = l.list + align_up(pairs * ((size_t)top + recent) * 4);
-  l.total = l.ids + align_up(pairs * ((size_t)top + recent) * 4);
+  l.ids = l.list + align_up(pairs * l.places * 4);
+  l.total = l.ids + align_up(pairs * l.places * 4);
   return l;
 }
 
@@ -504,10 +506,14 @@ kvc_status kvc_block_selected_attention(kvc_block_cache* c, int32_t seq_begin, i
   ch.ids = reinterpret_cast<int32_t*>(ws + sl.ids);
   ch.top = top_blocks;
   ch.recent = recent_blocks;
+  ch.list_row = d_blocks ? most : sl.places;
+  ch.ids_row = sl.places;
   kvc::BlockAttn a = attention_of(sl.ws, d_workspace, sm_scale, softcap, d_slopes);
   a.list = ch.list;
   a.ids = ch.ids;
   a.most = most;
+  a.list_row = ch.list_row;
+  a.ids_row = ch.ids_row;
   split_pairs(c, &a, batch, units);
   a.early = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -222,14 +222,14 @@ __global__ void __launch_bounds__(kChooseThreads) block_choose_kernel(BlockState
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pair = blockIdx.x, b = seq_begin + pair / s.hkv, most = ch.top + ch.recent;
   const int closed = block_closed(s.seq_pos[b], s.bt);
-  int32_t* list = ch.list + (size_t)pair * most;
-  int32_t* ids = ch.ids + (size_t)pair * most;
+  int32_t* list = ch.list + (size_t)pair * ch.list_row;
+  int32_t* ids = ch.ids + (size_t)pair * ch.ids_row;
   const int32_t* table = s.table + (size_t)b * s.max_bps;
   launch_dependents();
   for (int i = threadIdx.x; i < min(closed, kKeysStaged); i += kChooseThreads) sh_table[i] = table[i];
   wait_for_previous();  // the keys (and, for a list that stays, the call before)
   if (closed <= most) {
-    for (int i = threadIdx.x; i < most; i += kChooseThreads) {
+    for (int i = threadIdx.x; i < ch.list_row; i += kChooseThreads) {
       list[i] = i < closed ? i : -1;
       if (i < closed) ids[i] = table[i];
     }
