@@ -45,6 +45,7 @@ class BlockScaledCache:
                 "kvc_block_cache_create")
         self.handle = h
         self._ws = {}
+        self._ws_sized, self._ws_of = {}, {}  # buffers by size; those of recent calls' arguments
         self.bounds = None
         if key_bounds:
             nbytes = self.lib.kvc_block_key_bounds_bytes(h)
@@ -168,13 +169,22 @@ class BlockScaledCache:
         return out, 1.0 / math.sqrt(HEAD_DIM) if sm_scale is None else sm_scale
 
     def _workspace_of(self, workspace, key, nbytes):
-        """`workspace`, or the cache's own for the calls of `key`."""
+        """`workspace`, or the cache's own for the calls of `key`.  Calls on one cache
+        run one after another, so those of one size class (powers of two) share a
+        buffer, whatever they ask for; it lives as long as the cache, since captured
+        calls go on using it."""
         if workspace is not None:
             _need(workspace, torch.uint8, "workspace", self.device)
             return workspace
-        ws = self._ws.get(key)
+        ws = self._ws_of.get(key)
         if ws is None:
-            ws = self._ws[key] = torch.empty(max(int(nbytes()), 1), dtype=torch.uint8, device=self.device)
+            size = 1 << max(int(nbytes()) - 1, (1 << 16) - 1).bit_length()
+            ws = self._ws_sized.get(size)
+            if ws is None:
+                ws = self._ws_sized[size] = torch.empty(size, dtype=torch.uint8, device=self.device)
+            if len(self._ws_of) >= 256:
+                self._ws_of.clear()
+            self._ws_of[key] = ws
         return ws
 
     def decode_attention(self, q: torch.Tensor, out: torch.Tensor | None = None, seq_begin: int = 0,

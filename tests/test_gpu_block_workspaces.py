@@ -1,5 +1,5 @@
 """Workspaces of the block-scaled cache's attentions: choices larger than a
-sequence."""
+sequence, and what a cache keeps over many kinds of calls."""
 import pytest
 import torch
 
@@ -54,3 +54,35 @@ def test_choices_larger_than_a_sequence(top, recent, bias):
         if closed <= top + recent:
             torch.testing.assert_close(out[b].float(), whole[b].float(), rtol=2 ** -7, atol=1e-3)
     assert c.read_status() == 0
+
+
+def test_a_cache_keeps_few_workspaces():
+    """Calls of many batches and choices share a few buffers; the results are those of
+    workspaces of their own, also of calls captured before the buffers were shared."""
+    lengths = [900] + [40 + 7 * b for b in range(12)]
+    c, q = _cache(lengths)
+    lib, h = c.lib, c.handle
+    kinds = [(b, top, recent) for b in (1, 2, 5, 12) for top in range(1, 60) for recent in (0, 3)]
+    largest = max(max(lib.kvc_block_selected_workspace_bytes(h, *k) for k in kinds),
+                  max(lib.kvc_block_prefix_workspace_bytes(h, b) for b in range(1, 13)))
+    c.prefix_attention(q[1:6], 0, seq_begin=1)
+    held = torch.empty_like(q[1:6])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.prefix_attention(q[1:6], 0, seq_begin=1, out=held)
+    before = torch.cuda.memory_allocated()
+    for k in kinds:
+        got = c.selected_attention(q[:k[0]], k[1], recent_blocks=k[2])
+        if k[1] % 19 == 1:
+            own = torch.empty(lib.kvc_block_selected_workspace_bytes(h, *k), dtype=torch.uint8, device="cuda")
+            assert torch.equal(got, c.selected_attention(q[:k[0]], k[1], recent_blocks=k[2], workspace=own))
+    for b in range(1, 13):
+        got = c.prefix_attention(q[1:1 + b], 0, seq_begin=1)
+        own = torch.empty(lib.kvc_block_prefix_workspace_bytes(h, b), dtype=torch.uint8, device="cuda")
+        assert torch.equal(got, c.prefix_attention(q[1:1 + b], 0, seq_begin=1, workspace=own))
+    own = got = None
+    # size classes are powers of two: all buffers together are below four times the largest need
+    assert torch.cuda.memory_allocated() - before <= 4 * largest + (1 << 20)
+    graph.replay()
+    assert torch.equal(held, c.prefix_attention(q[1:6], 0, seq_begin=1)) and c.read_status() == 0
