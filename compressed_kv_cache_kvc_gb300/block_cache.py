@@ -210,9 +210,9 @@ class BlockScaledCache:
                            softcap: float = 0.0, slopes: torch.Tensor | None = None,
                            return_blocks: bool | torch.Tensor = False, workspace=None, stream=None):
         """`decode_attention` to the sinks, the open block, the `recent_blocks`
-        newest closed blocks and, of the others, the `top_blocks` whose keys'
-        bounds promise the largest products with the query heads of the KV head
-        (a cache made with key_bounds).  return_blocks: True, or an int32 tensor
+        newest closed blocks and, of the others, the `top_blocks` that score
+        highest: an estimate of a block's largest product with the query heads of
+        the KV head from its keys' bounds (a cache made with key_bounds).  return_blocks: True, or an int32 tensor
         [batch, Hkv, top_blocks + recent_blocks], returns (out, blocks) with the
         chosen blocks, ascending, -1 behind the last."""
         if stream is not None:

@@ -1,16 +1,17 @@
 // Attention to selected blocks of the block-scaled cache: a cheap score of every
 // closed block, the choice of the best, the attention over them.
 //
-// The score bounds the block's dot products from above.  With q8 the INT8 codes
+// The score estimates the largest dot product of the block's keys.  With q8 the INT8 codes
 // of a query row (s = amax / 127, code = round-half-even(q / s), IEEE fp32), lo and
 // hi the least and the largest INT8 code of a channel of the block's keys (scale
 // t) and
 //   I = sum over the channels of max(q8 lo, q8 hi)
 //     = sum of min(q8, 0) lo + max(q8, 0) hi,
 // the score is (I s) t, both products rounded to fp32, and a KV head's the largest
-// of its query heads'.  |I| <= 127^2 128 < 2^24: I is exact, and so the scores are
-// the same bits wherever they are computed, and the choice (ties to the lower
-// block) is too.
+// of its query heads'.  I is at least the product of the query's codes with those of any
+// key of the block; values, which the codes round, may have a larger product than the
+// score.  |I| <= 127^2 128 < 2^24: I is exact, and so the scores are the same bits
+// wherever they are computed, and the choice (ties to the lower block) is too.
 //
 // block_score_kernel: 260 bytes of bounds per block and KV head: 16 x 8 KV heads of up to
 // 65,536 tokens in blocks of 32, 48 MB: 11.5 us, 4.2 TB/s, the integer matrix pipe 46 %

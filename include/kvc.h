@@ -720,13 +720,14 @@ kvc_status kvc_block_attention(kvc_block_cache* cache, int32_t seq_begin, int32_
 /* The same over selected blocks of each (sequence, KV head): of the closed blocks
  * the `recent_blocks` newest and, of the others, the `top_blocks` whose score is
  * highest (ties to the lower block), beside the sinks and the open block.  Needs
- * the keys' bounds (kvc_block_set_key_bounds).  A block's score for a query head
- * bounds its products with the block's keys from above: with q8 the INT8 codes of
- * the query row and s their scale (as a row of kvc_quantize_append), lo, hi and t the
- * block's bounds and their scale,
+ * the keys' bounds (kvc_block_set_key_bounds).  A block's score for a query head: with
+ * q8 the INT8 codes of the query row and s their scale (as a row of
+ * kvc_quantize_append), lo, hi and t the block's bounds and their scale,
  *   I = sum over the 128 channels of max(q8 lo, q8 hi),  score = (I s) t,
  * I exact, both products rounded to fp32; a KV head takes the largest of its query
- * heads' scores.  Neither softcap (which keeps the order) nor slopes enter the choice;
+ * heads' scores.  I bounds the product of the query's codes with the INT8 codes of every
+ * key of the block from above; of the query's and the keys' values, which the codes
+ * round, the score is an estimate and may be less than their product.  Neither softcap (which keeps the order) nor slopes enter the choice;
  * both enter the attention.
  *   d_blocks: null, or i32 [batch][Hkv][top_blocks + recent_blocks]: the chosen
  *   blocks (0 holds positions 4 ..), ascending, -1 behind the last.
