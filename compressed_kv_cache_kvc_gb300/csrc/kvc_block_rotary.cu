@@ -47,9 +47,12 @@ constexpr int kTableRows = kUnitRows + kSinks;   // (the exact rows: at most 4 +
 constexpr int kTableRow = kRotPairs * 8;
 constexpr int kOffTable = kWarps * kStages * kStage;
 constexpr int kSmem = kOffTable + kTableRows * kTableRow;
-// rows of queries from which they are turned by a launch of their own (1 x 32 heads x
-// 512 / 1,024 / 8,192 tokens 25.2 / 29.3 / 55.9 us in the append's CTAs, 26.2 / 27.3 /
-// 53.9 apart, before the append; 64 x 8 x 41 31.4 both, for a launch more)
+// rows of queries from which they are turned by a launch of their own, under the append.
+// With the release, in a graph, in the append's CTAs / apart: 1 x 32 heads on 8 x 1,024 /
+// 2,048 / 8,192 tokens 29 / 31 / 56, 21 / 22 / 49 us; 64 x 32 on 8 x 16 / 41 16.4 / 30, 17.1 /
+// 26; 8 x 32 on 8 x 8,192 328, 299.  Fewer rows are left to one launch, which the host issues
+// 1.3 to 2.3 us sooner, although the GPU would gain by two there too: 1 x 32 on 8 x 64 /
+// 512 17 / 25, 15 / 21; 64 x 8 x 41 28, 23; 64 x 32 on 8 x 1 12.0, 9.9, but eager 14.9, 16.0.
 constexpr long long kManyQueryRows = 1 << 15;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
