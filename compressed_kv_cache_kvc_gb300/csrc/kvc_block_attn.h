@@ -67,9 +67,10 @@ enum { kPlain = 0, kSelected = 1, kPrefix = 2 };  // forms
 // exact rows go first, under the first pages' copies or the choice of the blocks (with
 // the launches overlapped and the merge without bank conflicts 64 x 32 heads after a
 // prefix of 32,768 tokens 119 -> 73 us, 16 x 32 heads of selected blocks 71 -> 60).
-// 16 x 32 heads with 128 of 2,048 blocks of 32 tokens each: 31 us, 4.4 TB/s, at two or
-// three CTAs per SM and four or six pages of ring alike: blocks of 4 KB in no order,
-// and the round trips and joins that one sequence's 11 us are made of.
+// 16 x 32 heads with 128 of 2,048 blocks of 32 tokens each: 31 us, 4.4 TB/s: blocks of
+// 4 KB in no order, the round trips and joins that one sequence's 11 us are made of,
+// and uneven CTAs (the busiest SM has 258 units, the mean is 217).  Two or three CTAs per
+// SM and four or six pages of ring took the same, with that busiest SM in each.
 // kPrefix joins the partials of the prefix's product with the pair's own.  Where the
 // pair has one CTA a warp has up to 20 rows of them on their way under the merge of the
 // warps, and nothing goes through memory (64 x 32 heads: 65.6 -> 61.4 us a call).

@@ -185,8 +185,8 @@ void split_attention(kvc_block_cache* c, kvc::BlockAttn* a, int per_sm, int batc
 // The parts of pairs of the selected and the prefix form: up to `parts` CTAs for every
 // pair, of at least part_units units each, so that the parts of all pairs make about
 // one wave (two CTAs per SM with all their registers; three with 168 measured 51.2
-// against 50.9 us for 16 x 32 heads of 65,536 selected tokens, 73.4 against 73.7 for a
-// prefix's 64 x 32).
+// against 50.9 us for 16 x 32 heads of 65,536 selected tokens, where the busiest SM has as
+// many units either way, 73.4 against 73.7 for a prefix's 64 x 32).
 constexpr int kCtasPerSm = 2;
 void split_pairs(kvc_block_cache* c, kvc::BlockAttn* a, int batch, long long units) {
   const long long pairs = (long long)batch * c->cfg.num_kv_heads, slots = kCtasPerSm * sm_count(c);

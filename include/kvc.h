@@ -702,7 +702,8 @@ kvc_status kvc_block_set_key_bounds(kvc_block_cache* cache, void* d_bounds, size
  * sums are fp32.  A probability enters its product with V's codes times the V scale
  * and in fp16: 11 bits down to 2^-14 of the largest such product of its query head, off
  * by 2^-25 of it below (with V held exactly in 16 bits).  V of any finite size, blocks
- * and exact rows of different sizes included: what has no weight costs no bits.
+ * and exact rows of different sizes included: a block or an exact row without weight
+ * costs the others no bits, whatever its V.
  *   d_workspace: kvc_block_workspace_bytes(cache, batch) bytes, 256-byte
  *   aligned, contents arbitrary.
  * One launch: the CTA that finishes a (sequence, KV head) last joins its
