@@ -113,3 +113,23 @@ def test_replays_of_several_units(queries):
         plain.append(kr, v.contiguous())
         _same(both, plain)
         assert not queries or torch.equal(out, qr)
+
+
+@pytest.mark.parametrize("n", [5, 3000])
+def test_in_place_broadcast_and_streams(n):
+    """Queries turned in place, keys and values broadcast over the batch, a call on
+    another stream."""
+    from compressed_kv_cache_kvc_gb300 import Rotary
+    rot = Rotary(32, adjacent=True)
+    b, hkv, block = 3, 4, 16
+    both, plain = (_cache(16, hkv, b, n, block, "int8", False) for _ in range(2))
+    q = _rows(1, b, n, 16)[0].contiguous()
+    k, v = (x.expand(b, -1, -1, -1) for x in _rows(2, 1, n, hkv, hkv))
+    qr, kr = rot.rotate(q, k, first=11)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert both.append_rotary(q, k, v, rot, first=11, out=q, stream=side) is q
+    side.synchronize()
+    assert torch.equal(q, qr)
+    plain.append(kr, v.contiguous())
+    _same(both, plain)

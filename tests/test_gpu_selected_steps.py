@@ -169,3 +169,48 @@ def test_prefix_on_both_sides_of_its_rule(batch, prefix, product, codes, cap, bi
     graph.replay()
     torch.testing.assert_close(held.float(), call().float(), rtol=2 ** -7, atol=1e-3)
     assert cache.read_status() == 0
+
+
+def _formula(got, qf, kd, vd, newest, at):
+    z = R.scores(qf, kd, SCALE, 0.0, 0.0, [newest], at)
+    p = R.softmax_rows(z)
+    ref = p @ vd
+    bound = R.output_bound(ref, p, vd, R.score_error(z, 0.0, np.ones_like(z, bool)))
+    assert (np.abs(got - ref[0]) <= bound[0]).all()
+
+
+@pytest.mark.parametrize("prefix", [3, 100, 900])
+def test_more_pairs_than_places(prefix):
+    """700 sequences of 4 KV heads: more pairs than an attention has places for parts."""
+    hq, hkv, block, B, top, recent = 8, 4, 16, 700, 3, 2
+    rand = _gen(prefix)
+    own = [1 + 7 * b % 211 for b in range(B)]
+    cache = _cache(hq, hkv, [prefix] + own, block, bounds=True)
+    kv = {}
+    for s, n in enumerate([prefix] + own):
+        k, v = rand(1, hkv, n, 128), rand(1, hkv, n, 128)
+        cache.append(k, v, seq_begin=s)
+        if s in (0, 1, 330, 700):
+            kv[s] = [x[0].float().cpu().numpy() for x in (k, v)]
+    q = rand(B, hq, 128)
+    out = T.bf16_tensor_to_f32(cache.prefix_attention(q, 0, seq_begin=1))
+    few, blocks = cache.selected_attention(q, top, recent_blocks=recent, seq_begin=1, return_blocks=True)
+    few, blocks, qf = T.bf16_tensor_to_f32(few), blocks.cpu().numpy(), q.float().cpu().numpy()
+    for s in (1, 330, 700):
+        n, closed = own[s - 1], max(own[s - 1] - 4, 0) // block
+        for j in (0, 3, 7):
+            h = j * hkv // hq
+            front, mine = ([R.held_block(x[h], block, False) for x in kv[i]] for i in (0, s))
+            _formula(out[s - 1, j], qf[s - 1, j:j + 1], *(np.concatenate(x) for x in zip(front, mine)), 0, np.zeros(prefix + n))
+            want = _choice(qf[s - 1, 2 * h:2 * h + 2], kv[s][0][h], block, top, recent) if closed else []
+            assert blocks[s - 1, h].tolist() == want + [-1] * (top + recent - len(want))
+            at = np.concatenate([np.arange(min(n, 4))] + [4 + c * block + np.arange(block) for c in want]
+                                + [np.arange(4 + closed * block, n)]).astype(int)
+            _formula(few[s - 1, j], qf[s - 1, j:j + 1], mine[0][at], mine[1][at], n - 1, at)
+    # slices of the same cache make the same choice
+    part, chosen = cache.selected_attention(q[200:203], top, recent_blocks=recent, seq_begin=201, return_blocks=True)
+    assert np.array_equal(chosen.cpu().numpy(), blocks[200:203])
+    torch.testing.assert_close(part.float().cpu(), torch.from_numpy(few[200:203]), rtol=2 ** -7, atol=1e-3)
+    part = cache.prefix_attention(q[200:203], 0, seq_begin=201)
+    torch.testing.assert_close(part.float().cpu(), torch.from_numpy(out[200:203]), rtol=2 ** -7, atol=1e-3)
+    assert cache.read_status() == 0 and (cache.buffer("TICKETS").view(torch.int32) == 0).all()
